@@ -19,6 +19,8 @@ from ._lib import (VT_BF16, VT_DEV_BAD_DRAFT, VT_DEV_BAD_ID,  # noqa: F401
 
 __all__ = ["vt_selftest_wait", "vt_calibrate_topk", "vt_calibrate_top_p", "vt_calibrate_min_count", "vt_trim_head",
            "vt_draft_logits", "vt_draft_step", "vt_draft_topk", "vt_verify", "vt_verify_tree",
+           "vt_quantize_head", "vt_draft_logits_fp8", "vt_draft_step_fp8", "vt_draft_topk_fp8",
+           "vt_token_logprobs",
            "BlockGraph",
            "workspace_bytes",
            "VtError", "lib"]
@@ -95,6 +97,10 @@ def workspace_bytes(kind: str, **kw) -> int:
         return L.vt_trim_head_workspace_bytes(kw["V"], kw["K"])
     if kind == "draft":
         return L.vt_draft_workspace_bytes(kw["B"], kw["H"], kw["K"])
+    if kind == "draft_fp8":
+        return L.vt_draft_fp8_workspace_bytes(kw["B"], kw["H"], kw["K"])
+    if kind == "draft_topk_fp8":
+        return L.vt_draft_topk_fp8_workspace_bytes(kw["B"], kw["H"], kw["K"], kw["k"])
     if kind == "verify":
         return L.vt_verify_workspace_bytes(kw["B"], kw["gamma"], kw["V"], kw["K"])
     raise ValueError(kind)
@@ -420,6 +426,282 @@ def vt_verify_tree(target_logits, parent, tokens, temperature: float = 0.0, out_
                           _stream_ptr(stream))
     _lib.check("vt_verify_tree", st)
     return out_tokens, out_num_accepted, out_path, dev_status
+
+
+def _fp8_dtypes():
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _on_current(stream, *named):
+    """The raw stream of a call whose tensors must all be on the current
+    device (and `stream`, where given, on the same one)."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    if stream is not None and stream.device.index != cur:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{cur}")
+    return _stream_ptr(stream)
+
+
+def _made(t, stream):
+    """A tensor allocated by a call that runs on `stream`: its memory is not
+    given to another before that stream has passed this point."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _head_fp8(W8, w_scale, H=None):
+    """(K, H, row stride) of an e4m3 head and its block scales."""
+    torch = _torch()
+    if not isinstance(W8, torch.Tensor):
+        raise TypeError("W8 must be a torch.Tensor")
+    if not W8.is_cuda:
+        raise ValueError("W8 must be a CUDA tensor")
+    if W8.dtype not in _fp8_dtypes():
+        raise TypeError(f"W8 has dtype {W8.dtype}, expected one of {_fp8_dtypes()}")
+    if W8.dim() != 2 or W8.shape[0] < 1 or W8.shape[1] < 1:
+        raise ValueError("W8 must be [K, H]")
+    K, H8 = W8.shape
+    ldw = W8.stride(0) if K > 1 else (H8 + 15) // 16 * 16
+    if (H8 > 1 and W8.stride(1) != 1) or ldw < H8 or ldw % 16 or W8.data_ptr() % 16:
+        raise ValueError("W8 must have unit inner stride, a row stride that is a multiple of 16 and "
+                         "a 16-byte aligned start")
+    if H is not None and H8 != H:
+        raise ValueError("hidden and W8 disagree on H")
+    _dev(w_scale, "w_scale", (torch.float32,), 2)
+    if tuple(w_scale.shape) != ((K + 127) // 128, (H8 + 127) // 128):
+        raise ValueError("w_scale must be [ceil(K/128), ceil(H/128)]")
+    return K, H8, ldw
+
+
+def vt_quantize_head(W, W8=None, w_scale=None, dev_status=None, stream=None):
+    """The head [K, H] (bf16) as e4m3 with one power-of-two scale per block of
+    128 x 128.
+
+    Returns (W8 [K, H] float8_e4m3fn, a view whose row stride is a multiple of
+    16, w_scale float32 [ceil(K/128), ceil(H/128)], dev_status).
+    """
+    torch = _torch()
+    _dev(W, "W", _bf16_dtypes(), 2)
+    K, H = W.shape
+    if K < 1 or H < 1:
+        raise ValueError("W must have rows and columns")
+    dev = W.device
+    if W8 is None:
+        W8 = _made(torch.empty((K, (H + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=dev),
+                   stream)[:, :H]
+    if w_scale is None:
+        w_scale = _made(torch.empty(((K + 127) // 128, (H + 127) // 128), dtype=torch.float32,
+                                    device=dev), stream)
+    if dev_status is None:
+        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
+    _, _, ldw = _head_fp8(W8, w_scale, H)
+    if W8.shape[0] != K:
+        raise ValueError("W8 must be [K, H]")
+    _dev(dev_status, "dev_status", (torch.int32,), 1)
+    s = _on_current(stream, ("W", W), ("W8", W8), ("w_scale", w_scale), ("dev_status", dev_status))
+    st = lib().vt_quantize_head(W.data_ptr(), K, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
+                                dev_status.data_ptr(), s)
+    _lib.check("vt_quantize_head", st)
+    return W8, w_scale, dev_status
+
+
+def vt_draft_logits_fp8(hidden, W8, w_scale, temperature: float = 1.0, logits=None, workspace=None,
+                        stream=None):
+    """vt_draft_logits through an e4m3 head (vt_quantize_head); the hidden
+    states are quantised inside the call."""
+    torch = _torch()
+    _dev(hidden, "hidden", _bf16_dtypes(), 2)
+    B, H = hidden.shape
+    K, _, ldw = _head_fp8(W8, w_scale, H)
+    dev = hidden.device
+    if logits is None:
+        logits = _made(torch.empty((B, K), dtype=torch.float32, device=dev), stream)
+    _rows_out(logits, "logits", B, K)
+    L = lib()
+    if workspace is None:
+        workspace = _made(_ws(L.vt_draft_fp8_workspace_bytes(B, H, K), dev), stream)
+    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
+                    ("logits", logits), ("workspace", workspace))
+    st = L.vt_draft_logits_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(), K,
+                               float(temperature), logits.data_ptr(),
+                               max(logits.stride(0), K), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), s)
+    _lib.check("vt_draft_logits_fp8", st)
+    return logits
+
+
+def _rows_out(t, name, B, K):
+    """An fp32 output of B rows and at least K columns, unit inner stride, rows apart."""
+    torch = _torch()
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or
+            t.dim() != 2 or t.shape[0] != B or t.shape[1] < K or (K > 1 and t.stride(1) != 1) or
+            (B > 1 and t.stride(0) < K)):
+        raise ValueError(f"{name} must be a float32 CUDA tensor [{B}, >= {K}] with unit inner stride")
+    return t
+
+
+def vt_draft_step_fp8(hidden, W8, w_scale, trim_ids, uniforms, temperature: float = 1.0, q=None,
+                      tokens=None, dev_status=None, workspace=None, stream=None):
+    """vt_draft_step through an e4m3 head; returns (q [B, K], tokens int32 [B],
+    dev_status).  q and tokens may be strided views as there; temperature == 0
+    drafts greedily (uniforms may then be None)."""
+    torch = _torch()
+    greedy = float(temperature) == 0.0
+    _dev(hidden, "hidden", _bf16_dtypes(), 2)
+    B, H = hidden.shape
+    K, _, ldw = _head_fp8(W8, w_scale, H)
+    _dev(trim_ids, "trim_ids", (torch.int32,), 1)
+    if uniforms is not None or not greedy:
+        _dev(uniforms, "uniforms", (torch.float32,), 1)
+    if (uniforms is not None and uniforms.numel() != B) or trim_ids.numel() != K:
+        raise ValueError("uniforms must have B and trim_ids K elements")
+    dev = hidden.device
+    if q is None:
+        q = _made(torch.empty((B, K), dtype=torch.float32, device=dev), stream)
+    _rows_out(q, "q", B, K)
+    if q.shape[1] != K:
+        raise ValueError("q must be [B, K]")
+    if tokens is None:
+        tokens = _made(torch.empty(B, dtype=torch.int32, device=dev), stream)
+    if (not tokens.is_cuda or tokens.dim() != 1 or tokens.shape[0] != B or
+            tokens.dtype != torch.int32 or (B > 1 and tokens.stride(0) < 1)):
+        raise ValueError("tokens must be an int32 CUDA vector of B entries (any positive stride)")
+    if dev_status is None:
+        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
+    _dev(dev_status, "dev_status", (torch.int32,), 1)
+    L = lib()
+    if workspace is None:
+        workspace = _made(_ws(L.vt_draft_fp8_workspace_bytes(B, H, K), dev), stream)
+    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
+                    ("trim_ids", trim_ids), ("uniforms", uniforms), ("q", q), ("tokens", tokens),
+                    ("dev_status", dev_status), ("workspace", workspace))
+    st = L.vt_draft_step_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
+                             trim_ids.data_ptr(), K,
+                             uniforms.data_ptr() if uniforms is not None else None,
+                             float(temperature), q.data_ptr(), max(q.stride(0), K),
+                             tokens.data_ptr(), max(tokens.stride(0), 1), dev_status.data_ptr(),
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    _lib.check("vt_draft_step_fp8", st)
+    return q, tokens, dev_status
+
+
+def vt_draft_topk_fp8(hidden, W8, w_scale, trim_ids, k: int, temperature: float = 1.0, out_ids=None,
+                      out_logq=None, dev_status=None, workspace=None, stream=None):
+    """vt_draft_topk through an e4m3 head.  Returns (out_ids int32 [B, k],
+    out_logq [B, k], dev_status [1])."""
+    torch = _torch()
+    _dev(hidden, "hidden", _bf16_dtypes(), 2)
+    B, H = hidden.shape
+    K, _, ldw = _head_fp8(W8, w_scale, H)
+    _dev(trim_ids, "trim_ids", (torch.int32,), 1)
+    if trim_ids.numel() != K:
+        raise ValueError("trim_ids must have K elements")
+    k = int(k)
+    if not 1 <= k <= min(32, K):
+        raise ValueError("k must be in [1, min(32, K)]")
+    dev = hidden.device
+    if out_ids is None:
+        out_ids = _made(torch.empty((B, k), dtype=torch.int32, device=dev), stream)
+    if out_logq is None:
+        out_logq = _made(torch.empty((B, k), dtype=torch.float32, device=dev), stream)
+    if dev_status is None:
+        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
+    _dev(out_ids, "out_ids", (torch.int32,), 2)
+    _dev(out_logq, "out_logq", (torch.float32,), 2)
+    _dev(dev_status, "dev_status", (torch.int32,), 1)
+    if tuple(out_ids.shape) != (B, k) or tuple(out_logq.shape) != (B, k):
+        raise ValueError("out_ids and out_logq must be [B, k]")
+    L = lib()
+    if workspace is None:
+        workspace = _made(_ws(L.vt_draft_topk_fp8_workspace_bytes(B, H, K, k), dev), stream)
+    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
+                    ("trim_ids", trim_ids), ("out_ids", out_ids), ("out_logq", out_logq),
+                    ("dev_status", dev_status), ("workspace", workspace))
+    st = L.vt_draft_topk_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
+                             trim_ids.data_ptr(), K, k, float(temperature), out_ids.data_ptr(),
+                             out_logq.data_ptr(), dev_status.data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), s)
+    _lib.check("vt_draft_topk_fp8", st)
+    return out_ids, out_logq, dev_status
+
+
+def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_logp=None,
+                      out_entropy=None, out_top_ids=None, out_top_logp=None, dev_status=None,
+                      stream=None, want_entropy: bool = True):
+    """Log probabilities of given tokens under rows of logits.
+
+    logits [R, V] or [B, R, V], float32 or bf16, unit inner stride and evenly
+    spaced rows; tokens int32 of logits' leading shape, -1 = row not scored.
+    Returns (logp, entropy or None, top_ids, top_logp, dev_status), logp and
+    entropy of tokens' shape, top_ids int32 and top_logp [..., k] (None where
+    k == 0): the k best ids, ties to the lower, with their log probabilities.
+    """
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype == torch.float32:
+        dt = VT_F32
+    elif logits.dtype in _bf16_dtypes():
+        dt = VT_BF16
+    else:
+        raise TypeError("logits must be float32 or bf16")
+    shape = tuple(logits.shape[:-1])
+    if logits.dim() not in (2, 3) or 0 in logits.shape:
+        raise ValueError("logits must be [R, V] or [B, R, V]")
+    V = logits.shape[-1]
+    R = shape[0] if len(shape) == 1 else shape[0] * shape[1]
+    st = logits.stride()
+    if shape[-1] > 1:
+        ld = st[-2]
+        even = len(shape) == 1 or shape[0] == 1 or st[0] == shape[1] * ld
+    else:
+        ld = st[0] if shape[0] > 1 else V
+        even = True
+    if (V > 1 and st[-1] != 1) or not even or ld < V:
+        raise ValueError("logits must have unit inner stride and evenly spaced rows")
+    k = int(k)
+    if not 0 <= k <= min(32, V):
+        raise ValueError("k must be in [0, min(32, V)]")
+    _dev(tokens, "tokens", (torch.int32,), len(shape))
+    if tuple(tokens.shape) != shape:
+        raise ValueError("tokens must have the leading shape of logits")
+    dev = logits.device
+    f32, i32 = (torch.float32,), (torch.int32,)
+
+    def out(t, name, want, dtypes):
+        if t is None:
+            return _made(torch.empty(want, dtype=dtypes[0], device=dev), stream)
+        _dev(t, name, dtypes)
+        if tuple(t.shape) != want:
+            raise ValueError(f"{name} must be {list(want)}")
+        return t
+
+    out_logp = out(out_logp, "out_logp", shape, f32)
+    if out_entropy is not None or want_entropy:
+        out_entropy = out(out_entropy, "out_entropy", shape, f32)
+    if k:
+        out_top_ids = out(out_top_ids, "out_top_ids", shape + (k,), i32)
+        out_top_logp = out(out_top_logp, "out_top_logp", shape + (k,), f32)
+    else:
+        out_top_ids = out_top_logp = None
+    dev_status = out(dev_status, "dev_status", (1,), i32)
+    s = _on_current(stream, ("logits", logits), ("tokens", tokens), ("out_logp", out_logp),
+                    ("out_entropy", out_entropy), ("out_top_ids", out_top_ids),
+                    ("out_top_logp", out_top_logp), ("dev_status", dev_status))
+    rc = lib().vt_token_logprobs(logits.data_ptr(), dt, R, V, ld, tokens.data_ptr(), k,
+                                 float(temperature), out_logp.data_ptr(),
+                                 out_entropy.data_ptr() if out_entropy is not None else None,
+                                 out_top_ids.data_ptr() if k else None,
+                                 out_top_logp.data_ptr() if k else None, dev_status.data_ptr(), s)
+    _lib.check("vt_token_logprobs", rc)
+    return out_logp, out_entropy, out_top_ids, out_top_logp, dev_status
 
 
 def vt_selftest_wait(which: int, limit: int, flag=None, dev_status=None, stream=None):

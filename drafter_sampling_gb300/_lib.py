@@ -69,6 +69,17 @@ SIGNATURES = {
     "vt_draft_topk_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
     "vt_draft_topk": (C.c_int, [_p, _i32, _i32, _p, _p, _i32, _i32, _f32, _p, _p, _p, _p, _sz,
                                 _p]),
+    "vt_quantize_head": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _p, _p]),
+    "vt_draft_fp8_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "vt_draft_logits_fp8": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _sz,
+                                      _p]),
+    "vt_draft_step_fp8": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _p, _i32, _p, _f32, _p, _i64,
+                                    _p, _i64, _p, _p, _sz, _p]),
+    "vt_draft_topk_fp8_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "vt_draft_topk_fp8": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _p, _i32, _i32, _f32, _p, _p,
+                                    _p, _p, _sz, _p]),
+    "vt_token_logprobs": (C.c_int, [_p, _i32, _i64, _i32, _i64, _p, _i32, _f32, _p, _p, _p, _p,
+                                    _p, _p]),
     "vt_verify_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
     "vt_verify": (C.c_int, [_p, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _p, _f32, _p,
                             _p, _p, _p, _p, _sz, _p]),

@@ -39,6 +39,22 @@
 namespace cg = cooperative_groups;
 
 namespace vt {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  // looked up once; the initialisation of a function-local static is
+  // thread-safe, so concurrent first calls from several host threads agree
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
 namespace {
 
 constexpr int kGemvNT = 256;        // 8 warps
@@ -543,7 +559,6 @@ __global__ void __launch_bounds__(kFinNT) draft_greedy_finalize_kernel(GreedyFin
 // writes z2 = z * log2(e) / T and the per-tile softmax partials; each CTA of
 // topk_chunk takes 1024 ids and leaves its k best in order; topk_final
 // merges the chunks' lists of a row and converts to log q.
-constexpr int kTopkMax = 32;
 constexpr int kTkNT = 256;               // 8 warps
 constexpr int kTkE = 16;                 // ids per lane per chunk
 constexpr int kTkSpan = kTkNT * kTkE;    // ids per CTA per pass
@@ -872,21 +887,6 @@ int launch_gemv(cudaStream_t s, const uint16_t* hidden, int B, int H, const uint
   return e == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  // looked up once; the initialisation of a function-local static is
-  // thread-safe, so concurrent first calls from several host threads agree
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
-  return fn;
-}
-
 // 2-D tensor map of a row-major bf16 [rows, cols] matrix, boxes of
 // 64 columns (128 bytes, 128-byte swizzle) x box_rows rows
 bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
@@ -1060,14 +1060,21 @@ int vt::draft_step_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint
                    ws.part, nullptr, 0, dev_status, status_reset, greedy ? 1 : 0, &grid,
                    &tile_rows, hidden_ready);
   if (st != VT_OK) return st;
+  return draft_finish(s, B, K, greedy, ws.part, grid, tile_rows, uniforms, trim_ids, q, ldq, tokens,
+                      ld_tokens, dev_status);
+}
+
+int vt::draft_finish(cudaStream_t s, int B, int K, bool greedy, const float2* part, int G,
+                     int tile_rows, const float* uniforms, const int32_t* trim_ids, float* q,
+                     int64_t ldq, int32_t* tokens, int64_t ld_tokens, int32_t* dev_status) {
   if (greedy) {
     GreedyFinArgs ga;
     ga.q = q;
     ga.ldq = ldq;
     ga.B = B;
     ga.K = K;
-    ga.part = ws.part;
-    ga.G = grid;
+    ga.part = part;
+    ga.G = G;
     ga.trim_ids = trim_ids;
     ga.tokens = tokens;
     ga.ldt = ld_tokens;
@@ -1093,8 +1100,8 @@ int vt::draft_step_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint
   fa.ldq = ldq;
   fa.B = B;
   fa.K = K;
-  fa.part = ws.part;
-  fa.G = grid;
+  fa.part = part;
+  fa.G = G;
   fa.tile_rows = tile_rows;
   fa.u = uniforms;
   fa.trim_ids = trim_ids;
@@ -1121,7 +1128,7 @@ int vt::draft_step_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint
 }
 
 extern "C" size_t vt_draft_topk_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t k) {
-  if (B < 1 || K < 1 || k < 1 || k > vt::kTopkMax || k > K) return 0;
+  if (B < 1 || K < 1 || k < 1 || k > vt::kDraftTopkMax || k > K) return 0;
   return vt::align_up(vt_draft_workspace_bytes(B, H, K), 256) +
          vt::align_up((size_t)B * K * 4, 256);
 }
@@ -1133,7 +1140,7 @@ extern "C" int vt_draft_topk(const uint16_t* hidden, int32_t B, int32_t H, const
   using namespace vt;
   int st = check_draft_args(hidden, B, H, W_trim, K, temperature, false);
   if (st != VT_OK) return st;
-  if (!trim_ids || !out_ids || !out_logq || !dev_status || k < 1 || k > kTopkMax || k > K)
+  if (!trim_ids || !out_ids || !out_logq || !dev_status || k < 1 || k > kDraftTopkMax || k > K)
     return VT_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return VT_ERR_WORKSPACE;
   if (workspace_bytes < vt_draft_topk_workspace_bytes(B, H, K, k)) return VT_ERR_WORKSPACE;
@@ -1146,13 +1153,19 @@ extern "C" int vt_draft_topk(const uint16_t* hidden, int32_t B, int32_t H, const
   st = launch_head(s, hidden, B, H, W_trim, K, VT_LOG2E / temperature, z2, K, dws.part, nullptr,
                    0, dev_status, 1, 0, &grid, &tile_rows);
   if (st != VT_OK) return st;
+  return draft_topk_finish(s, z2, B, K, k, dws.part, grid, trim_ids, out_ids, out_logq, dev_status);
+}
+
+int vt::draft_topk_finish(cudaStream_t s, const float* z2, int B, int K, int k, const float2* part,
+                          int G, const int32_t* trim_ids, int32_t* out_ids, float* out_logq,
+                          int32_t* dev_status) {
   TopkArgs a;
   a.z2 = z2;
   a.B = B;
   a.K = K;
   a.k = k;
-  a.part = dws.part;
-  a.G = grid;
+  a.part = part;
+  a.G = G;
   a.trim_ids = trim_ids;
   a.out_ids = out_ids;
   a.out_logq = out_logq;

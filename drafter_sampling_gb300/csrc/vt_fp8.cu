@@ -1,0 +1,629 @@
+// The drafter's head in 8-bit floating point (e4m3) on sm_103a.
+//
+//   quantise   W8[j, h] = e4m3(W[j, h] / s), s = w_scale[j / 128, h / 128] the
+//              smallest power of two >= 2^-126 with max |block| <= 448 s
+//   product    z[b, j] = out_scale * sum_g sw[j / 128, g] sx[b, g]
+//                                    * sum_{h in group g} x8[b, h] W8[j, h]
+//              with x8, sx the hidden states quantised by the same rule per
+//              row and group of 128 columns
+//
+// Power-of-two scales make every division exact, so the 8-bit values do not
+// depend on how a division rounds, and cost no precision: a floating-point
+// format has the same relative step at any scale (a block's largest value
+// lands in (224, 448] rather than on 448; at worst one of e4m3's 18 binades
+// is not used).  The product takes any fp32 weight scales.
+#include <algorithm>
+#include <cmath>
+
+#include <cudaTypedefs.h>
+
+#include "vt_common.cuh"
+#include "vt_internal.h"
+#include "vt_umma.cuh"
+
+namespace vt {
+namespace {
+
+constexpr int kQB = 128;  // side of a scale block
+
+// Exponent e of a block's scale 2^e from the bf16 bits of its largest
+// magnitude (sign cleared): the smallest e >= -126 with amax <= 448 * 2^e.
+// amax = f 2^p, 1 <= f < 2, 448 = 1.75 * 2^8: e = p - 8, one more when
+// f > 1.75 (bf16 mantissa above 0x60).
+__device__ __forceinline__ int scale_exponent(uint32_t amax_bf16) {
+  const int e = (int)(amax_bf16 >> 7) - 127 - 8 + ((amax_bf16 & 0x7fu) > 0x60u ? 1 : 0);
+  return max(e, -126);
+}
+__device__ __forceinline__ float exact_pow2(int e) {  // -126 <= e <= 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// two floats to two e4m3 bytes, round to nearest even: a in the low byte
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// one word of two bf16 values times inv (a power of two: exact)
+__device__ __forceinline__ uint32_t scale_e4m3x2(uint32_t w, float inv) {
+  return e4m3x2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
+}
+
+// ------------------------------------------------------------ weights
+constexpr int kQuantNT = 256;
+constexpr int kQuantU = kQB * kQB / 8 / kQuantNT;  // 16-byte loads per thread (8)
+
+// One CTA per 128 x 128 block: the block is read once (eight 16-byte loads
+// in flight per thread), its largest magnitude reduced, and the registers
+// scaled, rounded and stored.  HBM-bound: 2 bytes read, 1 written per weight.
+__global__ void __launch_bounds__(kQuantNT)
+quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __restrict__ W8,
+                     int64_t ldw, float* __restrict__ w_scale, int* __restrict__ dev_status,
+                     int vec_ok) {
+  __shared__ uint32_t smax[kQuantNT / 32];
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.y * kQB, h = blockIdx.x * kQB + (tid & 15) * 8;
+  uint4 v[kQuantU];
+  uint32_t mx = 0;  // largest magnitudes of the even and odd columns, packed
+#pragma unroll
+  for (int i = 0; i < kQuantU; ++i) {
+    const int r = r0 + i * (kQuantNT / 16) + (tid >> 4);
+    const uint16_t* p = W + (int64_t)r * H + h;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < K && h < H) {
+      if (vec_ok) {  // H % 8 == 0: the whole vector lies in the row
+        v[i] = __ldg(reinterpret_cast<const uint4*>(p));
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (h + e < H) w[e >> 1] |= (uint32_t)__ldg(p + e) << (16 * (e & 1));
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantU; ++i) {
+    mx = __vmaxu2(mx, v[i].x & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[i].y & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[i].z & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[i].w & 0x7fff7fffu);
+  }
+  uint32_t m = max(mx >> 16, mx & 0xffffu);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) smax[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantNT / 32; ++w) m = max(m, smax[w]);
+  const int e = scale_exponent(m);
+  const float inv = exact_pow2(-e);
+  if (tid == 0) {
+    w_scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = exact_pow2(e);
+    if (m >= 0x7f80u) atomicOr(dev_status, VT_DEV_NONFINITE);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantU; ++i) {
+    const int r = r0 + i * (kQuantNT / 16) + (tid >> 4);
+    if (r >= K || h >= H) continue;
+    uint2 o;
+    o.x = scale_e4m3x2(v[i].x, inv) | scale_e4m3x2(v[i].y, inv) << 16;
+    o.y = scale_e4m3x2(v[i].z, inv) | scale_e4m3x2(v[i].w, inv) << 16;
+    uint8_t* q = W8 + (int64_t)r * ldw + h;
+    if (vec_ok) {  // ldw % 16 == 0 and W8 16-byte aligned
+      *reinterpret_cast<uint2*>(q) = o;
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        if (h + b < H) q[b] = (uint8_t)((b < 4 ? o.x >> (8 * b) : o.y >> (8 * (b - 4))) & 0xffu);
+    }
+  }
+}
+
+// ------------------------------------------------------- hidden states
+// Quantises hidden [B, H] to x8 [B, ldx] (columns H..ldx zero) and sx
+// [groups][Bp] (rows B..Bp zero), one warp per (row, group of 128 columns).
+// A group with a NaN or an infinity gets the scale NaN, so that row's logits
+// are NaN.
+__global__ void __launch_bounds__(256)
+quantize_hidden_kernel(const uint16_t* __restrict__ hidden, int B, int H, uint8_t* __restrict__ x8,
+                       int ldx, float* __restrict__ sx, int Bp, int groups, int vec_ok,
+                       int* __restrict__ status, int status_reset) {
+  griddep_launch_dependents();  // the product prefetches weights before its own wait
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && status_reset) *status = 0;
+  const int64_t wid = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int b = (int)(wid / groups), g = (int)(wid % groups);
+  if (b >= Bp) return;
+  if (b >= B) {
+    if (lane == 0) sx[(int64_t)g * Bp + b] = 0.f;
+    return;
+  }
+  const int h = g * kQB + 4 * lane;
+  const uint16_t* p = hidden + (int64_t)b * H + h;
+  uint2 v = make_uint2(0, 0);
+  if (vec_ok) {  // H % 4 == 0 and 8-byte aligned rows
+    if (h < H) v = *reinterpret_cast<const uint2*>(p);
+  } else {
+    if (h < H) v.x = p[0];
+    if (h + 1 < H) v.x |= (uint32_t)p[1] << 16;
+    if (h + 2 < H) v.y = p[2];
+    if (h + 3 < H) v.y |= (uint32_t)p[3] << 16;
+  }
+  const uint32_t mx = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu));
+  const int e = scale_exponent(m);
+  const float inv = exact_pow2(-e);
+  *reinterpret_cast<uint32_t*>(x8 + (int64_t)b * ldx + h) =
+      scale_e4m3x2(v.x, inv) | scale_e4m3x2(v.y, inv) << 16;
+  if (lane == 0)
+    sx[(int64_t)g * Bp + b] = m >= 0x7f80u ? __int_as_float(0x7fc00000) : exact_pow2(e);
+}
+
+// --------------------------------------------------------------- product
+struct Fp8Args {
+  umma::HeadArgs h;     // batch, sizes, outputs and partials as in the bf16 projection
+  const float* sw;      // [K / 128][groups]
+  const float* sx;      // [groups][Bp]
+  int Bp, groups, nchunk;
+};
+
+constexpr int kMaxGroups = 512;  // H <= 65536
+constexpr int kMaxAcc = 4;
+
+// accumulator buffers in tensor memory (a power of two)
+template <int BN>
+constexpr int kAccBufs = BN <= 128 ? 4 : 2;
+// promoting threads: one per row of the tile; two per row (half the columns
+// each) for wide batches
+template <int BN>
+constexpr int kPromNT = BN >= 128 ? 256 : 128;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          umma::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(umma::smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One CTA per 128 rows of W8 and BN rows of the batch.  Each group of 128
+// reduction columns is one shared-memory stage (W8 128 x 128 bytes, x8
+// BN x 128 bytes, both K-major with the 128-byte swizzle, and the BN scales
+// sx) and one tcgen05 accumulation of four K = 32 steps into one of several
+// tensor-memory buffers.  The promoting warps read each finished buffer and
+// add it, times sw * sx, to fp32 sums in registers: the scales of a group
+// multiply its partial sum only, and the long sum is held in 32 bits by the
+// CUDA cores.  One warp issues the TMA loads and one the MMAs.
+template <int BN>
+__global__ void __launch_bounds__(kPromNT<BN> + 64, 1)
+head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                Fp8Args fa) {
+  using namespace umma;
+  const HeadArgs& a = fa.h;
+  constexpr int NP = kPromNT<BN>;
+  constexpr int kPromWarps = NP / 32;
+  constexpr int NBUF = kAccBufs<BN>;
+  constexpr int CW = BN / (NP / 128);  // columns of one promoting thread
+  constexpr int CH = CW >= 32 ? 32 : 16;
+  constexpr uint32_t kCols = (uint32_t)(NBUF * BN);  // 64..512, a power of two
+  constexpr int kBBytes = BN * 128;
+  constexpr int stage_bytes = kABytes + kBBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc];
+  __shared__ __align__(8) uint64_t done_bar;
+  __shared__ __align__(16) float sx_sh[kMaxStages][BN];
+  __shared__ float sw_sh[kMaxGroups];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int s_err;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = a.stages;
+  const int tile = blockIdx.x / fa.nchunk, n0 = (blockIdx.x % fa.nchunk) * BN;
+  const int m0 = tile * kBM;
+  const int nk = fa.groups;
+  // tiles start their reduction at different groups, so the rows streamed at
+  // any moment are spread over column offsets (DRAM channels)
+  const int rot = tile % nk;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1 + kPromWarps);
+    }
+    for (int p = 0; p < NBUF; ++p) {
+      mbar_init(&acc_full[p], 1);
+      mbar_init(&acc_empty[p], kPromWarps);
+    }
+    mbar_init(&done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_err = 0;
+    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&map_x);
+  }
+  if (warp == kPromWarps + 1) {
+    tmem_alloc(&tmem_base_sh, kCols);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+
+  float acc[CW];
+  if (warp == kPromWarps) {
+    if (lane == 0) {
+      // TMA producer: the first stages' weights before the wait on the
+      // kernel that quantises the hidden states
+      const int pre = min(S, nk);
+      auto load_x = [&](int kb) {
+        const int s = kb % S, g = (kb + rot) % nk;
+        tma_load_2d(smem + (size_t)s * stage_bytes + kABytes, &map_x, g * 128, n0, &full_bar[s]);
+        bulk_load(sx_sh[s], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &full_bar[s]);
+      };
+      for (int kb = 0; kb < pre; ++kb) {
+        mbar_expect_tx(&full_bar[kb], (uint32_t)(stage_bytes + BN * 4));
+        tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, ((kb + rot) % nk) * 128, m0,
+                    &full_bar[kb]);
+      }
+      griddep_wait();
+      for (int kb = 0; kb < pre; ++kb) load_x(kb);
+      int issued = pre;
+      for (int kb = pre; kb < nk; ++kb) {
+        const int s = kb % S;
+        if (!mbar_wait(&empty_bar[s], ((kb / S) - 1) & 1)) {
+          atomicExch(&s_err, 1);
+          break;
+        }
+        mbar_expect_tx(&full_bar[s], (uint32_t)(stage_bytes + BN * 4));
+        tma_load_2d(smem + (size_t)s * stage_bytes, &map_w, ((kb + rot) % nk) * 128, m0,
+                    &full_bar[s]);
+        load_x(kb);
+        issued = kb + 1;
+      }
+      // drain: every issued copy has landed before this CTA may exit
+      for (int kb = (issued > S ? issued - S : 0); kb < issued; ++kb)
+        mbar_wait(&full_bar[kb % S], (kb / S) & 1);
+    }
+  } else if (warp == kPromWarps + 1) {
+    if (lane == 0) {
+      // MMA issuer.  Instruction descriptor of kind::f8f6f4: fp32 accumulator
+      // (bits 4-5 = 1), e4m3 A and B (7-9 and 10-12 = 0), both K-major,
+      // N >> 3 at bit 17, M >> 4 at bit 24.
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+      for (int kb = 0; kb < nk; ++kb) {
+        const int s = kb % S, p = kb % NBUF;
+        if ((kb >= NBUF && !mbar_wait(&acc_empty[p], ((kb / NBUF) - 1) & 1)) ||
+            !mbar_wait(&full_bar[s], (kb / S) & 1)) {
+          atomicExch(&s_err, 1);
+          break;
+        }
+        fence_after_sync();
+        const uint32_t sa = smem_u32(smem + (size_t)s * stage_bytes);
+        const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + kABytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
+          mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+        mma_commit(&empty_bar[s]);
+        mma_commit(&acc_full[p]);
+      }
+      mma_commit(&done_bar);
+    }
+  } else {
+    griddep_wait();
+    for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
+    asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+#pragma unroll
+    for (int i = 0; i < CW; ++i) acc[i] = 0.f;
+    const int quad = warp & 3, col0 = (warp >> 2) * CW;
+    bool ok = true;
+    for (int kb = 0; kb < nk && ok; ++kb) {
+      const int s = kb % S, p = kb % NBUF;
+      ok = mbar_wait(&full_bar[s], (kb / S) & 1) && mbar_wait(&acc_full[p], (kb / NBUF) & 1);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) break;
+      fence_after_sync();
+      const float sw = sw_sh[(kb + rot) % nk];
+      const float4* sx4 = reinterpret_cast<const float4*>(sx_sh[s] + col0);
+#pragma unroll
+      for (int c0 = 0; c0 < CW; c0 += CH) {
+        float v[CH];
+        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0 + c0);
+        if constexpr (CH == 32) {
+          tmem_ld32(taddr, v);
+        } else {
+          tmem_ld16(taddr, v);
+        }
+#pragma unroll
+        for (int e = 0; e < CH; e += 4) {
+          const float4 f = sx4[(c0 + e) / 4];
+          acc[c0 + e] = fmaf(v[e], sw * f.x, acc[c0 + e]);
+          acc[c0 + e + 1] = fmaf(v[e + 1], sw * f.y, acc[c0 + e + 1]);
+          acc[c0 + e + 2] = fmaf(v[e + 2], sw * f.z, acc[c0 + e + 2]);
+          acc[c0 + e + 3] = fmaf(v[e + 3], sw * f.w, acc[c0 + e + 3]);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&acc_empty[p]);
+        mbar_arrive(&empty_bar[s]);
+      }
+    }
+    if (!ok && lane == 0) atomicExch(&s_err, 1);
+  }
+  __syncwarp();
+  // every role has finished or given up; the MMAs have completed
+  const bool all_ok = __syncthreads_and(mbar_wait(&done_bar, 0) && s_err == 0 ? 1 : 0) != 0;
+  griddep_launch_dependents();
+  fence_after_sync();
+  if (all_ok && warp < kPromWarps) {
+    const int quad = warp & 3, col0 = (warp >> 2) * CW;
+    const int row = quad * 32 + lane, j = m0 + row;
+    // the ring is idle: it holds the tile transposed for the partials
+    float* zt = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+      const int b = col0 + i;
+      const float z = acc[i] * a.out_scale;
+      if (n0 + b < a.B && j < a.K) a.out[(int64_t)(n0 + b) * a.ldo + j] = z;
+      if (a.part != nullptr) zt[b * zt_pitch<BN, NP>() + row] = z;
+    }
+    if (a.part != nullptr) {
+      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      tile_partials<BN, NP>(zt, a, min(kBM, a.K - m0), m0, tile, tid, n0);
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && !all_ok) atomicOr(a.status, VT_DEV_TIMEOUT);
+  if (warp == kPromWarps + 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+struct Fp8Ws {
+  uint8_t* x8;
+  float* sx;
+  float2* part;
+  int* status_sink;  // status word of calls that report none (vt_draft_logits_fp8)
+  size_t bytes;
+};
+
+int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : (B + 255) / 256 * 256; }
+
+Fp8Ws carve_fp8(void* base, int B, int H, int K) {
+  Fp8Ws w;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off = align_up(off + n, 256);
+    return o;
+  };
+  const size_t groups = (H + kQB - 1) / kQB;
+  const size_t o_x = take((size_t)B * groups * kQB);
+  const size_t o_sx = take(groups * pad_batch(B) * sizeof(float));
+  const size_t o_part = take((size_t)((K + umma::kBM - 1) / umma::kBM) * B * sizeof(float2));
+  const size_t o_s = take(sizeof(int));
+  char* p = static_cast<char*>(base);
+  w.x8 = reinterpret_cast<uint8_t*>(p + o_x);
+  w.sx = reinterpret_cast<float*>(p + o_sx);
+  w.part = reinterpret_cast<float2*>(p + o_part);
+  w.status_sink = reinterpret_cast<int*>(p + o_s);
+  w.bytes = off;
+  return w;
+}
+
+// 2-D tensor map of a row-major byte matrix [rows, cols] with a row stride of
+// ld bytes, boxes of 128 columns (128-byte swizzle) x box_rows rows
+bool make_e4m3_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
+                   uint32_t box_rows) {
+  auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+int launch_fp8_bn(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa,
+                  int tiles) {
+  constexpr int stage = umma::kABytes + BN * 128;
+  // narrow batches: two CTAs per SM
+  const int budget = (BN <= 64) ? 96 * 1024 : 200 * 1024;
+  fa.h.stages = std::max(2, std::min(umma::kMaxStages, budget / stage));
+  constexpr size_t kZt = (size_t)BN * umma::zt_pitch<BN, kPromNT<BN>>() * sizeof(float);
+  const size_t smem = std::max((size_t)fa.h.stages * stage, kZt) + 1024;
+  auto k = head_fp8_kernel<BN>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * fa.nchunk));
+  cfg.blockDim = dim3(kPromNT<BN> + 64);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, k, mw, mx, fa));
+  return VT_OK;
+}
+
+// z = out_scale * hidden @ (scaled W8)^T; part[tile][b] partials of 128-row
+// tiles (greedy: argmax partials)
+int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const uint8_t* W8,
+                    int64_t ldw, const float* w_scale, int K, float out_scale, float* out,
+                    int64_t ldo, const Fp8Ws& ws, float2* part, int* status, int status_reset,
+                    int greedy) {
+  const int groups = (H + kQB - 1) / kQB, Bp = pad_batch(B), ldx = groups * kQB;
+  const int BN = std::min(Bp, 256);
+  CUtensorMap mw, mx;
+  if (!make_e4m3_map(&mw, W8, (uint64_t)K, (uint64_t)H, (uint64_t)ldw, umma::kBM)) return VT_ERR_CUDA;
+  if (!make_e4m3_map(&mx, ws.x8, (uint64_t)B, (uint64_t)ldx, (uint64_t)ldx, (uint32_t)BN))
+    return VT_ERR_CUDA;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)Bp * groups + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int vec_ok = H % 4 == 0 && (reinterpret_cast<uintptr_t>(hidden) & 7) == 0;
+    VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, quantize_hidden_kernel, hidden, B, H, ws.x8, ldx,
+                                         ws.sx, Bp, groups, vec_ok, status, status_reset));
+  }
+  Fp8Args fa;
+  fa.h = umma::HeadArgs{};
+  fa.h.B = B;
+  fa.h.H = H;
+  fa.h.K = K;
+  fa.h.out_scale = out_scale;
+  fa.h.out = out;
+  fa.h.ldo = ldo;
+  fa.h.part = part;
+  fa.h.status = status;
+  fa.h.greedy = greedy;
+  fa.sw = w_scale;
+  fa.sx = ws.sx;
+  fa.Bp = Bp;
+  fa.groups = groups;
+  fa.nchunk = Bp / BN;
+  const int tiles = (K + umma::kBM - 1) / umma::kBM;
+  switch (BN) {
+    case 16: return launch_fp8_bn<16>(s, mw, mx, fa, tiles);
+    case 32: return launch_fp8_bn<32>(s, mw, mx, fa, tiles);
+    case 64: return launch_fp8_bn<64>(s, mw, mx, fa, tiles);
+    case 128: return launch_fp8_bn<128>(s, mw, mx, fa, tiles);
+    default: return launch_fp8_bn<256>(s, mw, mx, fa, tiles);
+  }
+}
+
+// T > 0, or T == 0 where greedy drafting is allowed
+int check_fp8_args(const uint16_t* hidden, int B, int H, const uint8_t* W8, int64_t ldw,
+                   const float* w_scale, int K, float T, bool allow_greedy) {
+  if (!hidden || !W8 || !w_scale) return VT_ERR_INVALID_ARG;
+  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1) return VT_ERR_INVALID_ARG;
+  if (ldw < H || ldw % 16 != 0 || (reinterpret_cast<uintptr_t>(W8) & 15) != 0)
+    return VT_ERR_INVALID_ARG;
+  if (!std::isfinite(T) || T < 0.f || (T == 0.f && !allow_greedy)) return VT_ERR_INVALID_ARG;
+  return VT_OK;
+}
+
+}  // namespace
+}  // namespace vt
+
+extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t* W8, int64_t ldw,
+                                float* w_scale, int32_t* dev_status, void* stream) {
+  using namespace vt;
+  if (!W || !W8 || !w_scale || !dev_status || K < 1 || H < 1 || H > 65536)
+    return VT_ERR_INVALID_ARG;
+  if (ldw < H || ldw % 16 != 0 || (reinterpret_cast<uintptr_t>(W8) & 15) != 0)
+    return VT_ERR_INVALID_ARG;
+  const int rows = (K + kQB - 1) / kQB;
+  if (rows > 65535) return VT_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  VT_RETURN_IF_CUDA(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s));
+  const int vec_ok = H % 8 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
+  quantize_head_kernel<<<dim3((unsigned)((H + kQB - 1) / kQB), (unsigned)rows), kQuantNT, 0, s>>>(
+      W, K, H, W8, ldw, w_scale, dev_status, vec_ok);
+  VT_RETURN_IF_LAUNCH_FAILED();
+  return VT_OK;
+}
+
+extern "C" size_t vt_draft_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K) {
+  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1) return 0;
+  return vt::carve_fp8(nullptr, B, H, K).bytes;
+}
+
+extern "C" int vt_draft_logits_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                                   int64_t ldw, const float* w_scale, int32_t K, float temperature,
+                                   float* logits, int64_t ld_logits, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  using namespace vt;
+  const int st = check_fp8_args(hidden, B, H, W8, ldw, w_scale, K, temperature, false);
+  if (st != VT_OK) return st;
+  if (!logits || ld_logits < K) return VT_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return VT_ERR_WORKSPACE;
+  const Fp8Ws ws = carve_fp8(workspace, B, H, K);
+  if (workspace_bytes < ws.bytes) return VT_ERR_WORKSPACE;
+  return launch_head_fp8(static_cast<cudaStream_t>(stream), hidden, B, H, W8, ldw, w_scale, K,
+                         1.0f / temperature, logits, ld_logits, ws, nullptr, ws.status_sink, 1, 0);
+}
+
+extern "C" int vt_draft_step_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                                 int64_t ldw, const float* w_scale, const int32_t* trim_ids,
+                                 int32_t K, const float* uniforms, float temperature, float* q,
+                                 int64_t ldq, int32_t* tokens, int64_t ld_tokens,
+                                 int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  using namespace vt;
+  const int st = check_fp8_args(hidden, B, H, W8, ldw, w_scale, K, temperature, true);
+  if (st != VT_OK) return st;
+  const bool greedy = temperature == 0.f;
+  if (!trim_ids || (!uniforms && !greedy) || !q || ldq < K || !tokens || ld_tokens < 1 ||
+      !dev_status)
+    return VT_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return VT_ERR_WORKSPACE;
+  const Fp8Ws ws = carve_fp8(workspace, B, H, K);
+  if (workspace_bytes < ws.bytes) return VT_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int rc = launch_head_fp8(s, hidden, B, H, W8, ldw, w_scale, K,
+                                 greedy ? 1.0f : VT_LOG2E / temperature, q, ldq, ws, ws.part,
+                                 dev_status, 1, greedy ? 1 : 0);
+  if (rc != VT_OK) return rc;
+  return draft_finish(s, B, K, greedy, ws.part, (K + umma::kBM - 1) / umma::kBM, umma::kBM,
+                      uniforms, trim_ids, q, ldq, tokens, ld_tokens, dev_status);
+}
+
+extern "C" size_t vt_draft_topk_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t k) {
+  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1 || k < 1 || k > vt::kDraftTopkMax || k > K)
+    return 0;
+  return vt::align_up(vt_draft_fp8_workspace_bytes(B, H, K), 256) +
+         vt::align_up((size_t)B * K * 4, 256);
+}
+
+extern "C" int vt_draft_topk_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                                 int64_t ldw, const float* w_scale, const int32_t* trim_ids,
+                                 int32_t K, int32_t k, float temperature, int32_t* out_ids,
+                                 float* out_logq, int32_t* dev_status, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  using namespace vt;
+  const int st = check_fp8_args(hidden, B, H, W8, ldw, w_scale, K, temperature, false);
+  if (st != VT_OK) return st;
+  if (!trim_ids || !out_ids || !out_logq || !dev_status || k < 1 || k > kDraftTopkMax || k > K)
+    return VT_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return VT_ERR_WORKSPACE;
+  if (workspace_bytes < vt_draft_topk_fp8_workspace_bytes(B, H, K, k)) return VT_ERR_WORKSPACE;
+  char* base = static_cast<char*>(workspace);
+  const Fp8Ws ws = carve_fp8(base, B, H, K);
+  float* z2 = reinterpret_cast<float*>(base + align_up(ws.bytes, 256));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int rc = launch_head_fp8(s, hidden, B, H, W8, ldw, w_scale, K, VT_LOG2E / temperature, z2,
+                                 K, ws, ws.part, dev_status, 1, 0);
+  if (rc != VT_OK) return rc;
+  return draft_topk_finish(s, z2, B, K, k, ws.part, (K + umma::kBM - 1) / umma::kBM, trim_ids,
+                           out_ids, out_logq, dev_status);
+}

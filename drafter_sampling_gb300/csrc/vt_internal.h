@@ -4,7 +4,28 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
 namespace vt {
+
+// cuTensorMapEncodeTiled of the loaded driver, or nullptr
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+constexpr int kDraftTopkMax = 32;  // largest k of the drafter's top-k
+
+// The second half of a drafting step, after a projection that left z (scaled
+// by log2(e) / T; raw when greedy) in q and one partial per tile_rows rows in
+// part[G][B]: softmax and draw, or the one-hot q and argmax when greedy.
+int draft_finish(cudaStream_t s, int B, int K, bool greedy, const float2* part, int G,
+                 int tile_rows, const float* uniforms, const int32_t* trim_ids, float* q,
+                 int64_t ldq, int32_t* tokens, int64_t ld_tokens, int32_t* dev_status);
+
+// The second half of the drafter's top-k: z2 [B, K] = z log2(e) / T and the
+// softmax partials part[G][B] of a projection.
+int draft_topk_finish(cudaStream_t s, const float* z2, int B, int K, int k, const float2* part,
+                      int G, const int32_t* trim_ids, int32_t* out_ids, float* out_logq,
+                      int32_t* dev_status);
 
 // vt_draft_step with two choices: status_reset = 1 zeroes *dev_status first
 // (vt_draft_step), 0 adds this step's flags to it (later steps of a block);

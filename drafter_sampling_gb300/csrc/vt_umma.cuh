@@ -248,12 +248,13 @@ __host__ __device__ constexpr int zt_pitch() {
 // Per-column partials of one accumulator tile held transposed in shared
 // memory (zt[b][r], r < nvalid rows of the tile starting at row r0):
 // sampling, (max z, sum 2^(z - max)); greedy, (max z, its lowest row), a
-// non-finite z counting as NaN, which wins.  P = NT/BN threads share a
+// non-finite z counting as NaN, which wins.  b0: the batch row of column 0
+// (batches cut into chunks of BN).  P = NT/BN threads share a
 // column (narrow batches), interleaved by 16-byte groups (see zt_pitch);
 // with BN > NT each thread owns BN/NT columns.
 template <int BN, int NT>
 __device__ __forceinline__ void tile_partials(const float* zt, const HeadArgs& a, int nvalid,
-                                              int r0, int tt, int tid) {
+                                              int r0, int tt, int tid, int b0 = 0) {
   constexpr int P = BN >= NT ? 1 : NT / BN;          // threads per column
   constexpr int CPT = BN > NT ? BN / NT : 1;         // columns per thread
   constexpr int NF = kBM / 4 / P;                    // 16-byte groups per thread
@@ -289,7 +290,8 @@ __device__ __forceinline__ void tile_partials(const float* zt, const HeadArgs& a
           idx = k;
         }
       }
-      if (p == 0 && b < a.B) a.part[(int64_t)tt * a.B + b] = make_float2(v, __int_as_float(idx));
+      if (p == 0 && b0 + b < a.B)
+        a.part[(int64_t)tt * a.B + b0 + b] = make_float2(v, __int_as_float(idx));
     } else {
       // two passes over the column: its max, then the sum of 2^(z - max);
       // a NaN or +inf z leaves the sum NaN
@@ -321,7 +323,7 @@ __device__ __forceinline__ void tile_partials(const float* zt, const HeadArgs& a
       }
 #pragma unroll
       for (int o = P / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (p == 0 && b < a.B) a.part[(int64_t)tt * a.B + b] = make_float2(m, s);
+      if (p == 0 && b0 + b < a.B) a.part[(int64_t)tt * a.B + b0 + b] = make_float2(m, s);
     }
   }
 }

@@ -369,6 +369,98 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The head in 8-bit floating point.  [VT] section 1 motivates the trimmed
+ * head by the memory traffic of the drafting step, which reads the whole
+ * head for every drafted token; e4m3 weights halve what is left of it.  The
+ * pages define no 8-bit head: the format below is this library's choice.
+ *
+ * e4m3 is the 8-bit float with 4 exponent and 3 mantissa bits, largest value
+ * 448, no infinities.  A scale covers a block of 128 x 128 weights (128
+ * consecutive rows, 128 consecutive columns; the last blocks may be smaller).
+ *
+ * vt_quantize_head: for each block, s = the smallest power of two >= 2^-126
+ * with max |W| <= 448 s, W8 = e4m3(W / s), round to nearest even.  Division
+ * by a power of two is exact, so W8 is defined bit for bit.
+ *
+ *  W        bf16 [K, H]       a head (usually W_trim), row stride H
+ *  W8       uint8 [K, ldw]    out: e4m3 bit patterns, columns 0..H-1 of each
+ *                             row; ldw >= H, a multiple of 16; W8 16-byte
+ *                             aligned.  Columns H..ldw-1 are not written.
+ *  w_scale  f32 [ceil(K/128), ceil(H/128)] out: s of each block
+ *  dev_status int32 [1]       out: VT_DEV_NONFINITE (a NaN or infinity in W;
+ *                             its block is unspecified)
+ * 1 <= H <= 65536, 1 <= K <= 8388480 (65535 blocks).
+ *
+ * vt_draft_logits_fp8, vt_draft_step_fp8 and vt_draft_topk_fp8 are
+ * vt_draft_logits, vt_draft_step and vt_draft_topk with
+ *
+ *   z[b, j] = sum_g w_scale[j/128, g] sx[b, g] sum_{h in g} x8[b, h] W8[j, h]
+ *
+ * in place of hidden . W_trim: g runs over the groups of 128 columns, and
+ * x8, sx are the hidden states quantised inside the call by the rule above
+ * per row and group.  A group's products are summed by the tensor cores and
+ * its sum enters the fp32 sum over the groups times its two scales, so
+ * w_scale may hold any finite fp32 values, not only powers of two.  A row of
+ * hidden states with a NaN or an infinity gives NaN logits in that row.
+ * hidden, logits, trim_ids, uniforms, q, tokens and the temperature are as
+ * there; W8, ldw and w_scale as vt_quantize_head leaves them.  Like W_trim,
+ * W8 must not be written by a kernel that may still be running when the
+ * call's first kernel starts and that triggers its dependents early.
+ * Workspace: vt_draft_fp8_workspace_bytes(B, H, K) bytes, or
+ * vt_draft_topk_fp8_workspace_bytes(B, H, K, k) for the top-k.
+ * ---------------------------------------------------------------------- */
+int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t* W8, int64_t ldw,
+                     float* w_scale, int32_t* dev_status, void* stream);
+size_t vt_draft_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K);
+int vt_draft_logits_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                        int64_t ldw, const float* w_scale, int32_t K, float temperature,
+                        float* logits, int64_t ld_logits,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int vt_draft_step_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                      int64_t ldw, const float* w_scale, const int32_t* trim_ids, int32_t K,
+                      const float* uniforms, float temperature, float* q, int64_t ldq,
+                      int32_t* tokens, int64_t ld_tokens, int32_t* dev_status,
+                      void* workspace, size_t workspace_bytes, void* stream);
+size_t vt_draft_topk_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t k);
+int vt_draft_topk_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                      int64_t ldw, const float* w_scale, const int32_t* trim_ids, int32_t K,
+                      int32_t k, float temperature, int32_t* out_ids, float* out_logq,
+                      int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, with the entropy of each row and its k
+ * best alternatives: what a server reports for the tokens a block emitted
+ * (vt_verify's out_tokens under the same target logits), and a drafter's own
+ * confidence (its logits and the drafted trimmed indices).
+ *
+ *  logits    [R, ld_logits] of logits_dtype; row r holds V logits
+ *            (ld_logits >= V; aligned to its element type, no more)
+ *  tokens    int32 [R]      the id to score in each row; -1: the row is not
+ *                           scored and not read (vt_verify pads with -1)
+ *  temperature              T finite and > 0: p = softmax(l / T) over the V
+ *                           ids; an id at -infinity has p = 0
+ *  out_logp     f32 [R]     out: ln p(token)
+ *  out_entropy  f32 [R]     out, may be NULL: -sum p ln p (nats)
+ *  out_top_ids  int32 [R,k] out: the k largest logits' ids, best first, ties
+ *                           to the lower id (ids at -infinity included when
+ *                           fewer than k are finite)
+ *  out_top_logp f32 [R,k]   out: ln p of each
+ *  dev_status int32 [1]     out: VT_DEV_BAD_ID (a token outside [0, V) other
+ *                           than -1; its out_logp is NaN, the rest of the row
+ *                           is as usual), VT_DEV_NONFINITE (a row with a NaN
+ *                           or +infinity, or without a finite logit: NaN, and
+ *                           ids -1)
+ * Rows with token -1 get NaN and ids -1.  0 <= k <= 32, k <= V <= 2^22,
+ * 1 <= R <= 2^24; out_top_ids and out_top_logp may be NULL when k == 0.
+ * No workspace.
+ * ---------------------------------------------------------------------- */
+int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64_t R, int32_t V,
+                      int64_t ld_logits, const int32_t* tokens, int32_t k, float temperature,
+                      float* out_logp, float* out_entropy, int32_t* out_top_ids,
+                      float* out_top_logp, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
  * One speculative block as a CUDA graph.  [VT] Appendix C.1, Algorithm 2:
  * draft k (= gamma) tokens through the trimmed head, then score and verify
  * them.  vt_block_graph_create records gamma vt_draft_step calls (step j

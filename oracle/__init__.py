@@ -64,6 +64,11 @@ pages or the mathematics fix (none is "parity unpinned"):
 * draft_topk             exact integer logits and ties; exp(log q) equals
                          the pinned draft_step's q; k = 1 is the greedy draft
                          (tests/test_oracle_tree.py)
+* fp8 (e4m3 head)        torch's e4m3 type on every bf16 in range; nearest
+                         values and ties by brute force; hand-worked scales
+                         (tests/test_oracle_fp8.py)
+* token_logprobs         closed forms, uniform rows, masks, shift invariance
+                         (tests/test_oracle_logprobs.py)
 """
 from .sampling import inverse_cdf, InverseCdfResult  # noqa: F401
 from .vocabtrim import (token_histogram, top_k, trim_head, bf16_to_f64,  # noqa: F401
@@ -73,3 +78,5 @@ from .speculative import (softmax, acceptance_probability, residual_weights,  # 
 from .greedy import (argmax_lowest, top2_gap, draft_step_greedy, verify_greedy,  # noqa: F401
                      GreedyResult)
 from .tree import verify_tree_greedy, draft_topk, TreeResult  # noqa: F401
+from . import fp8  # noqa: F401
+from .logprobs import token_logprobs  # noqa: F401

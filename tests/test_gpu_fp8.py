@@ -1,0 +1,294 @@
+"""The 8-bit head through the public entry points, against the fp64 oracle
+(oracle/fp8.py).
+
+Quantised values are defined bit for bit.  Logits: with u = 2^-23 (each
+addition rounded or truncated to fp32), a sum of n terms in any order is
+within n u A of the exact one, A the sum of the terms' magnitudes; here n =
+H products, one addition per group and the two scale factors, 1/T and the
+last rounding: |z - ref| <= (H + groups + 6) 2^-23 A.  On small integers every
+product and sum is exact, so the logits must be equal bit for bit.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synthetic
+from oracle import fp8
+from parity import assert_probs_close
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vt():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import drafter_sampling_gb300 as m
+    from drafter_sampling_gb300 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _bf(bits):
+    return _dev(np.ascontiguousarray(bits).view(np.int16))
+
+
+def _ints(g, shape, lo=-2, hi=3):
+    return (g.integers(lo, hi, shape).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+
+
+def _head(codes, scale):
+    """Codes [K, H] behind a row stride that is a multiple of 16, poison in the padding."""
+    K, H = codes.shape
+    buf = torch.full((K, (H + 15) // 16 * 16 + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    buf[:, :H] = _dev(codes)
+    return buf[:, :H], _dev(scale.astype(np.float32))
+
+
+def _logit_bound(H, A):
+    return (H + (H + 127) // 128 + 6) * 2.0 ** -23 * A
+
+
+# ------------------------------------------------------------- quantising
+@pytest.mark.parametrize("K,H", [(1, 1), (1, 128), (127, 129), (128, 128), (129, 16), (300, 1000),
+                                 (257, 333), (1000, 576), (2048, 2048)])
+def test_quantize_head_bit_exact(vt, K, H):
+    g = synthetic.rng(K * 7 + H, 5)
+    W = g.standard_normal((K, H)).astype(np.float32) * np.float32(0.02)
+    W *= (10.0 ** g.integers(-3, 3, (K, 1))).astype(np.float32)
+    bits = synthetic.to_bf16_bits(W)
+    W8, s, st = vt.vt_quantize_head(_bf(bits))
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and W8.dtype == torch.float8_e4m3fn and W8.stride(0) % 16 == 0
+    codes, scale = fp8.quantize_head(bits)
+    assert np.array_equal(W8.view(torch.uint8).cpu().numpy(), codes)
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), scale)
+
+
+def test_quantize_head_extremes(vt):
+    # zero blocks, subnormals, the largest bf16, and 448 on the boundary of two scales
+    blocks = [0.0, 1e-40, 3.3e38, 448.0, 450.0, 2.0 ** -118 * 1.75, 2.0 ** -130, 1.0]
+    W = np.zeros((128, 128 * len(blocks)), np.float32)
+    g = synthetic.rng(1, 5)
+    for i, v in enumerate(blocks):
+        W[:, 128 * i:128 * (i + 1)] = g.uniform(-1, 1, (128, 128)) * v
+        W[5, 128 * i + 7] = v
+    bits = synthetic.to_bf16_bits(W)
+    W8, s, st = vt.vt_quantize_head(_bf(bits))
+    codes, scale = fp8.quantize_head(bits)
+    assert int(st.item()) == 0
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), scale)
+    assert np.array_equal(W8.view(torch.uint8).cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_quantize_head_flags_nonfinite(vt, bad):
+    W = np.ones((200, 200), np.float32)
+    W[150, 10] = bad
+    W8, s, st = vt.vt_quantize_head(_dev(W).to(torch.bfloat16))
+    assert int(st.item()) == 8
+    assert float(s[0, 0]) == 2.0 ** -8 and bool((W8[:128].float() == 256.0).all())
+    W8, s, st = vt.vt_quantize_head(torch.ones((200, 200), dtype=torch.bfloat16, device="cuda"),
+                                    W8=W8, w_scale=s, dev_status=st)
+    assert int(st.item()) == 0                      # the status word starts at zero again
+
+
+def test_quantize_head_leaves_the_padding_alone(vt):
+    buf = torch.full((130, 160), 0x55, dtype=torch.uint8, device="cuda")
+    W = torch.randn((130, 133), device="cuda").to(torch.bfloat16)
+    vt.vt_quantize_head(W, W8=buf[:, :133])
+    assert bool((buf[:, 133:] == 0x55).all())
+
+
+# ------------------------------------------------------------------ logits
+SHAPES = [(1, 1, 1), (1, 128, 128), (2, 16, 5), (3, 127, 129), (7, 300, 1003), (16, 2048, 4096),
+          (17, 129, 256), (32, 512, 700), (33, 1000, 777), (64, 96, 130), (65, 640, 513),
+          (100, 264, 300), (128, 1100, 257), (129, 33, 640), (200, 2050, 400), (256, 128, 1300),
+          (257, 256, 200), (300, 1500, 1007), (1000, 200, 300), (4096, 64, 140)]
+
+
+@pytest.mark.parametrize("B,H,K", SHAPES)
+def test_logits_integer_inputs_bit_exact(vt, B, H, K):
+    g = synthetic.rng(B + H + K, 6)
+    hid, W = _ints(g, (B, H)), _ints(g, (K, H))
+    codes, scale = fp8.quantize_head(W)
+    z = vt.vt_draft_logits_fp8(_bf(hid), *_head(codes, scale), 0.5)
+    want = oracle.draft_logits(hid, W, 0.5)
+    assert np.array_equal(z.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("B,H,K", [s for s in SHAPES if s[0] <= 300])
+def test_logits_random_inputs(vt, B, H, K):
+    hid = synthetic.hidden_states((B, H), seed=B + K)
+    W = synthetic.head_weights(K, H, seed=H)
+    codes, scale = fp8.quantize_head(W)
+    scale = scale * synthetic.rng(H, 7).uniform(0.5, 2.0, scale.shape).astype(np.float32)
+    scale = scale.astype(np.float32).astype(np.float64)      # any fp32 scales, as another quantiser leaves
+    ref, A = fp8.draft_logits_fp8(hid, codes, scale, 0.7)
+    out = torch.full((B, K + 3), -7.0, device="cuda")
+    z = vt.vt_draft_logits_fp8(_bf(hid), *_head(codes, scale), 0.7, logits=out)
+    z = z.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(z[:, :K] - ref) <= _logit_bound(H, A) + 1e-30)
+    assert np.all(z[:, K:] == -7.0)                          # columns behind the head stay as they were
+
+
+def test_logits_rows_of_very_different_scale(vt):
+    # one row and one block of the head 2^40 above the others: the scales are per row, group and block
+    B, H, K = 5, 640, 400
+    g = synthetic.rng(9, 6)
+    x = g.standard_normal((B, H)).astype(np.float32)
+    x[2] *= 2.0 ** 40
+    x[:, 128:256] *= 2.0 ** -30
+    x[3] = 0
+    W = g.standard_normal((K, H)).astype(np.float32)
+    W[128:256] *= 2.0 ** -40
+    hid, Wb = synthetic.to_bf16_bits(x), synthetic.to_bf16_bits(W)
+    codes, scale = fp8.quantize_head(Wb)
+    ref, A = fp8.draft_logits_fp8(hid, codes, scale, 1.0)
+    z = vt.vt_draft_logits_fp8(_bf(hid), *_head(codes, scale)).cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(z - ref) <= _logit_bound(H, A) + 1e-30)
+    assert np.all(z[3] == 0)
+
+
+def test_nonfinite_hidden_rows_stay_apart(vt):
+    B, H, K = 6, 384, 300
+    hid = torch.randn((B, H), device="cuda").to(torch.bfloat16)
+    W8, s, _ = vt.vt_quantize_head(torch.randn((K, H), device="cuda").to(torch.bfloat16))
+    clean = vt.vt_draft_logits_fp8(hid, W8, s)
+    dirty = hid.clone()
+    dirty[1, 200], dirty[4, 3] = float("nan"), float("-inf")
+    z = vt.vt_draft_logits_fp8(dirty, W8, s)
+    rows = [0, 2, 3, 5]
+    assert torch.equal(z[rows], clean[rows]) and bool(torch.isnan(z[[1, 4]]).all())
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    u = torch.full((B,), 0.5, device="cuda")
+    for T in (1.0, 0.0):
+        _, tok, st = vt.vt_draft_step_fp8(dirty, W8, s, ids, u, T)
+        assert int(st.item()) == 8
+        assert tok.cpu().numpy()[[1, 4]].tolist() == [-1, -1] and bool((tok[rows] >= 0).all())
+
+
+def test_misaligned_hidden_and_odd_columns(vt):
+    B, H, K = 9, 301, 260
+    flat = torch.randn(B * H + 1, device="cuda").to(torch.bfloat16)
+    hid = flat[1:].view(B, H)
+    W8, s, _ = vt.vt_quantize_head(torch.randn((K, H), device="cuda").to(torch.bfloat16))
+    assert torch.equal(vt.vt_draft_logits_fp8(hid, W8, s), vt.vt_draft_logits_fp8(hid.clone(), W8, s))
+
+
+# -------------------------------------------------------- drafting on top
+@pytest.mark.parametrize("B,H,K", [(1, 64, 200), (5, 300, 1003), (16, 2048, 4096), (64, 512, 2000),
+                                   (100, 520, 3001), (256, 128, 1300), (300, 256, 700)])
+def test_greedy_step_integer_inputs_bit_exact(vt, B, H, K):
+    g = synthetic.rng(B + H + K, 8)
+    hid, W = _ints(g, (B, H)), _ints(g, (K, H))
+    W[K // 2] = W[K // 3]
+    ids = np.sort(g.permutation(3 * K)[:K]).astype(np.int32)
+    q, tok, st = vt.vt_draft_step_fp8(_bf(hid), *_head(*fp8.quantize_head(W)), _dev(ids), None, 0.0)
+    assert int(st.item()) == 0
+    ref = oracle.draft_step_greedy(hid, W, ids)
+    assert np.array_equal(tok.cpu().numpy(), ref["tokens"])
+    want = np.zeros((B, K), np.float32)
+    want[np.arange(B), ref["index"]] = 1.0
+    assert np.array_equal(q.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B,H,K,T", [(1, 256, 1000, 1.0), (16, 512, 3001, 0.7), (130, 200, 700, 1.3),
+                                     (300, 128, 500, 1.0)])
+def test_sampling_step(vt, B, H, K, T):
+    hid, W = synthetic.hidden_states((B, H), seed=3), synthetic.head_weights(K, H, seed=4)
+    u = synthetic.uniforms(5, 1, (B,))
+    ids = np.sort(synthetic.rng(6, 1).permutation(2 * K)[:K]).astype(np.int32)
+    codes, scale = fp8.quantize_head(W)
+    q_all = torch.full((B, 2, K), -1.0, device="cuda")
+    t_all = torch.full((B, 2), -5, dtype=torch.int32, device="cuda")
+    _, _, st = vt.vt_draft_step_fp8(_bf(hid), *_head(codes, scale), _dev(ids), _dev(u), T,
+                                    q=q_all[:, 1], tokens=t_all[:, 1])
+    assert int(st.item()) == 0
+    z, _ = fp8.draft_logits_fp8(hid, codes, scale, T)
+    q, tok = q_all[:, 1].cpu().numpy(), t_all[:, 1].cpu().numpy()
+    for b in range(B):
+        p = np.exp(z[b] - z[b].max())
+        p /= p.sum()
+        assert_probs_close(q[b], p)
+        r = oracle.inverse_cdf(p, u[b])
+        if r.margin > 1e-5:
+            assert tok[b] == ids[r.index], b
+    assert bool((q_all[:, 0] == -1).all()) and bool((t_all[:, 0] == -5).all())
+
+
+@pytest.mark.parametrize("B,H,K,k", [(1, 128, 40, 32), (5, 300, 1003, 8), (70, 256, 5000, 20)])
+def test_topk_matches_the_logits(vt, B, H, K, k):
+    # the ids are the k largest of the same product's logits, ties to the lower id
+    hid, W = synthetic.hidden_states((B, H), seed=7), synthetic.head_weights(K, H, seed=8)
+    codes, scale = fp8.quantize_head(W)
+    h, (W8, s) = _bf(hid), _head(codes, scale)
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    out, logq, st = vt.vt_draft_topk_fp8(h, W8, s, ids, k, 0.7)
+    assert int(st.item()) == 0
+    z, A = fp8.draft_logits_fp8(hid, codes, scale, 0.7)
+    tol = 2 * _logit_bound(H, A).max(axis=1)
+    out, logq = out.cpu().numpy(), logq.cpu().numpy()
+    for b in range(B):
+        lp = z[b] - z[b].max()
+        lp -= np.log(np.exp(lp).sum())
+        assert np.all(np.abs(logq[b] - lp[out[b]]) <= 2 * tol[b] + 1e-5)
+        assert np.all(z[b, out[b]] >= np.sort(z[b])[::-1][:k] - tol[b])
+        assert len(set(out[b].tolist())) == k
+
+
+def test_binding_refusals(vt):
+    hid = torch.zeros((2, 64), dtype=torch.bfloat16, device="cuda")
+    W8, s, _ = vt.vt_quantize_head(torch.ones((40, 64), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="disagree"):
+        vt.vt_draft_logits_fp8(hid[:, :32].contiguous(), W8, s)
+    with pytest.raises(ValueError, match="w_scale"):
+        vt.vt_draft_logits_fp8(hid, W8, s.repeat(2, 1))
+    with pytest.raises(ValueError, match="W8"):
+        vt.vt_draft_logits_fp8(hid, W8.t().contiguous().t(), s)
+    with pytest.raises(ValueError, match="W8"):                    # a row stride of 72
+        vt.vt_draft_logits_fp8(hid, torch.empty((40, 72), dtype=torch.uint8, device="cuda")[:, :64], s)
+    with pytest.raises(TypeError, match="W8"):
+        vt.vt_draft_logits_fp8(hid, W8.float(), s)
+    with pytest.raises(ValueError, match="logits"):
+        vt.vt_draft_logits_fp8(hid, W8, s, logits=torch.empty((2, 39), device="cuda"))
+    with pytest.raises(vt.VtError):
+        vt.vt_draft_logits_fp8(hid, W8, s, 0.0)
+    with pytest.raises(vt.VtError):
+        vt.vt_draft_logits_fp8(hid, W8, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="k must"):
+        vt.vt_draft_topk_fp8(hid, W8, s, torch.arange(40, dtype=torch.int32, device="cuda"), 33)
+
+
+def test_side_stream_and_graph(vt):
+    B, H, K = 20, 700, 900
+    W8, s, _ = vt.vt_quantize_head(torch.randn((K, H), device="cuda").to(torch.bfloat16))
+    hid = [torch.randn((B, H), device="cuda").to(torch.bfloat16) for _ in range(3)]
+    want = [vt.vt_draft_logits_fp8(h, W8, s) for h in hid]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = [vt.vt_draft_logits_fp8(h, W8, s, stream=st) for h in hid]
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # two captured graphs with workspaces of their own, replayed on new inputs, in turn and together
+    ins = [hid[0].clone(), hid[0].clone()]
+    graphs, outs = [], []
+    for x in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(vt.vt_draft_logits_fp8(x, W8, s))
+        graphs.append(g)
+    for i in range(3):
+        ins[0].copy_(hid[i])
+        ins[1].copy_(hid[2 - i])
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[i]) and torch.equal(outs[1], want[2 - i])
