@@ -180,15 +180,6 @@ constexpr int kAccBufs = BN <= 128 ? 4 : 2;
 template <int BN>
 constexpr int kPromNT = BN >= 128 ? 256 : 128;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          umma::smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(umma::smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(

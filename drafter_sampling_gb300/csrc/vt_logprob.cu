@@ -2,25 +2,36 @@
 // logits on sm_103a.
 //
 // With p = softmax(l / T) over the V ids of a row and c = log2(e) / T:
-//   m = max l,  d_i = (l_i - m) c,  S = sum 2^d_i,  D = sum 2^d_i d_i
-//   log p_x = (l_x - m) / T - ln S
-//   entropy = ln S - ln2 D / S
+//   m = max l,  y_i = l_i - m,  S = sum 2^(y_i c),  D = sum 2^(y_i c) y_i
+//   log p_x = y_x / T - ln S
+//   entropy = ln S - D / (T S)
 // and the k largest l (ties to the lower id) with their log p.  The maximum is
 // subtracted before the scale, so a row of the type's lowest value still gives
 // the uniform distribution; ids at -inf have p = 0 and add nothing.
 //
-// One pass over a row: one cluster of C thread blocks per row; block r takes the chunks r, r + C, ...
-// of a row.  A thread keeps a running (m, S, D) of what it has seen; the
-// candidates for the k best are the ids not after a bound tau that at least k
-// of the ids seen reach: the k-th best of 32 disjoint groups' best ids at
-// first, then the k-th best found.  About k pass; they are gathered in
-// shared memory and ranked by counting.  Blocks join through distributed
-// shared memory.
+// One pass over a row by a cluster of C thread blocks: block r takes the 16 KB
+// chunks r, r + C, ... .  One warp streams them by bulk copies into a ring of
+// four shared-memory stages, eight warps consume them, so the bytes in flight
+// do not depend on what the consumers are doing; a row's elements before its
+// first and after its last 16-byte boundary are loaded one by one.
+// A thread keeps a running (m, S, D) of what it has seen.  S is a sum of
+// vectors' sums carried with its rounding error, and log S is taken as
+// log1p(S - 1): a peaked row's S is 1 and little more, and that little is its
+// entropy.
+//
+// The k best are kept as 64-bit keys, ordered by (value, lower id first).  A
+// warp lists in shared memory the ids whose key reaches a bound that at least
+// k ids seen reach: first the k-th best of 32 disjoint groups' largest logits
+// (a block's first chunk), later the k-th best key of the block, renewed after
+// 2, 4, 8 ... chunks while more are to come than have been.  So about k ids of the first chunk are listed and few
+// later ones; lists are ranked by counting.  Ties and masked rows take no
+// other path.  Blocks join through distributed shared memory.
 #include <algorithm>
 #include <cmath>
 
 #include <cooperative_groups.h>
 
+#include "vt_umma.cuh"
 #include "vt_verify_common.cuh"
 
 namespace cg = cooperative_groups;
@@ -28,14 +39,16 @@ namespace cg = cooperative_groups;
 namespace vt {
 namespace {
 
-constexpr int kLpNT = 256;
+constexpr int kLpNT = 256;           // consuming threads
 constexpr int kLpWarps = kLpNT / 32;
-constexpr int kLpU = 8;            // 16-byte loads in flight per thread
+constexpr int kLpU = 4;              // 16-byte vectors per thread and chunk
+constexpr int kLpChunk = kLpNT * kLpU * 16;  // bytes
+constexpr int kLpStages = 4;
 constexpr int kLpMaxK = 32;
-constexpr int kLpCap = 1024;       // candidates gathered before a fallback
-constexpr int kLpCompact = 160;    // candidates kept before they are ranked
+constexpr int kLpList = 64;          // entries of a warp's list (2 * kLpMaxK: a cut leaves room)
 constexpr int kLpMaxC = 8;
-constexpr int kNoId = 0x7fffffff;
+constexpr int kLpSmem = kLpStages * kLpChunk;
+constexpr int kLpPerSm = 3;          // resident blocks per SM (shared memory)
 
 struct LpArgs {
   const void* logits;
@@ -48,11 +61,37 @@ struct LpArgs {
   int* out_ids;          // [R][k]
   float* out_top;        // [R][k]
   int* dev_status;
+  int own_status;        // one row: its block stores the status word; else it is zeroed beforehand
 };
 
-// (value, id) order of the alternatives: higher value, then lower id
-__device__ __forceinline__ bool lp_before(float av, int ai, float bv, int bi) {
-  return av > bv || (av == bv && ai < bi);
+// Order key of (value, id): higher value first, then lower id; 0 is after
+// every key.  -0 counts as 0.
+typedef unsigned long long lp_key;
+__device__ __forceinline__ uint32_t lp_ord(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ lp_key key_of(float v, int id) {
+  return (lp_key)lp_ord(v) << 32 | (uint32_t)~id;
+}
+__device__ __forceinline__ float key_value(lp_key q) {
+  const uint32_t o = (uint32_t)(q >> 32);
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int key_id(lp_key q) { return (int)~(uint32_t)q; }
+
+// how many of the n keys at `keys` come before q; keys is 16-byte aligned and
+// zero from n up to the next multiple of 8
+__device__ __forceinline__ int count_before(const lp_key* keys, int n, lp_key q) {
+  int r = 0;
+  for (int o = 0; o < n; o += 8) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(keys + o + h);
+      r += (two.x > q ? 1 : 0) + (two.y > q ? 1 : 0);
+    }
+  }
+  return r;
 }
 
 // larger of two, NaN if either is
@@ -62,46 +101,224 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// running statistics: maximum, sum 2^d and sum 2^d d with d = (x - m) c
-struct Lse {
-  float m, s, d;
+// two fp32 values in one 64-bit register, and arithmetic on both at once
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// the largest of a 16-byte vector's elements, NaN if one is
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  __device__ static float top(uint4 v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static constexpr uint32_t kMasked = 0xff800000u;  // -infinity
+};
+template <> struct Vec<uint16_t> {
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static float top(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static constexpr uint32_t kMasked = 0xff80ff80u;
 };
 
-// exponents below this contribute exactly nothing in fp32; bounding them keeps
-// -inf - m and its product with a zero weight finite
-constexpr float kLpLow = -1.0e4f;
+// running statistics: the maximum m, S = s + e (e: what rounding took from s)
+// and d = sum w y, with y = x - m and w = 2^(y c)
+struct Lse {
+  float m, s, e, d;
+};
 
-__device__ __forceinline__ void lse_rescale(Lse& a, float m, float c) {
-  const float u = fmaxf((a.m - m) * c, kLpLow);
-  const float f = exp2_approx(u);
-  a.d = f * fmaf(u, a.s, a.d);
+// y is bounded below at -kLpLow / c: 2^(y c) is zero there, and -inf times a
+// zero weight is not formed
+constexpr float kLpLow = 200.f;
+
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = a + b;
+  const float t = s - a;
+  e = (a - (s - t)) + (b - t);
+}
+// the same statistics relative to a maximum m >= a.m
+__device__ __forceinline__ void lse_rescale(Lse& a, float m, float c, float low) {
+  const float y = fmaxf(a.m - m, low);
+  const float f = exp2_approx(y * c);
+  a.d = f * fmaf(y, a.s, a.d);
   a.s *= f;
+  a.e *= f;
   a.m = m;
 }
-__device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c) {
+__device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c, float low) {
   const float m = max_nan(a.m, b.m);
-  lse_rescale(a, m, c);
-  lse_rescale(b, m, c);
-  return Lse{m, a.s + b.s, a.d + b.d};
+  lse_rescale(a, m, c, low);
+  lse_rescale(b, m, c, low);
+  Lse r;
+  r.m = m;
+  two_sum(a.s, b.s, r.s, r.e);
+  r.e += a.e + b.e;
+  r.d = a.d + b.d;
+  return r;
+}
+
+// Adds one chunk's vectors to a thread's statistics (their maximum is at most
+// st.m).  A chunk that holds -inf, or values so far below st.m that the
+// difference overflows, leaves st.d NaN.
+template <typename T>
+__device__ __forceinline__ Lse lse_add(Lse st, const uint4 (&v)[kLpU], float c) {
+  constexpr int VE = Elem<T>::kVec;
+  const f32x2 nm = pack2(-st.m, -st.m), c2 = pack2(c, c);
+  f32x2 sum[kLpU], d = pack2(st.d, 0.f);
+#pragma unroll
+  for (int u = 0; u < kLpU; ++u) {
+    float x[VE];
+    Elem<T>::unpack16(v[u], x);
+#pragma unroll
+    for (int e = 0; e < VE; e += 2) {
+      const f32x2 y = add2(pack2(x[e], x[e + 1]), nm);
+      float t0, t1;
+      unpack2(mul2(y, c2), t0, t1);
+      const f32x2 w = pack2(exp2_approx(t0), exp2_approx(t1));
+      sum[u] = e == 0 ? w : add2(sum[u], w);
+      d = fma2(w, y, d);
+    }
+  }
+#pragma unroll
+  for (int h = kLpU / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int u = 0; u < h; ++u) sum[u] = add2(sum[u], sum[u + h]);
+  float s0, s1, d0, d1, er;
+  unpack2(sum[0], s0, s1);
+  unpack2(d, d0, d1);
+  two_sum(st.s, s0 + s1, st.s, er);
+  st.e += er;
+  st.d = d0 + d1;
+  return st;
+}
+
+// The same with y bounded below, from the vectors at `src` (every kLpNT-th;
+// those from index `have` on hold nothing).
+template <typename T>
+__device__ __noinline__ Lse lse_add_bounded(Lse st, const uint4* src, int have, float c, float low) {
+  constexpr int VE = Elem<T>::kVec;
+  float s = 0.f;
+#pragma unroll 1
+  for (int u = 0; u < have; ++u) {
+    float x[VE], part = 0.f;
+    Elem<T>::unpack16(src[u * kLpNT], x);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float y = fmaxf(x[e] - st.m, low), w = exp2_approx(y * c);
+      part += w;
+      st.d = fmaf(w, y, st.d);
+    }
+    s += part;
+  }
+  float er;
+  two_sum(st.s, s, st.s, er);
+  st.e += er;
+  return st;
+}
+
+// Ranks a warp's list of n keys by counting and cuts it to its k best, in
+// order; returns how many are left.
+__device__ __noinline__ int list_cut(lp_key* list, int n, int k) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  lp_key q[kLpList / 32];
+  int r[kLpList / 32];
+#pragma unroll
+  for (int h = 0; h < kLpList / 32; ++h) {
+    const int j = lane + 32 * h;
+    q[h] = j < n ? list[j] : 0;
+    r[h] = j < n ? 0 : k;
+  }
+  for (int o = 0; o < n; ++o) {
+    const lp_key other = list[o];
+#pragma unroll
+    for (int h = 0; h < kLpList / 32; ++h) r[h] += other > q[h] ? 1 : 0;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < kLpList / 32; ++h)
+    if (r[h] < k) list[r[h]] = q[h];
+  __syncwarp();
+  return min(n, k);
+}
+
+// the consuming warps' barrier
+__device__ __forceinline__ void lp_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kLpNT) : "memory");
+}
+
+struct LpShared {
+  alignas(16) lp_key list[kLpWarps][kLpList];        // the warps' lists
+  alignas(16) lp_key all[kLpWarps * kLpList + kLpMaxK + 8];  // all lists, joined
+  alignas(16) lp_key best[kLpMaxK];                  // this block's k best, as published
+  alignas(16) float group[32];                       // largest logit of each of 32 groups of threads
+  alignas(8) uint64_t full[kLpStages], empty[kLpStages];
+  lp_key bound;
+  int n[kLpWarps];
+  Lse red[kLpWarps];
+  Lse blk;                                           // this block's statistics, as published
+  int timeout;
+};
+
+// Joins the warps' lists (n entries in this warp's) and the nbest keys of
+// sh.best into the block's k best, ranked in sh.best; the lists are
+// empty after.  Returns the new nbest.  All consuming warps call it.
+__device__ __forceinline__ int lists_join(LpShared& sh, int n, int nbest, int k, int warp, int lane) {
+  if (lane == 0) sh.n[warp] = n;
+  lp_bar();
+  int at = nbest, total = nbest;
+#pragma unroll
+  for (int w = 0; w < kLpWarps; ++w) {
+    const int nw = sh.n[w];
+    at += w < warp ? nw : 0;
+    total += nw;
+  }
+  for (int j = lane; j < n; j += 32) sh.all[at + j] = sh.list[warp][j];
+  if (warp == 0 && lane < nbest) sh.all[lane] = sh.best[lane];
+  if (warp == kLpWarps - 1 && lane < 8) sh.all[total + lane] = 0;
+  lp_bar();
+  for (int j = warp * 32 + lane; j < total; j += kLpNT) {
+    const lp_key q = sh.all[j];
+    const int r = count_before(sh.all, total, q);
+    if (r < k) sh.best[r] = q;
+    if (r == k - 1) sh.bound = q;
+  }
+  lp_bar();
+  return min(total, k);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpNT) token_logprobs_kernel(LpArgs a) {
-  constexpr int VE = Elem<T>::kVec;           // ids per 16-byte load
-  constexpr int CHUNK = kLpNT * kLpU * VE;    // ids per pass
-  __shared__ float cv[kLpCap];                // candidates; the list of the k best at the front
-  __shared__ int ci[kLpCap];
-  __shared__ float lv[kLpMaxK];               // ranked list, as published to the cluster
-  __shared__ int li[kLpMaxK];
-  __shared__ float gv[32];                    // best id of each of 32 groups of threads
-  __shared__ int gi[32];
-  __shared__ Lse red[kLpWarps];
-  __shared__ Lse blk;                         // this block's statistics, as published
-  __shared__ int s_n, s_listed;
-  __shared__ float s_tv;
-  __shared__ int s_ti;
-  __shared__ float wv[kLpWarps];
-  __shared__ int wi[kLpWarps];
+__global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(LpArgs a) {
+  constexpr int VE = Elem<T>::kVec;           // ids per 16-byte vector
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ LpShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int64_t row = blockIdx.x / C;
@@ -114,6 +331,7 @@ __global__ void __launch_bounds__(kLpNT) token_logprobs_kernel(LpArgs a) {
       if (tid == 0) {
         a.out_logp[row] = nan;
         if (a.out_entropy) a.out_entropy[row] = nan;
+        if (a.own_status) *a.dev_status = 0;
       }
       if (tid < k) {
         a.out_ids[row * k + tid] = -1;
@@ -123,271 +341,266 @@ __global__ void __launch_bounds__(kLpNT) token_logprobs_kernel(LpArgs a) {
     return;
   }
   const T* l = static_cast<const T*>(a.logits) + row * a.ld;
-  // ids of the row that precede its first 16-byte boundary are counted from a
-  // negative position: vector q of the aligned row holds ids q VE - off ...
+  // ids [0, head) precede the first 16-byte boundary, nvec whole vectors
+  // follow, then the rest
   const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
-  const int total = a.V + off;  // aligned positions of the row
-  float xt = 0.f;
-  if (rank == 0 && tid == 0 && token >= 0 && token < a.V) xt = Elem<T>::load(l + token);
+  const int head = min(a.V, off ? VE - off : 0);
+  const int nvec = (a.V - head) / VE;
+  const int nchunk = (nvec + kLpNT * kLpU - 1) / (kLpNT * kLpU);
+  const int mine = nchunk > rank ? (nchunk - rank + C - 1) / C : 0;  // chunks of this block
   if (tid == 0) {
-    s_n = 0;
-    s_listed = 0;
+    for (int s = 0; s < kLpStages; ++s) {
+      umma::mbar_init(&sh.full[s], 1);
+      umma::mbar_init(&sh.empty[s], kLpWarps);
+    }
+    sh.timeout = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-
-  Lse st{kNegBig, 0.f, 0.f};
-  bool first = true;
   __syncthreads();
-  for (int64_t base = (int64_t)rank * CHUNK; base < total; base += (int64_t)C * CHUNK) {
-    float x[kLpU][VE];
-#pragma unroll
-    for (int u = 0; u < kLpU; ++u) {
-      const int64_t id0 = base + (int64_t)(u * kLpNT + tid) * VE - off;
-      if (id0 >= 0 && id0 + VE <= a.V) {
-        Elem<T>::unpack16(__ldg(reinterpret_cast<const uint4*>(l + id0)), x[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          x[u][e] = (id0 + e >= 0 && id0 + e < a.V) ? Elem<T>::load(l + id0 + e) : -INFINITY;
-      }
-    }
-    // statistics
-    float pm = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kLpU; ++u)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) pm = max_nan(pm, x[u][e]);
-    if (!(pm <= st.m)) lse_rescale(st, pm, a.c);
-#pragma unroll
-    for (int u = 0; u < kLpU; ++u)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float d = fmaxf((x[u][e] - st.m) * a.c, kLpLow);
-        const float w = exp2_approx(d);
-        st.s += w;
-        st.d = fmaf(w, d, st.d);
-      }
-    if (k == 0) continue;
 
-    auto id_of = [&](int u, int e) {
-      return (int)(base + (int64_t)(u * kLpNT + tid) * VE - off) + e;
+  if (warp == kLpWarps) {
+    if (lane == 0) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(l + head);
+      bool ok = true;
+      for (int i = 0; i < mine && ok; ++i) {
+        const int s = i % kLpStages;
+        if (i >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((i / kLpStages) - 1) & 1);
+        if (!ok) break;
+        const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
+        const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)nvec * 16 - at);
+        umma::mbar_expect_tx(&sh.full[s], bytes);
+        umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
+      }
+      if (!ok) {
+        atomicExch(&sh.timeout, 1);
+        // every copy issued has landed before this block may exit
+        for (int s = 0; s < kLpStages; ++s)
+          for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
+      }
+    }
+  } else {
+    float xt = 0.f;
+    if (rank == 0 && tid == 0 && token >= 0 && token < a.V) xt = Elem<T>::load(l + token);
+    // one element per thread of the row's edges, in block 0
+    float xe = -INFINITY;
+    int ie = -1;
+    if (rank == 0) {
+      ie = tid < head ? tid : head + nvec * VE + (tid - head);
+      if (ie < a.V && tid < 2 * VE)
+        xe = Elem<T>::load(l + ie);
+      else
+        ie = -1;
+    }
+    const float c = a.c, low = -kLpLow / c;
+    Lse st{kNegBig, 0.f, 0.f, 0.f};
+    // this warp's list: n keys not after `bound`, whose value is tv
+    lp_key* const list = sh.list[warp];
+    int n = 0, nbest = 0;
+    lp_key bound = 0;
+    float tv = -INFINITY;
+    bool bounded = false;
+    uint32_t limit = umma::kWaitLimit;
+    auto add = [&](float x, int id, bool valid) {
+      const lp_key q = key_of(x, id);
+      const bool take = valid && q >= bound;
+      const unsigned m = __ballot_sync(0xffffffffu, take);
+      if (m == 0u) return;
+      if (n + __popc(m) > kLpList) {
+        n = list_cut(list, n, k);  // n > 32: k keys are left
+        if (list[k - 1] > bound) {
+          bound = list[k - 1];
+          tv = key_value(bound);
+        }
+      }
+      if (take) list[n + __popc(m & ((1u << lane) - 1u))] = q;
+      n += __popc(m);
     };
-    if (first) {
-      // bound: the k-th best of 32 groups' best ids (8 lanes each)
-      float bv = -INFINITY;
-      int bi = kNoId;
-#pragma unroll
-      for (int u = 0; u < kLpU; ++u)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int id = id_of(u, e);
-          if (id >= 0 && id < a.V && lp_before(x[u][e], id, bv, bi)) {
-            bv = x[u][e];
-            bi = id;
-          }
-        }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-        if (lp_before(ov, oi, bv, bi)) {
-          bv = ov;
-          bi = oi;
-        }
+
+    for (int i = 0; i < mine; ++i) {
+      const int s = i % kLpStages;
+      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (i / kLpStages) & 1, limit))) {
+        // gave up: go on without the data, so that no barrier is missed
+        limit = 1;
+        if (lane == 0) atomicExch(&sh.timeout, 1);
       }
-      if ((lane & 7) == 0) {
-        gv[tid >> 3] = bv;
-        gi[tid >> 3] = bi;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        const float v = gv[lane];
-        const int i = gi[lane];
-        int r = 0;
-        for (int o = 0; o < 32; ++o) r += lp_before(gv[o], gi[o], v, i) || (gv[o] == v && gi[o] == i && o < lane);
-        if (r == k - 1) {
-          s_tv = v;
-          s_ti = i;
-        }
-      }
-      __syncthreads();
-      first = false;
-    }
-    const float tv = s_tv;
-    const int ti = s_ti;
-    if (pm >= tv) {
-#pragma unroll
-      for (int u = 0; u < kLpU; ++u)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int id = id_of(u, e);
-          if (x[u][e] >= tv && id >= 0 && id < a.V && !lp_before(tv, ti, x[u][e], id)) {
-            const int slot = atomicAdd(&s_n, 1);
-            if (slot < kLpCap) {
-              cv[slot] = x[u][e];
-              ci[slot] = id;
-            }
-          }
-        }
-    }
-    __syncthreads();
-    int n = s_n;
-    if (n > kLpCap) {
-      // too many reach the bound: take this chunk's k best one by one, each
-      // the best after the one before, and join them to the list
-      const int n0 = s_listed;
-      float pv = INFINITY;
-      int pi = -1;
-      int got = 0;
-      for (; got < k; ++got) {
-        float bv = -INFINITY;
-        int bi = kNoId;
+      const int q0 = (rank + i * C) * (kLpNT * kLpU) + tid;  // first vector of this thread
+      const uint4* st4 = reinterpret_cast<const uint4*>(ring + s * kLpChunk) + tid;
+      const int have = min(kLpU, max(0, (nvec - q0 + kLpNT - 1) / kLpNT));  // vectors in the row
+      float top[kLpU], pm;
+      {
+        uint4 v[kLpU];
 #pragma unroll
         for (int u = 0; u < kLpU; ++u)
+          v[u] = u < have ? st4[u * kLpNT]
+                          : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked,
+                                       Vec<T>::kMasked);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const int id = id_of(u, e);
-            if (id >= 0 && id < a.V && lp_before(pv, pi, x[u][e], id) &&
-                lp_before(x[u][e], id, bv, bi)) {
-              bv = x[u][e];
-              bi = id;
-            }
-          }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-          const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-          if (lp_before(ov, oi, bv, bi)) {
-            bv = ov;
-            bi = oi;
-          }
+        for (int u = 0; u < kLpU; ++u) top[u] = Vec<T>::top(v[u]);
+        pm = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3]));
+        if (!(pm <= st.m)) lse_rescale(st, max_nan(st.m, pm), c, low);
+        if (!bounded) {
+          const Lse next = lse_add<T>(st, v, c);
+          if (__any_sync(0xffffffffu, next.d != next.d))
+            bounded = true;  // this warp's later chunks too: masks come in numbers
+          else
+            st = next;
         }
-        if (lane == 0) {
-          wv[warp] = bv;
-          wi[warp] = bi;
-        }
-        __syncthreads();
-        bv = wv[0];
-        bi = wi[0];
-        for (int w = 1; w < kLpWarps; ++w)
-          if (lp_before(wv[w], wi[w], bv, bi)) {
-            bv = wv[w];
-            bi = wi[w];
-          }
-        __syncthreads();
-        if (bi == kNoId) break;
-        if (tid == 0) {
-          cv[n0 + got] = bv;
-          ci[n0 + got] = bi;
-        }
-        pv = bv;
-        pi = bi;
+        if (bounded) st = lse_add_bounded<T>(st, st4, have, c, low);
       }
-      n = n0 + got;
-      __syncthreads();
-    }
-    if (n > kLpCompact) {
-      // rank by counting; the k best, in order, become the list
-      float mv[kLpCap / kLpNT];
-      int mi[kLpCap / kLpNT], mr[kLpCap / kLpNT];
-#pragma unroll
-      for (int q = 0; q < kLpCap / kLpNT; ++q) {
-        const int j = tid + q * kLpNT;
-        mr[q] = k;
-        if (j < n) {
-          mv[q] = cv[j];
-          mi[q] = ci[j];
-          int r = 0;
-          for (int o = 0; o < n; ++o) r += lp_before(cv[o], ci[o], mv[q], mi[q]) ? 1 : 0;
-          mr[q] = r;
-        }
+      if (k == 0) {
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
+        continue;
       }
-      __syncthreads();
+
+      if (i == 0) {
+        // the bound: the k-th largest of 32 groups' largest logits (8 lanes each)
+        float g = pm;
 #pragma unroll
-      for (int q = 0; q < kLpCap / kLpNT; ++q)
-        if (mr[q] < k) {
-          cv[mr[q]] = mv[q];
-          ci[mr[q]] = mi[q];
-          if (mr[q] == k - 1) {
-            s_tv = mv[q];
-            s_ti = mi[q];
+        for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if ((lane & 7) == 0) sh.group[tid >> 3] = g;
+        lp_bar();
+        g = sh.group[lane];
+        int r = 0;
+#pragma unroll
+        for (int o = 0; o < 32; o += 4) {
+          const float4 og = *reinterpret_cast<const float4*>(sh.group + o);
+          r += og.x > g || (og.x == g && o < lane) ? 1 : 0;
+          r += og.y > g || (og.y == g && o + 1 < lane) ? 1 : 0;
+          r += og.z > g || (og.z == g && o + 2 < lane) ? 1 : 0;
+          r += og.w > g || (og.w == g && o + 3 < lane) ? 1 : 0;
+        }
+        // one lane has rank k - 1 (in a row with a NaN maybe none; such a row reports nothing)
+        const unsigned at = __ballot_sync(0xffffffffu, r == k - 1);
+        if (at) tv = __shfl_sync(0xffffffffu, g, __ffs(at) - 1);
+        bound = (lp_key)lp_ord(tv) << 32;
+      }
+      if (__any_sync(0xffffffffu, pm >= tv)) {
+        // usually few lanes hold a candidate, and each takes a place of its own
+        if (lane == 0) sh.n[warp] = n;
+        __syncwarp();
+        if (pm >= tv) {
+#pragma unroll
+          for (int u = 0; u < kLpU; ++u) {
+            if (!(top[u] >= tv) || u >= have) continue;
+            float x[VE];
+            Elem<T>::unpack16(st4[u * kLpNT], x);
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+              if (x[e] >= tv) {
+                const lp_key q = key_of(x[e], head + (q0 + u * kLpNT) * VE + e);
+                if (q >= bound) {
+                  const int slot = atomicAdd(&sh.n[warp], 1);
+                  if (slot < kLpList) list[slot] = q;
+                }
+              }
           }
         }
-      if (tid == 0) s_n = s_listed = min(n, k);
-    } else if (tid == 0) {
-      s_n = s_listed = n;
+        __syncwarp();
+        const int now = sh.n[warp];
+        if (now <= kLpList) {
+          n = now;
+        } else {
+          // too many for the list: one element per lane at a time, cutting
+          // the list (and so raising the bound) whenever it is full
+#pragma unroll 1
+          for (int u = 0; u < kLpU; ++u) {
+            float x[VE];
+            Elem<T>::unpack16(st4[u * kLpNT], x);
+            const int qv = q0 + u * kLpNT;
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+              if (__any_sync(0xffffffffu, u < have && x[e] >= tv))
+                add(x[e], head + qv * VE + e, u < have && x[e] >= tv);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
+      if ((i & (i + 1)) == 0 && i > 0 && mine - 1 - i > i + 1) {  // after 2, 4, 8 ... chunks
+        nbest = lists_join(sh, n, nbest, k, warp, lane);
+        n = 0;
+        if (nbest == k && sh.bound > bound) {
+          bound = sh.bound;
+          tv = key_value(bound);
+        }
+      }
     }
-    __syncthreads();
+
+    // the edges
+    if (rank == 0) {
+      if (!(xe <= st.m)) lse_rescale(st, max_nan(st.m, xe), c, low);
+      const float y = fmaxf(xe - st.m, low), w = exp2_approx(y * c);
+      float er;
+      two_sum(st.s, w, st.s, er);
+      st.e += er;
+      st.d = fmaf(w, y, st.d);
+      if (k > 0) add(xe, ie, ie >= 0 && xe == xe);
+    }
+    // this block's statistics and ranked keys
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Lse w;
+      w.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+      w.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+      w.e = __shfl_xor_sync(0xffffffffu, st.e, o);
+      w.d = __shfl_xor_sync(0xffffffffu, st.d, o);
+      st = lse_join(st, w, c, low);
+    }
+    if (lane == 0) sh.red[warp] = st;
+    if (k > 0) {
+      nbest = lists_join(sh, n, nbest, k, warp, lane);
+      if (warp == 0 && lane >= nbest) sh.best[lane] = 0;
+    } else {
+      lp_bar();
+    }
+    if (tid == 0) {
+      Lse r = sh.red[0];
+      for (int w = 1; w < kLpWarps; ++w) r = lse_join(r, sh.red[w], c, low);
+      sh.blk = r;
+      sh.group[0] = xt;
+    }
   }
 
-  // this block's statistics and ranked list
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Lse w;
-    w.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    w.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    w.d = __shfl_xor_sync(0xffffffffu, st.d, o);
-    st = lse_join(st, w, a.c);
-  }
-  if (lane == 0) red[warp] = st;
-  if (tid < kLpMaxK) {
-    lv[tid] = -INFINITY;
-    li[tid] = kNoId;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    Lse r = red[0];
-    for (int w = 1; w < kLpWarps; ++w) r = lse_join(r, red[w], a.c);
-    blk = r;
-  }
-  if (k > 0) {
-    const int n = s_n;
-    for (int j = tid; j < n; j += kLpNT) {
-      int r = 0;
-      for (int o = 0; o < n; ++o) r += lp_before(cv[o], ci[o], cv[j], ci[j]) ? 1 : 0;
-      if (r < k) {
-        lv[r] = cv[j];
-        li[r] = ci[j];
-      }
-    }
-  }
   cl.sync();
+  lp_key q = 0;
   if (rank == 0) {
-    // all blocks' lists, ranked; thread (q, j) holds entry j of block q
-    const int q = tid >> 5, j = tid & 31;
-    float v = -INFINITY;
-    int i = kNoId;
-    if (q < C && j < k) {
-      v = cl.map_shared_rank(lv, q)[j];
-      i = cl.map_shared_rank(li, q)[j];
+    // all blocks' keys; warp w holds block w's
+    if (warp < C && warp < kLpMaxC) {
+      if (lane < k) {
+        q = cl.map_shared_rank(sh.best, warp)[lane];
+        sh.all[warp * k + lane] = q;
+      }
+      if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
     }
-    cv[tid] = v;
-    ci[tid] = i;
-    if (tid < C && tid > 0) red[tid] = *cl.map_shared_rank(&blk, tid);
-    if (tid == 0) red[0] = blk;
+    if (tid < C) sh.red[tid] = *cl.map_shared_rank(&sh.blk, tid);
+    if (tid < C && *cl.map_shared_rank(&sh.timeout, tid) != 0) atomicExch(&sh.timeout, 1);
   }
   cl.sync();  // the other blocks' memory has been read; they may exit
   if (rank != 0) return;
-  Lse r = red[0];
-  for (int w = 1; w < C; ++w) r = lse_join(r, red[w], a.c);
-  const bool ok = r.s > 0.f && isfinite(r.s) && isfinite(r.m);
-  const float ln2 = 0.6931471805599453f;
-  const float lnS = logf(r.s);
+  const float c = a.c, low = -kLpLow / c;
+  Lse r = sh.red[0];
+  for (int w = 1; w < C; ++w) r = lse_join(r, sh.red[w], c, low);
+  const bool late = sh.timeout != 0;
+  const bool ok = !late && r.s > 0.f && isfinite(r.s) && isfinite(r.m);
+  const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
   if (tid == 0) {
     const bool in = token >= 0 && token < a.V;
-    a.out_logp[row] = ok && in ? (xt - r.m) * a.inv_t - lnS : nan;
-    if (a.out_entropy) a.out_entropy[row] = ok ? lnS - ln2 * (r.d / r.s) : nan;
-    const int flags = (ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
-    if (flags) atomicOr(a.dev_status, flags);
+    a.out_logp[row] = ok && in ? (sh.group[0] - r.m) * a.inv_t - lnS : nan;
+    if (a.out_entropy) a.out_entropy[row] = ok ? lnS - a.inv_t * (r.d / r.s) : nan;
+    const int flags =
+        (late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
+    if (a.own_status)
+      *a.dev_status = flags;
+    else if (flags)
+      atomicOr(a.dev_status, flags);
   }
   if (k > 0) {
-    const float v = cv[tid];
-    const int i = ci[tid];
-    if (i != kNoId) {
-      int rk = 0;
-      for (int o = 0; o < 32 * C; ++o) rk += lp_before(cv[o], ci[o], v, i) ? 1 : 0;
-      if (rk < k && ok) {
-        a.out_ids[row * k + rk] = i;
-        a.out_top[row * k + rk] = (v - r.m) * a.inv_t - lnS;
+    if (ok && q != 0) {
+      const int rk = count_before(sh.all, C * k, q);
+      if (rk < k) {
+        a.out_ids[row * k + rk] = key_id(q);
+        a.out_top[row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
       }
     }
     if (!ok && tid < k) {
@@ -397,13 +610,43 @@ __global__ void __launch_bounds__(kLpNT) token_logprobs_kernel(LpArgs a) {
   }
 }
 
-// Thread blocks per row: enough rows fill the GPU with one block each; fewer
-// are cut into up to eight.
+// Thread blocks per row: the count that gives the shortest schedule, taking a
+// block's time as its chunks plus three more for its start and its join, and
+// kLpPerSm blocks of the 152 SMs running at once.
 int lp_cluster(int64_t R, int V, int elem) {
-  const int64_t chunks = ((int64_t)V * elem + 15) / 16 / (kLpNT * kLpU) + 1;
-  int C = 1;
-  while (C < kLpMaxC && R * C < 608 && C < chunks) C *= 2;
-  return C;
+  const int64_t chunks = ((int64_t)V * elem + kLpChunk - 1) / kLpChunk;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int C = 1; C <= kLpMaxC && C <= chunks; C *= 2) {
+    const int64_t waves = (R * C + 152 * kLpPerSm - 1) / (152 * kLpPerSm);
+    const int64_t t = waves * ((chunks + C - 1) / C + 3);
+    if (t < least) {
+      least = t;
+      best = C;
+    }
+  }
+  return best;
+}
+
+template <typename T>
+int launch_logprobs(cudaStream_t s, const LpArgs& a, int C) {
+  auto kern = token_logprobs_kernel<T>;
+  VT_RETURN_IF_CUDA(
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.R * C));
+  cfg.blockDim = dim3(kLpNT + 32);
+  cfg.dynamicSmemBytes = kLpSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+  return VT_OK;
 }
 
 }  // namespace
@@ -420,13 +663,13 @@ extern "C" int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64
   if (R < 1 || R > (1 << 24) || V < 1 || V > (1 << 22) || ld_logits < V) return VT_ERR_INVALID_ARG;
   if (k < 0 || k > kLpMaxK || k > V || (k > 0 && (!out_top_ids || !out_top_logp)))
     return VT_ERR_INVALID_ARG;
-  if (!std::isfinite(temperature) || temperature <= 0.f || !std::isfinite(VT_LOG2E / temperature))
-    return VT_ERR_INVALID_ARG;
+  if (!(temperature >= 1e-30f && temperature <= 1e30f)) return VT_ERR_INVALID_ARG;
   const int elem = logits_dtype == VT_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % elem != 0) return VT_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  VT_RETURN_IF_CUDA(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s));
   LpArgs a;
+  a.own_status = R == 1;
+  if (R > 1) VT_RETURN_IF_CUDA(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s));
   a.logits = logits;
   a.R = R;
   a.ld = ld_logits;
@@ -441,20 +684,5 @@ extern "C" int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64
   a.out_top = out_top_logp;
   a.dev_status = dev_status;
   const int C = lp_cluster(R, V, elem);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(R * C));
-  cfg.blockDim = dim3(kLpNT);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (elem == 4)
-    VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, a));
-  else
-    VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, token_logprobs_kernel<uint16_t>, a));
-  return VT_OK;
+  return elem == 4 ? launch_logprobs<float>(s, a, C) : launch_logprobs<uint16_t>(s, a, C);
 }

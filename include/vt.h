@@ -438,7 +438,7 @@ int vt_draft_topk_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_
  *            (ld_logits >= V; aligned to its element type, no more)
  *  tokens    int32 [R]      the id to score in each row; -1: the row is not
  *                           scored and not read (vt_verify pads with -1)
- *  temperature              T finite and > 0: p = softmax(l / T) over the V
+ *  temperature              1e-30 <= T <= 1e30: p = softmax(l / T) over the V
  *                           ids; an id at -infinity has p = 0
  *  out_logp     f32 [R]     out: ln p(token)
  *  out_entropy  f32 [R]     out, may be NULL: -sum p ln p (nats)
