@@ -9,9 +9,9 @@
 // subtracted before the scale, so a row of the type's lowest value still gives
 // the uniform distribution; ids at -inf have p = 0 and add nothing.
 //
-// One pass over a row by a cluster of C thread blocks: block r takes the 16 KB
+// One pass over a row by a cluster of C thread blocks: block r takes the 32 KB
 // chunks r, r + C, ... .  One warp streams them by bulk copies into a ring of
-// four shared-memory stages, eight warps consume them, so the bytes in flight
+// two shared-memory stages, eight warps consume them, so the bytes in flight
 // do not depend on what the consumers are doing; a row's elements before its
 // first and after its last 16-byte boundary are loaded one by one.
 // A thread keeps a running (m, S, D) of what it has seen.  S is a sum of
@@ -21,11 +21,11 @@
 //
 // The k best are kept as 64-bit keys, ordered by (value, lower id first).  A
 // warp lists in shared memory the ids whose key reaches a bound that at least
-// k ids seen reach: first the k-th best of 32 disjoint groups' largest logits
-// (a block's first chunk), later the k-th best key of the block, renewed after
-// 2, 4, 8 ... chunks while more are to come than have been.  So about k ids of the first chunk are listed and few
-// later ones; lists are ranked by counting.  Ties and masked rows take no
-// other path.  Blocks join through distributed shared memory.
+// k ids seen reach: the k-th best of 32 disjoint groups' largest logits,
+// renewed after 2, 4, 8 ... chunks.  So little more than k ids of the first
+// chunk are listed and few later ones; the lists are ranked by counting at the
+// end.  A list that fills (ties, masks, ordered rows) is cut to its k best
+// keys, the last of which is a bound too.  Blocks join through distributed shared memory.
 #include <algorithm>
 #include <cmath>
 
@@ -41,9 +41,9 @@ namespace {
 
 constexpr int kLpNT = 256;           // consuming threads
 constexpr int kLpWarps = kLpNT / 32;
-constexpr int kLpU = 4;              // 16-byte vectors per thread and chunk
+constexpr int kLpU = 8;              // 16-byte vectors per thread and chunk
 constexpr int kLpChunk = kLpNT * kLpU * 16;  // bytes
-constexpr int kLpStages = 4;
+constexpr int kLpStages = 2;
 constexpr int kLpMaxK = 32;
 constexpr int kLpList = 64;          // entries of a warp's list (2 * kLpMaxK: a cut leaves room)
 constexpr int kLpMaxC = 8;
@@ -133,6 +133,12 @@ template <> struct Vec<float> {
     return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                    max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
+  __device__ static float top(const uint4 (&v)[kLpU]) {
+    float m = top(v[0]);
+#pragma unroll
+    for (int u = 1; u < kLpU; ++u) m = max_nan(m, top(v[u]));
+    return m;
+  }
   static constexpr uint32_t kMasked = 0xff800000u;  // -infinity
 };
 template <> struct Vec<uint16_t> {
@@ -143,6 +149,13 @@ template <> struct Vec<uint16_t> {
   }
   __device__ static float top(uint4 v) {
     const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ static float top(const uint4 (&v)[kLpU]) {
+    uint32_t m = max2(max2(v[0].x, v[0].y), max2(v[0].z, v[0].w));
+#pragma unroll
+    for (int u = 1; u < kLpU; ++u)
+      m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
   static constexpr uint32_t kMasked = 0xff80ff80u;
@@ -269,31 +282,61 @@ __device__ __noinline__ int list_cut(lp_key* list, int n, int k) {
   return min(n, k);
 }
 
+// the k-th largest of the 32 lanes' values (1 <= k <= 32), by a bitonic sort
+__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, stride);
+      v = ((lane & size) == 0) == ((lane & stride) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return __shfl_sync(0xffffffffu, v, k - 1);
+}
+
 // the consuming warps' barrier
 __device__ __forceinline__ void lp_bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(kLpNT) : "memory");
 }
 
+// A row's layout for one block: ids [0, head) precede the first 16-byte
+// boundary, nvec whole vectors follow, then the rest; mine of the vectors'
+// chunks are this block's.
+struct Span {
+  int head, nvec, mine;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const LpArgs& a, int64_t row, int rank, int C) {
+  constexpr int VE = Elem<T>::kVec;
+  const T* l = static_cast<const T*>(a.logits) + row * a.ld;
+  const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
+  Span sp;
+  sp.head = min(a.V, off ? VE - off : 0);
+  sp.nvec = (a.V - sp.head) / VE;
+  const int chunks = (sp.nvec + kLpNT * kLpU - 1) / (kLpNT * kLpU);
+  sp.mine = chunks > rank ? (chunks - rank + C - 1) / C : 0;
+  return sp;
+}
+
 struct LpShared {
   alignas(16) lp_key list[kLpWarps][kLpList];        // the warps' lists
-  alignas(16) lp_key all[kLpWarps * kLpList + kLpMaxK + 8];  // all lists, joined
+  alignas(16) lp_key all[kLpWarps * kLpList + 8];    // all lists, joined
   alignas(16) lp_key best[kLpMaxK];                  // this block's k best, as published
   alignas(16) float group[32];                       // largest logit of each of 32 groups of threads
   alignas(8) uint64_t full[kLpStages], empty[kLpStages];
-  lp_key bound;
   int n[kLpWarps];
   Lse red[kLpWarps];
   Lse blk;                                           // this block's statistics, as published
   int timeout;
 };
 
-// Joins the warps' lists (n entries in this warp's) and the nbest keys of
-// sh.best into the block's k best, ranked in sh.best; the lists are
-// empty after.  Returns the new nbest.  All consuming warps call it.
-__device__ __forceinline__ int lists_join(LpShared& sh, int n, int nbest, int k, int warp, int lane) {
+// Joins the warps' lists (n entries in this warp's) into the block's k best,
+// ranked in sh.best (zero behind the last).  All consuming warps call it.
+__device__ __forceinline__ void lists_join(LpShared& sh, int n, int k, int warp, int lane) {
   if (lane == 0) sh.n[warp] = n;
+  if (warp == 0) sh.best[lane] = 0;
   lp_bar();
-  int at = nbest, total = nbest;
+  int at = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kLpWarps; ++w) {
     const int nw = sh.n[w];
@@ -301,17 +344,13 @@ __device__ __forceinline__ int lists_join(LpShared& sh, int n, int nbest, int k,
     total += nw;
   }
   for (int j = lane; j < n; j += 32) sh.all[at + j] = sh.list[warp][j];
-  if (warp == 0 && lane < nbest) sh.all[lane] = sh.best[lane];
   if (warp == kLpWarps - 1 && lane < 8) sh.all[total + lane] = 0;
   lp_bar();
   for (int j = warp * 32 + lane; j < total; j += kLpNT) {
     const lp_key q = sh.all[j];
     const int r = count_before(sh.all, total, q);
     if (r < k) sh.best[r] = q;
-    if (r == k - 1) sh.bound = q;
   }
-  lp_bar();
-  return min(total, k);
 }
 
 template <typename T>
@@ -321,33 +360,11 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
   __shared__ LpShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int64_t row = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int token = a.tokens[row];
   const int k = a.k;
   const float nan = __int_as_float(0x7fc00000);
-  if (token == -1) {  // not scored: the row is not read
-    if (rank == 0) {
-      if (tid == 0) {
-        a.out_logp[row] = nan;
-        if (a.out_entropy) a.out_entropy[row] = nan;
-        if (a.own_status) *a.dev_status = 0;
-      }
-      if (tid < k) {
-        a.out_ids[row * k + tid] = -1;
-        a.out_top[row * k + tid] = nan;
-      }
-    }
-    return;
-  }
-  const T* l = static_cast<const T*>(a.logits) + row * a.ld;
-  // ids [0, head) precede the first 16-byte boundary, nvec whole vectors
-  // follow, then the rest
-  const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
-  const int head = min(a.V, off ? VE - off : 0);
-  const int nvec = (a.V - head) / VE;
-  const int nchunk = (nvec + kLpNT * kLpU - 1) / (kLpNT * kLpU);
-  const int mine = nchunk > rank ? (nchunk - rank + C - 1) / C : 0;  // chunks of this block
+  // this cluster's rows (more than one only when C == 1)
+  const int64_t row0 = blockIdx.x / C, stride = gridDim.x / C;
   if (tid == 0) {
     for (int s = 0; s < kLpStages; ++s) {
       umma::mbar_init(&sh.full[s], 1);
@@ -359,17 +376,24 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
   __syncthreads();
 
   if (warp == kLpWarps) {
+    // the producing warp runs ahead of the consumers, into their next rows
     if (lane == 0) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(l + head);
       bool ok = true;
-      for (int i = 0; i < mine && ok; ++i) {
-        const int s = i % kLpStages;
-        if (i >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((i / kLpStages) - 1) & 1);
-        if (!ok) break;
-        const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
-        const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)nvec * 16 - at);
-        umma::mbar_expect_tx(&sh.full[s], bytes);
-        umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
+      int it = 0;  // chunks requested so far
+      for (int64_t row = row0; row < a.R && ok; row += stride) {
+        if (a.tokens[row] == -1) continue;
+        const Span sp = span_of<T>(a, row, rank, C);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+            static_cast<const T*>(a.logits) + row * a.ld + sp.head);
+        for (int i = 0; i < sp.mine; ++i, ++it) {
+          const int s = it % kLpStages;
+          if (it >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((it / kLpStages) - 1) & 1);
+          if (!ok) break;
+          const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
+          const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)sp.nvec * 16 - at);
+          umma::mbar_expect_tx(&sh.full[s], bytes);
+          umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
+        }
       }
       if (!ok) {
         atomicExch(&sh.timeout, 1);
@@ -378,7 +402,37 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
           for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
       }
     }
-  } else {
+    __syncwarp();
+    if (C > 1 && a.tokens[row0] != -1) {
+      cl.sync();
+      cl.sync();
+    }
+    return;
+  }
+
+  int it = 0;  // chunks consumed so far
+  uint32_t limit = umma::kWaitLimit;
+  int next_token = a.tokens[row0];
+  for (int64_t row = row0; row < a.R; row += stride) {
+    const int token = next_token;
+    if (row + stride < a.R) next_token = a.tokens[row + stride];
+    if (token == -1) {  // not scored: the row is not read
+      if (rank == 0) {
+        if (tid == 0) {
+          a.out_logp[row] = nan;
+          if (a.out_entropy) a.out_entropy[row] = nan;
+          if (a.own_status) *a.dev_status = 0;
+        }
+        if (tid < k) {
+          a.out_ids[row * k + tid] = -1;
+          a.out_top[row * k + tid] = nan;
+        }
+      }
+      continue;
+    }
+    const T* l = static_cast<const T*>(a.logits) + row * a.ld;
+    const Span sp = span_of<T>(a, row, rank, C);
+    const int head = sp.head, nvec = sp.nvec, mine = sp.mine;
     float xt = 0.f;
     if (rank == 0 && tid == 0 && token >= 0 && token < a.V) xt = Elem<T>::load(l + token);
     // one element per thread of the row's edges, in block 0
@@ -395,14 +449,14 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     Lse st{kNegBig, 0.f, 0.f, 0.f};
     // this warp's list: n keys not after `bound`, whose value is tv
     lp_key* const list = sh.list[warp];
-    int n = 0, nbest = 0;
+    int n = 0;
     lp_key bound = 0;
     float tv = -INFINITY;
     bool bounded = false;
-    uint32_t limit = umma::kWaitLimit;
+    volatile float* const group = sh.group;
     auto add = [&](float x, int id, bool valid) {
       const lp_key q = key_of(x, id);
-      const bool take = valid && q >= bound;
+      const bool take = valid && x >= tv && q >= bound;  // a NaN is none
       const unsigned m = __ballot_sync(0xffffffffu, take);
       if (m == 0u) return;
       if (n + __popc(m) > kLpList) {
@@ -416,9 +470,9 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       n += __popc(m);
     };
 
-    for (int i = 0; i < mine; ++i) {
-      const int s = i % kLpStages;
-      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (i / kLpStages) & 1, limit))) {
+    for (int i = 0; i < mine; ++i, ++it) {
+      const int s = it % kLpStages;
+      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (it / kLpStages) & 1, limit))) {
         // gave up: go on without the data, so that no barrier is missed
         limit = 1;
         if (lane == 0) atomicExch(&sh.timeout, 1);
@@ -426,17 +480,20 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       const int q0 = (rank + i * C) * (kLpNT * kLpU) + tid;  // first vector of this thread
       const uint4* st4 = reinterpret_cast<const uint4*>(ring + s * kLpChunk) + tid;
       const int have = min(kLpU, max(0, (nvec - q0 + kLpNT - 1) / kLpNT));  // vectors in the row
-      float top[kLpU], pm;
+      float pm;
       {
         uint4 v[kLpU];
+        if (have == kLpU) {
 #pragma unroll
-        for (int u = 0; u < kLpU; ++u)
-          v[u] = u < have ? st4[u * kLpNT]
-                          : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked,
-                                       Vec<T>::kMasked);
+          for (int u = 0; u < kLpU; ++u) v[u] = st4[u * kLpNT];
+        } else {
 #pragma unroll
-        for (int u = 0; u < kLpU; ++u) top[u] = Vec<T>::top(v[u]);
-        pm = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3]));
+          for (int u = 0; u < kLpU; ++u)
+            v[u] = u < have ? st4[u * kLpNT]
+                            : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked,
+                                         Vec<T>::kMasked);
+        }
+        pm = Vec<T>::top(v);
         if (!(pm <= st.m)) lse_rescale(st, max_nan(st.m, pm), c, low);
         if (!bounded) {
           const Lse next = lse_add<T>(st, v, c);
@@ -453,78 +510,44 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
         continue;
       }
 
-      if (i == 0) {
-        // the bound: the k-th largest of 32 groups' largest logits (8 lanes each)
-        float g = pm;
+      if ((i & (i + 1)) == 0) {
+        // after 1, 2, 4 ... chunks, the bound: the k-th largest of 32 groups'
+        // (8 lanes each) largest logits so far.  Only the first chunk needs every group's value;
+        // later a value of another warp may be an older one, which is as valid.
+        float g = st.s > 0.f ? st.m : -INFINITY;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if ((lane & 7) == 0) sh.group[tid >> 3] = g;
-        lp_bar();
-        g = sh.group[lane];
-        int r = 0;
-#pragma unroll
-        for (int o = 0; o < 32; o += 4) {
-          const float4 og = *reinterpret_cast<const float4*>(sh.group + o);
-          r += og.x > g || (og.x == g && o < lane) ? 1 : 0;
-          r += og.y > g || (og.y == g && o + 1 < lane) ? 1 : 0;
-          r += og.z > g || (og.z == g && o + 2 < lane) ? 1 : 0;
-          r += og.w > g || (og.w == g && o + 3 < lane) ? 1 : 0;
+        if ((lane & 7) == 0) group[tid >> 3] = g;
+        if (i == 0)
+          lp_bar();
+        else
+          __syncwarp();
+        const float gk = kth_of_lanes(group[lane], k, lane);
+        const lp_key b = (lp_key)lp_ord(gk) << 32;
+        if (b > bound) {
+          bound = b;
+          tv = gk;
         }
-        // one lane has rank k - 1 (in a row with a NaN maybe none; such a row reports nothing)
-        const unsigned at = __ballot_sync(0xffffffffu, r == k - 1);
-        if (at) tv = __shfl_sync(0xffffffffu, g, __ffs(at) - 1);
-        bound = (lp_key)lp_ord(tv) << 32;
       }
-      if (__any_sync(0xffffffffu, pm >= tv)) {
-        // usually few lanes hold a candidate, and each takes a place of its own
-        if (lane == 0) sh.n[warp] = n;
-        __syncwarp();
-        if (pm >= tv) {
-#pragma unroll
-          for (int u = 0; u < kLpU; ++u) {
-            if (!(top[u] >= tv) || u >= have) continue;
-            float x[VE];
-            Elem<T>::unpack16(st4[u * kLpNT], x);
-#pragma unroll
-            for (int e = 0; e < VE; ++e)
-              if (x[e] >= tv) {
-                const lp_key q = key_of(x[e], head + (q0 + u * kLpNT) * VE + e);
-                if (q >= bound) {
-                  const int slot = atomicAdd(&sh.n[warp], 1);
-                  if (slot < kLpList) list[slot] = q;
-                }
-              }
-          }
-        }
-        __syncwarp();
-        const int now = sh.n[warp];
-        if (now <= kLpList) {
-          n = now;
+      // the lanes that hold a candidate, usually few, one by one: the warp
+      // looks at that lane's vectors together, a word per lane
+      unsigned holders = __ballot_sync(0xffffffffu, pm >= tv);
+      while (holders) {
+        const int src = __ffs(holders) - 1;
+        holders &= holders - 1;
+        const int qv = q0 - lane + src + (lane >> 2) * kLpNT;
+        const uint32_t word =
+            reinterpret_cast<const uint32_t*>(st4 - lane + src + (lane >> 2) * kLpNT)[lane & 3];
+        const int id = head + qv * VE + (lane & 3) * (VE / 4);
+        if constexpr (VE == 4) {
+          add(__uint_as_float(word), id, qv < nvec);
         } else {
-          // too many for the list: one element per lane at a time, cutting
-          // the list (and so raising the bound) whenever it is full
-#pragma unroll 1
-          for (int u = 0; u < kLpU; ++u) {
-            float x[VE];
-            Elem<T>::unpack16(st4[u * kLpNT], x);
-            const int qv = q0 + u * kLpNT;
-#pragma unroll
-            for (int e = 0; e < VE; ++e)
-              if (__any_sync(0xffffffffu, u < have && x[e] >= tv))
-                add(x[e], head + qv * VE + e, u < have && x[e] >= tv);
-          }
+          add(__uint_as_float(word << 16), id, qv < nvec);
+          add(__uint_as_float(word & 0xffff0000u), id + 1, qv < nvec);
         }
       }
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
-      if ((i & (i + 1)) == 0 && i > 0 && mine - 1 - i > i + 1) {  // after 2, 4, 8 ... chunks
-        nbest = lists_join(sh, n, nbest, k, warp, lane);
-        n = 0;
-        if (nbest == k && sh.bound > bound) {
-          bound = sh.bound;
-          tv = key_value(bound);
-        }
-      }
     }
 
     // the edges
@@ -548,65 +571,69 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       st = lse_join(st, w, c, low);
     }
     if (lane == 0) sh.red[warp] = st;
-    if (k > 0) {
-      nbest = lists_join(sh, n, nbest, k, warp, lane);
-      if (warp == 0 && lane >= nbest) sh.best[lane] = 0;
+    if (k > 0) lists_join(sh, n, k, warp, lane);
+    lp_bar();
+    Lse r = sh.red[lane % kLpWarps];
+#pragma unroll
+    for (int o = kLpWarps / 2; o > 0; o >>= 1) {
+      Lse w;
+      w.m = __shfl_xor_sync(0xffffffffu, r.m, o);
+      w.s = __shfl_xor_sync(0xffffffffu, r.s, o);
+      w.e = __shfl_xor_sync(0xffffffffu, r.e, o);
+      w.d = __shfl_xor_sync(0xffffffffu, r.d, o);
+      r = lse_join(r, w, c, low);
+    }
+    lp_key q = 0;  // this thread's key of the row's candidates for the k best
+    int rk = 0;    // ... and its rank
+    bool late;
+    if (C == 1) {
+      if (warp == 0 && lane < k) q = sh.best[lane];
+      rk = lane;
+      late = sh.timeout != 0;
     } else {
-      lp_bar();
+      if (tid == 0) sh.blk = r;
+      cl.sync();
+      if (rank == 0) {
+        // all blocks' keys; warp w holds block w's
+        if (warp < C) {
+          if (lane < k) {
+            q = cl.map_shared_rank(sh.best, warp)[lane];
+            sh.all[warp * k + lane] = q;
+          }
+          if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
+        }
+        if (tid < C) sh.red[tid] = *cl.map_shared_rank(&sh.blk, tid);
+        if (tid < C && *cl.map_shared_rank(&sh.timeout, tid) != 0) atomicExch(&sh.timeout, 1);
+      }
+      cl.sync();  // the other blocks' memory has been read; they may exit
+      if (rank != 0) return;
+      if (q != 0) rk = count_before(sh.all, C * k, q);
+      r = sh.red[0];
+      for (int w = 1; w < C; ++w) r = lse_join(r, sh.red[w], c, low);
+      late = sh.timeout != 0;
     }
+    const bool ok = !late && r.s > 0.f && isfinite(r.s) && isfinite(r.m);
+    const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
     if (tid == 0) {
-      Lse r = sh.red[0];
-      for (int w = 1; w < kLpWarps; ++w) r = lse_join(r, sh.red[w], c, low);
-      sh.blk = r;
-      sh.group[0] = xt;
+      const bool in = token >= 0 && token < a.V;
+      a.out_logp[row] = ok && in ? (xt - r.m) * a.inv_t - lnS : nan;
+      if (a.out_entropy) a.out_entropy[row] = ok ? lnS - a.inv_t * (r.d / r.s) : nan;
+      const int flags =
+          (late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
+      if (a.own_status)
+        *a.dev_status = flags;
+      else if (flags)
+        atomicOr(a.dev_status, flags);
     }
-  }
-
-  cl.sync();
-  lp_key q = 0;
-  if (rank == 0) {
-    // all blocks' keys; warp w holds block w's
-    if (warp < C && warp < kLpMaxC) {
-      if (lane < k) {
-        q = cl.map_shared_rank(sh.best, warp)[lane];
-        sh.all[warp * k + lane] = q;
-      }
-      if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
-    }
-    if (tid < C) sh.red[tid] = *cl.map_shared_rank(&sh.blk, tid);
-    if (tid < C && *cl.map_shared_rank(&sh.timeout, tid) != 0) atomicExch(&sh.timeout, 1);
-  }
-  cl.sync();  // the other blocks' memory has been read; they may exit
-  if (rank != 0) return;
-  const float c = a.c, low = -kLpLow / c;
-  Lse r = sh.red[0];
-  for (int w = 1; w < C; ++w) r = lse_join(r, sh.red[w], c, low);
-  const bool late = sh.timeout != 0;
-  const bool ok = !late && r.s > 0.f && isfinite(r.s) && isfinite(r.m);
-  const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
-  if (tid == 0) {
-    const bool in = token >= 0 && token < a.V;
-    a.out_logp[row] = ok && in ? (sh.group[0] - r.m) * a.inv_t - lnS : nan;
-    if (a.out_entropy) a.out_entropy[row] = ok ? lnS - a.inv_t * (r.d / r.s) : nan;
-    const int flags =
-        (late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
-    if (a.own_status)
-      *a.dev_status = flags;
-    else if (flags)
-      atomicOr(a.dev_status, flags);
-  }
-  if (k > 0) {
-    if (ok && q != 0) {
-      const int rk = count_before(sh.all, C * k, q);
-      if (rk < k) {
-        a.out_ids[row * k + rk] = key_id(q);
-        a.out_top[row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
-      }
+    if (ok && q != 0 && rk < k) {
+      a.out_ids[row * k + rk] = key_id(q);
+      a.out_top[row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
     }
     if (!ok && tid < k) {
       a.out_ids[row * k + tid] = -1;
       a.out_top[row * k + tid] = nan;
     }
+    lp_bar();  // the next row writes what this one has read
   }
 }
 
@@ -634,7 +661,7 @@ int launch_logprobs(cudaStream_t s, const LpArgs& a, int C) {
   VT_RETURN_IF_CUDA(
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.R * C));
+  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min<int64_t>(a.R, 152 * kLpPerSm)));
   cfg.blockDim = dim3(kLpNT + 32);
   cfg.dynamicSmemBytes = kLpSmem;
   cfg.stream = s;
