@@ -330,9 +330,26 @@ struct LpShared {
   int timeout;
 };
 
-// Joins the warps' lists (n entries in this warp's) into the block's k best,
-// ranked in sh.best (zero behind the last).  All consuming warps call it.
-__device__ __forceinline__ void lists_join(LpShared& sh, int n, int k, int warp, int lane) {
+// Joins the warps' lists (n entries in this warp's, of which those not after
+// `bound` count) into the block's k best, ranked in sh.best (zero behind the
+// last).  All consuming warps call it.
+__device__ __forceinline__ void lists_join(LpShared& sh, int n, lp_key bound, int k, int warp,
+                                           int lane) {
+  lp_key mine[kLpList / 32];
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < kLpList / 32; ++h) {
+    const int j = lane + 32 * h;
+    mine[h] = j < n ? sh.list[warp][j] : 0;
+    if (mine[h] < bound) mine[h] = 0;
+  }
+  unsigned has[kLpList / 32];
+  n = 0;
+#pragma unroll
+  for (int h = 0; h < kLpList / 32; ++h) {
+    has[h] = __ballot_sync(0xffffffffu, mine[h] != 0);
+    n += __popc(has[h]);
+  }
   if (lane == 0) sh.n[warp] = n;
   if (warp == 0) sh.best[lane] = 0;
   lp_bar();
@@ -343,7 +360,11 @@ __device__ __forceinline__ void lists_join(LpShared& sh, int n, int k, int warp,
     at += w < warp ? nw : 0;
     total += nw;
   }
-  for (int j = lane; j < n; j += 32) sh.all[at + j] = sh.list[warp][j];
+#pragma unroll
+  for (int h = 0; h < kLpList / 32; ++h) {
+    if (mine[h] != 0) sh.all[at + __popc(has[h] & ((1u << lane) - 1u))] = mine[h];
+    at += __popc(has[h]);
+  }
   if (warp == kLpWarps - 1 && lane < 8) sh.all[total + lane] = 0;
   lp_bar();
   for (int j = warp * 32 + lane; j < total; j += kLpNT) {
@@ -351,6 +372,14 @@ __device__ __forceinline__ void lists_join(LpShared& sh, int n, int k, int warp,
     const int r = count_before(sh.all, total, q);
     if (r < k) sh.best[r] = q;
   }
+}
+
+// Clears the status word of a call over several rows.  The rows' kernel, whose
+// launch overlaps this one, needs nothing else of it: the threads that raise
+// flags wait for it.
+__global__ void zero_status_kernel(int* dev_status) {
+  griddep_launch_dependents();
+  *dev_status = 0;
 }
 
 template <typename T>
@@ -410,6 +439,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     return;
   }
 
+  if (tid == 0 && !a.own_status) griddep_wait();  // the status word is clear
   int it = 0;  // chunks consumed so far
   uint32_t limit = umma::kWaitLimit;
   int next_token = a.tokens[row0];
@@ -455,10 +485,10 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     bool bounded = false;
     volatile float* const group = sh.group;
     auto add = [&](float x, int id, bool valid) {
+      if (!__any_sync(0xffffffffu, valid && x >= tv)) return;  // a NaN is none
       const lp_key q = key_of(x, id);
-      const bool take = valid && x >= tv && q >= bound;  // a NaN is none
+      const bool take = valid && x >= tv && q >= bound;
       const unsigned m = __ballot_sync(0xffffffffu, take);
-      if (m == 0u) return;
       if (n + __popc(m) > kLpList) {
         n = list_cut(list, n, k);  // n > 32: k keys are left
         if (list[k - 1] > bound) {
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       st = lse_join(st, w, c, low);
     }
     if (lane == 0) sh.red[warp] = st;
-    if (k > 0) lists_join(sh, n, k, warp, lane);
+    if (k > 0) lists_join(sh, n, bound, k, warp, lane);
     lp_bar();
     Lse r = sh.red[lane % kLpWarps];
 #pragma unroll
@@ -665,13 +695,15 @@ int launch_logprobs(cudaStream_t s, const LpArgs& a, int C) {
   cfg.blockDim = dim3(kLpNT + 32);
   cfg.dynamicSmemBytes = kLpSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.own_status ? 1 : 2;
   VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   return VT_OK;
 }
@@ -696,7 +728,12 @@ extern "C" int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LpArgs a;
   a.own_status = R == 1;
-  if (R > 1) VT_RETURN_IF_CUDA(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s));
+  if (R > 1) {
+    // launched as an ordinary kernel: it, and so the kernel behind it, starts
+    // once everything before the call has completed
+    zero_status_kernel<<<1, 1, 0, s>>>(dev_status);
+    VT_RETURN_IF_LAUNCH_FAILED();
+  }
   a.logits = logits;
   a.R = R;
   a.ld = ld_logits;
