@@ -139,6 +139,12 @@ template <> struct Vec<float> {
     for (int u = 1; u < kLpU; ++u) m = max_nan(m, top(v[u]));
     return m;
   }
+  // elements e, e + 1 of a vector, plus s
+  __device__ static f32x2 diff2(uint4 v, int e, float s) {
+    return add2(e == 0 ? pack2(__uint_as_float(v.x), __uint_as_float(v.y))
+                       : pack2(__uint_as_float(v.z), __uint_as_float(v.w)),
+                pack2(s, s));
+  }
   static constexpr uint32_t kMasked = 0xff800000u;  // -infinity
 };
 template <> struct Vec<uint16_t> {
@@ -157,6 +163,16 @@ template <> struct Vec<uint16_t> {
     for (int u = 1; u < kLpU; ++u)
       m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  // elements e, e + 1 of a vector, plus s: bf16 operands widened by the addition
+  __device__ static f32x2 diff2(uint4 v, int e, float s) {
+    const uint32_t w = e == 0 ? v.x : e == 2 ? v.y : e == 4 ? v.z : v.w;
+    float a, b;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %3;\n\tadd.rn.f32.bf16 %1, hi, %3;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(w), "f"(s));
+    return pack2(a, b);
   }
   static constexpr uint32_t kMasked = 0xff80ff80u;
 };
@@ -203,15 +219,13 @@ __device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c, float low) {
 template <typename T>
 __device__ __forceinline__ Lse lse_add(Lse st, const uint4 (&v)[kLpU], float c) {
   constexpr int VE = Elem<T>::kVec;
-  const f32x2 nm = pack2(-st.m, -st.m), c2 = pack2(c, c);
+  const f32x2 c2 = pack2(c, c);
   f32x2 sum[kLpU], d = pack2(st.d, 0.f);
 #pragma unroll
   for (int u = 0; u < kLpU; ++u) {
-    float x[VE];
-    Elem<T>::unpack16(v[u], x);
 #pragma unroll
     for (int e = 0; e < VE; e += 2) {
-      const f32x2 y = add2(pack2(x[e], x[e + 1]), nm);
+      const f32x2 y = Vec<T>::diff2(v[u], e, -st.m);
       float t0, t1;
       unpack2(mul2(y, c2), t0, t1);
       const f32x2 w = pack2(exp2_approx(t0), exp2_approx(t1));
