@@ -167,18 +167,27 @@ struct Fp8Args {
   const float* sw;      // [K / 128][groups]
   const float* sx;      // [groups][Bp]
   int Bp, groups, nchunk;
+  int items;            // 128-row tiles times batch chunks
 };
 
-constexpr int kMaxGroups = 512;  // H <= 65536
-constexpr int kMaxAcc = 4;
+constexpr int kMaxGroups = 512;   // H <= 65536
+constexpr int kScaleSlots = 8;    // groups whose sx are in shared memory at once
 
-// accumulator buffers in tensor memory (a power of two)
+// accumulator buffers in tensor memory
 template <int BN>
 constexpr int kAccBufs = BN <= 128 ? 4 : 2;
-// promoting threads: one per row of the tile; two per row (half the columns
-// each) for wide batches
+// columns (batch rows) of one promoting warp, which has 32 of the tile's rows,
+// and the promoting threads
 template <int BN>
-constexpr int kPromNT = BN >= 128 ? 256 : 128;
+constexpr int kPromCols = BN < 64 ? BN : BN == 256 ? 128 : 64;
+template <int BN>
+constexpr int kPromNT = 128 * (BN / kPromCols<BN>);
+// resident CTAs per SM
+template <int BN>
+constexpr int kHeadPerSm = BN <= 64 ? 2 : 1;
+// columns whose partials are reduced at once
+template <int BN>
+constexpr int kPartCols = BN < 32 ? BN : 32;
 
 __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
@@ -190,16 +199,98 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
-// One CTA per 128 rows of W8 and BN rows of the batch.  Each group of 128
-// reduction columns is one shared-memory stage (W8 128 x 128 bytes, x8
-// BN x 128 bytes, both K-major with the 128-byte swizzle, and the BN scales
-// sx) and one tcgen05 accumulation of four K = 32 steps into one of several
-// tensor-memory buffers.  The promoting warps read each finished buffer and
-// add it, times sw * sx, to fp32 sums in registers: the scales of a group
-// multiply its partial sum only, and the long sum is held in 32 bits by the
-// CUDA cores.  One warp issues the TMA loads and one the MMAs.
+// two fp32 values in one 64-bit register
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(uint32_t a, uint32_t b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(f32x2& acc, f32x2 a, f32x2 b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
+// 8 NB consecutive columns of this warp's 32 TMEM lanes, spread over the warp
+// so that a thread has few columns and several rows (so few scales): thread t
+// gets of column block k the columns 8 k + 2 (t % 4) + {0, 1} of the rows
+// t / 4 + 8 i, in v[k][i].
+template <int NB>
+__device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, f32x2 (&v)[NB][4]) {
+  static_assert(NB == 2 || NB == 4, "16 or 32 columns");
+  uint32_t r[2][NB * 4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // lanes 0-15 and 16-31
+    const uint32_t at = taddr + ((uint32_t)(16 * h) << 16);
+    if constexpr (NB == 4) {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+          "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+          : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
+            "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]),
+            "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]),
+            "=r"(r[h][15])
+          : "r"(at)
+          : "memory");
+    } else {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
+            "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7])
+          : "r"(at)
+          : "memory");
+    }
+  }
+  // the wait names the registers, so that no use of them can precede it
+  if constexpr (NB == 4) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
+                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]),
+                   "+r"(r[0][10]), "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]),
+                   "+r"(r[0][14]), "+r"(r[0][15])::"memory");
+    asm volatile(""
+                 : "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]),
+                   "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]), "+r"(r[1][9]),
+                   "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]), "+r"(r[1][13]),
+                   "+r"(r[1][14]), "+r"(r[1][15])::"memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
+                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[1][0]), "+r"(r[1][1]),
+                   "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]),
+                   "+r"(r[1][7])::"memory");
+  }
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[k][2 * h] = pack2(r[h][4 * k], r[h][4 * k + 1]);
+      v[k][2 * h + 1] = pack2(r[h][4 * k + 2], r[h][4 * k + 3]);
+    }
+}
+
+// Blocks of 128 rows of W8 x BN rows of the batch, taken by a persistent CTA
+// one after another.  Each group of 128 reduction columns is one
+// shared-memory stage (W8 128 x 128 bytes, x8 BN x 128 bytes, both K-major
+// with the 128-byte swizzle) and one tcgen05 accumulation of four K = 32 steps
+// into one of the tensor-memory buffers.  The promoting warps read each
+// finished buffer, give it back at once, and add it, times sw * sx, to fp32
+// sums in registers: the scales of a group multiply its partial sum only, and
+// the long sum is held in 32 bits by the CUDA cores.  One warp issues the TMA
+// loads (and the copies of sx, in a ring of its own, so that a stage is free
+// as soon as its MMAs are done) and one the MMAs; both run ahead into the next
+// block while the promoting warps store the last one.
 template <int BN>
-__global__ void __launch_bounds__(kPromNT<BN> + 64, 1)
+__global__ void __launch_bounds__(kPromNT<BN> + 64, kHeadPerSm<BN>)
 head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 Fp8Args fa) {
   using namespace umma;
@@ -207,35 +298,36 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   constexpr int NP = kPromNT<BN>;
   constexpr int kPromWarps = NP / 32;
   constexpr int NBUF = kAccBufs<BN>;
-  constexpr int CW = BN / (NP / 128);  // columns of one promoting thread
-  constexpr int CH = CW >= 32 ? 32 : 16;
+  constexpr int CW = kPromCols<BN>;
+  constexpr int NB = CW >= 32 ? 4 : 2;  // 8-column blocks read at once
+  constexpr int PC = kPartCols<BN>;
   constexpr uint32_t kCols = (uint32_t)(NBUF * BN);  // 64..512, a power of two
-  constexpr int kBBytes = BN * 128;
-  constexpr int stage_bytes = kABytes + kBBytes;
+  constexpr int stage_bytes = kABytes + BN * 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc];
+  __shared__ __align__(8) uint64_t sx_full[kScaleSlots], sx_empty[kScaleSlots];
+  __shared__ __align__(8) uint64_t acc_full[NBUF], acc_empty[NBUF];
   __shared__ __align__(8) uint64_t done_bar;
-  __shared__ __align__(16) float sx_sh[kMaxStages][BN];
+  __shared__ __align__(16) float sx_sh[kScaleSlots][BN];
   __shared__ float sw_sh[kMaxGroups];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_err;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = a.stages;
-  const int tile = blockIdx.x / fa.nchunk, n0 = (blockIdx.x % fa.nchunk) * BN;
-  const int m0 = tile * kBM;
   const int nk = fa.groups;
-  // tiles start their reduction at different groups, so the rows streamed at
-  // any moment are spread over column offsets (DRAM channels)
-  const int rot = tile % nk;
+  const int items = fa.items;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1 + kPromWarps);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&sx_full[s], 1);
+      mbar_init(&sx_empty[s], kPromWarps);
     }
     for (int p = 0; p < NBUF; ++p) {
       mbar_init(&acc_full[p], 1);
@@ -256,40 +348,55 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
 
-  float acc[CW];
+  // item -> 128-row tile, first batch row.  The batch chunks of a tile are
+  // neighbours, so its weights are read from HBM once.  Tiles start their
+  // reduction at different groups, so the rows streamed at any moment are
+  // spread over column offsets (DRAM channels).
+  auto tile_of = [&](int item) { return item / fa.nchunk; };
+  auto group_of = [&](int tile, int kb) { return (kb + tile) % nk; };
+
   if (warp == kPromWarps) {
     if (lane == 0) {
       // TMA producer: the first stages' weights before the wait on the
       // kernel that quantises the hidden states
+      int it = 0;  // groups requested so far
+      bool ok = true;
       const int pre = min(S, nk);
-      auto load_x = [&](int kb) {
-        const int s = kb % S, g = (kb + rot) % nk;
-        tma_load_2d(smem + (size_t)s * stage_bytes + kABytes, &map_x, g * 128, n0, &full_bar[s]);
-        bulk_load(sx_sh[s], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &full_bar[s]);
-      };
-      for (int kb = 0; kb < pre; ++kb) {
-        mbar_expect_tx(&full_bar[kb], (uint32_t)(stage_bytes + BN * 4));
-        tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, ((kb + rot) % nk) * 128, m0,
-                    &full_bar[kb]);
+      {
+        const int tile = tile_of(blockIdx.x);
+        for (int kb = 0; kb < pre; ++kb) {
+          mbar_expect_tx(&full_bar[kb], (uint32_t)stage_bytes);
+          tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, group_of(tile, kb) * 128, tile * kBM,
+                      &full_bar[kb]);
+        }
       }
       griddep_wait();
-      for (int kb = 0; kb < pre; ++kb) load_x(kb);
-      int issued = pre;
-      for (int kb = pre; kb < nk; ++kb) {
-        const int s = kb % S;
-        if (!mbar_wait(&empty_bar[s], ((kb / S) - 1) & 1)) {
-          atomicExch(&s_err, 1);
-          break;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int tile = tile_of(item), n0 = (item % fa.nchunk) * BN;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % S, q = it % kScaleSlots, g = group_of(tile, kb);
+          uint8_t* st = smem + (size_t)s * stage_bytes;
+          if (it >= pre) {
+            if (it >= S) ok = mbar_wait(&empty_bar[s], ((it / S) - 1) & 1);
+            if (!ok) break;
+            mbar_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
+            tma_load_2d(st, &map_w, g * 128, tile * kBM, &full_bar[s]);
+          }
+          tma_load_2d(st + kABytes, &map_x, g * 128, n0, &full_bar[s]);
+          if (it >= kScaleSlots) ok = mbar_wait(&sx_empty[q], ((it / kScaleSlots) - 1) & 1);
+          if (!ok) {
+            ++it;
+            break;
+          }
+          mbar_expect_tx(&sx_full[q], BN * 4);
+          bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &sx_full[q]);
         }
-        mbar_expect_tx(&full_bar[s], (uint32_t)(stage_bytes + BN * 4));
-        tma_load_2d(smem + (size_t)s * stage_bytes, &map_w, ((kb + rot) % nk) * 128, m0,
-                    &full_bar[s]);
-        load_x(kb);
-        issued = kb + 1;
       }
+      if (!ok) atomicExch(&s_err, 1);
       // drain: every issued copy has landed before this CTA may exit
-      for (int kb = (issued > S ? issued - S : 0); kb < issued; ++kb)
-        mbar_wait(&full_bar[kb % S], (kb / S) & 1);
+      for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
+      for (int k = max(0, it - kScaleSlots); k < it; ++k)
+        mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
     }
   } else if (warp == kPromWarps + 1) {
     if (lane == 0) {
@@ -297,63 +404,118 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       // (bits 4-5 = 1), e4m3 A and B (7-9 and 10-12 = 0), both K-major,
       // N >> 3 at bit 17, M >> 4 at bit 24.
       const uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-      for (int kb = 0; kb < nk; ++kb) {
-        const int s = kb % S, p = kb % NBUF;
-        if ((kb >= NBUF && !mbar_wait(&acc_empty[p], ((kb / NBUF) - 1) & 1)) ||
-            !mbar_wait(&full_bar[s], (kb / S) & 1)) {
-          atomicExch(&s_err, 1);
-          break;
-        }
-        fence_after_sync();
-        const uint32_t sa = smem_u32(smem + (size_t)s * stage_bytes);
-        const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + kABytes);
+      int it = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x)
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % S, p = it % NBUF;
+          ok = (it < NBUF || mbar_wait(&acc_empty[p], ((it / NBUF) - 1) & 1)) &&
+               mbar_wait(&full_bar[s], (it / S) & 1);
+          if (!ok) break;
+          fence_after_sync();
+          const uint32_t sa = smem_u32(smem + (size_t)s * stage_bytes);
+          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + kABytes);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
-          mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-        mma_commit(&empty_bar[s]);
-        mma_commit(&acc_full[p]);
-      }
+          for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
+            mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc,
+                     kk > 0 ? 1u : 0u);
+          mma_commit(&empty_bar[s]);
+          mma_commit(&acc_full[p]);
+        }
+      if (!ok) atomicExch(&s_err, 1);
       mma_commit(&done_bar);
     }
   } else {
     griddep_wait();
-    for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
-    asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
-#pragma unroll
-    for (int i = 0; i < CW; ++i) acc[i] = 0.f;
     const int quad = warp & 3, col0 = (warp >> 2) * CW;
+    // this thread's first row of the tile (TMEM lane) and first column; it
+    // has the rows row0 + 8 i and the columns col0 + 8 k + cpair + {0, 1}
+    const int row0 = quad * 32 + (lane >> 2), cpair = 2 * (lane & 3);
+    // one block of columns transposed, for the partials
+    float* zt = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes);
+    int it = 0;
     bool ok = true;
-    for (int kb = 0; kb < nk && ok; ++kb) {
-      const int s = kb % S, p = kb % NBUF;
-      ok = mbar_wait(&full_bar[s], (kb / S) & 1) && mbar_wait(&acc_full[p], (kb / NBUF) & 1);
-      ok = __all_sync(0xffffffffu, ok) != 0;
-      if (!ok) break;
-      fence_after_sync();
-      const float sw = sw_sh[(kb + rot) % nk];
-      const float4* sx4 = reinterpret_cast<const float4*>(sx_sh[s] + col0);
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      const int tile = tile_of(item), n0 = (item % fa.nchunk) * BN, m0 = tile * kBM;
+      // the last item's weights' scales have been read by all
+      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
+      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      f32x2 acc[CW / 8][4];  // [column block][row]
 #pragma unroll
-      for (int c0 = 0; c0 < CW; c0 += CH) {
-        float v[CH];
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0 + c0);
-        if constexpr (CH == 32) {
-          tmem_ld32(taddr, v);
-        } else {
-          tmem_ld16(taddr, v);
-        }
+      for (int k = 0; k < CW / 8; ++k)
 #pragma unroll
-        for (int e = 0; e < CH; e += 4) {
-          const float4 f = sx4[(c0 + e) / 4];
-          acc[c0 + e] = fmaf(v[e], sw * f.x, acc[c0 + e]);
-          acc[c0 + e + 1] = fmaf(v[e + 1], sw * f.y, acc[c0 + e + 1]);
-          acc[c0 + e + 2] = fmaf(v[e + 2], sw * f.z, acc[c0 + e + 2]);
-          acc[c0 + e + 3] = fmaf(v[e + 3], sw * f.w, acc[c0 + e + 3]);
+        for (int i = 0; i < 4; ++i) acc[k][i] = 0;
+      for (int kb = 0; kb < nk && ok; ++kb, ++it) {
+        const int q = it % kScaleSlots, p = it % NBUF;
+        ok = mbar_wait(&sx_full[q], (it / kScaleSlots) & 1) &&
+             mbar_wait(&acc_full[p], (it / NBUF) & 1);
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t swb = __float_as_uint(sw_sh[group_of(tile, kb)]);
+        const f32x2 sw = pack2(swb, swb);
+        const float* sxq = sx_sh[q] + col0 + cpair;
+#pragma unroll
+        for (int k0 = 0; k0 < CW / 8; k0 += NB) {
+          f32x2 v[NB][4];
+          tmem_ld_spread<NB>(
+              tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0 + 8 * k0), v);
+          if (k0 + NB == CW / 8) {  // all of this warp's columns are in registers
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[p]);
+          }
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const f32x2 f =
+                mul2(*reinterpret_cast<const f32x2*>(sxq + 8 * (k0 + k)), sw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fma2(acc[k0 + k][i], v[k][i], f);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sx_empty[q]);
       }
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&acc_empty[p]);
-        mbar_arrive(&empty_bar[s]);
+      // a warp that gave up stores nothing more, but misses no barrier
+      if (a.part == nullptr) {
+        if (ok) {
+#pragma unroll
+          for (int k = 0; k < CW / 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 z = unpack2(acc[k][i]);
+              const int b = n0 + col0 + 8 * k + cpair, j = m0 + row0 + 8 * i;
+              if (j < a.K) {
+                if (b < a.B) a.out[(int64_t)b * a.ldo + j] = z.x * a.out_scale;
+                if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + j] = z.y * a.out_scale;
+              }
+            }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < BN; c += PC) {
+          if (c / CW == warp >> 2) {
+#pragma unroll
+            for (int k = 0; k < PC / 8; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 z = unpack2(acc[(c % CW) / 8 + k][i]);
+                z.x *= a.out_scale;
+                z.y *= a.out_scale;
+                const int col = 8 * k + cpair, b = n0 + c + col, r = row0 + 8 * i;
+                if (ok && m0 + r < a.K) {
+                  if (b < a.B) a.out[(int64_t)b * a.ldo + m0 + r] = z.x;
+                  if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + m0 + r] = z.y;
+                }
+                zt[col * zt_pitch<PC, NP>() + r] = z.x;
+                zt[(col + 1) * zt_pitch<PC, NP>() + r] = z.y;
+              }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+          tile_partials<PC, NP>(zt, a, min(kBM, a.K - m0), m0, tile, tid, n0 + c);
+          asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+        }
       }
     }
     if (!ok && lane == 0) atomicExch(&s_err, 1);
@@ -363,29 +525,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   const bool all_ok = __syncthreads_and(mbar_wait(&done_bar, 0) && s_err == 0 ? 1 : 0) != 0;
   griddep_launch_dependents();
   fence_after_sync();
-  if (all_ok && warp < kPromWarps) {
-    const int quad = warp & 3, col0 = (warp >> 2) * CW;
-    const int row = quad * 32 + lane, j = m0 + row;
-    // the ring is idle: it holds the tile transposed for the partials
-    float* zt = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int i = 0; i < CW; ++i) {
-      const int b = col0 + i;
-      const float z = acc[i] * a.out_scale;
-      if (n0 + b < a.B && j < a.K) a.out[(int64_t)(n0 + b) * a.ldo + j] = z;
-      if (a.part != nullptr) zt[b * zt_pitch<BN, NP>() + row] = z;
-    }
-    if (a.part != nullptr) {
-      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
-      tile_partials<BN, NP>(zt, a, min(kBM, a.K - m0), m0, tile, tid, n0);
-    }
-  }
-  __syncthreads();
   if (tid == 0 && !all_ok) atomicOr(a.status, VT_DEV_TIMEOUT);
-  if (warp == kPromWarps + 1) {
-    fence_after_sync();
-    tmem_dealloc(tmem, kCols);
-  }
+  if (warp == kPromWarps + 1) tmem_dealloc(tmem, kCols);
 }
 
 struct Fp8Ws {
@@ -439,15 +580,17 @@ template <int BN>
 int launch_fp8_bn(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa,
                   int tiles) {
   constexpr int stage = umma::kABytes + BN * 128;
-  // narrow batches: two CTAs per SM
-  const int budget = (BN <= 64) ? 96 * 1024 : 200 * 1024;
-  fa.h.stages = std::max(2, std::min(umma::kMaxStages, budget / stage));
-  constexpr size_t kZt = (size_t)BN * umma::zt_pitch<BN, kPromNT<BN>>() * sizeof(float);
-  const size_t smem = std::max((size_t)fa.h.stages * stage, kZt) + 1024;
+  constexpr int budget = BN <= 64 ? 96 * 1024 : 200 * 1024;
+  constexpr size_t kZt =
+      (size_t)kPartCols<BN> * umma::zt_pitch<kPartCols<BN>, kPromNT<BN>>() * sizeof(float);
+  const size_t zt = fa.h.part != nullptr ? kZt : 0;
+  fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((budget - zt) / stage)));
+  const size_t smem = (size_t)fa.h.stages * stage + zt + 1024;
+  fa.items = tiles * fa.nchunk;
   auto k = head_fp8_kernel<BN>;
   VT_RETURN_IF_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * fa.nchunk));
+  cfg.gridDim = dim3((unsigned)std::min(fa.items, 152 * kHeadPerSm<BN>));
   cfg.blockDim = dim3(kPromNT<BN> + 64);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
