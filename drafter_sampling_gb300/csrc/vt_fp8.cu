@@ -185,6 +185,13 @@ constexpr int kPromNT = 128 * (BN / kPromCols<BN>);
 // resident CTAs per SM
 template <int BN>
 constexpr int kHeadPerSm = BN <= 64 ? 2 : 1;
+// All threads: a warp for the loads and one for the MMAs follow the promoting
+// ones.  At BN = 256 a promoting thread sums 128 values and has another 64 in
+// flight, more registers than an even split over the block gives; there the
+// two warps are part of a third warpgroup (two of its warps idle), which gives
+// most of its registers to the promoting ones: 3 x 168 = 2 x 232 + 40 a thread.
+template <int BN>
+constexpr int kHeadNT = kPromNT<BN> + (BN == 256 ? 128 : 64);
 // columns whose partials are reduced at once
 template <int BN>
 constexpr int kPartCols = BN < 32 ? BN : 32;
@@ -223,11 +230,11 @@ __device__ __forceinline__ void fma2(f32x2& acc, f32x2 a, f32x2 b) {
 // 8 NB consecutive columns of this warp's 32 TMEM lanes, spread over the warp
 // so that a thread has few columns and several rows (so few scales): thread t
 // gets of column block k the columns 8 k + 2 (t % 4) + {0, 1} of the rows
-// t / 4 + 8 i, in v[k][i].
+// t / 4 + 8 i: pairs r[i / 2][4 k + 2 (i % 2)], + 1.  The registers hold them
+// after tmem_ld_wait.
 template <int NB>
-__device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, f32x2 (&v)[NB][4]) {
+__device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, uint32_t (&r)[2][NB * 4]) {
   static_assert(NB == 2 || NB == 4, "16 or 32 columns");
-  uint32_t r[2][NB * 4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // lanes 0-15 and 16-31
     const uint32_t at = taddr + ((uint32_t)(16 * h) << 16);
@@ -250,32 +257,27 @@ __device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, f32x2 (&v)[NB][4]
           : "memory");
     }
   }
-  // the wait names the registers, so that no use of them can precede it
-  if constexpr (NB == 4) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
-                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]),
-                   "+r"(r[0][10]), "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]),
-                   "+r"(r[0][14]), "+r"(r[0][15])::"memory");
-    asm volatile(""
-                 : "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]),
-                   "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]), "+r"(r[1][9]),
-                   "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]), "+r"(r[1][13]),
-                   "+r"(r[1][14]), "+r"(r[1][15])::"memory");
-  } else {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
-                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[1][0]), "+r"(r[1][1]),
-                   "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]),
-                   "+r"(r[1][7])::"memory");
-  }
+}
+// Waits for this thread's TMEM loads; it names the registers of one, so that
+// no use of them can precede it.
+template <int NB>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[2][NB * 4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int k = 0; k < NB; ++k)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v[k][2 * h] = pack2(r[h][4 * k], r[h][4 * k + 1]);
-      v[k][2 * h + 1] = pack2(r[h][4 * k + 2], r[h][4 * k + 3]);
-    }
+    for (int e = 0; e < NB * 4; ++e) asm volatile("" : "+r"(r[h][e])::"memory");
+}
+
+// Moves registers between the warpgroups of a block: the sum over the
+// warpgroups stays what the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Blocks of 128 rows of W8 x BN rows of the batch, taken by a persistent CTA
@@ -290,7 +292,7 @@ __device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, f32x2 (&v)[NB][4]
 // as soon as its MMAs are done) and one the MMAs; both run ahead into the next
 // block while the promoting warps store the last one.
 template <int BN>
-__global__ void __launch_bounds__(kPromNT<BN> + 64, kHeadPerSm<BN>)
+__global__ void __launch_bounds__(kHeadNT<BN>, kHeadPerSm<BN>)
 head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 Fp8Args fa) {
   using namespace umma;
@@ -355,8 +357,9 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   auto tile_of = [&](int item) { return item / fa.nchunk; };
   auto group_of = [&](int tile, int kb) { return (kb + tile) % nk; };
 
-  if (warp == kPromWarps) {
-    if (lane == 0) {
+  if (warp >= kPromWarps) {
+    if constexpr (BN == 256) regs_give<40>();
+    if (warp == kPromWarps && lane == 0) {
       // TMA producer: the first stages' weights before the wait on the
       // kernel that quantises the hidden states
       int it = 0;  // groups requested so far
@@ -397,9 +400,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
       for (int k = max(0, it - kScaleSlots); k < it; ++k)
         mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
-    }
-  } else if (warp == kPromWarps + 1) {
-    if (lane == 0) {
+    } else if (warp == kPromWarps + 1 && lane == 0) {
       // MMA issuer.  Instruction descriptor of kind::f8f6f4: fp32 accumulator
       // (bits 4-5 = 1), e4m3 A and B (7-9 and 10-12 = 0), both K-major,
       // N >> 3 at bit 17, M >> 4 at bit 24.
@@ -426,6 +427,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       mma_commit(&done_bar);
     }
   } else {
+    if constexpr (BN == 256) regs_take<232>();
     griddep_wait();
     const int quad = warp & 3, col0 = (warp >> 2) * CW;
     // this thread's first row of the tile (TMEM lane) and first column; it
@@ -456,12 +458,17 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         const uint32_t swb = __float_as_uint(sw_sh[group_of(tile, kb)]);
         const f32x2 sw = pack2(swb, swb);
         const float* sxq = sx_sh[q] + col0 + cpair;
+        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0);
+        uint32_t raw[2][2][NB * 4];
+        tmem_ld_spread<NB>(taddr, raw[0]);
 #pragma unroll
         for (int k0 = 0; k0 < CW / 8; k0 += NB) {
-          f32x2 v[NB][4];
-          tmem_ld_spread<NB>(
-              tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0 + 8 * k0), v);
-          if (k0 + NB == CW / 8) {  // all of this warp's columns are in registers
+          // the next block's load overlaps this one's arithmetic
+          uint32_t (&v)[2][NB * 4] = raw[(k0 / NB) & 1];
+          tmem_ld_wait<NB>(v);
+          if (k0 + NB < CW / 8) {
+            tmem_ld_spread<NB>(taddr + 8 * (k0 + NB), raw[(k0 / NB + 1) & 1]);
+          } else {  // all of this warp's columns are in registers
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[p]);
@@ -471,7 +478,10 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             const f32x2 f =
                 mul2(*reinterpret_cast<const f32x2*>(sxq + 8 * (k0 + k)), sw);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fma2(acc[k0 + k][i], v[k][i], f);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* e = &v[i / 2][4 * k + 2 * (i % 2)];
+              fma2(acc[k0 + k][i], pack2(e[0], e[1]), f);
+            }
           }
         }
         __syncwarp();
@@ -591,7 +601,7 @@ int launch_fp8_bn(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, 
   VT_RETURN_IF_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(fa.items, 152 * kHeadPerSm<BN>));
-  cfg.blockDim = dim3(kPromNT<BN> + 64);
+  cfg.blockDim = dim3(kHeadNT<BN>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
