@@ -206,6 +206,15 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
+// one thread of a converged warp, the same at every call
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // two fp32 values in one 64-bit register
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(uint32_t a, uint32_t b) {
@@ -350,49 +359,66 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
 
-  // item -> 128-row tile, first batch row.  The batch chunks of a tile are
-  // neighbours, so its weights are read from HBM once.  Tiles start their
-  // reduction at different groups, so the rows streamed at any moment are
-  // spread over column offsets (DRAM channels).
-  auto tile_of = [&](int item) { return item / fa.nchunk; };
-  auto group_of = [&](int tile, int kb) { return (kb + tile) % nk; };
-
+  // item -> 128-row tile, batch chunk.  The chunks of a tile are neighbours,
+  // so its weights are read from HBM once.  Tiles start their reduction at
+  // different groups, so the rows streamed at any moment are spread over
+  // column offsets (DRAM channels).  The loops below count stages, slots and
+  // groups up by hand: a division by a runtime value in each would be most of
+  // the time between two groups.
   if (warp >= kPromWarps) {
     if constexpr (BN == 256) regs_give<40>();
-    if (warp == kPromWarps && lane == 0) {
+    const bool leader = elect_one();  // one thread issues; the warp stays together
+    if (warp == kPromWarps) {
       // TMA producer: the first stages' weights before the wait on the
       // kernel that quantises the hidden states
-      int it = 0;  // groups requested so far
-      bool ok = true;
       const int pre = min(S, nk);
-      {
-        const int tile = tile_of(blockIdx.x);
+      if (leader) {
+        const int tile = blockIdx.x / fa.nchunk;
+        int g = tile % nk;
         for (int kb = 0; kb < pre; ++kb) {
           mbar_expect_tx(&full_bar[kb], (uint32_t)stage_bytes);
-          tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, group_of(tile, kb) * 128, tile * kBM,
-                      &full_bar[kb]);
+          tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, g * 128, tile * kBM, &full_bar[kb]);
+          g = g + 1 == nk ? 0 : g + 1;
         }
       }
       griddep_wait();
+      int it = 0;                     // groups requested so far
+      int s = 0, q = 0;               // stage and scale slot of the next one
+      uint32_t sphase = 1, qphase = 1;  // parity that says they are free
+      bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int tile = tile_of(item), n0 = (item % fa.nchunk) * BN;
+        const int tile = item / fa.nchunk, n0 = (item - tile * fa.nchunk) * BN;
+        int g = tile % nk;
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % S, q = it % kScaleSlots, g = group_of(tile, kb);
           uint8_t* st = smem + (size_t)s * stage_bytes;
           if (it >= pre) {
-            if (it >= S) ok = mbar_wait(&empty_bar[s], ((it / S) - 1) & 1);
+            // a fresh barrier counts as having completed the phase before
+            ok = mbar_wait(&empty_bar[s], sphase);
             if (!ok) break;
-            mbar_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
-            tma_load_2d(st, &map_w, g * 128, tile * kBM, &full_bar[s]);
+            if (leader) {
+              mbar_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
+              tma_load_2d(st, &map_w, g * 128, tile * kBM, &full_bar[s]);
+            }
           }
-          tma_load_2d(st + kABytes, &map_x, g * 128, n0, &full_bar[s]);
-          if (it >= kScaleSlots) ok = mbar_wait(&sx_empty[q], ((it / kScaleSlots) - 1) & 1);
+          if (leader) tma_load_2d(st + kABytes, &map_x, g * 128, n0, &full_bar[s]);
+          ok = mbar_wait(&sx_empty[q], qphase);
           if (!ok) {
             ++it;
             break;
           }
-          mbar_expect_tx(&sx_full[q], BN * 4);
-          bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &sx_full[q]);
+          if (leader) {
+            mbar_expect_tx(&sx_full[q], BN * 4);
+            bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &sx_full[q]);
+          }
+          if (++s == S) {
+            s = 0;
+            sphase ^= 1;
+          }
+          if (++q == kScaleSlots) {
+            q = 0;
+            qphase ^= 1;
+          }
+          g = g + 1 == nk ? 0 : g + 1;
         }
       }
       if (!ok) atomicExch(&s_err, 1);
@@ -400,31 +426,43 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
       for (int k = max(0, it - kScaleSlots); k < it; ++k)
         mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
-    } else if (warp == kPromWarps + 1 && lane == 0) {
+    } else if (warp == kPromWarps + 1) {
       // MMA issuer.  Instruction descriptor of kind::f8f6f4: fp32 accumulator
       // (bits 4-5 = 1), e4m3 A and B (7-9 and 10-12 = 0), both K-major,
       // N >> 3 at bit 17, M >> 4 at bit 24.
-      const uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-      int it = 0;
+      constexpr uint32_t idesc =
+          (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      int s = 0, p = 0;
+      uint32_t sphase = 0, pphase = 1;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x)
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % S, p = it % NBUF;
-          ok = (it < NBUF || mbar_wait(&acc_empty[p], ((it / NBUF) - 1) & 1)) &&
-               mbar_wait(&full_bar[s], (it / S) & 1);
+        for (int kb = 0; kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&acc_empty[p], pphase) && mbar_wait(&full_bar[s], sphase)) != 0;
           if (!ok) break;
           fence_after_sync();
-          const uint32_t sa = smem_u32(smem + (size_t)s * stage_bytes);
-          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + kABytes);
+          if (leader) {
+            const uint64_t adesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
+            const uint64_t bdesc = adesc + (kABytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
-            mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc,
-                     kk > 0 ? 1u : 0u);
-          mma_commit(&empty_bar[s]);
-          mma_commit(&acc_full[p]);
+            for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
+              mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc,
+                       kk > 0 ? 1u : 0u);
+            mma_commit(&empty_bar[s]);
+            mma_commit(&acc_full[p]);
+          }
+          if (++s == S) {
+            s = 0;
+            sphase ^= 1;
+          }
+          if (++p == NBUF) {
+            p = 0;
+            pphase ^= 1;
+          }
         }
       if (!ok) atomicExch(&s_err, 1);
-      mma_commit(&done_bar);
+      if (leader) mma_commit(&done_bar);
     }
   } else {
     if constexpr (BN == 256) regs_take<232>();
@@ -438,7 +476,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     int it = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      const int tile = tile_of(item), n0 = (item % fa.nchunk) * BN, m0 = tile * kBM;
+      const int tile = item / fa.nchunk, n0 = (item - tile * fa.nchunk) * BN, m0 = tile * kBM;
       // the last item's weights' scales have been read by all
       asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
       for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
@@ -448,6 +486,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = 0; k < CW / 8; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[k][i] = 0;
+      int g = tile % nk;
       for (int kb = 0; kb < nk && ok; ++kb, ++it) {
         const int q = it % kScaleSlots, p = it % NBUF;
         ok = mbar_wait(&sx_full[q], (it / kScaleSlots) & 1) &&
@@ -455,7 +494,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         ok = __all_sync(0xffffffffu, ok) != 0;
         if (!ok) break;
         fence_after_sync();
-        const uint32_t swb = __float_as_uint(sw_sh[group_of(tile, kb)]);
+        const uint32_t swb = __float_as_uint(sw_sh[g]);
+        g = g + 1 == nk ? 0 : g + 1;
         const f32x2 sw = pack2(swb, swb);
         const float* sxq = sx_sh[q] + col0 + cpair;
         const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0);
