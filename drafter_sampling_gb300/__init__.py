@@ -428,54 +428,124 @@ def vt_verify_tree(target_logits, parent, tokens, temperature: float = 0.0, out_
     return out_tokens, out_num_accepted, out_path, dev_status
 
 
-def _fp8_dtypes():
+# Dtype tuples of the arguments below and torch's current-device getter, filled
+# at the first call.  These calls take a few microseconds on the GPU, so what
+# the binding does per tensor is kept to four attribute reads.
+_F32 = _I32 = _FP8 = _U8 = None
+_CUR_DEVICE = None
+_DEVICES = ()
+
+
+def _fast():
+    global _F32, _I32, _FP8, _U8, _CUR_DEVICE, _DEVICES
     torch = _torch()
-    return (torch.float8_e4m3fn, torch.uint8)
+    _DEVICES = tuple(torch.device("cuda", i) for i in range(torch.cuda.device_count()))
+    _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+    _CUR_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _bf16_dtypes()
+    _FP8 = (torch.float8_e4m3fn, torch.uint8)
+    return torch
 
 
-def _on_current(stream, *named):
-    """The raw stream of a call whose tensors must all be on the current
-    device (and `stream`, where given, on the same one)."""
-    torch = _torch()
-    cur = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
-    if stream is not None and stream.device.index != cur:
-        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{cur}")
-    return _stream_ptr(stream)
+def _first(t, name):
+    """The device index of the leading tensor argument, which has to be the
+    current device."""
+    torch = _TORCH if _FP8 is not None else _fast()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    cur = _CUR_DEVICE()
+    if d != cur:
+        raise ValueError(f"{name} is on cuda:{d}, the current device is cuda:{cur}")
+    return d
 
 
-def _made(t, stream):
-    """A tensor allocated by a call that runs on `stream`: its memory is not
-    given to another before that stream has passed this point."""
+def _arg(t, name, dtypes, shape, dev):
+    """A contiguous tensor of the given shape (None: any) on device dev; returns its address."""
+    try:
+        if (t.get_device() == dev and t.dtype in dtypes and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtypes)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor made by a call that runs on `stream`: its memory is not given
+    to another before that stream has passed this point."""
+    t = _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _head_fp8(W8, w_scale, H=None):
-    """(K, H, row stride) of an e4m3 head and its block scales."""
-    torch = _torch()
-    if not isinstance(W8, torch.Tensor):
+def _on(stream, dev):
+    """The raw stream of a call on device dev."""
+    if stream is None:
+        return _RAW_STREAM(dev) if _RAW_STREAM else _stream_ptr(None)
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _head_fp8(W8, w_scale, dev):
+    """(K, H, row stride, addresses) of an e4m3 head and its block scales."""
+    if not isinstance(W8, _TORCH.Tensor):
         raise TypeError("W8 must be a torch.Tensor")
-    if not W8.is_cuda:
-        raise ValueError("W8 must be a CUDA tensor")
-    if W8.dtype not in _fp8_dtypes():
-        raise TypeError(f"W8 has dtype {W8.dtype}, expected one of {_fp8_dtypes()}")
-    if W8.dim() != 2 or W8.shape[0] < 1 or W8.shape[1] < 1:
+    if W8.get_device() != dev:
+        raise ValueError(f"W8 must be a CUDA tensor on cuda:{dev}, it is on {W8.device}")
+    if W8.dtype not in _FP8:
+        raise TypeError(f"W8 has dtype {W8.dtype}, expected one of {_FP8}")
+    if W8.dim() != 2 or 0 in W8.shape:
         raise ValueError("W8 must be [K, H]")
-    K, H8 = W8.shape
-    ldw = W8.stride(0) if K > 1 else (H8 + 15) // 16 * 16
-    if (H8 > 1 and W8.stride(1) != 1) or ldw < H8 or ldw % 16 or W8.data_ptr() % 16:
+    K, H = W8.shape
+    ldw, inner = W8.stride()
+    if K == 1:
+        ldw = (H + 15) // 16 * 16
+    ptr = W8.data_ptr()
+    if (inner != 1 and H > 1) or ldw < H or ldw % 16 or ptr % 16:
         raise ValueError("W8 must have unit inner stride, a row stride that is a multiple of 16 and "
                          "a 16-byte aligned start")
-    if H is not None and H8 != H:
+    return K, H, ldw, ptr, _arg(w_scale, "w_scale", _F32, ((K + 127) // 128, (H + 127) // 128), dev)
+
+
+def _hidden(hidden, H, dev):
+    """(B, address) of hidden states [B, H]."""
+    p = _arg(hidden, "hidden", _BF16, None, dev)
+    if hidden.dim() != 2:
+        raise ValueError("hidden must be [B, H]")
+    if hidden.shape[1] != H:
         raise ValueError("hidden and W8 disagree on H")
-    _dev(w_scale, "w_scale", (torch.float32,), 2)
-    if tuple(w_scale.shape) != ((K + 127) // 128, (H8 + 127) // 128):
-        raise ValueError("w_scale must be [ceil(K/128), ceil(H/128)]")
-    return K, H8, ldw
+    return hidden.shape[0], p
+
+
+def _rows_out(t, name, B, K, dev, wide):
+    """(address, row stride) of an fp32 output of B rows and K columns (or
+    more, where `wide`), unit inner stride, rows apart."""
+    try:
+        b, k = t.shape
+        ld, inner = t.stride()
+        if (t.get_device() == dev and t.dtype in _F32 and b == B and (k == K or (wide and k > K)) and
+                (inner == 1 or K == 1) and (ld >= K or B == 1)):
+            return t.data_ptr(), ld if B > 1 else k
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError(f"{name} must be a float32 tensor on cuda:{dev}, [{B}, {'>= ' if wide else ''}{K}] "
+                     "with unit inner stride")
+
+
+def _scratch(t, nbytes, dev, stream):
+    """(address, bytes) of the workspace given, or of a new one."""
+    if t is None:
+        t = _new(max(int(nbytes), 256), _U8[0], dev, stream)
+    p = _arg(t, "workspace", _U8, None, dev)
+    return p, t.numel(), t
 
 
 def vt_quantize_head(W, W8=None, w_scale=None, dev_status=None, stream=None):
@@ -485,28 +555,24 @@ def vt_quantize_head(W, W8=None, w_scale=None, dev_status=None, stream=None):
     Returns (W8 [K, H] float8_e4m3fn, a view whose row stride is a multiple of
     16, w_scale float32 [ceil(K/128), ceil(H/128)], dev_status).
     """
-    torch = _torch()
-    _dev(W, "W", _bf16_dtypes(), 2)
+    dev = _first(W, "W")
+    wp = _arg(W, "W", _BF16, None, dev)
+    if W.dim() != 2 or 0 in W.shape:
+        raise ValueError("W must be [K, H]")
     K, H = W.shape
-    if K < 1 or H < 1:
-        raise ValueError("W must have rows and columns")
-    dev = W.device
     if W8 is None:
-        W8 = _made(torch.empty((K, (H + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=dev),
-                   stream)[:, :H]
+        W8 = _new((K, (H + 15) // 16 * 16), _FP8[0], dev, stream)[:, :H]
     if w_scale is None:
-        w_scale = _made(torch.empty(((K + 127) // 128, (H + 127) // 128), dtype=torch.float32,
-                                    device=dev), stream)
+        w_scale = _new(((K + 127) // 128, (H + 127) // 128), _F32[0], dev, stream)
     if dev_status is None:
-        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
-    _, _, ldw = _head_fp8(W8, w_scale, H)
-    if W8.shape[0] != K:
+        dev_status = _new(1, _I32[0], dev, stream)
+    K8, H8, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
+    if K8 != K or H8 != H:
         raise ValueError("W8 must be [K, H]")
-    _dev(dev_status, "dev_status", (torch.int32,), 1)
-    s = _on_current(stream, ("W", W), ("W8", W8), ("w_scale", w_scale), ("dev_status", dev_status))
-    st = lib().vt_quantize_head(W.data_ptr(), K, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
-                                dev_status.data_ptr(), s)
-    _lib.check("vt_quantize_head", st)
+    st = lib().vt_quantize_head(wp, K, H, p8, ldw, sp, _arg(dev_status, "dev_status", _I32, (1,), dev),
+                                _on(stream, dev))
+    if st:
+        _lib.check("vt_quantize_head", st)
     return W8, w_scale, dev_status
 
 
@@ -514,35 +580,20 @@ def vt_draft_logits_fp8(hidden, W8, w_scale, temperature: float = 1.0, logits=No
                         stream=None):
     """vt_draft_logits through an e4m3 head (vt_quantize_head); the hidden
     states are quantised inside the call."""
-    torch = _torch()
-    _dev(hidden, "hidden", _bf16_dtypes(), 2)
-    B, H = hidden.shape
-    K, _, ldw = _head_fp8(W8, w_scale, H)
-    dev = hidden.device
+    dev = _first(hidden, "hidden")
+    K, H, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
+    B, hp = _hidden(hidden, H, dev)
     if logits is None:
-        logits = _made(torch.empty((B, K), dtype=torch.float32, device=dev), stream)
-    _rows_out(logits, "logits", B, K)
+        logits = _new((B, K), _F32[0], dev, stream)
+    zp, ldz = _rows_out(logits, "logits", B, K, dev, True)
     L = lib()
-    if workspace is None:
-        workspace = _made(_ws(L.vt_draft_fp8_workspace_bytes(B, H, K), dev), stream)
-    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
-                    ("logits", logits), ("workspace", workspace))
-    st = L.vt_draft_logits_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(), K,
-                               float(temperature), logits.data_ptr(),
-                               max(logits.stride(0), K), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), s)
-    _lib.check("vt_draft_logits_fp8", st)
+    ws, n, workspace = _scratch(
+        workspace, L.vt_draft_fp8_workspace_bytes(B, H, K) if workspace is None else 0, dev, stream)
+    st = L.vt_draft_logits_fp8(hp, B, H, p8, ldw, sp, K, float(temperature), zp, ldz, ws, n,
+                               _on(stream, dev))
+    if st:
+        _lib.check("vt_draft_logits_fp8", st)
     return logits
-
-
-def _rows_out(t, name, B, K):
-    """An fp32 output of B rows and at least K columns, unit inner stride, rows apart."""
-    torch = _torch()
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or
-            t.dim() != 2 or t.shape[0] != B or t.shape[1] < K or (K > 1 and t.stride(1) != 1) or
-            (B > 1 and t.stride(0) < K)):
-        raise ValueError(f"{name} must be a float32 CUDA tensor [{B}, >= {K}] with unit inner stride")
-    return t
 
 
 def vt_draft_step_fp8(hidden, W8, w_scale, trim_ids, uniforms, temperature: float = 1.0, q=None,
@@ -550,43 +601,32 @@ def vt_draft_step_fp8(hidden, W8, w_scale, trim_ids, uniforms, temperature: floa
     """vt_draft_step through an e4m3 head; returns (q [B, K], tokens int32 [B],
     dev_status).  q and tokens may be strided views as there; temperature == 0
     drafts greedily (uniforms may then be None)."""
-    torch = _torch()
-    greedy = float(temperature) == 0.0
-    _dev(hidden, "hidden", _bf16_dtypes(), 2)
-    B, H = hidden.shape
-    K, _, ldw = _head_fp8(W8, w_scale, H)
-    _dev(trim_ids, "trim_ids", (torch.int32,), 1)
-    if uniforms is not None or not greedy:
-        _dev(uniforms, "uniforms", (torch.float32,), 1)
-    if (uniforms is not None and uniforms.numel() != B) or trim_ids.numel() != K:
-        raise ValueError("uniforms must have B and trim_ids K elements")
-    dev = hidden.device
+    dev = _first(hidden, "hidden")
+    K, H, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
+    B, hp = _hidden(hidden, H, dev)
+    temperature = float(temperature)
+    ip = _arg(trim_ids, "trim_ids", _I32, (K,), dev)
+    up = None
+    if uniforms is not None or temperature != 0.0:
+        up = _arg(uniforms, "uniforms", _F32, (B,), dev)
     if q is None:
-        q = _made(torch.empty((B, K), dtype=torch.float32, device=dev), stream)
-    _rows_out(q, "q", B, K)
-    if q.shape[1] != K:
-        raise ValueError("q must be [B, K]")
+        q = _new((B, K), _F32[0], dev, stream)
+    qp, ldq = _rows_out(q, "q", B, K, dev, False)
     if tokens is None:
-        tokens = _made(torch.empty(B, dtype=torch.int32, device=dev), stream)
-    if (not tokens.is_cuda or tokens.dim() != 1 or tokens.shape[0] != B or
-            tokens.dtype != torch.int32 or (B > 1 and tokens.stride(0) < 1)):
-        raise ValueError("tokens must be an int32 CUDA vector of B entries (any positive stride)")
+        tokens = _new(B, _I32[0], dev, stream)
+    if (tokens.get_device() != dev or tokens.dim() != 1 or tokens.shape[0] != B or
+            tokens.dtype not in _I32 or (B > 1 and tokens.stride(0) < 1)):
+        raise ValueError(f"tokens must be an int32 vector of B entries on cuda:{dev} (any positive stride)")
     if dev_status is None:
-        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
-    _dev(dev_status, "dev_status", (torch.int32,), 1)
+        dev_status = _new(1, _I32[0], dev, stream)
+    dp = _arg(dev_status, "dev_status", _I32, (1,), dev)
     L = lib()
-    if workspace is None:
-        workspace = _made(_ws(L.vt_draft_fp8_workspace_bytes(B, H, K), dev), stream)
-    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
-                    ("trim_ids", trim_ids), ("uniforms", uniforms), ("q", q), ("tokens", tokens),
-                    ("dev_status", dev_status), ("workspace", workspace))
-    st = L.vt_draft_step_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
-                             trim_ids.data_ptr(), K,
-                             uniforms.data_ptr() if uniforms is not None else None,
-                             float(temperature), q.data_ptr(), max(q.stride(0), K),
-                             tokens.data_ptr(), max(tokens.stride(0), 1), dev_status.data_ptr(),
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
-    _lib.check("vt_draft_step_fp8", st)
+    ws, n, workspace = _scratch(
+        workspace, L.vt_draft_fp8_workspace_bytes(B, H, K) if workspace is None else 0, dev, stream)
+    st = L.vt_draft_step_fp8(hp, B, H, p8, ldw, sp, ip, K, up, temperature, qp, ldq, tokens.data_ptr(),
+                             tokens.stride(0) if B > 1 else 1, dp, ws, n, _on(stream, dev))
+    if st:
+        _lib.check("vt_draft_step_fp8", st)
     return q, tokens, dev_status
 
 
@@ -594,39 +634,30 @@ def vt_draft_topk_fp8(hidden, W8, w_scale, trim_ids, k: int, temperature: float 
                       out_logq=None, dev_status=None, workspace=None, stream=None):
     """vt_draft_topk through an e4m3 head.  Returns (out_ids int32 [B, k],
     out_logq [B, k], dev_status [1])."""
-    torch = _torch()
-    _dev(hidden, "hidden", _bf16_dtypes(), 2)
-    B, H = hidden.shape
-    K, _, ldw = _head_fp8(W8, w_scale, H)
-    _dev(trim_ids, "trim_ids", (torch.int32,), 1)
-    if trim_ids.numel() != K:
-        raise ValueError("trim_ids must have K elements")
+    dev = _first(hidden, "hidden")
+    K, H, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
+    B, hp = _hidden(hidden, H, dev)
+    ip = _arg(trim_ids, "trim_ids", _I32, (K,), dev)
     k = int(k)
     if not 1 <= k <= min(32, K):
         raise ValueError("k must be in [1, min(32, K)]")
-    dev = hidden.device
     if out_ids is None:
-        out_ids = _made(torch.empty((B, k), dtype=torch.int32, device=dev), stream)
+        out_ids = _new((B, k), _I32[0], dev, stream)
     if out_logq is None:
-        out_logq = _made(torch.empty((B, k), dtype=torch.float32, device=dev), stream)
+        out_logq = _new((B, k), _F32[0], dev, stream)
     if dev_status is None:
-        dev_status = _made(torch.empty(1, dtype=torch.int32, device=dev), stream)
-    _dev(out_ids, "out_ids", (torch.int32,), 2)
-    _dev(out_logq, "out_logq", (torch.float32,), 2)
-    _dev(dev_status, "dev_status", (torch.int32,), 1)
-    if tuple(out_ids.shape) != (B, k) or tuple(out_logq.shape) != (B, k):
-        raise ValueError("out_ids and out_logq must be [B, k]")
+        dev_status = _new(1, _I32[0], dev, stream)
+    op = _arg(out_ids, "out_ids", _I32, (B, k), dev)
+    lp = _arg(out_logq, "out_logq", _F32, (B, k), dev)
+    dp = _arg(dev_status, "dev_status", _I32, (1,), dev)
     L = lib()
-    if workspace is None:
-        workspace = _made(_ws(L.vt_draft_topk_fp8_workspace_bytes(B, H, K, k), dev), stream)
-    s = _on_current(stream, ("hidden", hidden), ("W8", W8), ("w_scale", w_scale),
-                    ("trim_ids", trim_ids), ("out_ids", out_ids), ("out_logq", out_logq),
-                    ("dev_status", dev_status), ("workspace", workspace))
-    st = L.vt_draft_topk_fp8(hidden.data_ptr(), B, H, W8.data_ptr(), ldw, w_scale.data_ptr(),
-                             trim_ids.data_ptr(), K, k, float(temperature), out_ids.data_ptr(),
-                             out_logq.data_ptr(), dev_status.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), s)
-    _lib.check("vt_draft_topk_fp8", st)
+    ws, n, workspace = _scratch(
+        workspace, L.vt_draft_topk_fp8_workspace_bytes(B, H, K, k) if workspace is None else 0, dev,
+        stream)
+    st = L.vt_draft_topk_fp8(hp, B, H, p8, ldw, sp, ip, K, k, float(temperature), op, lp, dp, ws, n,
+                             _on(stream, dev))
+    if st:
+        _lib.check("vt_draft_topk_fp8", st)
     return out_ids, out_logq, dev_status
 
 
@@ -641,66 +672,58 @@ def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_
     entropy of tokens' shape, top_ids int32 and top_logp [..., k] (None where
     k == 0): the k best ids, ties to the lower, with their log probabilities.
     """
-    torch = _torch()
-    if not isinstance(logits, torch.Tensor):
-        raise TypeError("logits must be a torch.Tensor")
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor")
-    if logits.dtype == torch.float32:
+    dev = _first(logits, "logits")
+    dt = logits.dtype
+    if dt in _F32:
         dt = VT_F32
-    elif logits.dtype in _bf16_dtypes():
+    elif dt in _BF16:
         dt = VT_BF16
     else:
         raise TypeError("logits must be float32 or bf16")
-    shape = tuple(logits.shape[:-1])
-    if logits.dim() not in (2, 3) or 0 in logits.shape:
+    full, st = logits.shape, logits.stride()
+    if len(full) not in (2, 3) or 0 in full:
         raise ValueError("logits must be [R, V] or [B, R, V]")
-    V = logits.shape[-1]
-    R = shape[0] if len(shape) == 1 else shape[0] * shape[1]
-    st = logits.stride()
-    if shape[-1] > 1:
-        ld = st[-2]
-        even = len(shape) == 1 or shape[0] == 1 or st[0] == shape[1] * ld
-    else:
-        ld = st[0] if shape[0] > 1 else V
+    shape, V = full[:-1], full[-1]
+    if len(full) == 2:
+        R = shape[0]
+        ld = st[0] if R > 1 else V
         even = True
-    if (V > 1 and st[-1] != 1) or not even or ld < V:
+    else:
+        B, n = shape
+        R = B * n
+        ld = st[1] if n > 1 else st[0] if B > 1 else V
+        even = B == 1 or n == 1 or st[0] == n * ld
+    if (st[-1] != 1 and V > 1) or not even or ld < V:
         raise ValueError("logits must have unit inner stride and evenly spaced rows")
     k = int(k)
     if not 0 <= k <= min(32, V):
         raise ValueError("k must be in [0, min(32, V)]")
-    _dev(tokens, "tokens", (torch.int32,), len(shape))
-    if tuple(tokens.shape) != shape:
-        raise ValueError("tokens must have the leading shape of logits")
-    dev = logits.device
-    f32, i32 = (torch.float32,), (torch.int32,)
-
-    def out(t, name, want, dtypes):
-        if t is None:
-            return _made(torch.empty(want, dtype=dtypes[0], device=dev), stream)
-        _dev(t, name, dtypes)
-        if tuple(t.shape) != want:
-            raise ValueError(f"{name} must be {list(want)}")
-        return t
-
-    out_logp = out(out_logp, "out_logp", shape, f32)
-    if out_entropy is not None or want_entropy:
-        out_entropy = out(out_entropy, "out_entropy", shape, f32)
+    tp = _arg(tokens, "tokens", _I32, shape, dev)
+    if out_logp is None:
+        out_logp = _new(shape, _F32[0], dev, stream)
+    lp = _arg(out_logp, "out_logp", _F32, shape, dev)
+    ep = ip = pp = None
+    if out_entropy is None and want_entropy:
+        out_entropy = _new(shape, _F32[0], dev, stream)
+    if out_entropy is not None:
+        ep = _arg(out_entropy, "out_entropy", _F32, shape, dev)
     if k:
-        out_top_ids = out(out_top_ids, "out_top_ids", shape + (k,), i32)
-        out_top_logp = out(out_top_logp, "out_top_logp", shape + (k,), f32)
+        top = shape + (k,)
+        if out_top_ids is None:
+            out_top_ids = _new(top, _I32[0], dev, stream)
+        if out_top_logp is None:
+            out_top_logp = _new(top, _F32[0], dev, stream)
+        ip = _arg(out_top_ids, "out_top_ids", _I32, top, dev)
+        pp = _arg(out_top_logp, "out_top_logp", _F32, top, dev)
     else:
         out_top_ids = out_top_logp = None
-    dev_status = out(dev_status, "dev_status", (1,), i32)
-    s = _on_current(stream, ("logits", logits), ("tokens", tokens), ("out_logp", out_logp),
-                    ("out_entropy", out_entropy), ("out_top_ids", out_top_ids),
-                    ("out_top_logp", out_top_logp), ("dev_status", dev_status))
-    rc = lib().vt_token_logprobs(logits.data_ptr(), dt, R, V, ld, tokens.data_ptr(), k,
-                                 float(temperature), out_logp.data_ptr(),
-                                 out_entropy.data_ptr() if out_entropy is not None else None,
-                                 out_top_ids.data_ptr() if k else None,
-                                 out_top_logp.data_ptr() if k else None, dev_status.data_ptr(), s)
-    _lib.check("vt_token_logprobs", rc)
+    if dev_status is None:
+        dev_status = _new(1, _I32[0], dev, stream)
+    dp = _arg(dev_status, "dev_status", _I32, (1,), dev)
+    rc = lib().vt_token_logprobs(logits.data_ptr(), dt, R, V, ld, tp, k, float(temperature), lp, ep, ip,
+                                 pp, dp, _on(stream, dev))
+    if rc:
+        _lib.check("vt_token_logprobs", rc)
     return out_logp, out_entropy, out_top_ids, out_top_logp, dev_status
 
 

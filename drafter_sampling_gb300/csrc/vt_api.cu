@@ -1,6 +1,7 @@
 // Library-wide entry points of libvt: status text, ABI version and the
 // self-test of the bounded waits.
 #include "vt_common.cuh"
+#include "vt_internal.h"
 #include "vt_umma.cuh"
 
 extern "C" const char* vt_status_string(int status) {
@@ -41,7 +42,19 @@ __global__ void selftest_wait_kernel(int which, uint32_t limit, const unsigned* 
   if (!done) atomicOr(dev_status, VT_DEV_TIMEOUT);
 }
 
+__global__ void clear_status_kernel(int* dev_status) {
+  griddep_launch_dependents();
+  *dev_status = 0;
+}
+
 }  // namespace
+
+int clear_status(cudaStream_t s, int32_t* dev_status) {
+  clear_status_kernel<<<1, 1, 0, s>>>(dev_status);
+  VT_RETURN_IF_LAUNCH_FAILED();
+  return VT_OK;
+}
+
 }  // namespace vt
 
 extern "C" int vt_selftest_wait(int32_t which, uint32_t limit, const uint32_t* flag,

@@ -99,6 +99,7 @@ quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __re
   const int e = scale_exponent(m);
   const float inv = exact_pow2(-e);
   if (tid == 0) {
+    griddep_wait();  // the status word is clear
     w_scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = exact_pow2(e);
     if (m >= 0x7f80u) atomicOr(dev_status, VT_DEV_NONFINITE);
   }
@@ -729,11 +730,20 @@ extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t
   const int rows = (K + kQB - 1) / kQB;
   if (rows > 65535) return VT_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  VT_RETURN_IF_CUDA(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s));
+  const int st = clear_status(s, dev_status);
+  if (st != VT_OK) return st;
   const int vec_ok = H % 8 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
-  quantize_head_kernel<<<dim3((unsigned)((H + kQB - 1) / kQB), (unsigned)rows), kQuantNT, 0, s>>>(
-      W, K, H, W8, ldw, w_scale, dev_status, vec_ok);
-  VT_RETURN_IF_LAUNCH_FAILED();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((H + kQB - 1) / kQB), (unsigned)rows);
+  cfg.blockDim = dim3(kQuantNT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, quantize_head_kernel, W, K, H, W8, ldw, w_scale,
+                                       dev_status, vec_ok));
   return VT_OK;
 }
 

@@ -12,6 +12,15 @@ namespace vt {
 // cuTensorMapEncodeTiled of the loaded driver, or nullptr
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Clears the status word of a call whose one kernel would otherwise need a
+// memset before it (which costs the call 2.5 us more).  The kernel behind it
+// is launched with programmatic stream serialization, so the two launches
+// overlap; it has to wait (griddepcontrol.wait) in the threads that raise
+// flags, and needs to for nothing else: the clearing kernel is launched
+// without that attribute, so everything before the call has completed when
+// either starts.
+int clear_status(cudaStream_t s, int32_t* dev_status);
+
 constexpr int kDraftTopkMax = 32;  // largest k of the drafter's top-k
 
 // The second half of a drafting step, after a projection that left z (scaled

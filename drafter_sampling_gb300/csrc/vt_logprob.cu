@@ -31,6 +31,7 @@
 
 #include <cooperative_groups.h>
 
+#include "vt_internal.h"
 #include "vt_umma.cuh"
 #include "vt_verify_common.cuh"
 
@@ -388,14 +389,6 @@ __device__ __forceinline__ void lists_join(LpShared& sh, int n, lp_key bound, in
   }
 }
 
-// Clears the status word of a call over several rows.  The rows' kernel, whose
-// launch overlaps this one, needs nothing else of it: the threads that raise
-// flags wait for it.
-__global__ void zero_status_kernel(int* dev_status) {
-  griddep_launch_dependents();
-  *dev_status = 0;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(LpArgs a) {
   constexpr int VE = Elem<T>::kVec;           // ids per 16-byte vector
@@ -743,10 +736,8 @@ extern "C" int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64
   LpArgs a;
   a.own_status = R == 1;
   if (R > 1) {
-    // launched as an ordinary kernel: it, and so the kernel behind it, starts
-    // once everything before the call has completed
-    zero_status_kernel<<<1, 1, 0, s>>>(dev_status);
-    VT_RETURN_IF_LAUNCH_FAILED();
+    const int st = clear_status(s, dev_status);
+    if (st != VT_OK) return st;
   }
   a.logits = logits;
   a.R = R;
