@@ -168,43 +168,93 @@ struct Fp8Args {
   const float* sw;      // [K / 128][groups]
   const float* sx;      // [groups][Bp]
   int Bp, groups, nchunk;
-  int items;            // 128-row tiles times batch chunks
+  int items;            // blocks of W8 rows times batch chunks
 };
 
 constexpr int kMaxGroups = 512;   // H <= 65536
 constexpr int kScaleSlots = 8;    // groups whose sx are in shared memory at once
 
-// accumulator buffers in tensor memory
-template <int BN>
-constexpr int kAccBufs = BN <= 128 ? 4 : 2;
-// columns (batch rows) of one promoting warp, which has 32 of the tile's rows,
-// and the promoting threads
-template <int BN>
-constexpr int kPromCols = BN < 64 ? BN : BN == 256 ? 128 : 64;
-template <int BN>
-constexpr int kPromNT = 128 * (BN / kPromCols<BN>);
-// resident CTAs per SM
-template <int BN>
-constexpr int kHeadPerSm = BN <= 64 ? 2 : 1;
-// All threads: a warp for the loads and one for the MMAs follow the promoting
-// ones.  At BN = 256 a promoting thread sums 128 values and has another 64 in
-// flight, more registers than an even split over the block gives; there the
-// two warps are part of a third warpgroup (two of its warps idle), which gives
-// most of its registers to the promoting ones: 3 x 168 = 2 x 232 + 40 a thread.
-template <int BN>
-constexpr int kHeadNT = kPromNT<BN> + (BN == 256 ? 128 : 64);
-// columns whose partials are reduced at once
-template <int BN>
-constexpr int kPartCols = BN < 32 ? BN : 32;
+// Two kernels, by the batch.  Up to 64 rows (head_fp8_kernel) the batch is the
+// MMA's N operand, 128 rows of W8 its M: the weights are streamed at N = 16,
+// 32 or 64, whichever holds the batch.  Wider batches (batch_fp8_kernel) are
+// the M operand and 256 rows of W8 the N: a promoting thread then has one
+// batch row, so one factor sw * sx a group instead of one per column (the
+// factors' shared-memory reads cost as much as the MMAs otherwise).
 
+// columns (batch rows) and warps that promote a narrow tile
+template <int BN>
+constexpr int kPartCols = BN < 32 ? BN : 32;  // columns whose partials are reduced at once
+constexpr int kNarrowBufs = 4;                // accumulator buffers in tensor memory
+constexpr int kNarrowNP = 128;                // promoting threads
+constexpr int kNarrowNT = kNarrowNP + 64;     // and a warp for the loads, one for the MMAs
+
+template <bool kTwo>
 __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kTwo)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), e4m3
+// A and B (7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Counterparts for a pair of CTAs (a cluster of two) of the single-CTA helpers.
+// Barriers of the pair's first CTA are named by their cluster address.
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(umma::smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int x, int y,
+                                             uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(umma::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+// arrive on `bar` of both CTAs once every MMA issued so far has completed
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(umma::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// No data in memory is handed over with this arrival (the tensor-memory reads
+// before it have completed), so it needs no release at cluster scope, which
+// would cost some 1000 cycles a group.
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   umma::smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
 }
 
 // one thread of a converged warp, the same at every call
@@ -290,8 +340,8 @@ __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Blocks of 128 rows of W8 x BN rows of the batch, taken by a persistent CTA
-// one after another.  Each group of 128 reduction columns is one
+// Narrow batches: tiles of 128 rows of W8, taken by a persistent CTA one after
+// another, with the batch (BN rows) as the N operand.  Each group of 128 reduction columns is one
 // shared-memory stage (W8 128 x 128 bytes, x8 BN x 128 bytes, both K-major
 // with the 128-byte swizzle) and one tcgen05 accumulation of four K = 32 steps
 // into one of the tensor-memory buffers.  The promoting warps read each
@@ -300,20 +350,21 @@ __device__ __forceinline__ void regs_take() {
 // the long sum is held in 32 bits by the CUDA cores.  One warp issues the TMA
 // loads (and the copies of sx, in a ring of its own, so that a stage is free
 // as soon as its MMAs are done) and one the MMAs; both run ahead into the next
-// block while the promoting warps store the last one.
+// tile while the promoting warps store the last one.
 template <int BN>
-__global__ void __launch_bounds__(kHeadNT<BN>, kHeadPerSm<BN>)
+__global__ void __launch_bounds__(kNarrowNT, 2)
 head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 Fp8Args fa) {
   using namespace umma;
   const HeadArgs& a = fa.h;
-  constexpr int NP = kPromNT<BN>;
+  static_assert(BN <= 64, "wider batches have their own kernel");
+  constexpr int NP = kNarrowNP;
   constexpr int kPromWarps = NP / 32;
-  constexpr int NBUF = kAccBufs<BN>;
-  constexpr int CW = kPromCols<BN>;
+  constexpr int NBUF = kNarrowBufs;
+  constexpr int CW = BN;                // columns of a promoting warp, which has 32 of the rows
   constexpr int NB = CW >= 32 ? 4 : 2;  // 8-column blocks read at once
   constexpr int PC = kPartCols<BN>;
-  constexpr uint32_t kCols = (uint32_t)(NBUF * BN);  // 64..512, a power of two
+  constexpr uint32_t kCols = (uint32_t)(NBUF * BN);  // 64..256, a power of two
   constexpr int stage_bytes = kABytes + BN * 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -360,25 +411,22 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
 
-  // item -> 128-row tile, batch chunk.  The chunks of a tile are neighbours,
-  // so its weights are read from HBM once.  Tiles start their reduction at
-  // different groups, so the rows streamed at any moment are spread over
-  // column offsets (DRAM channels).  The loops below count stages, slots and
-  // groups up by hand: a division by a runtime value in each would be most of
-  // the time between two groups.
+  // Tiles start their reduction at different groups, so the rows streamed at
+  // any moment are spread over column offsets (DRAM channels).  The loops below
+  // count stages, slots and groups up by hand: a division by a runtime value in
+  // each would be most of the time between two groups.
   if (warp >= kPromWarps) {
-    if constexpr (BN == 256) regs_give<40>();
     const bool leader = elect_one();  // one thread issues; the warp stays together
     if (warp == kPromWarps) {
       // TMA producer: the first stages' weights before the wait on the
       // kernel that quantises the hidden states
       const int pre = min(S, nk);
       if (leader) {
-        const int tile = blockIdx.x / fa.nchunk;
-        int g = tile % nk;
+        int g = (int)blockIdx.x % nk;
         for (int kb = 0; kb < pre; ++kb) {
           mbar_expect_tx(&full_bar[kb], (uint32_t)stage_bytes);
-          tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, g * 128, tile * kBM, &full_bar[kb]);
+          tma_load_2d(smem + (size_t)kb * stage_bytes, &map_w, g * 128, (int)blockIdx.x * kBM,
+                      &full_bar[kb]);
           g = g + 1 == nk ? 0 : g + 1;
         }
       }
@@ -387,8 +435,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       int s = 0, q = 0;               // stage and scale slot of the next one
       uint32_t sphase = 1, qphase = 1;  // parity that says they are free
       bool ok = true;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int tile = item / fa.nchunk, n0 = (item - tile * fa.nchunk) * BN;
+      for (int tile = blockIdx.x; tile < items && ok; tile += gridDim.x) {
         int g = tile % nk;
         for (int kb = 0; kb < nk; ++kb, ++it) {
           uint8_t* st = smem + (size_t)s * stage_bytes;
@@ -401,7 +448,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
               tma_load_2d(st, &map_w, g * 128, tile * kBM, &full_bar[s]);
             }
           }
-          if (leader) tma_load_2d(st + kABytes, &map_x, g * 128, n0, &full_bar[s]);
+          if (leader) tma_load_2d(st + kABytes, &map_x, g * 128, 0, &full_bar[s]);
           ok = mbar_wait(&sx_empty[q], qphase);
           if (!ok) {
             ++it;
@@ -409,7 +456,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
           }
           if (leader) {
             mbar_expect_tx(&sx_full[q], BN * 4);
-            bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + n0, BN * 4, &sx_full[q]);
+            bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp, BN * 4, &sx_full[q]);
           }
           if (++s == S) {
             s = 0;
@@ -428,16 +475,13 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = max(0, it - kScaleSlots); k < it; ++k)
         mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
     } else if (warp == kPromWarps + 1) {
-      // MMA issuer.  Instruction descriptor of kind::f8f6f4: fp32 accumulator
-      // (bits 4-5 = 1), e4m3 A and B (7-9 and 10-12 = 0), both K-major,
-      // N >> 3 at bit 17, M >> 4 at bit 24.
-      constexpr uint32_t idesc =
-          (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+      // MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
       int s = 0, p = 0;
       uint32_t sphase = 0, pphase = 1;
       bool ok = true;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x)
+      for (int tile = blockIdx.x; tile < items && ok; tile += gridDim.x)
         for (int kb = 0; kb < nk; ++kb) {
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&acc_empty[p], pphase) && mbar_wait(&full_bar[s], sphase)) != 0;
@@ -448,8 +492,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             const uint64_t bdesc = adesc + (kABytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
-              mma_e4m3(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc,
-                       kk > 0 ? 1u : 0u);
+              mma_e4m3<false>(tmem + (uint32_t)(p * BN), adesc + 2 * kk, bdesc + 2 * kk, idesc,
+                              kk > 0 ? 1u : 0u);
             mma_commit(&empty_bar[s]);
             mma_commit(&acc_full[p]);
           }
@@ -466,18 +510,17 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       if (leader) mma_commit(&done_bar);
     }
   } else {
-    if constexpr (BN == 256) regs_take<232>();
     griddep_wait();
-    const int quad = warp & 3, col0 = (warp >> 2) * CW;
+    const int quad = warp;
     // this thread's first row of the tile (TMEM lane) and first column; it
-    // has the rows row0 + 8 i and the columns col0 + 8 k + cpair + {0, 1}
+    // has the rows row0 + 8 i and the columns 8 k + cpair + {0, 1}
     const int row0 = quad * 32 + (lane >> 2), cpair = 2 * (lane & 3);
     // one block of columns transposed, for the partials
     float* zt = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes);
     int it = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      const int tile = item / fa.nchunk, n0 = (item - tile * fa.nchunk) * BN, m0 = tile * kBM;
+    for (int tile = blockIdx.x; tile < items; tile += gridDim.x) {
+      const int m0 = tile * kBM;
       // the last item's weights' scales have been read by all
       asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
       for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
@@ -498,8 +541,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         const uint32_t swb = __float_as_uint(sw_sh[g]);
         g = g + 1 == nk ? 0 : g + 1;
         const f32x2 sw = pack2(swb, swb);
-        const float* sxq = sx_sh[q] + col0 + cpair;
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN + col0);
+        const float* sxq = sx_sh[q] + cpair;
+        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * BN);
         uint32_t raw[2][2][NB * 4];
         tmem_ld_spread<NB>(taddr, raw[0]);
 #pragma unroll
@@ -536,7 +579,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 z = unpack2(acc[k][i]);
-              const int b = n0 + col0 + 8 * k + cpair, j = m0 + row0 + 8 * i;
+              const int b = 8 * k + cpair, j = m0 + row0 + 8 * i;
               if (j < a.K) {
                 if (b < a.B) a.out[(int64_t)b * a.ldo + j] = z.x * a.out_scale;
                 if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + j] = z.y * a.out_scale;
@@ -546,25 +589,23 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       } else {
 #pragma unroll
         for (int c = 0; c < BN; c += PC) {
-          if (c / CW == warp >> 2) {
 #pragma unroll
-            for (int k = 0; k < PC / 8; ++k)
+          for (int k = 0; k < PC / 8; ++k)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 z = unpack2(acc[(c % CW) / 8 + k][i]);
-                z.x *= a.out_scale;
-                z.y *= a.out_scale;
-                const int col = 8 * k + cpair, b = n0 + c + col, r = row0 + 8 * i;
-                if (ok && m0 + r < a.K) {
-                  if (b < a.B) a.out[(int64_t)b * a.ldo + m0 + r] = z.x;
-                  if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + m0 + r] = z.y;
-                }
-                zt[col * zt_pitch<PC, NP>() + r] = z.x;
-                zt[(col + 1) * zt_pitch<PC, NP>() + r] = z.y;
+            for (int i = 0; i < 4; ++i) {
+              float2 z = unpack2(acc[c / 8 + k][i]);
+              z.x *= a.out_scale;
+              z.y *= a.out_scale;
+              const int col = 8 * k + cpair, b = c + col, r = row0 + 8 * i;
+              if (ok && m0 + r < a.K) {
+                if (b < a.B) a.out[(int64_t)b * a.ldo + m0 + r] = z.x;
+                if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + m0 + r] = z.y;
               }
-          }
+              zt[col * zt_pitch<PC, NP>() + r] = z.x;
+              zt[(col + 1) * zt_pitch<PC, NP>() + r] = z.y;
+            }
           asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
-          tile_partials<PC, NP>(zt, a, min(kBM, a.K - m0), m0, tile, tid, n0 + c);
+          tile_partials<PC, NP>(zt, a, min(kBM, a.K - m0), m0, tile, tid, c);
           asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
         }
       }
@@ -578,6 +619,361 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   fence_after_sync();
   if (tid == 0 && !all_ok) atomicOr(a.status, VT_DEV_TIMEOUT);
   if (warp == kPromWarps + 1) tmem_dealloc(tmem, kCols);
+}
+
+// Issues the load of 32 consecutive columns of this thread's TMEM lane; the
+// registers hold them after tmem_ld_done.
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(r[e])::"memory");
+}
+
+// Threads of batch_fp8_kernel: two promoting warpgroups, and a third of which
+// one warp issues the loads and one the MMAs.  A promoting thread sums 128
+// values and has another 64 in flight, more registers than an even split over
+// the block gives, so the third warpgroup gives most of its own to the others:
+// 3 x 168 = 2 x 232 + 40 a thread.
+constexpr int kBatchNP = 256;
+constexpr int kBatchNT = kBatchNP + 128;
+constexpr int kBatchRowsW = 256;   // rows of W8 of an item
+constexpr int kBatchBufs = 2;      // accumulator buffers of 256 columns: all of tensor memory
+constexpr int kOutPitch = 17;      // floats: a warp's 32 x 16 block on its way out
+
+// Wide batches: items of 256 rows of W8 x 128 batch rows, or, as a pair of CTAs
+// (TWO), x 256 batch rows with one MMA of 256 x 256: each CTA of a pair stages
+// its 128 batch rows and half of the weights, half the shared-memory traffic
+// of the same work on one CTA, which is what bounds it there.  The roles are
+// those of head_fp8_kernel; in a pair the first CTA issues the MMAs for both
+// and holds the barriers that they wait on.
+template <bool TWO>
+__global__ void __launch_bounds__(kBatchNT, 1)
+batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                 Fp8Args fa) {
+  using namespace umma;
+  const HeadArgs& a = fa.h;
+  constexpr int NP = kBatchNP;
+  constexpr int kPromWarps = NP / 32;
+  constexpr int NBUF = kBatchBufs;
+  constexpr int NR = kBatchRowsW;
+  constexpr int WR = TWO ? NR / 2 : NR;  // rows of W8 staged by one CTA
+  constexpr int kXBytes = kBM * 128;     // and 128 batch rows
+  constexpr int stage_bytes = kXBytes + WR * 128;
+  constexpr uint32_t kCols = NBUF * NR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t sx_full[kScaleSlots], sx_empty[kScaleSlots];
+  __shared__ __align__(8) uint64_t acc_full[NBUF], acc_empty[NBUF];
+  __shared__ __align__(8) uint64_t done_bar;
+  __shared__ __align__(16) float sx_sh[kScaleSlots][kBM];
+  __shared__ float sw_sh[NR / 128][kMaxGroups];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int s_err;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = a.stages;
+  const int nk = fa.groups;
+  const int items = fa.items;
+  // this CTA's part of a pair; the items of a CTA or pair: first, first + step ...
+  const int part = TWO ? (int)(blockIdx.x & 1) : 0;
+  const int first = TWO ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int step = TWO ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&sx_full[s], 1);
+      mbar_init(&sx_empty[s], kPromWarps);
+    }
+    for (int p = 0; p < NBUF; ++p) {
+      mbar_init(&acc_full[p], 1);
+      mbar_init(&acc_empty[p], kPromWarps * (TWO ? 2 : 1));
+    }
+    mbar_init(&done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_err = 0;
+    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&map_x);
+  }
+  if (warp == kPromWarps + 1) {
+    if constexpr (TWO) {
+      pair_tmem_alloc(&tmem_base_sh, kCols);
+    } else {
+      tmem_alloc(&tmem_base_sh, kCols);
+      tmem_relinquish();
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if constexpr (TWO) cluster_sync_all();  // both CTAs' barriers are ready
+  fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+
+  // item -> block of W8 rows, batch chunk.  The chunks of a block are
+  // neighbours, so its weights are read from HBM once.
+  if (warp >= kPromWarps) {
+    regs_give<40>();
+    const bool leader = elect_one();  // one thread issues; the warp stays together
+    if (warp == kPromWarps) {
+      // TMA producer: the first stages' weights before the wait on the kernel
+      // that quantises the hidden states.  A stage is announced by the (first)
+      // CTA, for both, and loaded by each.
+      auto announce = [&](int s) {
+        if (part == 0) mbar_expect_tx(&full_bar[s], (uint32_t)(stage_bytes * (TWO ? 2 : 1)));
+      };
+      auto load = [&](void* dst, const CUtensorMap* map, int x, int y, int s) {
+        if constexpr (TWO)
+          pair_load_2d(dst, map, x, y, first_cta(&full_bar[s]));
+        else
+          tma_load_2d(dst, map, x, y, &full_bar[s]);
+      };
+      const int pre = min(S, nk);
+      if (leader) {
+        const int blk = first / fa.nchunk;
+        int g = blk % nk;
+        for (int kb = 0; kb < pre; ++kb) {
+          announce(kb);
+          load(smem + (size_t)kb * stage_bytes + kXBytes, &map_w, g * 128, blk * NR + part * WR, kb);
+          g = g + 1 == nk ? 0 : g + 1;
+        }
+      }
+      griddep_wait();
+      int it = 0;                       // groups requested so far
+      int s = 0, q = 0;                 // stage and scale slot of the next one
+      uint32_t sphase = 1, qphase = 1;  // parity that says they are free
+      bool ok = true;
+      for (int item = first; item < items && ok; item += step) {
+        const int blk = item / fa.nchunk;
+        const int b0 = (item - blk * fa.nchunk) * (TWO ? 2 * kBM : kBM) + part * kBM;
+        int g = blk % nk;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          uint8_t* st = smem + (size_t)s * stage_bytes;
+          if (it >= pre) {
+            // a fresh barrier counts as having completed the phase before
+            ok = mbar_wait(&empty_bar[s], sphase);
+            if (!ok) break;
+            if (leader) {
+              announce(s);
+              load(st + kXBytes, &map_w, g * 128, blk * NR + part * WR, s);
+            }
+          }
+          if (leader) load(st, &map_x, g * 128, b0, s);
+          ok = mbar_wait(&sx_empty[q], qphase);
+          if (!ok) {
+            ++it;
+            break;
+          }
+          if (leader) {
+            mbar_expect_tx(&sx_full[q], kBM * 4);
+            bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + b0, kBM * 4, &sx_full[q]);
+          }
+          if (++s == S) {
+            s = 0;
+            sphase ^= 1;
+          }
+          if (++q == kScaleSlots) {
+            q = 0;
+            qphase ^= 1;
+          }
+          g = g + 1 == nk ? 0 : g + 1;
+        }
+      }
+      if (!ok) atomicExch(&s_err, 1);
+      // drain: every issued copy has landed before this CTA may exit (a pair's
+      // second CTA: the first waits for its copies too, and it for the first)
+      if (part == 0)
+        for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
+      for (int k = max(0, it - kScaleSlots); k < it; ++k)
+        mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
+    } else if (warp == kPromWarps + 1 && part == 0) {
+      // MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3(TWO ? 2 * kBM : kBM, NR);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (TWO)
+          pair_commit(bar);
+        else
+          mma_commit(bar);
+      };
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      int s = 0, p = 0;
+      uint32_t sphase = 0, pphase = 1;
+      bool ok = true;
+      for (int item = first; item < items && ok; item += step)
+        for (int kb = 0; kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&acc_empty[p], pphase) && mbar_wait(&full_bar[s], sphase)) != 0;
+          if (!ok) break;
+          fence_after_sync();
+          if (leader) {
+            const uint64_t xdesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
+            const uint64_t wdesc = xdesc + (kXBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
+              mma_e4m3<TWO>(tmem + (uint32_t)(p * NR), xdesc + 2 * kk, wdesc + 2 * kk, idesc,
+                            kk > 0 ? 1u : 0u);
+            commit(&empty_bar[s]);
+            commit(&acc_full[p]);
+          }
+          if (++s == S) {
+            s = 0;
+            sphase ^= 1;
+          }
+          if (++p == NBUF) {
+            p = 0;
+            pphase ^= 1;
+          }
+        }
+      if (!ok) atomicExch(&s_err, 1);
+      if (leader) commit(&done_bar);
+    }
+  } else {
+    regs_take<232>();
+    griddep_wait();
+    // this thread's batch row (TMEM lane) and its half of the W8 rows
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    float* ob = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes) + warp * 32 * kOutPitch;
+    int it = 0;
+    bool ok = true;
+    for (int item = first; item < items; item += step) {
+      const int blk = item / fa.nchunk;
+      const int b0 = (item - blk * fa.nchunk) * (TWO ? 2 * kBM : kBM) + part * kBM;
+      const int tile = blk * (NR / 128) + half, j0 = tile * 128;  // 128-row tile of W8
+      const int nvalid = min(128, a.K - j0);                      // <= 0: past the end
+      // the last item's weights' scales have been read by all
+      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      for (int g = tid & 127; g < nk; g += 128)
+        sw_sh[half][g] = nvalid > 0 ? fa.sw[(int64_t)tile * nk + g] : 0.f;
+      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      f32x2 acc[64];  // sums of this batch row and 128 rows of W8
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      int g = blk % nk;
+      for (int kb = 0; kb < nk && ok; ++kb, ++it) {
+        const int q = it % kScaleSlots, p = it % NBUF;
+        ok = mbar_wait(&sx_full[q], (it / kScaleSlots) & 1) &&
+             mbar_wait(&acc_full[p], (it / NBUF) & 1);
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * NR + half * 128);
+        uint32_t raw[2][32];
+        tmem_ld_issue(taddr, raw[0]);
+        const uint32_t fb = __float_as_uint(sw_sh[half][g] * sx_sh[q][row]);
+        const f32x2 f = pack2(fb, fb);
+        g = g + 1 == nk ? 0 : g + 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // the next 32 columns' load overlaps these ones' arithmetic
+          uint32_t (&v)[32] = raw[c & 1];
+          tmem_ld_done(v);
+          if (c < 3) {
+            tmem_ld_issue(taddr + 32 * (c + 1), raw[(c + 1) & 1]);
+          } else {  // all of this warp's columns are in registers
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (TWO)
+                remote_arrive(first_cta(&acc_empty[p]));
+              else
+                mbar_arrive(&acc_empty[p]);
+              mbar_arrive(&sx_empty[q]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) fma2(acc[16 * c + e], pack2(v[2 * e], v[2 * e + 1]), f);
+        }
+      }
+      // a warp that gave up stores nothing more, but misses no barrier
+      if (!ok || nvalid <= 0) continue;
+      const int b = b0 + row;
+      if (a.part != nullptr && b < a.B) {
+        // this row's partial over the tile's rows, as tile_partials leaves it
+        if (a.greedy) {
+          float v = -INFINITY;
+          int idx = 0x7fffffff;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            const float2 z2 = unpack2(acc[i / 2]);
+            const float z = (i & 1 ? z2.y : z2.x) * a.out_scale;
+            const float w = isfinite(z) ? z : __int_as_float(0x7fc00000);
+            if (i < nvalid && argmax_better(v, idx, w, j0 + i)) {
+              v = w;
+              idx = j0 + i;
+            }
+          }
+          a.part[(int64_t)tile * a.B + b] = make_float2(v, __int_as_float(idx));
+        } else {
+          float m = kNegBig, sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            const float2 z2 = unpack2(acc[i / 2]);
+            if (i < nvalid) m = fmaxf(m, (i & 1 ? z2.y : z2.x) * a.out_scale);
+          }
+#pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            const float2 z2 = unpack2(acc[i / 2]);
+            if (i < nvalid) sum += exp2_approx((i & 1 ? z2.y : z2.x) * a.out_scale - m);
+          }
+          a.part[(int64_t)tile * a.B + b] = make_float2(m, sum);
+        }
+      }
+      // 32 batch rows x 16 columns at a time through shared memory, so that a
+      // row's 16 values leave in one piece
+      float* out = a.out + (int64_t)(b0 + quad * 32 + (lane >> 4)) * a.ldo + j0 + (lane & 15);
+      const int rows = a.B - (b0 + quad * 32 + (lane >> 4));  // of this lane's, in steps of two
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 z2 = unpack2(acc[c / 2 + i]);
+          ob[lane * kOutPitch + 2 * i] = z2.x * a.out_scale;
+          ob[lane * kOutPitch + 2 * i + 1] = z2.y * a.out_scale;
+        }
+        __syncwarp();
+        if (c + (lane & 15) < nvalid) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (2 * r < rows)
+              out[(int64_t)(2 * r) * a.ldo + c] = ob[(2 * r + (lane >> 4)) * kOutPitch + (lane & 15)];
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicExch(&s_err, 1);
+  }
+  __syncwarp();
+  // every role has finished or given up; the MMAs have completed
+  const bool all_ok = __syncthreads_and(mbar_wait(&done_bar, 0) && s_err == 0 ? 1 : 0) != 0;
+  griddep_launch_dependents();
+  fence_after_sync();
+  if (tid == 0 && !all_ok) atomicOr(a.status, VT_DEV_TIMEOUT);
+  if constexpr (TWO) {
+    fence_before_sync();
+    __syncwarp();
+    cluster_sync_all();  // nothing of the pair's is on its way to either CTA
+    fence_after_sync();
+    if (warp == kPromWarps + 1) pair_tmem_dealloc(tmem, kCols);
+  } else {
+    if (warp == kPromWarps + 1) tmem_dealloc(tmem, kCols);
+  }
 }
 
 struct Fp8Ws {
@@ -627,31 +1023,56 @@ bool make_e4m3_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-int launch_fp8_bn(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa,
-                  int tiles) {
-  constexpr int stage = umma::kABytes + BN * 128;
-  constexpr int budget = BN <= 64 ? 96 * 1024 : 200 * 1024;
-  constexpr size_t kZt =
-      (size_t)kPartCols<BN> * umma::zt_pitch<kPartCols<BN>, kPromNT<BN>>() * sizeof(float);
-  const size_t zt = fa.h.part != nullptr ? kZt : 0;
-  fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((budget - zt) / stage)));
-  const size_t smem = (size_t)fa.h.stages * stage + zt + 1024;
-  fa.items = tiles * fa.nchunk;
-  auto k = head_fp8_kernel<BN>;
-  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+// a launch that overlaps the kernel that quantises the hidden states, as a
+// grid of clusters of `cluster` CTAs
+template <typename K>
+int launch_product(cudaStream_t s, K kern, int grid, int threads, size_t smem, int cluster,
+                   const CUtensorMap& mw, const CUtensorMap& mx, const Fp8Args& fa) {
+  VT_RETURN_IF_CUDA(
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(fa.items, 152 * kHeadPerSm<BN>));
-  cfg.blockDim = dim3(kHeadNT<BN>);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, k, mw, mx, fa));
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, mw, mx, fa));
   return VT_OK;
+}
+
+constexpr int kSms = 152;
+
+template <int BN>
+int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
+  constexpr int stage = umma::kABytes + BN * 128;
+  constexpr size_t kZt =
+      (size_t)kPartCols<BN> * umma::zt_pitch<kPartCols<BN>, kNarrowNP>() * sizeof(float);
+  const size_t zt = fa.h.part != nullptr ? kZt : 0;
+  // two CTAs per SM
+  fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((96 * 1024 - zt) / stage)));
+  fa.items = (fa.h.K + umma::kBM - 1) / umma::kBM;
+  return launch_product(s, head_fp8_kernel<BN>, std::min(fa.items, 2 * kSms), kNarrowNT,
+                        (size_t)fa.h.stages * stage + zt + 1024, 1, mw, mx, fa);
+}
+
+template <bool TWO>
+int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
+  constexpr int stage = umma::kBM * 128 + (TWO ? 128 : 256) * 128;
+  constexpr size_t out = (size_t)(kBatchNP / 32) * 32 * kOutPitch * sizeof(float);
+  fa.h.stages = std::min(umma::kMaxStages, 196 * 1024 / stage);
+  fa.nchunk = fa.Bp / (TWO ? 256 : 128);
+  fa.items = (fa.h.K + kBatchRowsW - 1) / kBatchRowsW * fa.nchunk;
+  const int ctas = TWO ? 2 : 1;
+  return launch_product(s, batch_fp8_kernel<TWO>, ctas * std::min(fa.items, kSms / ctas), kBatchNT,
+                        (size_t)fa.h.stages * stage + out + 1024, ctas, mw, mx, fa);
 }
 
 // z = out_scale * hidden @ (scaled W8)^T; part[tile][b] partials of 128-row
@@ -661,10 +1082,12 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
                     int64_t ldo, const Fp8Ws& ws, float2* part, int* status, int status_reset,
                     int greedy) {
   const int groups = (H + kQB - 1) / kQB, Bp = pad_batch(B), ldx = groups * kQB;
-  const int BN = std::min(Bp, 256);
   CUtensorMap mw, mx;
-  if (!make_e4m3_map(&mw, W8, (uint64_t)K, (uint64_t)H, (uint64_t)ldw, umma::kBM)) return VT_ERR_CUDA;
-  if (!make_e4m3_map(&mx, ws.x8, (uint64_t)B, (uint64_t)ldx, (uint64_t)ldx, (uint32_t)BN))
+  // the boxes: the rows that one CTA stages
+  if (!make_e4m3_map(&mw, W8, (uint64_t)K, (uint64_t)H, (uint64_t)ldw, Bp == 128 ? 256 : 128))
+    return VT_ERR_CUDA;
+  if (!make_e4m3_map(&mx, ws.x8, (uint64_t)B, (uint64_t)ldx, (uint64_t)ldx,
+                     (uint32_t)std::min(Bp, 128)))
     return VT_ERR_CUDA;
   {
     cudaLaunchConfig_t cfg = {};
@@ -695,14 +1118,13 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
   fa.sx = ws.sx;
   fa.Bp = Bp;
   fa.groups = groups;
-  fa.nchunk = Bp / BN;
-  const int tiles = (K + umma::kBM - 1) / umma::kBM;
-  switch (BN) {
-    case 16: return launch_fp8_bn<16>(s, mw, mx, fa, tiles);
-    case 32: return launch_fp8_bn<32>(s, mw, mx, fa, tiles);
-    case 64: return launch_fp8_bn<64>(s, mw, mx, fa, tiles);
-    case 128: return launch_fp8_bn<128>(s, mw, mx, fa, tiles);
-    default: return launch_fp8_bn<256>(s, mw, mx, fa, tiles);
+  fa.nchunk = 1;
+  switch (Bp) {
+    case 16: return launch_narrow<16>(s, mw, mx, fa);
+    case 32: return launch_narrow<32>(s, mw, mx, fa);
+    case 64: return launch_narrow<64>(s, mw, mx, fa);
+    case 128: return launch_wide<false>(s, mw, mx, fa);
+    default: return launch_wide<true>(s, mw, mx, fa);
   }
 }
 
