@@ -621,37 +621,43 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   if (warp == kPromWarps + 1) tmem_dealloc(tmem, kCols);
 }
 
-// Issues the load of 32 consecutive columns of this thread's TMEM lane; the
-// registers hold them after tmem_ld_done.
-__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
+// 64 consecutive columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "
+      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, "
+      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // no use of the registers can precede the wait
 #pragma unroll
-  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(r[e])::"memory");
+  for (int e = 0; e < 64; ++e) asm volatile("" : "+r"(r[e])::"memory");
 }
 
 // Threads of batch_fp8_kernel: two promoting warpgroups, and a third of which
 // one warp issues the loads and one the MMAs.  A promoting thread sums 128
-// values and has another 64 in flight, more registers than an even split over
+// values and reads another 64 at a time, more registers than an even split over
 // the block gives, so the third warpgroup gives most of its own to the others:
 // 3 x 168 = 2 x 232 + 40 a thread.
 constexpr int kBatchNP = 256;
 constexpr int kBatchNT = kBatchNP + 128;
 constexpr int kBatchRowsW = 256;   // rows of W8 of an item
 constexpr int kBatchBufs = 2;      // accumulator buffers of 256 columns: all of tensor memory
-constexpr int kOutPitch = 17;      // floats: a warp's 32 x 16 block on its way out
+constexpr int kOutPitch = 33;      // floats: a warp's 32 x 32 block on its way out
 
 // Wide batches: items of 256 rows of W8 x 128 batch rows, or, as a pair of CTAs
 // (TWO), x 256 batch rows with one MMA of 256 x 256: each CTA of a pair stages
@@ -659,7 +665,11 @@ constexpr int kOutPitch = 17;      // floats: a warp's 32 x 16 block on its way 
 // of the same work on one CTA, which is what bounds it there.  The roles are
 // those of head_fp8_kernel; in a pair the first CTA issues the MMAs for both
 // and holds the barriers that they wait on.
-template <bool TWO>
+// MMAs into one accumulator buffer stand still while the other is read, so a
+// promoting thread reads its 128 columns in two bursts of 64 and does nothing
+// else meanwhile (four reads of 32 with the arithmetic between them: 189
+// against 165 us at B = 1000, K = 38016, H = 4096).
+template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                  Fp8Args fa) {
@@ -819,7 +829,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       for (int item = first; item < items && ok; item += step)
         for (int kb = 0; kb < nk; ++kb) {
           ok = __all_sync(0xffffffffu,
-                          mbar_wait(&acc_empty[p], pphase) && mbar_wait(&full_bar[s], sphase)) != 0;
+                          mbar_wait(&full_bar[s], sphase) && mbar_wait(&acc_empty[p], pphase)) != 0;
           if (!ok) break;
           fence_after_sync();
           if (leader) {
@@ -874,19 +884,14 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         if (!ok) break;
         fence_after_sync();
         const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * NR + half * 128);
-        uint32_t raw[2][32];
-        tmem_ld_issue(taddr, raw[0]);
         const uint32_t fb = __float_as_uint(sw_sh[half][g] * sx_sh[q][row]);
         const f32x2 f = pack2(fb, fb);
         g = g + 1 == nk ? 0 : g + 1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // the next 32 columns' load overlaps these ones' arithmetic
-          uint32_t (&v)[32] = raw[c & 1];
-          tmem_ld_done(v);
-          if (c < 3) {
-            tmem_ld_issue(taddr + 32 * (c + 1), raw[(c + 1) & 1]);
-          } else {  // all of this warp's columns are in registers
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[64];
+          tmem_ld64(taddr + 64 * c, v);
+          if (c == 1) {  // all of this warp's columns are in registers
             fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -898,13 +903,13 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             }
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) fma2(acc[16 * c + e], pack2(v[2 * e], v[2 * e + 1]), f);
+          for (int e = 0; e < 32; ++e) fma2(acc[32 * c + e], pack2(v[2 * e], v[2 * e + 1]), f);
         }
       }
       // a warp that gave up stores nothing more, but misses no barrier
       if (!ok || nvalid <= 0) continue;
       const int b = b0 + row;
-      if (a.part != nullptr && b < a.B) {
+      if (PART && b < a.B) {
         // this row's partial over the tile's rows, as tile_partials leaves it
         if (a.greedy) {
           float v = -INFINITY;
@@ -935,25 +940,27 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           a.part[(int64_t)tile * a.B + b] = make_float2(m, sum);
         }
       }
-      // 32 batch rows x 16 columns at a time through shared memory, so that a
-      // row's 16 values leave in one piece
-      float* out = a.out + (int64_t)(b0 + quad * 32 + (lane >> 4)) * a.ldo + j0 + (lane & 15);
-      const int rows = a.B - (b0 + quad * 32 + (lane >> 4));  // of this lane's, in steps of two
+      // 32 batch rows x 32 columns at a time through shared memory, so that a
+      // row's 128 bytes leave in one piece
+      float* out = a.out + (int64_t)(b0 + quad * 32) * a.ldo + j0 + lane;
+      const int rows = a.B - (b0 + quad * 32);
 #pragma unroll
-      for (int c = 0; c < 128; c += 16) {
+      for (int c = 0; c < 128; c += 32) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const float2 z2 = unpack2(acc[c / 2 + i]);
           ob[lane * kOutPitch + 2 * i] = z2.x * a.out_scale;
           ob[lane * kOutPitch + 2 * i + 1] = z2.y * a.out_scale;
         }
         __syncwarp();
-        if (c + (lane & 15) < nvalid) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (2 * r < rows)
-              out[(int64_t)(2 * r) * a.ldo + c] = ob[(2 * r + (lane >> 4)) * kOutPitch + (lane & 15)];
+        if (c + lane < nvalid) {
+          float* o = out + c;
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
+            if (r < rows) *o = ob[r * kOutPitch + lane];
+            o += a.ldo;
+          }
         }
       }
     }
@@ -1067,11 +1074,12 @@ template <bool TWO>
 int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
   constexpr int stage = umma::kBM * 128 + (TWO ? 128 : 256) * 128;
   constexpr size_t out = (size_t)(kBatchNP / 32) * 32 * kOutPitch * sizeof(float);
-  fa.h.stages = std::min(umma::kMaxStages, 196 * 1024 / stage);
+  fa.h.stages = 160 * 1024 / stage;  // five of a pair, three of a single CTA
   fa.nchunk = fa.Bp / (TWO ? 256 : 128);
   fa.items = (fa.h.K + kBatchRowsW - 1) / kBatchRowsW * fa.nchunk;
   const int ctas = TWO ? 2 : 1;
-  return launch_product(s, batch_fp8_kernel<TWO>, ctas * std::min(fa.items, kSms / ctas), kBatchNT,
+  return launch_product(s, fa.h.part != nullptr ? batch_fp8_kernel<TWO, true> : batch_fp8_kernel<TWO, false>,
+                        ctas * std::min(fa.items, kSms / ctas), kBatchNT,
                         (size_t)fa.h.stages * stage + out + 1024, ctas, mw, mx, fa);
 }
 
