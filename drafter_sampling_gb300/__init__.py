@@ -755,15 +755,25 @@ class BlockGraph:
     reads what they hold when it runs.  Outputs (q, draft_tokens,
     out_tokens, out_num_accepted, out_accept_prob, dev_status [2]) are
     attributes.  temperature == 0 captures the greedy block (u_draft,
-    u_accept and u_resample may then be None)."""
+    u_accept and u_resample may then be None).  With w_scale, W_trim is an
+    e4m3 head as vt_quantize_head leaves it (vt_block_graph_create_fp8)."""
 
     def __init__(self, hidden, W_trim, trim_ids, inv_map, target_logits, u_draft=None,
                  u_accept=None, u_resample=None, temperature: float = 1.0,
-                 want_accept_prob: bool = True):
+                 want_accept_prob: bool = True, w_scale=None):
         torch = _torch()
         greedy = float(temperature) == 0.0
         _dev(hidden, "hidden", _bf16_dtypes(), 3)
-        _dev(W_trim, "W_trim", _bf16_dtypes(), 2)
+        fp8 = None
+        if w_scale is None:
+            _dev(W_trim, "W_trim", _bf16_dtypes(), 2)
+        else:
+            K8, H8, ldw, p8, sp = _head_fp8(W_trim, w_scale, _first(hidden, "hidden"))
+            if H8 != hidden.shape[2]:
+                raise ValueError("hidden and W_trim disagree on H")
+            if trim_ids.numel() != K8:
+                raise ValueError("trim_ids must have K elements")
+            fp8 = (p8, ldw, sp)
         _dev(trim_ids, "trim_ids", (torch.int32,), 1)
         _dev(inv_map, "inv_map", (torch.int32,), 1)
         if target_logits.dtype == torch.float32:
@@ -796,11 +806,13 @@ class BlockGraph:
                                 if want_accept_prob else None)
         self.dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
         L = lib()
-        self.workspace = _ws(L.vt_block_workspace_bytes(B, H, K, V, gamma), dev)
+        self.workspace = _ws((L.vt_block_fp8_workspace_bytes if fp8 else L.vt_block_workspace_bytes)(
+            B, H, K, V, gamma), dev)
         self._keep = (hidden, W_trim, trim_ids, inv_map, target_logits, u_draft, u_accept,
-                      u_resample)
+                      u_resample, w_scale)
         ptr = lambda x: x.data_ptr() if x is not None else None
-        d = _lib.BlockDesc(B, H, K, V, gamma, dt, float(temperature), ptr(hidden), ptr(W_trim),
+        d = _lib.BlockDesc(B, H, K, V, gamma, dt, float(temperature), ptr(hidden),
+                           None if fp8 else ptr(W_trim),
                            ptr(trim_ids), ptr(inv_map), ptr(u_draft), ptr(target_logits),
                            ptr(u_accept), ptr(u_resample), ptr(self.q), ptr(self.draft_tokens),
                            ptr(self.out_tokens), ptr(self.out_num_accepted),
@@ -808,7 +820,12 @@ class BlockGraph:
                            ptr(self.workspace), self.workspace.numel())
         import ctypes
         h = ctypes.c_void_p()
-        _lib.check("vt_block_graph_create", L.vt_block_graph_create(ctypes.byref(d), ctypes.byref(h)))
+        if fp8:
+            _lib.check("vt_block_graph_create_fp8",
+                       L.vt_block_graph_create_fp8(ctypes.byref(d), *fp8, ctypes.byref(h)))
+        else:
+            _lib.check("vt_block_graph_create",
+                       L.vt_block_graph_create(ctypes.byref(d), ctypes.byref(h)))
         self._handle = h
 
     def launch(self, stream=None):

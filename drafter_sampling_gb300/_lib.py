@@ -90,6 +90,9 @@ SIGNATURES = {
                                  _p, _sz, _p]),
     "vt_block_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "vt_block_graph_create": (C.c_int, [C.POINTER(BlockDesc), C.POINTER(C.c_void_p)]),
+    "vt_block_fp8_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "vt_block_graph_create_fp8": (C.c_int, [C.POINTER(BlockDesc), _p, _i64, _p,
+                                            C.POINTER(C.c_void_p)]),
     "vt_block_graph_launch": (C.c_int, [_p, _p]),
     "vt_block_graph_destroy": (C.c_int, [_p]),
 }

@@ -17,7 +17,7 @@ extern "C" const char* vt_status_string(int status) {
   }
 }
 
-extern "C" int vt_abi_version(void) { return 100; }
+extern "C" int vt_abi_version(void) { return 101; }
 
 namespace vt {
 namespace {

@@ -54,35 +54,52 @@ __device__ __forceinline__ uint32_t scale_e4m3x2(uint32_t w, float inv) {
 constexpr int kQuantNT = 256;
 constexpr int kQuantU = kQB * kQB / 8 / kQuantNT;  // 16-byte loads per thread (8)
 
+// The eight bf16 values from column h of row r (zero past the row) as four
+// words.  `by` 16: rows of whole 16-byte vectors; 4: W is 4-byte aligned, rows
+// may start in the middle of a word, so five words are read and shifted; 2:
+// value by value, as is what the words would reach past the matrix.
+__device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ W, int K, int H, int r,
+                                             int h, int by) {
+  if (r >= K || h >= H) return make_uint4(0, 0, 0, 0);
+  const int64_t at = (int64_t)r * H + h;
+  if (by == 16) return __ldg(reinterpret_cast<const uint4*>(W + at));
+  uint32_t w[5];
+  if (by == 4 && at + 10 <= (int64_t)K * H) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(W) + (at >> 1);
+    const unsigned shift = (unsigned)(at & 1) * 16;
+#pragma unroll
+    for (int e = 0; e < 5; ++e) w[e] = __ldg(p + e);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], shift);
+    const int left = H - h;  // values of this row
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (2 * e + 2 > left) w[e] = 2 * e + 1 > left ? 0u : w[e] & 0xffffu;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (h + e < H) w[e >> 1] |= (uint32_t)__ldg(W + at + e) << (16 * (e & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // One CTA per 128 x 128 block: the block is read once (eight 16-byte loads
 // in flight per thread), its largest magnitude reduced, and the registers
 // scaled, rounded and stored.  HBM-bound: 2 bytes read, 1 written per weight.
 __global__ void __launch_bounds__(kQuantNT)
 quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __restrict__ W8,
                      int64_t ldw, float* __restrict__ w_scale, int* __restrict__ dev_status,
-                     int vec_ok) {
+                     int by) {
   __shared__ uint32_t smax[kQuantNT / 32];
   const int tid = threadIdx.x;
   const int r0 = blockIdx.y * kQB, h = blockIdx.x * kQB + (tid & 15) * 8;
   uint4 v[kQuantU];
   uint32_t mx = 0;  // largest magnitudes of the even and odd columns, packed
 #pragma unroll
-  for (int i = 0; i < kQuantU; ++i) {
-    const int r = r0 + i * (kQuantNT / 16) + (tid >> 4);
-    const uint16_t* p = W + (int64_t)r * H + h;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r < K && h < H) {
-      if (vec_ok) {  // H % 8 == 0: the whole vector lies in the row
-        v[i] = __ldg(reinterpret_cast<const uint4*>(p));
-      } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (h + e < H) w[e >> 1] |= (uint32_t)__ldg(p + e) << (16 * (e & 1));
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  }
+  for (int i = 0; i < kQuantU; ++i)
+    v[i] = load_bf16x8(W, K, H, r0 + i * (kQuantNT / 16) + (tid >> 4), h, by);
 #pragma unroll
   for (int i = 0; i < kQuantU; ++i) {
     mx = __vmaxu2(mx, v[i].x & 0x7fff7fffu);
@@ -111,7 +128,7 @@ quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __re
     o.x = scale_e4m3x2(v[i].x, inv) | scale_e4m3x2(v[i].y, inv) << 16;
     o.y = scale_e4m3x2(v[i].z, inv) | scale_e4m3x2(v[i].w, inv) << 16;
     uint8_t* q = W8 + (int64_t)r * ldw + h;
-    if (vec_ok) {  // ldw % 16 == 0 and W8 16-byte aligned
+    if (h + 8 <= H) {  // ldw % 16 == 0 and W8 is 16-byte aligned
       *reinterpret_cast<uint2*>(q) = o;
     } else {
 #pragma unroll
@@ -1162,7 +1179,8 @@ extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int st = clear_status(s, dev_status);
   if (st != VT_OK) return st;
-  const int vec_ok = H % 8 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
+  const uintptr_t wa = reinterpret_cast<uintptr_t>(W);
+  const int by = H % 8 == 0 && (wa & 15) == 0 ? 16 : (wa & 3) == 0 ? 4 : 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((H + kQB - 1) / kQB), (unsigned)rows);
   cfg.blockDim = dim3(kQuantNT);
@@ -1173,7 +1191,7 @@ extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, quantize_head_kernel, W, K, H, W8, ldw, w_scale,
-                                       dev_status, vec_ok));
+                                       dev_status, by));
   return VT_OK;
 }
 
@@ -1203,7 +1221,17 @@ extern "C" int vt_draft_step_fp8(const uint16_t* hidden, int32_t B, int32_t H, c
                                  int64_t ldq, int32_t* tokens, int64_t ld_tokens,
                                  int32_t* dev_status, void* workspace, size_t workspace_bytes,
                                  void* stream) {
-  using namespace vt;
+  return vt::draft_step_fp8_impl(hidden, B, H, W8, ldw, w_scale, trim_ids, K, uniforms, temperature,
+                                 q, ldq, tokens, ld_tokens, dev_status, workspace, workspace_bytes,
+                                 stream, 1);
+}
+
+int vt::draft_step_fp8_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                            int64_t ldw, const float* w_scale, const int32_t* trim_ids, int32_t K,
+                            const float* uniforms, float temperature, float* q, int64_t ldq,
+                            int32_t* tokens, int64_t ld_tokens, int32_t* dev_status,
+                            void* workspace, size_t workspace_bytes, void* stream,
+                            int status_reset) {
   const int st = check_fp8_args(hidden, B, H, W8, ldw, w_scale, K, temperature, true);
   if (st != VT_OK) return st;
   const bool greedy = temperature == 0.f;
@@ -1216,7 +1244,7 @@ extern "C" int vt_draft_step_fp8(const uint16_t* hidden, int32_t B, int32_t H, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rc = launch_head_fp8(s, hidden, B, H, W8, ldw, w_scale, K,
                                  greedy ? 1.0f : VT_LOG2E / temperature, q, ldq, ws, ws.part,
-                                 dev_status, 1, greedy ? 1 : 0);
+                                 dev_status, status_reset, greedy ? 1 : 0);
   if (rc != VT_OK) return rc;
   return draft_finish(s, B, K, greedy, ws.part, (K + umma::kBM - 1) / umma::kBM, umma::kBM,
                       uniforms, trim_ids, q, ldq, tokens, ld_tokens, dev_status);

@@ -47,4 +47,11 @@ int draft_step_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint16_t
                     int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream,
                     int status_reset, int hidden_ready);
 
+// vt_draft_step_fp8 with the same choice of status_reset.
+int draft_step_fp8_impl(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,
+                        int64_t ldw, const float* w_scale, const int32_t* trim_ids, int32_t K,
+                        const float* uniforms, float temperature, float* q, int64_t ldq,
+                        int32_t* tokens, int64_t ld_tokens, int32_t* dev_status, void* workspace,
+                        size_t workspace_bytes, void* stream, int status_reset);
+
 }  // namespace vt

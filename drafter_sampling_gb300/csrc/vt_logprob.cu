@@ -22,7 +22,7 @@
 // The k best are kept as 64-bit keys, ordered by (value, lower id first).  A
 // warp lists in shared memory the ids whose key reaches a bound that at least
 // k ids seen reach: the k-th best of 32 disjoint groups' largest logits,
-// renewed after 2, 4, 8 ... chunks.  So little more than k ids of the first
+// renewed after 2, 4 ... chunks.  So little more than k ids of the first
 // chunk are listed and few later ones; the lists are ranked by counting at the
 // end.  A list that fills (ties, masks, ordered rows) is cut to its k best
 // keys, the last of which is a bound too.  Blocks join through distributed shared memory.
@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
         continue;
       }
 
-      if ((i & (i + 1)) == 0) {
-        // after 1, 2, 4 ... chunks, the bound: the k-th largest of 32 groups'
+      if ((i & (i + 1)) == 0 && (i == 0 || mine - 1 - i > i + 1)) {
+        // after 1, 2, 4 ... chunks, while more are to come than have been, the bound: the k-th largest of 32 groups'
         // (8 lanes each) largest logits so far.  Only the first chunk needs every group's value;
         // later a value of another warp may be an older one, which is as valid.
         float g = st.s > 0.f ? st.m : -INFINITY;
@@ -630,24 +630,40 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     } else {
       if (tid == 0) sh.blk = r;
       cl.sync();
-      if (rank == 0) {
-        // all blocks' keys; warp w holds block w's
-        if (warp < C) {
-          if (lane < k) {
-            q = cl.map_shared_rank(sh.best, warp)[lane];
-            sh.all[warp * k + lane] = q;
-          }
-          if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
-        }
-        if (tid < C) sh.red[tid] = *cl.map_shared_rank(&sh.blk, tid);
-        if (tid < C && *cl.map_shared_rank(&sh.timeout, tid) != 0) atomicExch(&sh.timeout, 1);
+      if (rank != 0) {
+        // the first block reads this one's memory before it arrives in turn
+        cl.sync();
+        return;
       }
-      cl.sync();  // the other blocks' memory has been read; they may exit
-      if (rank != 0) return;
+      // all blocks' statistics, one per lane, and keys; warp w holds block w's
+      const int from = lane < C ? lane : 0;
+      r = *cl.map_shared_rank(&sh.blk, from);
+      if (lane >= C) r.s = r.e = r.d = 0.f;
+      const bool gave_up = *cl.map_shared_rank(&sh.timeout, from) != 0;
+      if (warp < C) {
+        if (lane < k) {
+          q = cl.map_shared_rank(sh.best, warp)[lane];
+          sh.all[warp * k + lane] = q;
+        }
+        if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
+      }
+      late = __any_sync(0xffffffffu, gave_up);
+#pragma unroll
+      for (int o = kLpMaxC / 2; o > 0; o >>= 1) {
+        Lse w;
+        w.m = __shfl_xor_sync(0xffffffffu, r.m, o);
+        w.s = __shfl_xor_sync(0xffffffffu, r.s, o);
+        w.e = __shfl_xor_sync(0xffffffffu, r.e, o);
+        w.d = __shfl_xor_sync(0xffffffffu, r.d, o);
+        r = lse_join(r, w, c, low);
+      }
+      r.m = __shfl_sync(0xffffffffu, r.m, 0);
+      r.s = __shfl_sync(0xffffffffu, r.s, 0);
+      r.e = __shfl_sync(0xffffffffu, r.e, 0);
+      r.d = __shfl_sync(0xffffffffu, r.d, 0);
+      lp_bar();  // every read of the other blocks' memory has returned
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // they may exit
       if (q != 0) rk = count_before(sh.all, C * k, q);
-      r = sh.red[0];
-      for (int w = 1; w < C; ++w) r = lse_join(r, sh.red[w], c, low);
-      late = sh.timeout != 0;
     }
     const bool ok = !late && r.s > 0.f && isfinite(r.s) && isfinite(r.m);
     const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
@@ -670,7 +686,10 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       a.out_ids[row * k + tid] = -1;
       a.out_top[row * k + tid] = nan;
     }
-    lp_bar();  // the next row writes what this one has read
+    if (C > 1)
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    else
+      lp_bar();  // the next row writes what this one has read
   }
 }
 

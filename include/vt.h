@@ -514,6 +514,12 @@ typedef struct {
 
 size_t vt_block_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t V, int32_t gamma);
 int vt_block_graph_create(const vt_block_desc* desc, void** graph);
+/* The same block drafted through an e4m3 head (gamma vt_draft_step_fp8 calls):
+ * W8, ldw and w_scale as there, desc->W_trim is not read, and the workspace has
+ * vt_block_fp8_workspace_bytes(B, H, K, V, gamma) bytes. */
+size_t vt_block_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t V, int32_t gamma);
+int vt_block_graph_create_fp8(const vt_block_desc* desc, const uint8_t* W8, int64_t ldw,
+                              const float* w_scale, void** graph);
 int vt_block_graph_launch(void* graph, void* stream);
 int vt_block_graph_destroy(void* graph);
 

@@ -71,6 +71,20 @@ def test_fp8_draft_refusals(lib):
     assert lib.vt_draft_topk_fp8_workspace_bytes(2, 64, 16, 17) == 0
 
 
+def test_fp8_block_refusals(lib):
+    from drafter_sampling_gb300 import _lib
+    bad, _, _ = _bad()
+    h = ctypes.c_void_p()
+    d = _lib.BlockDesc()
+    assert lib.vt_block_graph_create_fp8(None, FAKE, 64, FAKE, ctypes.byref(h)) == bad
+    assert lib.vt_block_graph_create_fp8(ctypes.byref(d), None, 64, FAKE, ctypes.byref(h)) == bad
+    assert lib.vt_block_graph_create_fp8(ctypes.byref(d), FAKE, 64, None, ctypes.byref(h)) == bad
+    assert lib.vt_block_graph_create_fp8(ctypes.byref(d), FAKE, 64, FAKE, ctypes.byref(h)) == bad
+    assert lib.vt_block_fp8_workspace_bytes(16, 2048, 32768, 128256, 6) >= \
+        lib.vt_verify_workspace_bytes(16, 6, 128256, 32768)
+    assert lib.vt_block_fp8_workspace_bytes(0, 2048, 32768, 128256, 6) == 0
+
+
 def test_token_logprobs_refusals(lib):
     bad, _, _ = _bad()
     ok = dict(l=FAKE, dt=0, R=2, V=10, ld=10, tok=FAKE, k=3, T=1.0, lp=FAKE, en=FAKE, ids=FAKE, top=FAKE,

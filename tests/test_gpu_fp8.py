@@ -71,6 +71,19 @@ def test_quantize_head_bit_exact(vt, K, H):
     assert np.array_equal(s.cpu().numpy().astype(np.float64), scale)
 
 
+@pytest.mark.parametrize("K,H", [(1, 1), (3, 5), (129, 129), (200, 136), (130, 1001), (260, 254)])
+@pytest.mark.parametrize("lead", [1, 2, 3, 4, 7])
+def test_quantize_head_misaligned_rows(vt, K, H, lead):
+    # rows that start at any 2-byte boundary, the last ending at the end of the allocation's data
+    bits = synthetic.head_weights(K, H, seed=K + H + lead)
+    flat = torch.zeros(lead + K * H, dtype=torch.int16, device="cuda")
+    flat[lead:] = _bf(bits).view(-1)
+    W8, s, st = vt.vt_quantize_head(flat[lead:].view(K, H))
+    codes, scale = fp8.quantize_head(bits)
+    assert int(st.item()) == 0 and np.array_equal(W8.view(torch.uint8).cpu().numpy(), codes)
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), scale)
+
+
 def test_quantize_head_extremes(vt):
     # zero blocks, subnormals, the largest bf16, and 448 on the boundary of two scales
     blocks = [0.0, 1e-40, 3.3e38, 448.0, 450.0, 2.0 ** -118 * 1.75, 2.0 ** -130, 1.0]
@@ -241,6 +254,38 @@ def test_topk_matches_the_logits(vt, B, H, K, k):
         assert np.all(np.abs(logq[b] - lp[out[b]]) <= 2 * tol[b] + 1e-5)
         assert np.all(z[b, out[b]] >= np.sort(z[b])[::-1][:k] - tol[b])
         assert len(set(out[b].tolist())) == k
+
+
+@pytest.mark.parametrize("T", [1.0, 0.0])
+@pytest.mark.parametrize("B,H,K,V,gamma", [(4, 256, 600, 2000, 3), (130, 128, 300, 700, 2)])
+def test_block_graph_equals_the_calls(vt, B, H, K, V, gamma, T):
+    # the captured block drafts and verifies exactly what the calls made one by one do, at every replay
+    g = synthetic.rng(B, 9)
+    trim = np.sort(g.permutation(V)[:K]).astype(np.int32)
+    inv = np.full(V, -1, np.int32)
+    inv[trim] = np.arange(K)
+    trim, inv = _dev(trim), _dev(inv)
+    W8, s, _ = vt.vt_quantize_head(_bf(synthetic.head_weights(K, H, seed=5)))
+    hid = _bf(synthetic.hidden_states((gamma, B, H), seed=6))
+    logits = torch.randn((B, gamma + 1, V), device="cuda")
+    ud, ua, ur = (_dev(synthetic.uniforms(7, i, sh)) for i, sh in
+                  enumerate([(gamma, B), (B, gamma), (B, gamma + 1)]))
+    blk = vt.BlockGraph(hid, W8, trim, inv, logits, ud, ua, ur, T, w_scale=s)
+    for seed in (6, 60):
+        hid.copy_(_bf(synthetic.hidden_states((gamma, B, H), seed=seed)))
+        blk.launch()
+        q = torch.empty((B, gamma, K), device="cuda")
+        tok = torch.empty((B, gamma), dtype=torch.int32, device="cuda")
+        for j in range(gamma):
+            _, _, st = vt.vt_draft_step_fp8(hid[j], W8, s, trim, ud[j], T, q=q[:, j], tokens=tok[:, j])
+            assert int(st.item()) == 0
+        out, n, acc, st = vt.vt_verify(logits, q, inv, tok, ua, ur, T)
+        torch.cuda.synchronize()
+        assert blk.dev_status.tolist() == [0, int(st.item())]
+        for a, b in ((blk.q, q), (blk.draft_tokens, tok), (blk.out_tokens, out), (blk.out_num_accepted, n)):
+            assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="trim_ids"):
+        vt.BlockGraph(hid, W8, trim[:-1], inv, logits, ud, ua, ur, T, w_scale=s)
 
 
 def test_binding_refusals(vt):
