@@ -186,6 +186,7 @@ struct Fp8Args {
   const float* sx;      // [groups][Bp]
   int Bp, groups, nchunk;
   int items;            // blocks of W8 rows times batch chunks
+  int vec_out;          // the output's rows are 16-byte aligned
 };
 
 constexpr int kMaxGroups = 512;   // H <= 65536
@@ -674,7 +675,9 @@ constexpr int kBatchNP = 256;
 constexpr int kBatchNT = kBatchNP + 128;
 constexpr int kBatchRowsW = 256;   // rows of W8 of an item
 constexpr int kBatchBufs = 2;      // accumulator buffers of 256 columns: all of tensor memory
-constexpr int kOutPitch = 33;      // floats: a warp's 32 x 32 block on its way out
+// floats: a warp's 32 x 32 block on its way out; 16-byte accesses by row and by
+// column of eight lanes then meet all banks
+constexpr int kOutPitch = 36;
 
 // Wide batches: items of 256 rows of W8 x 128 batch rows, or, as a pair of CTAs
 // (TWO), x 256 batch rows with one MMA of 256 x 256: each CTA of a pair stages
@@ -876,7 +879,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     griddep_wait();
     // this thread's batch row (TMEM lane) and its half of the W8 rows
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
-    float* ob = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes) + warp * 32 * kOutPitch;
+    float* ob = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes) + warp * 32 * kOutPitch;  // 16-byte aligned
     int it = 0;
     bool ok = true;
     for (int item = first; item < items; item += step) {
@@ -958,25 +961,42 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
       }
       // 32 batch rows x 32 columns at a time through shared memory, so that a
-      // row's 128 bytes leave in one piece
-      float* out = a.out + (int64_t)(b0 + quad * 32) * a.ldo + j0 + lane;
+      // row's 128 bytes leave in one piece: four rows in an instruction where
+      // the output's rows are 16-byte aligned, one otherwise
+      float* out = a.out + (int64_t)(b0 + quad * 32) * a.ldo + j0;
       const int rows = a.B - (b0 + quad * 32);
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 z2 = unpack2(acc[c / 2 + i]);
-          ob[lane * kOutPitch + 2 * i] = z2.x * a.out_scale;
-          ob[lane * kOutPitch + 2 * i + 1] = z2.y * a.out_scale;
+        for (int i = 0; i < 8; ++i) {
+          const float2 x = unpack2(acc[c / 2 + 2 * i]), y = unpack2(acc[c / 2 + 2 * i + 1]);
+          *reinterpret_cast<float4*>(ob + lane * kOutPitch + 4 * i) = make_float4(
+              x.x * a.out_scale, x.y * a.out_scale, y.x * a.out_scale, y.y * a.out_scale);
         }
         __syncwarp();
-        if (c + lane < nvalid) {
-          float* o = out + c;
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            if (r < rows) *o = ob[r * kOutPitch + lane];
-            o += a.ldo;
+        if (fa.vec_out && c + 32 <= nvalid) {
+          const int r0 = lane >> 3, col = 4 * (lane & 7);
+          float4 t[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            t[r] = *reinterpret_cast<const float4*>(ob + (4 * r + r0) * kOutPitch + col);
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (4 * r + r0 < rows)
+              *reinterpret_cast<float4*>(out + (int64_t)(4 * r + r0) * a.ldo + c + col) = t[r];
+        } else if (c + lane < nvalid) {
+          float* o = out + c + lane;
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {
+            float t[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t[r] = ob[(h + r) * kOutPitch + lane];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              if (h + r < rows) *o = t[r];
+              o += a.ldo;
+            }
           }
         }
       }
@@ -1144,6 +1164,7 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
   fa.Bp = Bp;
   fa.groups = groups;
   fa.nchunk = 1;
+  fa.vec_out = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 4 == 0;
   switch (Bp) {
     case 16: return launch_narrow<16>(s, mw, mx, fa);
     case 32: return launch_narrow<32>(s, mw, mx, fa);
