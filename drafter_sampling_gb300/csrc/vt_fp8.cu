@@ -681,14 +681,15 @@ constexpr int kOutPitch = 36;
 
 // Wide batches: items of 256 rows of W8 x 128 batch rows, or, as a pair of CTAs
 // (TWO), x 256 batch rows with one MMA of 256 x 256: each CTA of a pair stages
-// its 128 batch rows and half of the weights, half the shared-memory traffic
-// of the same work on one CTA, which is what bounds it there.  The roles are
-// those of head_fp8_kernel; in a pair the first CTA issues the MMAs for both
-// and holds the barriers that they wait on.
+// its 128 batch rows and half of the weights, two thirds of the shared-memory
+// traffic of the same work on one CTA.  The roles are those of
+// head_fp8_kernel; in a pair the first CTA issues the MMAs for both and holds
+// the barriers that they wait on.
 // MMAs into one accumulator buffer stand still while the other is read, so a
 // promoting thread reads its 128 columns in two bursts of 64 and does nothing
 // else meanwhile (four reads of 32 with the arithmetic between them: 189
-// against 165 us at B = 1000, K = 38016, H = 4096).
+// against 165 us at B = 1000, K = 38016, H = 4096).  No register may spill: 24
+// bytes of spills in the loop over the groups cost a tenth of the time.
 template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -929,37 +930,11 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // a warp that gave up stores nothing more, but misses no barrier
       if (!ok || nvalid <= 0) continue;
       const int b = b0 + row;
-      if (PART && b < a.B) {
-        // this row's partial over the tile's rows, as tile_partials leaves it
-        if (a.greedy) {
-          float v = -INFINITY;
-          int idx = 0x7fffffff;
-#pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const float2 z2 = unpack2(acc[i / 2]);
-            const float z = (i & 1 ? z2.y : z2.x) * a.out_scale;
-            const float w = isfinite(z) ? z : __int_as_float(0x7fc00000);
-            if (i < nvalid && argmax_better(v, idx, w, j0 + i)) {
-              v = w;
-              idx = j0 + i;
-            }
-          }
-          a.part[(int64_t)tile * a.B + b] = make_float2(v, __int_as_float(idx));
-        } else {
-          float m = kNegBig, sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const float2 z2 = unpack2(acc[i / 2]);
-            if (i < nvalid) m = fmaxf(m, (i & 1 ? z2.y : z2.x) * a.out_scale);
-          }
-#pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const float2 z2 = unpack2(acc[i / 2]);
-            if (i < nvalid) sum += exp2_approx((i & 1 ? z2.y : z2.x) * a.out_scale - m);
-          }
-          a.part[(int64_t)tile * a.B + b] = make_float2(m, sum);
-        }
-      }
+      // this row's partial over the tile's rows, like tile_partials': greedy,
+      // (largest z, its lowest row), a non-finite z counting as NaN, which wins;
+      // sampling, (max, sum 2^(z - max)), a NaN or +inf z leaving the sum NaN
+      float pm = a.greedy ? -INFINITY : kNegBig, ps = 0.f;
+      int pidx = 0x7fffffff;
       // 32 batch rows x 32 columns at a time through shared memory, so that a
       // row's 128 bytes leave in one piece: four rows in an instruction where
       // the output's rows are 16-byte aligned, one otherwise
@@ -975,6 +950,27 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
               x.x * a.out_scale, x.y * a.out_scale, y.x * a.out_scale, y.y * a.out_scale);
         }
         __syncwarp();
+        if constexpr (PART) {
+          // from this thread's row in shared memory, 32 values at a time
+          const float* mine = ob + lane * kOutPitch;
+          const int some = min(32, nvalid - c);
+          if (a.greedy) {
+            for (int i = 0; i < some; ++i) {
+              const float z = mine[i];
+              const float w = isfinite(z) ? z : __int_as_float(0x7fc00000);
+              if (argmax_better(pm, pidx, w, j0 + c + i)) {
+                pm = w;
+                pidx = j0 + c + i;
+              }
+            }
+          } else if (some > 0) {
+            float top = pm;
+            for (int i = 0; i < some; ++i) top = fmaxf(top, mine[i]);
+            ps *= exp2_approx(pm - top);
+            pm = top;
+            for (int i = 0; i < some; ++i) ps += exp2_approx(mine[i] - pm);
+          }
+        }
         if (fa.vec_out && c + 32 <= nvalid) {
           const int r0 = lane >> 3, col = 4 * (lane & 7);
           float4 t[8];
@@ -987,19 +983,15 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
               *reinterpret_cast<float4*>(out + (int64_t)(4 * r + r0) * a.ldo + c + col) = t[r];
         } else if (c + lane < nvalid) {
           float* o = out + c + lane;
-#pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            float t[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) t[r] = ob[(h + r) * kOutPitch + lane];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              if (h + r < rows) *o = t[r];
-              o += a.ldo;
-            }
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
+            if (r < rows) *o = ob[r * kOutPitch + lane];
+            o += a.ldo;
           }
         }
       }
+      if (PART && b < a.B)
+        a.part[(int64_t)tile * a.B + b] = make_float2(pm, a.greedy ? __int_as_float(pidx) : ps);
     }
     if (!ok && lane == 0) atomicExch(&s_err, 1);
   }
@@ -1028,7 +1020,12 @@ struct Fp8Ws {
   size_t bytes;
 };
 
-int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : (B + 255) / 256 * 256; }
+int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : (B + 127) / 128 * 128; }
+
+// Wide batches of an even number of 128-row chunks go to pairs of CTAs (B = 256,
+// K = 38016, H = 4096: 46.8 against 48.9 us on single CTAs, in one process), an
+// odd number to single ones (B = 300: 64.6 us against 83.4 padded to pairs).
+bool paired(int Bp) { return Bp % 256 == 0; }
 
 Fp8Ws carve_fp8(void* base, int B, int H, int K) {
   Fp8Ws w;
@@ -1129,7 +1126,8 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
   const int groups = (H + kQB - 1) / kQB, Bp = pad_batch(B), ldx = groups * kQB;
   CUtensorMap mw, mx;
   // the boxes: the rows that one CTA stages
-  if (!make_e4m3_map(&mw, W8, (uint64_t)K, (uint64_t)H, (uint64_t)ldw, Bp == 128 ? 256 : 128))
+  if (!make_e4m3_map(&mw, W8, (uint64_t)K, (uint64_t)H, (uint64_t)ldw,
+                     Bp > 64 && !paired(Bp) ? 256 : 128))
     return VT_ERR_CUDA;
   if (!make_e4m3_map(&mx, ws.x8, (uint64_t)B, (uint64_t)ldx, (uint64_t)ldx,
                      (uint32_t)std::min(Bp, 128)))
@@ -1169,8 +1167,7 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
     case 16: return launch_narrow<16>(s, mw, mx, fa);
     case 32: return launch_narrow<32>(s, mw, mx, fa);
     case 64: return launch_narrow<64>(s, mw, mx, fa);
-    case 128: return launch_wide<false>(s, mw, mx, fa);
-    default: return launch_wide<true>(s, mw, mx, fa);
+    default: return paired(Bp) ? launch_wide<true>(s, mw, mx, fa) : launch_wide<false>(s, mw, mx, fa);
   }
 }
 
