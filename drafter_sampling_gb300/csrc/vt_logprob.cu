@@ -53,8 +53,8 @@ constexpr int kLpPerSm = 3;          // resident blocks per SM (shared memory)
 
 struct LpArgs {
   const void* logits;
-  int64_t R, ld;
-  int V, k;
+  int64_t ld;
+  int R, V, k;
   float c, inv_t;        // log2(e) / T and 1 / T
   const int* tokens;     // [R]
   float* out_logp;       // [R]
@@ -321,9 +321,9 @@ struct Span {
   int head, nvec, mine;
 };
 template <typename T>
-__device__ __forceinline__ Span span_of(const LpArgs& a, int64_t row, int rank, int C) {
+__device__ __forceinline__ Span span_of(const LpArgs& a, int row, int rank, int C) {
   constexpr int VE = Elem<T>::kVec;
-  const T* l = static_cast<const T*>(a.logits) + row * a.ld;
+  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
   const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
   Span sp;
   sp.head = min(a.V, off ? VE - off : 0);
@@ -331,6 +331,12 @@ __device__ __forceinline__ Span span_of(const LpArgs& a, int64_t row, int rank, 
   const int chunks = (sp.nvec + kLpNT * kLpU - 1) / (kLpNT * kLpU);
   sp.mine = chunks > rank ? (chunks - rank + C - 1) / C : 0;
   return sp;
+}
+
+// the id of a row's edge element t: first those before the vectors, then those behind
+template <int VE>
+__device__ __forceinline__ int edge_id(const Span& sp, int t) {
+  return t < sp.head ? t : sp.nvec * VE + t;
 }
 
 struct LpShared {
@@ -342,6 +348,7 @@ struct LpShared {
   int n[kLpWarps];
   Lse red[kLpWarps];
   Lse blk;                                           // this block's statistics, as published
+  float edge[16], xt;                                // the row's edges; the given token's logit
   int timeout;
 };
 
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
   const int k = a.k;
   const float nan = __int_as_float(0x7fc00000);
   // this cluster's rows (more than one only when C == 1)
-  const int64_t row0 = blockIdx.x / C, stride = gridDim.x / C;
+  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
   if (tid == 0) {
     for (int s = 0; s < kLpStages; ++s) {
       umma::mbar_init(&sh.full[s], 1);
@@ -416,11 +423,11 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     if (lane == 0) {
       bool ok = true;
       int it = 0;  // chunks requested so far
-      for (int64_t row = row0; row < a.R && ok; row += stride) {
+      for (int row = row0; row < a.R && ok; row += stride) {
         if (a.tokens[row] == -1) continue;
         const Span sp = span_of<T>(a, row, rank, C);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(
-            static_cast<const T*>(a.logits) + row * a.ld + sp.head);
+            static_cast<const T*>(a.logits) + (int64_t)row * a.ld + sp.head);
         for (int i = 0; i < sp.mine; ++i, ++it) {
           const int s = it % kLpStages;
           if (it >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((it / kLpStages) - 1) & 1);
@@ -450,7 +457,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
   int it = 0;  // chunks consumed so far
   uint32_t limit = umma::kWaitLimit;
   int next_token = a.tokens[row0];
-  for (int64_t row = row0; row < a.R; row += stride) {
+  for (int row = row0; row < a.R; row += stride) {
     const int token = next_token;
     if (row + stride < a.R) next_token = a.tokens[row + stride];
     if (token == -1) {  // not scored: the row is not read
@@ -461,26 +468,22 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
           if (a.own_status) *a.dev_status = 0;
         }
         if (tid < k) {
-          a.out_ids[row * k + tid] = -1;
-          a.out_top[row * k + tid] = nan;
+          a.out_ids[(int64_t)row * k + tid] = -1;
+          a.out_top[(int64_t)row * k + tid] = nan;
         }
       }
       continue;
     }
-    const T* l = static_cast<const T*>(a.logits) + row * a.ld;
+    const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
     const Span sp = span_of<T>(a, row, rank, C);
     const int head = sp.head, nvec = sp.nvec, mine = sp.mine;
-    float xt = 0.f;
-    if (rank == 0 && tid == 0 && token >= 0 && token < a.V) xt = Elem<T>::load(l + token);
-    // one element per thread of the row's edges, in block 0
-    float xe = -INFINITY;
-    int ie = -1;
-    if (rank == 0) {
-      ie = tid < head ? tid : head + nvec * VE + (tid - head);
-      if (ie < a.V && tid < 2 * VE)
-        xe = Elem<T>::load(l + ie);
-      else
-        ie = -1;
+    // the given token's logit and the row's edges, one element per thread of
+    // block 0, kept in shared memory until the end: registers are short
+    const bool edge = rank == 0 && tid < 2 * VE;
+    if (edge) {
+      if (tid == 0) sh.xt = token >= 0 && token < a.V ? Elem<T>::load(l + token) : 0.f;
+      const int id = edge_id<VE>(sp, tid);
+      sh.edge[tid] = id < a.V ? Elem<T>::load(l + id) : -INFINITY;
     }
     const float c = a.c, low = -kLpLow / c;
     Lse st{kNegBig, 0.f, 0.f, 0.f};
@@ -589,13 +592,17 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
 
     // the edges
     if (rank == 0) {
+      const float xe = edge ? sh.edge[tid] : -INFINITY;
       if (!(xe <= st.m)) lse_rescale(st, max_nan(st.m, xe), c, low);
       const float y = fmaxf(xe - st.m, low), w = exp2_approx(y * c);
       float er;
       two_sum(st.s, w, st.s, er);
       st.e += er;
       st.d = fmaf(w, y, st.d);
-      if (k > 0) add(xe, ie, ie >= 0 && xe == xe);
+      if (k > 0) {
+        const int id = edge_id<VE>(sp, tid);
+        add(xe, id, edge && id < a.V && xe == xe);
+      }
     }
     // this block's statistics and ranked keys
 #pragma unroll
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
     if (tid == 0) {
       const bool in = token >= 0 && token < a.V;
-      a.out_logp[row] = ok && in ? (xt - r.m) * a.inv_t - lnS : nan;
+      a.out_logp[row] = ok && in ? (sh.xt - r.m) * a.inv_t - lnS : nan;
       if (a.out_entropy) a.out_entropy[row] = ok ? lnS - a.inv_t * (r.d / r.s) : nan;
       const int flags =
           (late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
@@ -679,12 +686,12 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
         atomicOr(a.dev_status, flags);
     }
     if (ok && q != 0 && rk < k) {
-      a.out_ids[row * k + rk] = key_id(q);
-      a.out_top[row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
+      a.out_ids[(int64_t)row * k + rk] = key_id(q);
+      a.out_top[(int64_t)row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
     }
     if (!ok && tid < k) {
-      a.out_ids[row * k + tid] = -1;
-      a.out_top[row * k + tid] = nan;
+      a.out_ids[(int64_t)row * k + tid] = -1;
+      a.out_top[(int64_t)row * k + tid] = nan;
     }
     if (C > 1)
       asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -717,7 +724,7 @@ int launch_logprobs(cudaStream_t s, const LpArgs& a, int C) {
   VT_RETURN_IF_CUDA(
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min<int64_t>(a.R, 152 * kLpPerSm)));
+  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min(a.R, 152 * kLpPerSm)));
   cfg.blockDim = dim3(kLpNT + 32);
   cfg.dynamicSmemBytes = kLpSmem;
   cfg.stream = s;
@@ -759,7 +766,7 @@ extern "C" int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64
     if (st != VT_OK) return st;
   }
   a.logits = logits;
-  a.R = R;
+  a.R = (int)R;
   a.ld = ld_logits;
   a.V = V;
   a.k = k;
