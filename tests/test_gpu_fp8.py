@@ -126,7 +126,12 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (2, 16, 5), (3, 127, 129), (7, 300, 1003), (
           (257, 256, 200), (300, 1500, 1007), (1000, 200, 300), (4096, 64, 140)]
 
 
-@pytest.mark.parametrize("B,H,K", SHAPES)
+# more tiles than CTAs that run at once, with fewer groups than stages and with more
+MANY = [(3, 100, 45000), (3, 900, 41000), (40, 130, 45001), (64, 64, 50000), (100, 200, 45000),
+        (256, 136, 45000), (256, 900, 20003), (300, 64, 30000), (1000, 64, 12000)]
+
+
+@pytest.mark.parametrize("B,H,K", SHAPES + MANY + [(2, 65536, 130), (70, 65536, 130), (130, 20000, 300)])
 def test_logits_integer_inputs_bit_exact(vt, B, H, K):
     g = synthetic.rng(B + H + K, 6)
     hid, W = _ints(g, (B, H)), _ints(g, (K, H))
@@ -197,7 +202,7 @@ def test_misaligned_hidden_and_odd_columns(vt):
 
 # -------------------------------------------------------- drafting on top
 @pytest.mark.parametrize("B,H,K", [(1, 64, 200), (5, 300, 1003), (16, 2048, 4096), (64, 512, 2000),
-                                   (100, 520, 3001), (256, 128, 1300), (300, 256, 700)])
+                                   (100, 520, 3001), (256, 128, 1300), (300, 256, 700)] + MANY)
 def test_greedy_step_integer_inputs_bit_exact(vt, B, H, K):
     g = synthetic.rng(B + H + K, 8)
     hid, W = _ints(g, (B, H)), _ints(g, (K, H))
@@ -213,7 +218,8 @@ def test_greedy_step_integer_inputs_bit_exact(vt, B, H, K):
 
 
 @pytest.mark.parametrize("B,H,K,T", [(1, 256, 1000, 1.0), (16, 512, 3001, 0.7), (130, 200, 700, 1.3),
-                                     (300, 128, 500, 1.0)])
+                                     (300, 128, 500, 1.0), (5, 130, 45000, 1.0), (70, 64, 40001, 0.8),
+                                     (140, 64, 20500, 1.0)])
 def test_sampling_step(vt, B, H, K, T):
     hid, W = synthetic.hidden_states((B, H), seed=3), synthetic.head_weights(K, H, seed=4)
     u = synthetic.uniforms(5, 1, (B,))
@@ -337,3 +343,25 @@ def test_side_stream_and_graph(vt):
         graphs[1].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[i]) and torch.equal(outs[1], want[2 - i])
+
+
+def test_calls_on_two_streams_at_once(vt):
+    # without an order between them; each call has a workspace of its own
+    heads = []
+    for i in range(2):
+        W8, s, _ = vt.vt_quantize_head(torch.randn((5000, 1024), device="cuda").to(torch.bfloat16))
+        heads.append((W8, s))
+    ids = torch.arange(5000, dtype=torch.int32, device="cuda")
+    hid = [torch.randn((b, 1024), device="cuda").to(torch.bfloat16) for b in (9, 200)]
+    u = [torch.rand(b, device="cuda") for b in (9, 200)]
+    want = [vt.vt_draft_step_fp8(hid[i], *heads[i], ids, u[i], 1.0) for i in range(2)]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(vt.vt_draft_step_fp8(hid[i], *heads[i], ids, u[i], 1.0, stream=st[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for q, tok, status in got[i]:
+            assert torch.equal(q, want[i][0]) and torch.equal(tok, want[i][1]) and int(status.item()) == 0

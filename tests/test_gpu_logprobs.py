@@ -235,6 +235,36 @@ def test_side_stream_and_graph(vt):
         assert all(torch.equal(p, q) for p, q in zip(out, w))
 
 
+def test_more_rows_than_blocks_with_gaps(vt):
+    # persistent blocks walk over scored, unscored, flagged and ragged rows in turn
+    R, V = 2000, 20011
+    x = _rows(21, R, V, torch.bfloat16, 5, 1).clone()
+    tok = synthetic.rng(21, 1).integers(0, V, R).astype(np.int64)
+    tok[::3] = -1
+    tok[5] = V
+    x[7, 11] = torch.nan
+    x[10, 40:] = -torch.inf
+    _check(vt, x, tok, 7, 0.9, status=9)
+
+
+def test_temperature_extremes(vt):
+    x = _rows(22, 4, 3000, torch.float32)
+    _check(vt, x, [0, 1, 2, 3], 5, 100.0)
+    _check(vt, x, [0, 1, 2, 3], 5, 0.05)
+    y = x.clone()
+    y[0, ::2] = -torch.inf
+    for T in (1e-30, 1e30):       # the limits: one id, or all that are not masked, alike
+        lp, en, ids, top, st = vt.vt_token_logprobs(y, torch.tensor([1, 1, 2, 3], dtype=torch.int32,
+                                                                    device="cuda"), k=3, temperature=T)
+        assert int(st.item()) == 0
+        if T > 1:
+            want = np.log([1500, 3000, 3000, 3000])
+            assert np.allclose(en.cpu().numpy(), want, atol=1e-4)
+            assert np.allclose(lp.cpu().numpy(), -want, atol=1e-4)
+        else:
+            assert bool((en == 0).all()) and bool((top[:, 0] == 0).all())
+
+
 def test_draft_verify_and_report(vt):
     # the operators as they are used together: quantise the trimmed head, draft a block through it,
     # verify it against the target's logits, report the emitted tokens
