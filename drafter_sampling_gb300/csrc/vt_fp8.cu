@@ -199,6 +199,41 @@ constexpr int kScaleSlots = 8;    // groups whose sx are in shared memory at onc
 // batch row, so one factor sw * sx a group instead of one per column (the
 // factors' shared-memory reads cost as much as the MMAs otherwise).
 
+// z of row j as a key that ascends with z and, at equal z, with descending j
+// (-0 counts as +0); a non-finite z is above all.  No key of a row is 0.
+constexpr uint32_t kKeyNonFinite = 0xffffffffu;
+__device__ __forceinline__ uint64_t greedy_key(float z, int j) {
+  const uint32_t u = __float_as_uint(z + 0.f);
+  const uint32_t o = !isfinite(z) ? kKeyNonFinite : (u >> 31) ? ~u : u | 0x80000000u;
+  return (uint64_t)o << 32 | (uint32_t)~j;
+}
+__device__ __forceinline__ uint64_t max_key(uint64_t x, uint64_t y) { return x > y ? x : y; }
+
+// Folds N columns' keys over the 8 lanes that share lane % 4, halving the
+// columns that a lane holds while it can: lane l ends with the keys of
+// max(1, N / 8) columns, the first of which is returned.
+template <int N>
+__device__ __forceinline__ int fold_keys(uint64_t (&key)[N], int lane) {
+  int first = 0, n = N;
+#pragma unroll
+  for (int o = 16; o >= 4; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        if (j >= n) break;
+        const uint64_t send = up ? key[j] : key[j + n], keep = up ? key[j + n] : key[j];
+        key[j] = max_key(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      }
+      first += up ? n : 0;
+    } else {
+      key[0] = max_key(key[0], __shfl_xor_sync(0xffffffffu, key[0], o));
+    }
+  }
+  return first;
+}
+
 // columns (batch rows) and warps that promote a narrow tile
 template <int BN>
 constexpr int kPartCols = BN < 32 ? BN : 32;  // columns whose partials are reduced at once
@@ -543,6 +578,20 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
       for (int g = tid; g < nk; g += NP) sw_sh[g] = fa.sw[(int64_t)tile * nk + g];
       asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      // greedy: the tile's part of the one-hot q, while the first weights are
+      // on their way; the 1 follows once all tiles are done
+      if (a.greedy) {
+        for (int b = warp; b < a.B; b += kPromWarps) {
+          float* to = a.out + (int64_t)b * a.ldo + m0;
+          if (fa.vec_out && m0 + kBM <= a.K) {
+            reinterpret_cast<float4*>(to)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kBM; e += 32)
+              if (m0 + e + lane < a.K) to[e + lane] = 0.f;
+          }
+        }
+      }
       f32x2 acc[CW / 8][4];  // [column block][row]
 #pragma unroll
       for (int k = 0; k < CW / 8; ++k)
@@ -603,6 +652,41 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + j] = z.y * a.out_scale;
               }
             }
+        }
+      } else if (a.greedy) {
+        // each column's best key: over this thread's rows, the warp's, the tile's
+        uint64_t* best = reinterpret_cast<uint64_t*>(zt);  // [warp][column]
+#pragma unroll
+        for (int c = 0; c < BN; c += PC) {
+          uint64_t key[PC / 4];
+#pragma unroll
+          for (int k = 0; k < PC / 4; ++k) {
+            // seen is NaN once a z is not finite
+            float top = -INFINITY, seen = 0.f;
+            int j = m0 + row0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 zz = unpack2(acc[c / 8 + k / 2][i]);
+              const float z = (k % 2 ? zz.y : zz.x) * a.out_scale;
+              if (m0 + row0 + 8 * i < a.K) {
+                seen = fmaf(z, 0.f, seen);
+                if (z > top) {
+                  top = z;
+                  j = m0 + row0 + 8 * i;
+                }
+              }
+            }
+            key[k] = m0 + row0 < a.K ? greedy_key(top + seen, j) : 0;
+          }
+          const int n = fold_keys(key, lane);
+          best[warp * BN + c + 8 * (n / 2) + cpair + n % 2] = key[0];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+        if (tid < a.B) {
+          uint64_t key = best[tid];
+#pragma unroll
+          for (int w = 1; w < kPromWarps; ++w) key = max_key(key, best[w * BN + tid]);
+          reinterpret_cast<uint64_t*>(a.part)[(int64_t)tile * a.B + tid] = key;
         }
       } else {
 #pragma unroll
@@ -930,11 +1014,12 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // a warp that gave up stores nothing more, but misses no barrier
       if (!ok || nvalid <= 0) continue;
       const int b = b0 + row;
-      // this row's partial over the tile's rows, like tile_partials': greedy,
-      // (largest z, its lowest row), a non-finite z counting as NaN, which wins;
-      // sampling, (max, sum 2^(z - max)), a NaN or +inf z leaving the sum NaN
-      float pm = a.greedy ? -INFINITY : kNegBig, ps = 0.f;
-      int pidx = 0x7fffffff;
+      // this row's partial over the tile's rows: greedy, its best key (the rows
+      // out are q's zeros then); sampling, like tile_partials', (max, sum
+      // 2^(z - max)), a NaN or +inf z leaving the sum NaN
+      float pm = kNegBig, ps = 0.f;
+      uint64_t key = 0;
+      const bool zero = PART && a.greedy;
       // 32 batch rows x 32 columns at a time through shared memory, so that a
       // row's 128 bytes leave in one piece: four rows in an instruction where
       // the output's rows are 16-byte aligned, one otherwise
@@ -955,14 +1040,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           const float* mine = ob + lane * kOutPitch;
           const int some = min(32, nvalid - c);
           if (a.greedy) {
-            for (int i = 0; i < some; ++i) {
-              const float z = mine[i];
-              const float w = isfinite(z) ? z : __int_as_float(0x7fc00000);
-              if (argmax_better(pm, pidx, w, j0 + c + i)) {
-                pm = w;
-                pidx = j0 + c + i;
-              }
-            }
+            for (int i = 0; i < some; ++i) key = max_key(key, greedy_key(mine[i], j0 + c + i));
           } else if (some > 0) {
             float top = pm;
             for (int i = 0; i < some; ++i) top = fmaxf(top, mine[i]);
@@ -976,7 +1054,8 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           float4 t[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            t[r] = *reinterpret_cast<const float4*>(ob + (4 * r + r0) * kOutPitch + col);
+            t[r] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : *reinterpret_cast<const float4*>(ob + (4 * r + r0) * kOutPitch + col);
 #pragma unroll
           for (int r = 0; r < 8; ++r)
             if (4 * r + r0 < rows)
@@ -985,13 +1064,18 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           float* o = out + c + lane;
 #pragma unroll 8
           for (int r = 0; r < 32; ++r) {
-            if (r < rows) *o = ob[r * kOutPitch + lane];
+            if (r < rows) *o = zero ? 0.f : ob[r * kOutPitch + lane];
             o += a.ldo;
           }
         }
       }
-      if (PART && b < a.B)
-        a.part[(int64_t)tile * a.B + b] = make_float2(pm, a.greedy ? __int_as_float(pidx) : ps);
+      if (PART && b < a.B) {
+        const int64_t at = (int64_t)tile * a.B + b;
+        if (a.greedy)
+          reinterpret_cast<uint64_t*>(a.part)[at] = key;
+        else
+          a.part[at] = make_float2(pm, ps);
+      }
     }
     if (!ok && lane == 0) atomicExch(&s_err, 1);
   }
@@ -1118,7 +1202,7 @@ int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp
 }
 
 // z = out_scale * hidden @ (scaled W8)^T; part[tile][b] partials of 128-row
-// tiles (greedy: argmax partials)
+// tiles; greedy, out is q without its ones and part holds each tile's best keys
 int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const uint8_t* W8,
                     int64_t ldw, const float* w_scale, int K, float out_scale, float* out,
                     int64_t ldo, const Fp8Ws& ws, float2* part, int* status, int status_reset,
@@ -1169,6 +1253,36 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
     case 64: return launch_narrow<64>(s, mw, mx, fa);
     default: return paired(Bp) ? launch_wide<true>(s, mw, mx, fa) : launch_wide<false>(s, mw, mx, fa);
   }
+}
+
+// The greedy step's token of a batch row (grid B): the best key of all tiles.
+// The product has left q's zeros, so that only the one is written here; a row
+// with a non-finite z stays all zero and gets the token -1.
+constexpr int kTokenNT = 256;
+__global__ void __launch_bounds__(kTokenNT)
+greedy_token_kernel(const uint64_t* __restrict__ part, int B, int G, int K,
+                    const int* __restrict__ trim_ids, float* __restrict__ q, int64_t ldq,
+                    int* __restrict__ tokens, int64_t ldt, int* __restrict__ status) {
+  __shared__ uint64_t of_warp[kTokenNT / 32];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  griddep_launch_dependents();  // the next kernel waits for this grid before reading
+  griddep_wait();
+  uint64_t key = 0;
+  for (int t = tid; t < G; t += kTokenNT) key = max_key(key, part[(int64_t)t * B + b]);
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
+  if ((tid & 31) == 0) of_warp[tid >> 5] = (uint64_t)hi << 32 | lo;
+  __syncthreads();
+  if (tid != 0) return;
+  key = of_warp[0];
+#pragma unroll
+  for (int w = 1; w < kTokenNT / 32; ++w) key = max_key(key, of_warp[w]);
+  const int j = (int)~(uint32_t)key;
+  const bool ok = (uint32_t)(key >> 32) != kKeyNonFinite && j >= 0 && j < K;
+  if (ok) q[(int64_t)b * ldq + j] = 1.f;
+  tokens[(int64_t)b * ldt] = ok ? trim_ids[j] : -1;
+  if (!ok) atomicOr(status, VT_DEV_NONFINITE);
 }
 
 // T > 0, or T == 0 where greedy drafting is allowed
@@ -1264,7 +1378,23 @@ int vt::draft_step_fp8_impl(const uint16_t* hidden, int32_t B, int32_t H, const 
                                  greedy ? 1.0f : VT_LOG2E / temperature, q, ldq, ws, ws.part,
                                  dev_status, status_reset, greedy ? 1 : 0);
   if (rc != VT_OK) return rc;
-  return draft_finish(s, B, K, greedy, ws.part, (K + umma::kBM - 1) / umma::kBM, umma::kBM,
+  if (greedy) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)B);
+    cfg.blockDim = dim3(kTokenNT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, greedy_token_kernel,
+                                         reinterpret_cast<const uint64_t*>(ws.part), B,
+                                         (K + umma::kBM - 1) / umma::kBM, K, trim_ids, q, ldq,
+                                         tokens, ld_tokens, dev_status));
+    return VT_OK;
+  }
+  return draft_finish(s, B, K, false, ws.part, (K + umma::kBM - 1) / umma::kBM, umma::kBM,
                       uniforms, trim_ids, q, ldq, tokens, ld_tokens, dev_status);
 }
 

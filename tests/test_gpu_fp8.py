@@ -217,6 +217,33 @@ def test_greedy_step_integer_inputs_bit_exact(vt, B, H, K):
     assert np.array_equal(q.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("gap", [0, 1, 4])
+@pytest.mark.parametrize("B,H,K", [(1, 40, 1), (3, 64, 129), (16, 130, 260), (33, 128, 1003), (64, 256, 39000),
+                                   (65, 128, 300), (256, 64, 1028), (130, 72, 515)])
+def test_greedy_step_rows(vt, B, H, K, gap):
+    """Equal, only negative and non-finite logits, in rows with a gap behind them."""
+    g = synthetic.rng(B * K + H, 11)
+    hid, W = _ints(g, (B, H), 1, 3), _ints(g, (K, H), -3, 0)  # every z is negative
+    W[:, 1:] = 0
+    hid[B // 2] = 0                                           # every z is 0: the lowest index
+    bad = sorted({0, B - 1} - {B // 2})
+    ids = np.sort(g.permutation(3 * K)[:K]).astype(np.int32)
+    ref = oracle.draft_step_greedy(hid, W, ids)
+    dirty = hid.copy()
+    for n, b in enumerate(bad):
+        dirty[b, H - 1 - n] = (0x7FC0, 0xFF80)[n]  # NaN, -inf
+    q_all = torch.full((B, K + gap), -7.0, device="cuda")
+    q, tok, st = vt.vt_draft_step_fp8(_bf(dirty), *_head(*fp8.quantize_head(W)), _dev(ids), None, 0.0,
+                                      q=q_all[:, :K])
+    assert int(st.item()) == (vt.VT_DEV_NONFINITE if bad else 0)
+    want, tokens = np.zeros((B, K), np.float32), ref["tokens"].copy()
+    want[np.arange(B), ref["index"]] = 1.0
+    want[bad], tokens[bad] = 0.0, -1
+    assert np.array_equal(q.cpu().numpy(), want)
+    assert np.array_equal(tok.cpu().numpy(), tokens)
+    assert bool((q_all[:, K:] == -7).all())
+
+
 @pytest.mark.parametrize("B,H,K,T", [(1, 256, 1000, 1.0), (16, 512, 3001, 0.7), (130, 200, 700, 1.3),
                                      (300, 128, 500, 1.0), (5, 130, 45000, 1.0), (70, 64, 40001, 0.8),
                                      (140, 64, 20500, 1.0)])
