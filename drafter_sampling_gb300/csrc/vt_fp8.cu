@@ -755,13 +755,91 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
 // values and reads another 64 at a time, more registers than an even split over
 // the block gives, so the third warpgroup gives most of its own to the others:
 // 3 x 168 = 2 x 232 + 40 a thread.
-constexpr int kBatchNP = 256;
-constexpr int kBatchNT = kBatchNP + 128;
-constexpr int kBatchRowsW = 256;   // rows of W8 of an item
-constexpr int kBatchBufs = 2;      // accumulator buffers of 256 columns: all of tensor memory
+constexpr int kBatchNP = 256;                // promoting threads
+constexpr int kBatchNT = kBatchNP + 128;     // and a warpgroup: loads, MMAs, two idle warps
+constexpr int kBatchRowsW = 256;             // rows of W8 of an item: two tiles of 128
+constexpr int kTurn = 4;                     // groups whose scales are handed over at once
+constexpr int kUnit = 32;                    // groups that the tensor cores sum up
+constexpr int kTurns = 4;                    // turns whose scales are in tensor memory at once
+constexpr int kGroupCols = 16;               // tensor-memory columns of a group's scales
 // floats: a warp's 32 x 32 block on its way out; 16-byte accesses by row and by
 // column of eight lanes then meet all banks
 constexpr int kOutPitch = 36;
+
+// MMA whose products of 32 elements are scaled by a power of two per row of A and
+// per row of B: one byte each, the exponent plus 127, in tensor memory (bits 4-5
+// and 29-30 of the descriptor name the byte of a word; all four hold the same
+// here).
+template <bool kTwo>
+__device__ __forceinline__ void mma_e4m3_scaled(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t scale_a, uint32_t scale_b,
+                                                uint32_t accumulate) {
+  if constexpr (kTwo)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(accumulate)
+        : "memory");
+}
+// Its instruction descriptor: e4m3 A and B, both K-major, N >> 3 at bit 17,
+// scales in ue8m0 (bit 23), M >> 7 at bit 27.
+__host__ __device__ constexpr uint32_t idesc_e4m3_scaled(int M, int N) {
+  return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
+}
+// The scales of 128 rows of an operand and one group: row 32 c + l is in lane l
+// of column c, and in the same lane of the other three quarters of the lanes.
+// This writes A's four columns and B's eight, whose rows have one scale per 128.
+__device__ __forceinline__ void tmem_st_scales(uint32_t taddr, const uint32_t (&x)[4], uint32_t w0,
+                                               uint32_t w1) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %5, %5, %5};" ::"r"(taddr),
+      "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(w0)
+      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr + 8),
+               "r"(w1)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// a normal power of two, which ue8m0 holds as the float's exponent bits
+__device__ __forceinline__ bool is_pow2(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x807fffffu) == 0 && u - 0x00800000u < 0x7f000000u;
+}
+// four times the exponent byte of a power of two (or of NaN, which is ue8m0's too)
+__device__ __forceinline__ uint32_t ue8m0x4(float s) {
+  return (__float_as_uint(s) >> 23 & 0xffu) * 0x01010101u;
+}
+// Tensor-memory columns of a turn's scales: those of even and odd turns are where
+// the accumulators of the two halves are in units of one group.
+__device__ __forceinline__ uint32_t scale_cols(int t) {
+  static_assert(kTurns * kTurn * kGroupCols == kBatchRowsW, "they share an accumulator's columns");
+  return (uint32_t)(kBatchRowsW + (t & 1) * 128 + (t % kTurns / 2) * kTurn * kGroupCols);
+}
+// barrier of n threads that also tells whether x holds in all of them
+__device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
 
 // Wide batches: items of 256 rows of W8 x 128 batch rows, or, as a pair of CTAs
 // (TWO), x 256 batch rows with one MMA of 256 x 256: each CTA of a pair stages
@@ -769,34 +847,50 @@ constexpr int kOutPitch = 36;
 // traffic of the same work on one CTA.  The roles are those of
 // head_fp8_kernel; in a pair the first CTA issues the MMAs for both and holds
 // the barriers that they wait on.
-// MMAs into one accumulator buffer stand still while the other is read, so a
-// promoting thread reads its 128 columns in two bursts of 64 and does nothing
-// else meanwhile (four reads of 32 with the arithmetic between them: 189
-// against 165 us at B = 1000, K = 38016, H = 4096).  No register may spill: 24
-// bytes of spills in the loop over the groups cost a tenth of the time.
+//
+// Where all weight scales of an item are powers of two, as this library's
+// quantiser leaves them, the tensor cores scale the products: both scales of a
+// group are then bytes in tensor memory, written by the promoting warps up to
+// four turns of four groups ahead, and a unit of up to 32 groups is summed there
+// before it is read and added to fp32 sums in registers.  The tensor cores hold
+// the running sum in fp32 but cut off, rather than round, each addition: 2.1e-7 of
+// the result (2-norm, H = 4096 and 8192) against 0.7e-7 with units of eight groups
+// or of one, which are slower.  Any other scales: units of one group, not scaled
+// by the tensor cores, in two accumulators (the second where the scales would
+// be), promoted times the scales.
+//
+// What bounds it, at B = 1000, K = 38016, H = 4096 (117 us, 2670 TFLOP/s): a group
+// is 513 cycles of MMAs, about 660 pass, of which 180 are waits for the loads (a
+// pair asks L2 for 64 KB a group; four stages instead of five: 123 us).  MMAs
+// stand still while tensor memory is read, so reading every group's sums took
+// 380 of 890 cycles a group (145 us).  Two accumulators of 128 columns in turn,
+// to hide the reads, made every MMA slower: they read the batch's stage twice,
+// and shared memory has the loads' traffic too (161 us).  A row's 64 instead of
+// 128 bytes out in one piece, for a sixth stage: 127 us.
 template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                  Fp8Args fa) {
   using namespace umma;
   const HeadArgs& a = fa.h;
-  constexpr int NP = kBatchNP;
-  constexpr int kPromWarps = NP / 32;
-  constexpr int NBUF = kBatchBufs;
+  constexpr int kPromWarps = kBatchNP / 32;
   constexpr int NR = kBatchRowsW;
-  constexpr int WR = TWO ? NR / 2 : NR;  // rows of W8 staged by one CTA
-  constexpr int kXBytes = kBM * 128;     // and 128 batch rows
+  constexpr int kXBytes = kBM * 128;      // 128 batch rows
+  constexpr int WR = TWO ? NR / 2 : NR;   // and as many rows of W8
   constexpr int stage_bytes = kXBytes + WR * 128;
-  constexpr uint32_t kCols = NBUF * NR;
+  constexpr int kCtas = TWO ? 2 : 1;
+  constexpr uint32_t kCols = 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
-  __shared__ __align__(8) uint64_t sx_full[kScaleSlots], sx_empty[kScaleSlots];
-  __shared__ __align__(8) uint64_t acc_full[NBUF], acc_empty[NBUF];
+  // [unit & 1]: a unit may be summed; its sums are complete
+  __shared__ __align__(8) uint64_t ready[2], acc_full[2];
+  // [turn % kTurns]: a turn's scales are in tensor memory; its MMAs are done with them
+  __shared__ __align__(8) uint64_t scales_full[kTurns], scales_free[kTurns];
   __shared__ __align__(8) uint64_t done_bar;
-  __shared__ __align__(16) float sx_sh[kScaleSlots][kBM];
-  __shared__ float sw_sh[NR / 128][kMaxGroups];
+  __shared__ float sw_sh[2][2][kMaxGroups];  // [item & 1][half]
+  __shared__ int scaled_sh[2];               // [item & 1]
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_err;
 
@@ -806,21 +900,20 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   const int items = fa.items;
   // this CTA's part of a pair; the items of a CTA or pair: first, first + step ...
   const int part = TWO ? (int)(blockIdx.x & 1) : 0;
-  const int first = TWO ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int step = TWO ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(&sx_full[s], 1);
-      mbar_init(&sx_empty[s], kPromWarps);
-    }
-    for (int p = 0; p < NBUF; ++p) {
+    for (int p = 0; p < 2; ++p) {
+      mbar_init(&ready[p], kPromWarps * kCtas);
       mbar_init(&acc_full[p], 1);
-      mbar_init(&acc_empty[p], kPromWarps * (TWO ? 2 : 1));
+    }
+    for (int p = 0; p < kTurns; ++p) {
+      mbar_init(&scales_full[p], kPromWarps / 2 * kCtas);  // four warps of each CTA
+      mbar_init(&scales_free[p], 1);
     }
     mbar_init(&done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -852,7 +945,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // that quantises the hidden states.  A stage is announced by the (first)
       // CTA, for both, and loaded by each.
       auto announce = [&](int s) {
-        if (part == 0) mbar_expect_tx(&full_bar[s], (uint32_t)(stage_bytes * (TWO ? 2 : 1)));
+        if (part == 0) mbar_expect_tx(&full_bar[s], (uint32_t)(stage_bytes * kCtas));
       };
       auto load = [&](void* dst, const CUtensorMap* map, int x, int y, int s) {
         if constexpr (TWO)
@@ -860,53 +953,43 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         else
           tma_load_2d(dst, map, x, y, &full_bar[s]);
       };
+      auto load_w = [&](int s, int g, int blk) {
+        load(smem + (size_t)s * stage_bytes + kXBytes, &map_w, g * 128, blk * NR + part * WR, s);
+      };
       const int pre = min(S, nk);
       if (leader) {
         const int blk = first / fa.nchunk;
         int g = blk % nk;
         for (int kb = 0; kb < pre; ++kb) {
           announce(kb);
-          load(smem + (size_t)kb * stage_bytes + kXBytes, &map_w, g * 128, blk * NR + part * WR, kb);
+          load_w(kb, g, blk);
           g = g + 1 == nk ? 0 : g + 1;
         }
       }
       griddep_wait();
-      int it = 0;                       // groups requested so far
-      int s = 0, q = 0;                 // stage and scale slot of the next one
-      uint32_t sphase = 1, qphase = 1;  // parity that says they are free
+      int it = 0;           // groups requested so far
+      int s = 0;            // stage of the next one
+      uint32_t sphase = 1;  // parity that says it is free
       bool ok = true;
       for (int item = first; item < items && ok; item += step) {
         const int blk = item / fa.nchunk;
-        const int b0 = (item - blk * fa.nchunk) * (TWO ? 2 * kBM : kBM) + part * kBM;
+        const int b0 = (item - blk * fa.nchunk) * kCtas * kBM + part * kBM;
         int g = blk % nk;
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          uint8_t* st = smem + (size_t)s * stage_bytes;
           if (it >= pre) {
             // a fresh barrier counts as having completed the phase before
             ok = mbar_wait(&empty_bar[s], sphase);
             if (!ok) break;
             if (leader) {
               announce(s);
-              load(st + kXBytes, &map_w, g * 128, blk * NR + part * WR, s);
+              load_w(s, g, blk);
             }
           }
-          if (leader) load(st, &map_x, g * 128, b0, s);
-          ok = mbar_wait(&sx_empty[q], qphase);
-          if (!ok) {
-            ++it;
-            break;
-          }
-          if (leader) {
-            mbar_expect_tx(&sx_full[q], kBM * 4);
-            bulk_load(sx_sh[q], fa.sx + (int64_t)g * fa.Bp + b0, kBM * 4, &sx_full[q]);
-          }
+          if (leader)
+            load(smem + (size_t)s * stage_bytes, &map_x, g * 128, b0, s);
           if (++s == S) {
             s = 0;
             sphase ^= 1;
-          }
-          if (++q == kScaleSlots) {
-            q = 0;
-            qphase ^= 1;
           }
           g = g + 1 == nk ? 0 : g + 1;
         }
@@ -916,11 +999,10 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // second CTA: the first waits for its copies too, and it for the first)
       if (part == 0)
         for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
-      for (int k = max(0, it - kScaleSlots); k < it; ++k)
-        mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
     } else if (warp == kPromWarps + 1 && part == 0) {
       // MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3(TWO ? 2 * kBM : kBM, NR);
+      constexpr uint32_t idesc = idesc_e4m3(kCtas * kBM, NR);
+      constexpr uint32_t idesc_scaled = idesc_e4m3_scaled(kCtas * kBM, NR);
       auto commit = [&](uint64_t* bar) {
         if constexpr (TWO)
           pair_commit(bar);
@@ -928,89 +1010,207 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           mma_commit(bar);
       };
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
-      int s = 0, p = 0;
-      uint32_t sphase = 0, pphase = 1;
+      int u = 0, t = 0, s = 0;  // units and turns so far; the next group's stage
+      uint32_t sphase = 0;
       bool ok = true;
-      for (int item = first; item < items && ok; item += step)
-        for (int kb = 0; kb < nk; ++kb) {
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&full_bar[s], sphase) && mbar_wait(&acc_empty[p], pphase)) != 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+      };
+      int at = 0;
+      for (int item = first; item < items && ok; item += step, at ^= 1) {
+        bool scaled = false;
+        for (int k = 0; k < nk && ok;) {
+          wait(&ready[u & 1], (u >> 1) & 1);
           if (!ok) break;
-          fence_after_sync();
-          if (leader) {
-            const uint64_t xdesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
-            const uint64_t wdesc = xdesc + (kXBytes >> 4);
+          if (k == 0) scaled = scaled_sh[at] != 0;
+          const int end = scaled ? min(nk, k + kUnit) : k + 1;
+          const uint32_t acc = tmem + (scaled ? 0u : (uint32_t)((u & 1) * NR));
+          uint32_t add = 0;
+          for (; k < end; ++k) {
+            if (scaled && k % kTurn == 0) wait(&scales_full[t % kTurns], t / kTurns & 1);
+            if (ok) wait(&full_bar[s], sphase);
+            if (!ok) break;
+            fence_after_sync();
+            const uint32_t scales = tmem + scale_cols(t) + (uint32_t)(k % kTurn * kGroupCols);
+            const bool turn_ends = scaled && (k % kTurn == kTurn - 1 || k + 1 == nk);
+            if (leader) {
+              const uint64_t xdesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
+              const uint64_t wdesc = xdesc + (kXBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
-              mma_e4m3<TWO>(tmem + (uint32_t)(p * NR), xdesc + 2 * kk, wdesc + 2 * kk, idesc,
-                            kk > 0 ? 1u : 0u);
-            commit(&empty_bar[s]);
-            commit(&acc_full[p]);
+              for (int kk = 0; kk < 4; ++kk) {  // 32 elements = 32 bytes per step
+                if (scaled)
+                  mma_e4m3_scaled<TWO>(acc, xdesc + 2 * kk, wdesc + 2 * kk, idesc_scaled, scales,
+                                       scales + 4, add);
+                else
+                  mma_e4m3<TWO>(acc, xdesc + 2 * kk, wdesc + 2 * kk, idesc, add);
+                add = 1;
+              }
+              commit(&empty_bar[s]);
+              if (turn_ends) commit(&scales_free[t % kTurns]);
+            }
+            if (turn_ends) ++t;
+            if (++s == S) {
+              s = 0;
+              sphase ^= 1;
+            }
           }
-          if (++s == S) {
-            s = 0;
-            sphase ^= 1;
-          }
-          if (++p == NBUF) {
-            p = 0;
-            pphase ^= 1;
-          }
+          if (ok && leader) commit(&acc_full[u & 1]);
+          ++u;
         }
+      }
       if (!ok) atomicExch(&s_err, 1);
       if (leader) commit(&done_bar);
     }
   } else {
     regs_take<232>();
-    griddep_wait();
     // this thread's batch row (TMEM lane) and its half of the W8 rows
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
     float* ob = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes) + warp * 32 * kOutPitch;  // 16-byte aligned
-    int it = 0;
+    int u = 0, t = 0;  // units read, and turns whose scales have been written, so far
     bool ok = true;
+    auto chunk_of = [&](int item) { return (item - item / fa.nchunk * fa.nchunk) * kCtas * kBM + part * kBM; };
+    // one of this warp's arrivals, once its accesses to tensor memory are complete
+    auto give = [&](uint64_t* bar) {
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (!TWO || part == 0)
+          mbar_arrive(bar);
+        else
+          remote_arrive(first_cta(bar));
+      }
+    };
+    // an item's weight scales; whether all are powers of two
+    auto fetch = [&](int item, int at) {
+      const int tile = item / fa.nchunk * (NR / 128) + half;
+      bool two = true;
+      for (int g = tid & 127; g < nk; g += 128) {
+        const float s = tile * 128 < a.K ? fa.sw[(uint32_t)(tile * nk + g)] : 1.f;
+        two = two && is_pow2(s);
+        sw_sh[at][half][g] = s;
+      }
+      return barrier_and(1, kBatchNP, two);
+    };
+    // The scales of the next turn, of up to n groups from group g on.  Turns
+    // alternate between the two halves' warps, each of which writes where its own
+    // accumulator is in units of one group.
+    auto put_scales = [&](int b0, int at, int g, int n) {
+      if ((t & 1) == half) {
+        float x[kTurn][4], w[kTurn][2];  // loaded together, groups past n too
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+          const float* sx = fa.sx + (uint32_t)(g * fa.Bp + b0 + lane);  // B <= 4096, 512 groups
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[i][c] = sx[32 * c];
+          w[i][0] = sw_sh[at][0][g];
+          w[i][1] = sw_sh[at][1][g];
+          g = g + 1 == nk ? 0 : g + 1;
+        }
+        // a fresh barrier counts as having completed the phase before
+        ok = __all_sync(0xffffffffu, mbar_wait(&scales_free[t % kTurns], (t / kTurns & 1) ^ 1)) != 0;
+        fence_after_sync();
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < kTurn; ++i) {
+            uint32_t xb[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) xb[c] = ue8m0x4(x[i][c]);
+            if (i < n)
+              tmem_st_scales(tmem + ((uint32_t)(quad * 32) << 16) + scale_cols(t) + (uint32_t)(kGroupCols * i),
+                             xb, ue8m0x4(w[i][0]), ue8m0x4(w[i][1]));
+          }
+          tmem_st_wait();
+          give(&scales_full[t % kTurns]);
+        }
+      }
+      ++t;
+    };
+    int at = 0;
+    bool scaled = false;
+    if (first < items) {
+      scaled = fetch(first, 0);  // like the weights, before the wait
+      if (part == 0 && tid == 0) scaled_sh[0] = scaled;
+      give(&ready[0]);
+      if (!scaled && nk > 1) give(&ready[1]);
+    }
+    griddep_wait();
+    int ahead = 0;  // groups of the item whose scales have been written
     for (int item = first; item < items; item += step) {
-      const int blk = item / fa.nchunk;
-      const int b0 = (item - blk * fa.nchunk) * (TWO ? 2 * kBM : kBM) + part * kBM;
+      const int blk = item / fa.nchunk, b0 = chunk_of(item);
       const int tile = blk * (NR / 128) + half, j0 = tile * 128;  // 128-row tile of W8
       const int nvalid = min(128, a.K - j0);                      // <= 0: past the end
-      // the last item's weights' scales have been read by all
-      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
-      for (int g = tid & 127; g < nk; g += 128)
-        sw_sh[half][g] = nvalid > 0 ? fa.sw[(int64_t)tile * nk + g] : 0.f;
-      asm volatile("bar.sync 1, %0;" ::"n"(NP) : "memory");
+      const int next = item + step;
+      int g = blk % nk;                                           // of group `kb`, or `ahead`
+      if (scaled) {
+        for (; ahead < min(nk, kTurns * kTurn) && ok; ahead += kTurn) {
+          int ga = g + ahead;
+          if (ga >= nk) ga -= nk;
+          put_scales(b0, at, ga, nk - ahead);
+        }
+        g += ahead;
+        if (g >= nk) g -= nk;
+      }
+      // the last item's scales have been read by all
+      asm volatile("bar.sync 1, %0;" ::"n"(kBatchNP) : "memory");
+      const bool next_scaled = next < items && fetch(next, at ^ 1);
       f32x2 acc[64];  // sums of this batch row and 128 rows of W8
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      int g = blk % nk;
-      for (int kb = 0; kb < nk && ok; ++kb, ++it) {
-        const int q = it % kScaleSlots, p = it % NBUF;
-        ok = mbar_wait(&sx_full[q], (it / kScaleSlots) & 1) &&
-             mbar_wait(&acc_full[p], (it / NBUF) & 1);
-        ok = __all_sync(0xffffffffu, ok) != 0;
+      for (int kb = 0; kb < nk && ok;) {
+        const int end = scaled ? min(nk, kb + kUnit) : kb + 1;
+        float factor = 1.f;
+        if (scaled) {
+          // those of the next unit's first turns too
+          for (; ahead < min(nk, end + kTurns * kTurn) && ok; ahead += kTurn) {
+            put_scales(b0, at, g, nk - ahead);
+            g += kTurn;
+            if (g >= nk) g -= nk;
+          }
+          if (!ok) break;
+        } else {
+          factor = sw_sh[at][half][g] * fa.sx[(uint32_t)(g * fa.Bp + b0 + row)];
+          g = g + 1 == nk ? 0 : g + 1;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[u & 1], (u >> 1) & 1)) != 0;
         if (!ok) break;
         fence_after_sync();
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(p * NR + half * 128);
-        const uint32_t fb = __float_as_uint(sw_sh[half][g] * sx_sh[q][row]);
+        const uint32_t taddr = lanes + (scaled ? 0u : (uint32_t)((u & 1) * NR));
+        const uint32_t fb = __float_as_uint(factor);
         const f32x2 f = pack2(fb, fb);
-        g = g + 1 == nk ? 0 : g + 1;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[64];
-          tmem_ld64(taddr + 64 * c, v);
-          if (c == 1) {  // all of this warp's columns are in registers
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (TWO)
-                remote_arrive(first_cta(&acc_empty[p]));
-              else
-                mbar_arrive(&acc_empty[p]);
-              mbar_arrive(&sx_empty[q]);
-            }
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(taddr + 32 * c, v);
+          // all of this warp's columns are in registers: on to the next unit
+          if (c == 3) {
+            if (scaled ? end < nk : kb + 2 < nk) give(&ready[(scaled ? u + 1 : u) & 1]);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) fma2(acc[32 * c + e], pack2(v[2 * e], v[2 * e + 1]), f);
+          for (int e = 0; e < 16; ++e)
+            fma2(acc[16 * c + e], pack2(__float_as_uint(v[2 * e]), __float_as_uint(v[2 * e + 1])), f);
+        }
+        ++u;
+        kb = end;
+      }
+      // the next item's sums start while this one's rows go out
+      ahead = 0;
+      if (ok && next < items) {
+        if (part == 0 && tid == 0) scaled_sh[at ^ 1] = next_scaled;
+        give(&ready[u & 1]);
+        if (!next_scaled && nk > 1) give(&ready[(u + 1) & 1]);
+        if (next_scaled) {
+          const int bn = chunk_of(next);
+          int gn = next / fa.nchunk % nk;
+          for (; ahead < min(nk, kTurns * kTurn) && ok; ahead += kTurn) {
+            put_scales(bn, at ^ 1, gn, nk - ahead);
+            gn += kTurn;
+            if (gn >= nk) gn -= nk;
+          }
         }
       }
+      at ^= 1;
+      scaled = next_scaled;
       // a warp that gave up stores nothing more, but misses no barrier
       if (!ok || nvalid <= 0) continue;
       const int b = b0 + row;
@@ -1028,6 +1228,14 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         __syncwarp();
+        // the MMAs may be through with the next item's first turns
+        if (!PART && c > 0 && scaled && ahead > 0 && ahead < nk) {
+          const int chunk = chunk_of(next);
+          int ga = next / fa.nchunk % nk + ahead;
+          if (ga >= nk) ga -= nk;
+          put_scales(chunk, at, ga, nk - ahead);
+          ahead += kTurn;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 x = unpack2(acc[c / 2 + 2 * i]), y = unpack2(acc[c / 2 + 2 * i + 1]);
@@ -1106,9 +1314,8 @@ struct Fp8Ws {
 
 int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : (B + 127) / 128 * 128; }
 
-// Wide batches of an even number of 128-row chunks go to pairs of CTAs (B = 256,
-// K = 38016, H = 4096: 46.8 against 48.9 us on single CTAs, in one process), an
-// odd number to single ones (B = 300: 64.6 us against 83.4 padded to pairs).
+// Wide batches of an even number of 128-row chunks go to pairs of CTAs, an odd
+// number to single ones
 bool paired(int Bp) { return Bp % 256 == 0; }
 
 Fp8Ws carve_fp8(void* base, int B, int H, int K) {
@@ -1190,12 +1397,11 @@ int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, 
 
 template <bool TWO>
 int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
-  constexpr int stage = umma::kBM * 128 + (TWO ? 128 : 256) * 128;
+  constexpr int stage = umma::kBM * 128 + (TWO ? 128 : 256) * 128, ctas = TWO ? 2 : 1;
   constexpr size_t out = (size_t)(kBatchNP / 32) * 32 * kOutPitch * sizeof(float);
   fa.h.stages = 160 * 1024 / stage;  // five of a pair, three of a single CTA
-  fa.nchunk = fa.Bp / (TWO ? 256 : 128);
+  fa.nchunk = fa.Bp / (128 * ctas);
   fa.items = (fa.h.K + kBatchRowsW - 1) / kBatchRowsW * fa.nchunk;
-  const int ctas = TWO ? 2 : 1;
   return launch_product(s, fa.h.part != nullptr ? batch_fp8_kernel<TWO, true> : batch_fp8_kernel<TWO, false>,
                         ctas * std::min(fa.items, kSms / ctas), kBatchNT,
                         (size_t)fa.h.stages * stage + out + 1024, ctas, mw, mx, fa);

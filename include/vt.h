@@ -400,11 +400,14 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
  * x8, sx are the hidden states quantised inside the call by the rule above
  * per row and group.  A group's products are summed by the tensor cores and
  * its sum enters the fp32 sum over the groups times its two scales, so
- * w_scale may hold any finite fp32 values, not only powers of two.  A row of
- * hidden states with a NaN or an infinity gives NaN logits in that row.
+ * w_scale may hold any finite fp32 values, not only powers of two.  For more
+ * than 64 rows, blocks of 256 rows of W8 whose scales are all powers of two
+ * are faster: the tensor cores apply both scales and sum up to 32 groups (in
+ * fp32, cutting off instead of rounding).  A row of hidden states with a NaN
+ * or an infinity gives NaN logits in that row.
  * hidden, logits, trim_ids, uniforms, q, tokens and the temperature are as
  * there; W8, ldw and w_scale as vt_quantize_head leaves them.  Like W_trim,
- * W8 must not be written by a kernel that may still be running when the
+ * W8 and w_scale must not be written by a kernel that may still be running when the
  * call's first kernel starts and that triggers its dependents early.
  * Workspace: vt_draft_fp8_workspace_bytes(B, H, K) bytes, or
  * vt_draft_topk_fp8_workspace_bytes(B, H, K, k) for the top-k.

@@ -141,6 +141,24 @@ def test_logits_integer_inputs_bit_exact(vt, B, H, K):
     assert np.array_equal(z.cpu().numpy().astype(np.float64), want)
 
 
+@pytest.mark.parametrize("every", [1, 2, 3, 1000])
+@pytest.mark.parametrize("B,H,K", [(16, 300, 1000), (130, 300, 41000), (256, 130, 40100), (256, 4225, 700),
+                                   (300, 128, 20000), (1000, 640, 10500)])
+def test_logits_mixed_scales_bit_exact(vt, B, H, K, every):
+    """Some blocks of rows have a scale that is no power of two, others none; all sums are exact."""
+    g = synthetic.rng(B + H + K, 12)
+    hid, W = _ints(g, (B, H)), _ints(g, (K, H))
+    codes, scale = fp8.quantize_head(W)
+    scale = scale.copy()
+    rows = np.arange(scale.shape[0])[::every]
+    scale[rows, rows % scale.shape[1]] *= 1.5
+    scale[rows[1::3], 0] *= -0.75
+    z, again = (vt.vt_draft_logits_fp8(_bf(hid), *_head(codes, scale), 0.5) for _ in range(2))
+    ref, _ = fp8.draft_logits_fp8(hid, codes, scale, 0.5)
+    assert np.array_equal(z.cpu().numpy(), ref.astype(np.float32))
+    assert torch.equal(z, again)
+
+
 @pytest.mark.parametrize("B,H,K", [s for s in SHAPES if s[0] <= 300])
 def test_logits_random_inputs(vt, B, H, K):
     hid = synthetic.hidden_states((B, H), seed=B + K)
