@@ -1387,10 +1387,16 @@ int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, 
   constexpr int stage = umma::kABytes + BN * 128;
   constexpr size_t kZt =
       (size_t)kPartCols<BN> * umma::zt_pitch<kPartCols<BN>, kNarrowNP>() * sizeof(float);
-  const size_t zt = fa.h.part != nullptr ? kZt : 0;
-  // two CTAs per SM
-  fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((96 * 1024 - zt) / stage)));
+  const size_t zt = fa.h.part == nullptr ? 0
+                    : fa.h.greedy        ? (size_t)kNarrowNP / 32 * BN * sizeof(uint64_t)
+                                         : kZt;
   fa.items = (fa.h.K + umma::kBM - 1) / umma::kBM;
+  // Two CTAs per SM.  Where no SM gets a second tile, a tile of 64 columns has a
+  // longer ring (B = 50, K = 10007, H = 1500, greedy: 11.6 against 12.9 us; B = 64,
+  // K = 19000, H = 4096: 19.0 against 20.0); with fewer columns that was slower by
+  // up to 4%, the next call's product then starting later.
+  const int ring = (fa.items > kSms || BN < 64 ? 96 : 150) * 1024;
+  fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((ring - zt) / stage)));
   return launch_product(s, head_fp8_kernel<BN>, std::min(fa.items, 2 * kSms), kNarrowNT,
                         (size_t)fa.h.stages * stage + zt + 1024, 1, mw, mx, fa);
 }
