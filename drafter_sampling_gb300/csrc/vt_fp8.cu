@@ -87,7 +87,9 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ W, int
 
 // One CTA per 128 x 128 block: the block is read once (eight 16-byte loads
 // in flight per thread), its largest magnitude reduced, and the registers
-// scaled, rounded and stored.  HBM-bound: 2 bytes read, 1 written per weight.
+// scaled, rounded and stored.  HBM-bound: 2 bytes read, 1 written per weight
+// (K = 128256, H = 4096: 219 us, 7.2 TB/s; K = 32768, H = 2048: 32 us, 6.3 TB/s;
+// rows that are read by shifted words, H = 2047: 53 us).
 __global__ void __launch_bounds__(kQuantNT)
 quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __restrict__ W8,
                      int64_t ldw, float* __restrict__ w_scale, int* __restrict__ dev_status,
@@ -142,7 +144,8 @@ quantize_head_kernel(const uint16_t* __restrict__ W, int K, int H, uint8_t* __re
 // Quantises hidden [B, H] to x8 [B, ldx] (columns H..ldx zero) and sx
 // [groups][Bp] (rows B..Bp zero), one warp per (row, group of 128 columns).
 // A group with a NaN or an infinity gets the scale NaN, so that row's logits
-// are NaN.
+// are NaN.  The product starts over it and loads weights meanwhile, so that it
+// adds 0.3 to 0.5 us to a call of 16 rows.
 __global__ void __launch_bounds__(256)
 quantize_hidden_kernel(const uint16_t* __restrict__ hidden, int B, int H, uint8_t* __restrict__ x8,
                        int ldx, float* __restrict__ sx, int Bp, int groups, int vec_ok,
@@ -336,6 +339,9 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ void add2(f32x2& acc, f32x2 a) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(a));
+}
 __device__ __forceinline__ void fma2(f32x2& acc, f32x2 a, f32x2 b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
@@ -394,9 +400,9 @@ __device__ __forceinline__ void regs_take() {
 }
 
 // Narrow batches: tiles of 128 rows of W8, taken by a persistent CTA one after
-// another, with the batch (BN rows) as the N operand.  Each group of 128 reduction columns is one
-// shared-memory stage (W8 128 x 128 bytes, x8 BN x 128 bytes, both K-major
-// with the 128-byte swizzle) and one tcgen05 accumulation of four K = 32 steps
+// another, with the batch (BN rows) as the N operand.  Each group of 128
+// reduction columns is one shared-memory stage (W8 128 x 128 bytes, x8 BN x 128
+// bytes, both K-major with the 128-byte swizzle) and one tcgen05 accumulation of four K = 32 steps
 // into one of the tensor-memory buffers.  The promoting warps read each
 // finished buffer, give it back at once, and add it, times sw * sx, to fp32
 // sums in registers: the scales of a group multiply its partial sum only, and
@@ -404,6 +410,14 @@ __device__ __forceinline__ void regs_take() {
 // loads (and the copies of sx, in a ring of its own, so that a stage is free
 // as soon as its MMAs are done) and one the MMAs; both run ahead into the next
 // tile while the promoting warps store the last one.
+//
+// Bound by HBM and by how a call starts: B = 16, K = 32768, H = 2048 takes 13.7 us
+// (5.0 TB/s; the weights alone are 9.9), of which 1.5 are the launch, 2.3 pass
+// from the first request for weights to the first MMA, 7 are the stream (6.7 of
+// HBM at its copy rate) and 0.6 the last tile's rows.  B = 1: 13.6, B = 64: 15.6.
+// One row and all columns per promoting thread, rather than four rows and a
+// quarter of the columns, cost as much time in broadcast reads of the columns'
+// scales as the MMAs take.  One CTA per SM with twice the ring: 16.3.
 template <int BN>
 __global__ void __launch_bounds__(kNarrowNT, 2)
 head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -723,36 +737,9 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   if (warp == kPromWarps + 1) tmem_dealloc(tmem, kCols);
 }
 
-// 64 consecutive columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "
-      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, "
-      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
-        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
-        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
-        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  // no use of the registers can precede the wait
-#pragma unroll
-  for (int e = 0; e < 64; ++e) asm volatile("" : "+r"(r[e])::"memory");
-}
-
 // Threads of batch_fp8_kernel: two promoting warpgroups, and a third of which
 // one warp issues the loads and one the MMAs.  A promoting thread sums 128
-// values and reads another 64 at a time, more registers than an even split over
+// values and reads another 32 at a time, more registers than an even split over
 // the block gives, so the third warpgroup gives most of its own to the others:
 // 3 x 168 = 2 x 232 + 40 a thread.
 constexpr int kBatchNP = 256;                // promoting threads
@@ -859,14 +846,14 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
 // by the tensor cores, in two accumulators (the second where the scales would
 // be), promoted times the scales.
 //
-// What bounds it, at B = 1000, K = 38016, H = 4096 (117 us, 2670 TFLOP/s): a group
+// What bounds it, at B = 1000, K = 38016, H = 4096 (117 us, 2660 TFLOP/s): a group
 // is 513 cycles of MMAs, about 660 pass, of which 180 are waits for the loads (a
-// pair asks L2 for 64 KB a group; four stages instead of five: 123 us).  MMAs
-// stand still while tensor memory is read, so reading every group's sums took
-// 380 of 890 cycles a group (145 us).  Two accumulators of 128 columns in turn,
-// to hide the reads, made every MMA slower: they read the batch's stage twice,
-// and shared memory has the loads' traffic too (161 us).  A row's 64 instead of
-// 128 bytes out in one piece, for a sixth stage: 127 us.
+// pair asks L2 for 64 KB a group; four stages instead of five: 123 us).  Other
+// scales: 195 us, as MMAs stand still while tensor memory is read, some 380 cycles
+// for a group's sums (B = 256: 53 against 41).  Two accumulators of 128 columns in
+// turn, to hide the reads, made every MMA slower: they read the batch's stage
+// twice, and shared memory has the loads' traffic too (161 us).  A row's 64
+// instead of 128 bytes out in one piece, for a sixth stage: 127 us.
 template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -1157,41 +1144,52 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       f32x2 acc[64];  // sums of this batch row and 128 rows of W8
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      for (int kb = 0; kb < nk && ok;) {
-        const int end = scaled ? min(nk, kb + kUnit) : kb + 1;
-        float factor = 1.f;
-        if (scaled) {
-          // those of the next unit's first turns too
-          for (; ahead < min(nk, end + kTurns * kTurn) && ok; ahead += kTurn) {
+      if (scaled) {
+        for (int kb = 0; kb < nk && ok; kb += kUnit) {
+          // with the scales of the next unit's first turns
+          const int upto = min(nk, kb + kUnit + kTurns * kTurn);
+          for (; ahead < upto && ok; ahead += kTurn) {
             put_scales(b0, at, g, nk - ahead);
             g += kTurn;
             if (g >= nk) g -= nk;
           }
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[u & 1], (u >> 1) & 1)) != 0;
           if (!ok) break;
-        } else {
-          factor = sw_sh[at][half][g] * fa.sx[(uint32_t)(g * fa.Bp + b0 + row)];
-          g = g + 1 == nk ? 0 : g + 1;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[u & 1], (u >> 1) & 1)) != 0;
-        if (!ok) break;
-        fence_after_sync();
-        const uint32_t taddr = lanes + (scaled ? 0u : (uint32_t)((u & 1) * NR));
-        const uint32_t fb = __float_as_uint(factor);
-        const f32x2 f = pack2(fb, fb);
+          fence_after_sync();
+          ++u;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(taddr + 32 * c, v);
-          // all of this warp's columns are in registers: on to the next unit
-          if (c == 3) {
-            if (scaled ? end < nk : kb + 2 < nk) give(&ready[(scaled ? u + 1 : u) & 1]);
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(lanes + 32 * c, v);
+            // all of this warp's columns are in registers: on to the next unit
+            if (c == 3 && kb + kUnit < nk) give(&ready[u & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              add2(acc[16 * c + e], pack2(__float_as_uint(v[2 * e]), __float_as_uint(v[2 * e + 1])));
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            fma2(acc[16 * c + e], pack2(__float_as_uint(v[2 * e]), __float_as_uint(v[2 * e + 1])), f);
         }
-        ++u;
-        kb = end;
+      } else {
+        float sx = fa.sx[(uint32_t)(g * fa.Bp + b0 + row)];
+        for (int kb = 0; kb < nk; ++kb, ++u) {
+          const uint32_t fb = __float_as_uint(sw_sh[at][half][g] * sx);
+          const f32x2 f = pack2(fb, fb);
+          g = g + 1 == nk ? 0 : g + 1;
+          sx = fa.sx[(uint32_t)(g * fa.Bp + b0 + row)];  // the next group's
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[u & 1], (u >> 1) & 1)) != 0;
+          if (!ok) break;
+          fence_after_sync();
+          const uint32_t taddr = lanes + (uint32_t)((u & 1) * NR);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(taddr + 32 * c, v);
+            // all of this warp's columns are in registers: on to the next group but one
+            if (c == 3 && kb + 2 < nk) give(&ready[u & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              fma2(acc[16 * c + e], pack2(__float_as_uint(v[2 * e]), __float_as_uint(v[2 * e + 1])), f);
+          }
+        }
       }
       // the next item's sums start while this one's rows go out
       ahead = 0;
@@ -1315,7 +1313,8 @@ struct Fp8Ws {
 int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : (B + 127) / 128 * 128; }
 
 // Wide batches of an even number of 128-row chunks go to pairs of CTAs, an odd
-// number to single ones
+// number to single ones (K = 38016, H = 4096, B = 300: 60.5 us against 62.0 padded
+// to pairs; K = 32768, H = 2048, B = 128: 18.9 against 23.4)
 bool paired(int Bp) { return Bp % 256 == 0; }
 
 Fp8Ws carve_fp8(void* base, int B, int H, int K) {
@@ -1469,7 +1468,9 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
 
 // The greedy step's token of a batch row (grid B): the best key of all tiles.
 // The product has left q's zeros, so that only the one is written here; a row
-// with a non-finite z stays all zero and gets the token -1.
+// with a non-finite z stays all zero and gets the token -1.  Bound by its latency:
+// the step takes 2.4 us more than the logits at B = 16, K = 32768, H = 2048 (3.8
+// when all of q was written behind the product, and 7.5 at B = 64).
 constexpr int kTokenNT = 256;
 __global__ void __launch_bounds__(kTokenNT)
 greedy_token_kernel(const uint64_t* __restrict__ part, int B, int G, int K,
