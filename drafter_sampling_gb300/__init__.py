@@ -579,7 +579,8 @@ def vt_quantize_head(W, W8=None, w_scale=None, dev_status=None, stream=None):
 def vt_draft_logits_fp8(hidden, W8, w_scale, temperature: float = 1.0, logits=None, workspace=None,
                         stream=None):
     """vt_draft_logits through an e4m3 head (vt_quantize_head); the hidden
-    states are quantised inside the call."""
+    states are quantised inside the call.  w_scale may hold any finite values;
+    with more than 64 rows, powers of two are faster."""
     dev = _first(hidden, "hidden")
     K, H, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
     B, hp = _hidden(hidden, H, dev)
@@ -667,7 +668,8 @@ def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_
     """Log probabilities of given tokens under rows of logits.
 
     logits [R, V] or [B, R, V], float32 or bf16, unit inner stride and evenly
-    spaced rows; tokens int32 of logits' leading shape, -1 = row not scored.
+    spaced rows; tokens int32 of logits' leading shape, contiguous, -1 = row
+    not scored.  All tensors are on the current device.
     Returns (logp, entropy or None, top_ids, top_logp, dev_status), logp and
     entropy of tokens' shape, top_ids int32 and top_logp [..., k] (None where
     k == 0): the k best ids, ties to the lower, with their log probabilities.

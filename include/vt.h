@@ -407,8 +407,8 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
  * or an infinity gives NaN logits in that row.
  * hidden, logits, trim_ids, uniforms, q, tokens and the temperature are as
  * there; W8, ldw and w_scale as vt_quantize_head leaves them.  Like W_trim,
- * W8 and w_scale must not be written by a kernel that may still be running when the
- * call's first kernel starts and that triggers its dependents early.
+ * W8 and w_scale must not be written by a kernel that may still be running
+ * when the call's first kernel starts and that triggers its dependents early.
  * Workspace: vt_draft_fp8_workspace_bytes(B, H, K) bytes, or
  * vt_draft_topk_fp8_workspace_bytes(B, H, K, k) for the top-k.
  * ---------------------------------------------------------------------- */
