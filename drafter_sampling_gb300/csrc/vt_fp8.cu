@@ -888,6 +888,12 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   // this CTA's part of a pair; the items of a CTA or pair: first, first + step ...
   const int part = TWO ? (int)(blockIdx.x & 1) : 0;
   const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
+  // the first item's weight scales come from HBM while the block is set up
+  {
+    const int tile = first / fa.nchunk * (NR / 128) + (tid >> 7), g = 32 * (tid & 127);
+    if (tid < kBatchNP && tile * 128 < a.K && g < nk)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(fa.sw + (uint32_t)(tile * nk + g)));
+  }
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
