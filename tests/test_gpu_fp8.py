@@ -410,3 +410,33 @@ def test_calls_on_two_streams_at_once(vt):
     for i in range(2):
         for q, tok, status in got[i]:
             assert torch.equal(q, want[i][0]) and torch.equal(tok, want[i][1]) and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("B,H,K", [(50, 300, 1003), (130, 300, 20000), (256, 4300, 21000)])
+def test_wide_and_greedy_calls_captured_and_on_two_streams(vt, B, H, K):
+    W8, s, _ = vt.vt_quantize_head(torch.randn((K, H), device="cuda").to(torch.bfloat16))
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    hid = [torch.randn((B, H), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    want = [(*vt.vt_draft_step_fp8(h, W8, s, ids, None, 0.0)[:2], vt.vt_draft_logits_fp8(h, W8, s)) for h in hid]
+    x = hid[0].clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q, tok, st = vt.vt_draft_step_fp8(x, W8, s, ids, None, 0.0)
+        z = vt.vt_draft_logits_fp8(x, W8, s)
+    for i in (1, 0, 1):
+        x.copy_(hid[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip((q, tok, z), want[i]))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        for i in range(2):
+            got.append((i, vt.vt_draft_step_fp8(hid[i], W8, s, ids, None, 0.0, stream=streams[i]),
+                        vt.vt_draft_logits_fp8(hid[i], W8, s, stream=streams[i])))
+    torch.cuda.synchronize()
+    for i, (q, tok, st), z in got:
+        assert int(st.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip((q, tok, z), want[i]))
