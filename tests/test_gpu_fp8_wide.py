@@ -1,0 +1,100 @@
+"""The 8-bit product for more than 64 rows, whose scales differ in every block
+of the head and every group of the hidden states, against 64-bit products.
+
+Exact cases: hidden states are integers in [-2, 2] times 2^e, e in [-2, 2]
+drawn per row and group, weights such integers times a scale 2^f, f in [-2, 2],
+drawn per block (times 1.5 or -0.75 in blocks of rows that take the other loop).
+Every term is a multiple of 2^-6 and every sum of terms at most A, the sum of
+their magnitudes; A < 2^18 (asserted) makes every partial sum, in any order
+and on either side of a rounding, a 24-bit multiple of 2^-6, so the logits are
+equal bit for bit.
+"""
+import numpy as np
+import pytest
+
+import synthetic
+from oracle import fp8
+from parity import assert_probs_close
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# e4m3 codes of -2 .. 2
+CODES = np.array([0xC0, 0xB8, 0x00, 0x38, 0x40], np.uint8)
+
+
+@pytest.fixture(scope="module")
+def vt():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import drafter_sampling_gb300 as m
+    from drafter_sampling_gb300 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _case(B, H, K, other):
+    """(hidden bf16, W8, w_scale, z fp64 [B, K] at temperature 1), on the GPU.
+    other: every how many blocks of rows have scales that are no powers of two (0: none)."""
+    g = synthetic.rng(B + H + K + other, 21)
+    n, kb = -(-H // 128), -(-K // 128)
+    x = g.integers(-2, 3, (B, H)).astype(np.float64)
+    x *= np.repeat(2.0 ** g.integers(-2, 3, (B, n)), 128, 1)[:, :H]
+    w = g.integers(-2, 3, (K, H))
+    s = 2.0 ** g.integers(-2, 3, (kb, n))
+    if other:
+        s[::other] *= np.where(g.integers(0, 2, s[::other].shape) == 0, 1.5, -0.75)
+    xd, wd = _dev(x), _dev(w.astype(np.int8)).double()
+    wd *= _dev(s).repeat_interleave(128, 0)[:K].repeat_interleave(128, 1)[:, :H]
+    assert float((xd.abs() @ wd.abs().T).max()) < 2.0 ** 18
+    buf = torch.full((K, (H + 15) // 16 * 16 + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    buf[:, :H] = _dev(CODES[w + 2])
+    return xd.bfloat16(), buf[:, :H], _dev(s.astype(np.float32)), xd @ wd.T
+
+
+# 5, 17, 33, 65 and 100 groups; up to several items per CTA or pair; one and more chunks, odd and even
+CASES = [(65, 600, 45000), (100, 2110, 700), (130, 2110, 41000), (256, 4200, 20003), (256, 640, 40100),
+         (300, 8300, 15000), (384, 2110, 4001), (1000, 12800, 10007), (1000, 600, 9999)]
+
+
+@pytest.mark.parametrize("other", [0, 1, 2, 5])
+@pytest.mark.parametrize("B,H,K", CASES)
+def test_logits_of_differing_scales_bit_exact(vt, B, H, K, other):
+    hid, W8, s, z = _case(B, H, K, other)
+    got = vt.vt_draft_logits_fp8(hid, W8, s, 0.5)
+    assert torch.equal(got.double(), 2 * z)
+    assert torch.equal(got, vt.vt_draft_logits_fp8(hid, W8, s, 0.5))
+
+
+@pytest.mark.parametrize("other", [0, 3])
+@pytest.mark.parametrize("B,H,K", CASES)
+def test_greedy_step_of_differing_scales(vt, B, H, K, other):
+    hid, W8, s, z = _case(B, H, K, other)
+    ids = torch.arange(K, dtype=torch.int32, device="cuda") * 3
+    q, tok, st = vt.vt_draft_step_fp8(hid, W8, s, ids, None, 0.0)
+    first = (z == z.amax(1, keepdim=True)).int().argmax(1)      # the lowest of equal ones
+    want = torch.zeros_like(q)
+    want[torch.arange(B), first] = 1.0
+    assert int(st.item()) == 0 and torch.equal(tok, ids[first]) and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("other", [0, 3])
+@pytest.mark.parametrize("B,H,K", [c for c in CASES if c[0] * c[2] < 6e6])
+def test_sampling_and_topk_of_differing_scales(vt, B, H, K, other):
+    hid, W8, s, z = _case(B, H, K, other)
+    T = float(z.std())
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    q, _, st = vt.vt_draft_step_fp8(hid, W8, s, ids, torch.full((B,), 0.5, device="cuda"), T)
+    assert int(st.item()) == 0
+    assert_probs_close(q.cpu().numpy(), torch.softmax(z / T, 1).cpu().numpy())
+    out, logq, st = vt.vt_draft_topk_fp8(hid, W8, s, ids, 8, T)
+    assert int(st.item()) == 0
+    assert torch.equal(torch.gather(z, 1, out.long()), z.topk(8, dim=1).values)
+    # z2 = z log2(e) / T is rounded three times and |z| / T <= 8 here, the sum and its logarithm to 1e-6
+    lq = torch.gather(torch.log_softmax(z / T, 1), 1, out.long())
+    assert float((logq - lq).abs().max()) <= 8 * 4 * 2.0 ** -24 + 1e-5
