@@ -15,9 +15,12 @@
 // do not depend on what the consumers are doing; a row's elements before its
 // first and after its last 16-byte boundary are loaded one by one.
 // A thread keeps a running (m, S, D) of what it has seen.  S is a sum of
-// vectors' sums carried with its rounding error, and log S is taken as
-// log1p(S - 1): a peaked row's S is 1 and little more, and that little is its
-// entropy.
+// chunks' sums carried with its rounding error, so that it does not lose with
+// the row's length, and ln S is taken as log1p(S - 1).  A chunk's own sum (32 or 64
+// weights of a thread) is a plain fp32 one: next to a peak's weight of 1 it loses
+// up to 16 roundings of 2^-24, so ln S and a peaked row's entropy are good to
+// 1e-6, not to all their digits.  Adding the peak's chunk once more with the 1
+// apart keeps them, and costs 0.6 to 0.9 us of one row's 6.8 and 2% of many rows.
 //
 // The k best are kept as 64-bit keys, ordered by (value, lower id first).  A
 // warp lists in shared memory the ids whose key reaches a bound that at least

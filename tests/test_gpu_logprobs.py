@@ -310,3 +310,45 @@ def test_draft_verify_and_report(vt):
     assert np.array_equal(top.view(-1, 3).cpu().numpy(), ref["top_ids"])
     assert np.allclose(lp.view(-1).cpu().numpy(), ref["logp"], atol=1e-5, equal_nan=True)
     assert np.allclose(en.view(-1).cpu().numpy(), ref["entropy"], atol=1e-4, equal_nan=True)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", [-300.0, -np.inf])
+@pytest.mark.parametrize("V", [2000, 40001])
+def test_peaked_rows(vt, V, low, dt):
+    """A peak and runners-up at distance d, in the peak's own 16 bytes, its thread's chunk, and elsewhere.
+
+    With w = e^-d the row's S - 1 is a sum of w, and ln S and the entropy are w (1 + d) and the like.
+    Relative to it: w's argument d log2(e) is off by two roundings, which is d 2^-23 of w; its exponential
+    by 2^-22, once more when the runner-up's thread is rescaled to the peak; the sums and their joins, two
+    products, the logarithm and the last additions by 20 roundings of 2^-24.  And in absolute terms by 16
+    roundings of S, half a step of 2^-23 each: those of the additions to the peak's 1 in its thread's chunk,
+    at most 7 in a 16-byte vector and 8 over the vectors, where they are added one by one.
+    """
+    peak = 1000
+    near = [peak + 1, peak - 1, peak + 3, peak + 256 * (16 // dt.itemsize), 3, V - 2]
+    for T in (1.0, 0.5):
+        rows, given, dist = [], [], []
+        for d in (2.0, 5.0, 12.0, 20.0, 40.0):
+            for ids in [[i] for i in near if i < V] + [[peak + 1, 7], [peak - 1, peak + 1, V - 2]]:
+                x = torch.full((V,), low)
+                x[peak] = 6.0
+                x[ids] = 6.0 - d * T
+                rows.append(x)
+                given.append(peak)
+                dist.append(d)
+        x = torch.stack(rows).to(dt).cuda()
+        lp, en, _, _, st = vt.vt_token_logprobs(x, torch.tensor(given, dtype=torch.int32, device="cuda"), temperature=T)
+        assert int(st.item()) == 0
+        y = (x.double().cpu().numpy() - 6.0) / T
+        y[:, peak] = -np.inf                                # the others, apart from the peak's 1
+        w = np.exp(y)
+        rest = w.sum(axis=1)                                # S - 1 with its digits
+        want = -np.log1p(rest)
+        entropy = np.log1p(rest) - np.where(w > 0, w * np.maximum(y, -1e9), 0.0).sum(axis=1) / (1 + rest)
+        d = np.array(dist)
+        rel = (d + 16) * 2.0 ** -23
+        floor = 16 * 2.0 ** -24 * (1 + rest)
+        lp, en = lp.cpu().numpy().astype(np.float64), en.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(lp - want) <= rel * np.abs(want) + floor)
+        assert np.all(np.abs(en - entropy) <= rel * entropy + floor * (1 + entropy))
