@@ -105,6 +105,11 @@ __device__ __forceinline__ int count_before(const lp_key* keys, int n, lp_key q)
   return r;
 }
 
+// (x - m) / T, where x - m itself may lie beyond fp32 (halves differ exactly)
+__device__ __forceinline__ float scaled_diff(float x, float m, float inv_t) {
+  return (0.5f * x - 0.5f * m) * (2.f * inv_t);
+}
+
 // larger of two, NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
     if (tid == 0) {
       const bool in = token >= 0 && token < a.V;
-      a.out_logp[row] = ok && in ? (sh.xt - r.m) * a.inv_t - lnS : nan;
+      a.out_logp[row] = ok && in ? scaled_diff(sh.xt, r.m, a.inv_t) - lnS : nan;
       if (a.out_entropy) a.out_entropy[row] = ok ? lnS - a.inv_t * (r.d / r.s) : nan;
       const int flags =
           (late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE) | (in ? 0 : VT_DEV_BAD_ID);
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     }
     if (ok && q != 0 && rk < k) {
       a.out_ids[(int64_t)row * k + rk] = key_id(q);
-      a.out_top[(int64_t)row * k + rk] = (key_value(q) - r.m) * a.inv_t - lnS;
+      a.out_top[(int64_t)row * k + rk] = scaled_diff(key_value(q), r.m, a.inv_t) - lnS;
     }
     if (!ok && tid < k) {
       a.out_ids[(int64_t)row * k + tid] = -1;

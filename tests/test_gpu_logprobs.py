@@ -352,3 +352,15 @@ def test_peaked_rows(vt, V, low, dt):
         lp, en = lp.cpu().numpy().astype(np.float64), en.cpu().numpy().astype(np.float64)
         assert np.all(np.abs(lp - want) <= rel * np.abs(want) + floor)
         assert np.all(np.abs(en - entropy) <= rel * entropy + floor * (1 + entropy))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(3, 9), (3, 60000)])
+def test_differences_beyond_fp32(vt, R, V, dt):
+    # log p = (l - m) / T is finite where l - m alone is not: 6e38 apart, T = 4 and the largest T
+    x = torch.full((R, V), -3e38)
+    x[:, 4] = 3e38
+    x[1, 5] = 0.0
+    x = x.to(dt).cuda()
+    _check(vt, x, [1, 5, 4], 5, 4.0)
+    _check(vt, x, [1, 5, 4], 5, 1e30)
