@@ -476,12 +476,18 @@ def _arg(t, name, dtypes, shape, dev):
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _new(shape, dtype, dev, stream):
-    """A tensor made by a call that runs on `stream`: its memory is not given
-    to another before that stream has passed this point."""
-    t = _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape, dtype, dev, stream, returned=True):
+    """A tensor made by a call that runs on `stream`.  Its memory comes from that
+    stream's own pool: from the current stream's, it could be a block whose last
+    owner's kernels, still running there, write it meanwhile.  Where it is
+    returned, the current stream may read it, so its memory is not given to
+    another before that stream has passed the point where it is freed."""
+    if stream is None:
+        return _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
+    with _TORCH.cuda.stream(stream):
+        t = _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
+    if returned:
+        t.record_stream(_TORCH.cuda.current_stream(dev))
     return t
 
 
@@ -543,7 +549,7 @@ def _rows_out(t, name, B, K, dev, wide):
 def _scratch(t, nbytes, dev, stream):
     """(address, bytes) of the workspace given, or of a new one."""
     if t is None:
-        t = _new(max(int(nbytes), 256), _U8[0], dev, stream)
+        t = _new(max(int(nbytes), 256), _U8[0], dev, stream, returned=False)
     p = _arg(t, "workspace", _U8, None, dev)
     return p, t.numel(), t
 
