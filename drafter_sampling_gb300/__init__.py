@@ -82,9 +82,32 @@ def _bf16_dtypes():
     return _BF16
 
 
-def _ws(nbytes, device):
+def _as_stream(stream, device):
+    """`stream` as a torch stream, where it is another object that has the raw one."""
     torch = _torch()
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """A tensor for a call that runs on `stream`.  Its memory comes from that
+    stream's own pool: from the current stream's, it could be a block whose last
+    owner's kernels, still running there, write it meanwhile.  Where it is
+    returned, the current stream may read it, so its memory is not given to
+    another before that stream has passed the point where it is freed."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_as_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _ws(nbytes, device, stream=None):
+    return _empty(max(int(nbytes), 256), _torch().uint8, device, stream, returned=False)
 
 
 def workspace_bytes(kind: str, **kw) -> int:
@@ -117,18 +140,18 @@ def vt_calibrate_topk(ids, V: int, K: int, counts=None, topk_ids=None, dev_statu
     dev = ids.device
     n = ids.numel()
     if counts is None:
-        counts = torch.empty(V, dtype=torch.int32, device=dev)
+        counts = _empty(V, torch.int32, dev, stream)
     if topk_ids is None:
-        topk_ids = torch.empty(K, dtype=torch.int32, device=dev)
+        topk_ids = _empty(K, torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     _dev(counts, "counts", (torch.int32, torch.uint32), 1)
     _dev(topk_ids, "topk_ids", (torch.int32,), 1)
     if counts.numel() != V or topk_ids.numel() != K:
         raise ValueError("counts must have V elements and topk_ids K elements")
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_calibrate_topk_workspace_bytes(n, V, K), dev)
+        workspace = _ws(L.vt_calibrate_topk_workspace_bytes(n, V, K), dev, stream)
     st = L.vt_calibrate_topk(ids.data_ptr(), n, V, K, counts.data_ptr(), topk_ids.data_ptr(),
                              dev_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
                              _stream_ptr(stream))
@@ -143,20 +166,20 @@ def _calibrate_select(fn: str, ids, V: int, param, counts, ranked_ids, k_out, de
     dev = ids.device
     n = ids.numel()
     if counts is None:
-        counts = torch.empty(V, dtype=torch.int32, device=dev)
+        counts = _empty(V, torch.int32, dev, stream)
     if ranked_ids is None:
-        ranked_ids = torch.empty(V, dtype=torch.int32, device=dev)
+        ranked_ids = _empty(V, torch.int32, dev, stream)
     if k_out is None:
-        k_out = torch.empty(1, dtype=torch.int32, device=dev)
+        k_out = _empty(1, torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     _dev(counts, "counts", (torch.int32, torch.uint32), 1)
     _dev(ranked_ids, "ranked_ids", (torch.int32,), 1)
     if counts.numel() != V or ranked_ids.numel() != V:
         raise ValueError("counts and ranked_ids must have V elements")
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_calibrate_select_workspace_bytes(n, V), dev)
+        workspace = _ws(L.vt_calibrate_select_workspace_bytes(n, V), dev, stream)
     st = getattr(L, fn)(ids.data_ptr(), n, V, param, counts.data_ptr(), ranked_ids.data_ptr(),
                         k_out.data_ptr(), dev_status.data_ptr(), workspace.data_ptr(),
                         workspace.numel(), _stream_ptr(stream))
@@ -194,19 +217,19 @@ def vt_trim_head(W, topk_ids, W_trim=None, trim_ids=None, inv_map=None, dev_stat
     K = topk_ids.numel()
     dev = W.device
     if W_trim is None:
-        W_trim = torch.empty((K, H), dtype=W.dtype, device=dev)
+        W_trim = _empty((K, H), W.dtype, dev, stream)
     if trim_ids is None:
-        trim_ids = torch.empty(K, dtype=torch.int32, device=dev)
+        trim_ids = _empty(K, torch.int32, dev, stream)
     if inv_map is None:
-        inv_map = torch.empty(V, dtype=torch.int32, device=dev)
+        inv_map = _empty(V, torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     _dev(W_trim, "W_trim", _bf16_dtypes(), 2)
     if tuple(W_trim.shape) != (K, H) or trim_ids.numel() != K or inv_map.numel() != V:
         raise ValueError("output shapes do not match (K, H), K and V")
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_trim_head_workspace_bytes(V, K), dev)
+        workspace = _ws(L.vt_trim_head_workspace_bytes(V, K), dev, stream)
     st = L.vt_trim_head(W.data_ptr(), V, H, topk_ids.data_ptr(), K, W_trim.data_ptr(),
                         trim_ids.data_ptr(), inv_map.data_ptr(), dev_status.data_ptr(),
                         workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
@@ -225,12 +248,12 @@ def vt_draft_logits(hidden, W_trim, temperature: float = 1.0, logits=None, works
     if H2 != H:
         raise ValueError("hidden and W_trim disagree on H")
     if logits is None:
-        logits = torch.empty((B, K), dtype=torch.float32, device=hidden.device)
+        logits = _empty((B, K), torch.float32, hidden.device, stream)
     if logits.dim() != 2 or logits.shape[0] != B or logits.stride(1) != 1 or logits.shape[1] < K:
         raise ValueError("logits must be [B, >=K] with unit inner stride")
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_draft_workspace_bytes(B, H, K), hidden.device)
+        workspace = _ws(L.vt_draft_workspace_bytes(B, H, K), hidden.device, stream)
     st = L.vt_draft_logits(hidden.data_ptr(), B, H, W_trim.data_ptr(), K, float(temperature),
                            logits.data_ptr(), logits.stride(0), workspace.data_ptr(),
                            workspace.numel(), _stream_ptr(stream))
@@ -258,20 +281,20 @@ def vt_draft_step(hidden, W_trim, trim_ids, uniforms, temperature: float = 1.0, 
     K = W_trim.shape[0]
     dev = hidden.device
     if q is None:
-        q = torch.empty((B, K), dtype=torch.float32, device=dev)
+        q = _empty((B, K), torch.float32, dev, stream)
     if q.dim() != 2 or q.shape[0] != B or q.shape[1] != K or q.stride(1) != 1:
         raise ValueError("q must be [B, K] with unit inner stride")
     if tokens is None:
-        tokens = torch.empty(B, dtype=torch.int32, device=dev)
+        tokens = _empty(B, torch.int32, dev, stream)
     if tokens.dim() != 1 or tokens.shape[0] != B or tokens.dtype != torch.int32:
         raise ValueError("tokens must be an int32 vector of B entries (any stride)")
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     if (uniforms is not None and uniforms.numel() != B) or trim_ids.numel() != K:
         raise ValueError("uniforms must have B and trim_ids K elements")
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_draft_workspace_bytes(B, H, K), dev)
+        workspace = _ws(L.vt_draft_workspace_bytes(B, H, K), dev, stream)
     st = L.vt_draft_step(hidden.data_ptr(), B, H, W_trim.data_ptr(), trim_ids.data_ptr(), K,
                          uniforms.data_ptr() if uniforms is not None else None,
                          float(temperature), q.data_ptr(), q.stride(0),
@@ -329,16 +352,16 @@ def vt_verify(target_logits, q, inv_map, draft_tokens, u_accept, u_resample,
     ptr = lambda x: x.data_ptr() if x is not None else None
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty((B, R), dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, R), torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _empty(B, torch.int32, dev, stream)
     if out_accept_prob is None and want_accept_prob:
-        out_accept_prob = torch.empty((B, gamma), dtype=torch.float32, device=dev)
+        out_accept_prob = _empty((B, gamma), torch.float32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_verify_workspace_bytes(B, gamma, V, K), dev)
+        workspace = _ws(L.vt_verify_workspace_bytes(B, gamma, V, K), dev, stream)
     st = L.vt_verify(target_logits.data_ptr(), dt, B, gamma, V, ptr(q), ptr(inv_map),
                      K, draft_tokens.data_ptr(), ptr(u_accept), ptr(u_resample),
                      float(temperature), out_tokens.data_ptr(), out_num_accepted.data_ptr(),
@@ -362,14 +385,14 @@ def vt_draft_topk(hidden, W_trim, trim_ids, k: int, temperature: float = 1.0, ou
     K = W_trim.shape[0]
     dev = hidden.device
     if out_ids is None:
-        out_ids = torch.empty((B, k), dtype=torch.int32, device=dev)
+        out_ids = _empty((B, k), torch.int32, dev, stream)
     if out_logq is None:
-        out_logq = torch.empty((B, k), dtype=torch.float32, device=dev)
+        out_logq = _empty((B, k), torch.float32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_draft_topk_workspace_bytes(B, H, K, k), dev)
+        workspace = _ws(L.vt_draft_topk_workspace_bytes(B, H, K, k), dev, stream)
     st = L.vt_draft_topk(hidden.data_ptr(), B, H, W_trim.data_ptr(), trim_ids.data_ptr(), K, k,
                          float(temperature), out_ids.data_ptr(), out_logq.data_ptr(),
                          dev_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -408,16 +431,16 @@ def vt_verify_tree(target_logits, parent, tokens, temperature: float = 0.0, out_
         raise ValueError("parent must be [N] or [B, N]")
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty((B, R), dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, R), torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _empty(B, torch.int32, dev, stream)
     if out_path is None and want_path:
-        out_path = torch.empty((B, N), dtype=torch.int32, device=dev)
+        out_path = _empty((B, N), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
     L = lib()
     if workspace is None:
-        workspace = _ws(L.vt_verify_tree_workspace_bytes(B, N, V), dev)
+        workspace = _ws(L.vt_verify_tree_workspace_bytes(B, N, V), dev, stream)
     st = L.vt_verify_tree(target_logits.data_ptr(), dt, B, N, V, parent.data_ptr(), pstride,
                           tokens.data_ptr(), float(temperature), out_tokens.data_ptr(),
                           out_num_accepted.data_ptr(),
@@ -477,18 +500,10 @@ def _arg(t, name, dtypes, shape, dev):
 
 
 def _new(shape, dtype, dev, stream, returned=True):
-    """A tensor made by a call that runs on `stream`.  Its memory comes from that
-    stream's own pool: from the current stream's, it could be a block whose last
-    owner's kernels, still running there, write it meanwhile.  Where it is
-    returned, the current stream may read it, so its memory is not given to
-    another before that stream has passed the point where it is freed."""
+    """A tensor on device dev for a call that runs on `stream` (see _empty)."""
     if stream is None:
         return _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
-    with _TORCH.cuda.stream(stream):
-        t = _TORCH.empty(shape, dtype=dtype, device=_DEVICES[dev])
-    if returned:
-        t.record_stream(_TORCH.cuda.current_stream(dev))
-    return t
+    return _empty(shape, dtype, _DEVICES[dev], stream, returned)
 
 
 def _on(stream, dev):
@@ -744,7 +759,9 @@ def vt_selftest_wait(which: int, limit: int, flag=None, dev_status=None, stream=
     torch = _torch()
     if dev_status is None:
         dev = flag.device if flag is not None else torch.device("cuda", torch.cuda.current_device())
-        dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        dev_status = _empty(1, torch.int32, dev, stream)
+        with torch.cuda.stream(_as_stream(stream, dev)):  # zeroed there, ahead of the kernel
+            dev_status.zero_()
     _dev(dev_status, "dev_status", (torch.int32,), 1)
     if flag is not None:
         _dev(flag, "flag", (torch.int32, torch.uint32), 1)
@@ -760,7 +777,10 @@ class BlockGraph:
     as a CUDA graph by vt_block_graph_create and replayed by launch().
 
     The tensors are fixed at capture and kept alive by this object; a replay
-    reads what they hold when it runs.  Outputs (q, draft_tokens,
+    reads what they hold when it runs.  Replays may run on any stream: the
+    constructor waits until the current stream has no other use of their
+    memory, and their memory is not given to another while a stream that
+    launched the graph is at it.  Outputs (q, draft_tokens,
     out_tokens, out_num_accepted, out_accept_prob, dev_status [2]) are
     attributes.  temperature == 0 captures the greedy block (u_draft,
     u_accept and u_resample may then be None).  With w_scale, W_trim is an
@@ -835,10 +855,20 @@ class BlockGraph:
             _lib.check("vt_block_graph_create",
                        L.vt_block_graph_create(ctypes.byref(d), ctypes.byref(h)))
         self._handle = h
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
+        self._known = set()  # raw streams that the allocator knows as users
 
     def launch(self, stream=None):
-        _lib.check("vt_block_graph_launch",
-                   lib().vt_block_graph_launch(self._handle, _stream_ptr(stream)))
+        ptr = _stream_ptr(stream)
+        if ptr not in self._known:
+            self._known.add(ptr)
+            s = _TORCH.cuda.ExternalStream(ptr, device=self.q.device)
+            for t in (*self._keep, self.q, self.draft_tokens, self.out_tokens, self.out_num_accepted,
+                      self.out_accept_prob, self.dev_status, self.workspace):
+                if t is not None:
+                    t.record_stream(s)
+        _lib.check("vt_block_graph_launch", lib().vt_block_graph_launch(self._handle, ptr))
 
     def close(self):
         if getattr(self, "_handle", None):

@@ -27,6 +27,17 @@ class FakeTorch:
         return t
 
 
+def test_the_older_calls_tensors_too(monkeypatch):
+    import drafter_sampling_gb300 as vt
+    fake = FakeTorch()
+    fake.uint8 = "uint8"
+    monkeypatch.setattr(vt, "_TORCH", fake)
+    assert vt._empty(3, None, "cuda:0", "side").recorded == ["current"]
+    assert vt._ws(100, "cuda:0", "side").recorded == []         # used by that stream alone
+    assert vt._ws(100, "cuda:0").on == "current"
+    assert [t.on for t in fake.made] == ["side", "side", "current"]
+
+
 def test_tensors_are_made_on_the_stream_of_the_call(monkeypatch):
     import drafter_sampling_gb300 as vt
     fake = FakeTorch()
@@ -53,7 +64,33 @@ def _calls(vt):
     x = torch.randn((B, K), device="cuda")
     tok = torch.zeros(B, dtype=torch.int32, device="cuda")
     ws = vt.workspace_bytes("draft_fp8", B=B, H=H, K=K)
+    trim = torch.randperm(2 * K, device="cuda")[:K].to(torch.int32)
+    inv = torch.full((2 * K,), -1, dtype=torch.int32, device="cuda")
+    inv[trim.sort().values.long()] = ids
+    Wfull = torch.randn((2 * K, H), device="cuda").to(torch.bfloat16)
+    stream_ids = torch.randint(0, 2 * K, (10000,), device="cuda", dtype=torch.int32)
+    q = torch.full((B, 2, K), 1.0 / K, device="cuda")
+    drafted = trim.sort().values[torch.randint(0, K, (B, 2), device="cuda")].contiguous()
+    ua, ur = torch.rand((B, 2), device="cuda"), torch.rand((B, 3), device="cuda")
+    z = torch.randn((B, 3, 2 * K), device="cuda")
+    parent = torch.tensor([-1, 0], dtype=torch.int32, device="cuda")
+    old = {
+        "calibrate_topk": (lambda st: vt.vt_calibrate_topk(stream_ids, 2 * K, K, stream=st),
+                           [vt.workspace_bytes("calibrate", n=10000, V=2 * K, K=K), 8 * K, 4 * K]),
+        "calibrate_top_p": (lambda st: vt.vt_calibrate_top_p(stream_ids, 2 * K, 0.5, stream=st),
+                            [vt.workspace_bytes("select", n=10000, V=2 * K), 8 * K]),
+        "trim": (lambda st: vt.vt_trim_head(Wfull, trim, stream=st), [2 * K * H, 8 * K, 4 * K]),
+        "bf16_logits": (lambda st: [vt.vt_draft_logits(hid, W, stream=st)], [4 * B * K]),
+        "bf16_step": (lambda st: vt.vt_draft_step(hid, W, ids, u, stream=st),
+                      [4 * B * K, vt.workspace_bytes("draft", B=B, H=H, K=K)]),
+        "bf16_topk": (lambda st: vt.vt_draft_topk(hid, W, ids, 8, stream=st), [32 * B, 4 * B * K]),
+        "verify": (lambda st: vt.vt_verify(z, q, inv, drafted, ua, ur, stream=st),
+                   [vt.workspace_bytes("verify", B=B, gamma=2, V=2 * K, K=K), 12 * B, 8 * B, 4 * B]),
+        "verify_tree": (lambda st: vt.vt_verify_tree(z, parent, drafted, stream=st), [12 * B, 8 * B, 4 * B]),
+        "selftest": (lambda st: [vt.vt_selftest_wait(1, 1000, stream=st)], [4]),
+    }
     return {
+        **old,
         "quantize": (lambda st: vt.vt_quantize_head(W, stream=st)[:2], [K * 304]),
         "logits": (lambda st: [vt.vt_draft_logits_fp8(hid, W8, s, stream=st)], [4 * B * K, ws]),
         "step": (lambda st: vt.vt_draft_step_fp8(hid, W8, s, ids, u, stream=st), [4 * B * K, ws]),
@@ -69,7 +106,9 @@ def _bytes(tensors):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("name", ["quantize", "logits", "step", "topk", "logprobs"])
+@pytest.mark.parametrize("name", ["quantize", "logits", "step", "topk", "logprobs", "calibrate_topk", "calibrate_top_p",
+                                  "trim", "bf16_logits", "bf16_step", "bf16_topk", "verify", "verify_tree",
+                                  "selftest"])
 def test_a_busy_current_stream_writes_nothing_of_a_side_streams_call(name):
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
@@ -119,3 +158,45 @@ def test_a_side_streams_calls_within_a_capture():
         torch.cuda.synchronize()
         for n, w in want.items():
             assert all(torch.equal(a, b) for a, b in zip(_bytes(got[n]), w)), n
+
+
+@pytest.mark.gpu
+def test_a_block_graph_made_while_its_stream_is_busy_and_launched_on_another():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import drafter_sampling_gb300 as vt
+    gamma, V = 2, 2 * K
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    inv = torch.full((V,), -1, dtype=torch.int32, device="cuda")
+    inv[:K] = ids
+    args = (torch.randn((gamma, B, H), device="cuda").to(torch.bfloat16),
+            torch.randn((K, H), device="cuda").to(torch.bfloat16), ids, inv,
+            torch.randn((B, gamma + 1, V), device="cuda"), torch.rand((gamma, B), device="cuda"),
+            torch.rand((B, gamma), device="cuda"), torch.rand((B, gamma + 1), device="cuda"), 8.0)
+    outputs = lambda g: _bytes([g.q, g.draft_tokens, g.out_tokens, g.out_num_accepted, g.dev_status])
+    first = vt.BlockGraph(*args)
+    first.launch()
+    want = outputs(first)
+    sizes = [first.workspace.numel(), first.q.numel() * 4, first.out_tokens.numel() * 4]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        torch.cuda._sleep(10_000_000)
+        for b in blocks:
+            b.fill_(0x7F)
+        del blocks, b
+        g = vt.BlockGraph(*args)
+        g.launch(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, w) for a, w in zip(outputs(g), want))
+        # dropped while a replay has yet to run: the current stream's next tensors lie elsewhere
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(10_000_000)
+        out = g.out_tokens
+        g.launch(side)
+        del g
+        others = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x7F) for n in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.uint8), want[2])
+        del others, out
