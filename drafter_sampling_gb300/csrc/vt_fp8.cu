@@ -189,6 +189,8 @@ struct Fp8Args {
   const float* sx;      // [groups][Bp]
   int Bp, groups, nchunk;
   int items;            // blocks of W8 rows times batch chunks
+  int give_up;          // self-test: from this item of a CTA on, the promoting threads act as if
+                        // a wait had run out (-1: never)
   int vec_out;          // the output's rows are 16-byte aligned
 };
 
@@ -611,6 +613,7 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = 0; k < CW / 8; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[k][i] = 0;
+      if (tile == (int)blockIdx.x + fa.give_up * (int)gridDim.x) ok = false;
       int g = tile % nk;
       for (int kb = 0; kb < nk && ok; ++kb, ++it) {
         const int q = it % kScaleSlots, p = it % NBUF;
@@ -1061,7 +1064,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
     float* ob = reinterpret_cast<float*>(smem + (size_t)S * stage_bytes) + warp * 32 * kOutPitch;  // 16-byte aligned
     int u = 0, t = 0;  // units read, and turns whose scales have been written, so far
-    bool ok = true;
+    bool ok = true;  // once false it stays so: what a late wait would find belongs to another item
     auto chunk_of = [&](int item) { return (item - item / fa.nchunk * fa.nchunk) * kCtas * kBM + part * kBM; };
     // one of this warp's arrivals, once its accesses to tensor memory are complete
     auto give = [&](uint64_t* bar) {
@@ -1147,6 +1150,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // the last item's scales have been read by all
       asm volatile("bar.sync 1, %0;" ::"n"(kBatchNP) : "memory");
       const bool next_scaled = next < items && fetch(next, at ^ 1);
+      if (item == first + fa.give_up * step) ok = false;
       f32x2 acc[64];  // sums of this batch row and 128 rows of W8
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -1176,7 +1180,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
       } else {
         float sx = fa.sx[(uint32_t)(g * fa.Bp + b0 + row)];
-        for (int kb = 0; kb < nk; ++kb, ++u) {
+        for (int kb = ok ? 0 : nk; kb < nk; ++kb, ++u) {
           const uint32_t fb = __float_as_uint(sw_sh[at][half][g] * sx);
           const f32x2 f = pack2(fb, fb);
           g = g + 1 == nk ? 0 : g + 1;
@@ -1233,7 +1237,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       for (int c = 0; c < 128; c += 32) {
         __syncwarp();
         // the MMAs may be through with the next item's first turns
-        if (!PART && c > 0 && scaled && ahead > 0 && ahead < nk) {
+        if (!PART && c > 0 && ok && scaled && ahead > 0 && ahead < nk) {
           const int chunk = chunk_of(next);
           int ga = next / fa.nchunk % nk + ahead;
           if (ga >= nk) ga -= nk;
@@ -1423,7 +1427,7 @@ int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp
 int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const uint8_t* W8,
                     int64_t ldw, const float* w_scale, int K, float out_scale, float* out,
                     int64_t ldo, const Fp8Ws& ws, float2* part, int* status, int status_reset,
-                    int greedy) {
+                    int greedy, int give_up = -1) {
   const int groups = (H + kQB - 1) / kQB, Bp = pad_batch(B), ldx = groups * kQB;
   CUtensorMap mw, mx;
   // the boxes: the rows that one CTA stages
@@ -1463,6 +1467,7 @@ int launch_head_fp8(cudaStream_t s, const uint16_t* hidden, int B, int H, const 
   fa.Bp = Bp;
   fa.groups = groups;
   fa.nchunk = 1;
+  fa.give_up = give_up;
   fa.vec_out = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 4 == 0;
   switch (Bp) {
     case 16: return launch_narrow<16>(s, mw, mx, fa);
@@ -1564,6 +1569,24 @@ extern "C" int vt_draft_logits_fp8(const uint16_t* hidden, int32_t B, int32_t H,
   if (workspace_bytes < ws.bytes) return VT_ERR_WORKSPACE;
   return launch_head_fp8(static_cast<cudaStream_t>(stream), hidden, B, H, W8, ldw, w_scale, K,
                          1.0f / temperature, logits, ld_logits, ws, nullptr, ws.status_sink, 1, 0);
+}
+
+extern "C" int vt_selftest_draft_fp8(int32_t give_up, const uint16_t* hidden, int32_t B, int32_t H,
+                                     const uint8_t* W8, int64_t ldw, const float* w_scale,
+                                     int32_t K, float temperature, float* logits,
+                                     int64_t ld_logits, int32_t* dev_status, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  using namespace vt;
+  const int st = check_fp8_args(hidden, B, H, W8, ldw, w_scale, K, temperature, false);
+  if (st != VT_OK) return st;
+  if (give_up < -1 || give_up > 65535 || !logits || ld_logits < K || !dev_status)
+    return VT_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return VT_ERR_WORKSPACE;
+  const Fp8Ws ws = carve_fp8(workspace, B, H, K);
+  if (workspace_bytes < ws.bytes) return VT_ERR_WORKSPACE;
+  return launch_head_fp8(static_cast<cudaStream_t>(stream), hidden, B, H, W8, ldw, w_scale, K,
+                         1.0f / temperature, logits, ld_logits, ws, nullptr, dev_status, 1, 0,
+                         give_up);
 }
 
 extern "C" int vt_draft_step_fp8(const uint16_t* hidden, int32_t B, int32_t H, const uint8_t* W8,

@@ -549,6 +549,20 @@ int vt_block_graph_destroy(void* graph);
 int vt_selftest_wait(int32_t which, uint32_t limit, const uint32_t* flag, int32_t* dev_status,
                      void* stream);
 
+/* vt_selftest_draft_fp8 — vt_draft_logits_fp8 with a status word, in which the
+ * threads that take over a thread block's sums act, from its item number give_up
+ * (from 0, at most 65535) on, as if a wait of theirs had run out (-1: never).
+ * The block's other waits then run out in earnest, after about a second, and
+ * VT_DEV_TIMEOUT is set.
+ * An item is 128 rows of W8 for up to 64 batch rows, and 256 rows with up to 128
+ * or 256 batch rows otherwise; a block takes them one after another.
+ */
+int vt_selftest_draft_fp8(int32_t give_up, const uint16_t* hidden, int32_t B, int32_t H,
+                          const uint8_t* W8, int64_t ldw, const float* w_scale, int32_t K,
+                          float temperature, float* logits, int64_t ld_logits,
+                          int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif
