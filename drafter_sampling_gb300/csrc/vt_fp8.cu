@@ -655,21 +655,21 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&sx_empty[q]);
       }
-      // a warp that gave up stores nothing more, but misses no barrier
+      // a warp that gave up misses no barrier; logits, whose call returns no
+      // status word, are NaN then, and with one nothing more is stored
       if (a.part == nullptr) {
-        if (ok) {
+        const float scale = ok ? a.out_scale : __int_as_float(0x7fc00000);
 #pragma unroll
-          for (int k = 0; k < CW / 8; ++k)
+        for (int k = 0; k < CW / 8; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 z = unpack2(acc[k][i]);
-              const int b = 8 * k + cpair, j = m0 + row0 + 8 * i;
-              if (j < a.K) {
-                if (b < a.B) a.out[(int64_t)b * a.ldo + j] = z.x * a.out_scale;
-                if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + j] = z.y * a.out_scale;
-              }
+          for (int i = 0; i < 4; ++i) {
+            const float2 z = unpack2(acc[k][i]);
+            const int b = 8 * k + cpair, j = m0 + row0 + 8 * i;
+            if (j < a.K) {
+              if (b < a.B) a.out[(int64_t)b * a.ldo + j] = z.x * scale;
+              if (b + 1 < a.B) a.out[(int64_t)(b + 1) * a.ldo + j] = z.y * scale;
             }
-        }
+          }
       } else if (a.greedy) {
         // each column's best key: over this thread's rows, the warp's, the tile's
         uint64_t* best = reinterpret_cast<uint64_t*>(zt);  // [warp][column]
@@ -1219,8 +1219,10 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       }
       at ^= 1;
       scaled = next_scaled;
-      // a warp that gave up stores nothing more, but misses no barrier
-      if (!ok || nvalid <= 0) continue;
+      // a warp that gave up misses no barrier; logits, whose call returns no
+      // status word, are NaN then, and with one nothing more is stored
+      if (nvalid <= 0 || (PART && !ok)) continue;
+      const float scale = PART || ok ? a.out_scale : __int_as_float(0x7fc00000);
       const int b = b0 + row;
       // this row's partial over the tile's rows: greedy, its best key (the rows
       // out are q's zeros then); sampling, like tile_partials', (max, sum
@@ -1248,7 +1250,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         for (int i = 0; i < 8; ++i) {
           const float2 x = unpack2(acc[c / 2 + 2 * i]), y = unpack2(acc[c / 2 + 2 * i + 1]);
           *reinterpret_cast<float4*>(ob + lane * kOutPitch + 4 * i) = make_float4(
-              x.x * a.out_scale, x.y * a.out_scale, y.x * a.out_scale, y.y * a.out_scale);
+              x.x * scale, x.y * scale, y.x * scale, y.y * scale);
         }
         __syncwarp();
         if constexpr (PART) {

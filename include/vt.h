@@ -404,7 +404,9 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
  * than 64 rows, blocks of 256 rows of W8 whose scales are all powers of two
  * are faster: the tensor cores apply both scales and sum up to 32 groups (in
  * fp32, cutting off instead of rounding).  A row of hidden states with a NaN
- * or an infinity gives NaN logits in that row.
+ * or an infinity gives NaN logits in that row.  vt_draft_logits_fp8 returns no
+ * status word: the logits that a wait which ran out (VT_DEV_TIMEOUT) kept from
+ * being computed are NaN.
  * hidden, logits, trim_ids, uniforms, q, tokens and the temperature are as
  * there; W8, ldw and w_scale as vt_quantize_head leaves them.  Like W_trim,
  * W8 and w_scale must not be written by a kernel that may still be running

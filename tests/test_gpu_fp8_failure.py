@@ -63,3 +63,17 @@ def test_selftest_refusals():
     for kw in (dict(give_up=-2), dict(give_up=65536), dict(z=None), dict(st=None), dict(ld=15)):
         assert call(**kw) == _lib.VT_ERR_INVALID_ARG, kw
     assert call(n=16) == _lib.VT_ERR_WORKSPACE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,K,other", CASES + [(64, 300, 300, False), (200, 300, 333, False)])
+def test_logits_that_were_not_computed_are_nan(B, H, K, other):
+    # vt_draft_logits_fp8 has no status word to say so
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import drafter_sampling_gb300 as vt
+    n = _first_rows(B)
+    z, status, want = _run(vt, 1 if n < K else 0, B, H, K, other)
+    n = n if n < K else 0
+    assert status == vt.VT_DEV_TIMEOUT
+    assert torch.equal(z[:, :n], want[:, :n]) and bool(z[:, n:].isnan().all())
