@@ -73,6 +73,7 @@ SIGNATURES = {
     "vt_draft_fp8_workspace_bytes": (_sz, [_i32, _i32, _i32]),
     "vt_draft_logits_fp8": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _sz,
                                       _p]),
+    "vt_selftest_overlap": (C.c_int, [C.c_uint32, _p]),
     "vt_selftest_draft_fp8": (C.c_int, [_i32, _p, _i32, _i32, _p, _i64, _p, _i32, _f32, _p, _i64, _p,
                                         _p, _sz, _p]),
     "vt_draft_step_fp8": (C.c_int, [_p, _i32, _i32, _p, _i64, _p, _p, _i32, _p, _f32, _p, _i64,

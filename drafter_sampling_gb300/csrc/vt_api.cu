@@ -42,6 +42,14 @@ __global__ void selftest_wait_kernel(int which, uint32_t limit, const unsigned* 
   if (!done) atomicOr(dev_status, VT_DEV_TIMEOUT);
 }
 
+__global__ void selftest_overlap_kernel(uint32_t limit) {
+  __shared__ __align__(8) uint64_t bar;
+  griddep_launch_dependents();
+  umma::mbar_init(&bar, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  umma::mbar_wait(&bar, 0, limit);
+}
+
 __global__ void clear_status_kernel(int* dev_status) {
   griddep_launch_dependents();
   *dev_status = 0;
@@ -64,6 +72,13 @@ extern "C" int vt_selftest_wait(int32_t which, uint32_t limit, const uint32_t* f
     return VT_ERR_INVALID_ARG;
   vt::selftest_wait_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(
       which, limit, reinterpret_cast<const unsigned*>(flag), dev_status);
+  VT_RETURN_IF_LAUNCH_FAILED();
+  return VT_OK;
+}
+
+extern "C" int vt_selftest_overlap(uint32_t limit, void* stream) {
+  if (limit < 1 || limit > vt::kSelftestMaxLimit) return VT_ERR_INVALID_ARG;
+  vt::selftest_overlap_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(limit);
   VT_RETURN_IF_LAUNCH_FAILED();
   return VT_OK;
 }

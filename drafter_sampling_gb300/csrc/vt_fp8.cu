@@ -544,7 +544,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (int k = max(0, it - kScaleSlots); k < it; ++k)
         mbar_wait(&sx_full[k % kScaleSlots], (k / kScaleSlots) & 1, ok ? kWaitLimit : 1u << 12);
     } else if (warp == kPromWarps + 1) {
-      // MMA issuer
+      // MMA issuer.  The limits of its waits do not count what the kernels ahead take.
+      griddep_wait();
       constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
       int s = 0, p = 0;
@@ -732,7 +733,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     if (!ok && lane == 0) atomicExch(&s_err, 1);
   }
   __syncwarp();
-  // every role has finished or given up; the MMAs have completed
+  __syncthreads();  // every role has finished or given up: no wait counts another's work
+  // the MMAs have completed
   const bool all_ok = __syncthreads_and(mbar_wait(&done_bar, 0) && s_err == 0 ? 1 : 0) != 0;
   griddep_launch_dependents();
   fence_after_sync();
@@ -996,7 +998,8 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       if (part == 0)
         for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full_bar[k % S], (k / S) & 1);
     } else if (warp == kPromWarps + 1 && part == 0) {
-      // MMA issuer
+      // MMA issuer.  The limits of its waits do not count what the kernels ahead take.
+      griddep_wait();
       constexpr uint32_t idesc = idesc_e4m3(kCtas * kBM, NR);
       constexpr uint32_t idesc_scaled = idesc_e4m3_scaled(kCtas * kBM, NR);
       auto commit = [&](uint64_t* bar) {
@@ -1298,7 +1301,8 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     if (!ok && lane == 0) atomicExch(&s_err, 1);
   }
   __syncwarp();
-  // every role has finished or given up; the MMAs have completed
+  __syncthreads();  // every role has finished or given up: no wait counts another's work
+  // the MMAs have completed
   const bool all_ok = __syncthreads_and(mbar_wait(&done_bar, 0) && s_err == 0 ? 1 : 0) != 0;
   griddep_launch_dependents();
   fence_after_sync();

@@ -551,6 +551,13 @@ int vt_block_graph_destroy(void* graph);
 int vt_selftest_wait(int32_t which, uint32_t limit, const uint32_t* flag, int32_t* dev_status,
                      void* stream);
 
+/* vt_selftest_overlap — a kernel of one thread that lets the kernel behind it
+ * start at once and then takes `limit` polls (about 3.8 us each, 1 <= limit <=
+ * 2^20) of an mbarrier that nothing arrives on: a predecessor that outlasts the
+ * limits of its successors' waits, which must not count it.
+ */
+int vt_selftest_overlap(uint32_t limit, void* stream);
+
 /* vt_selftest_draft_fp8 — vt_draft_logits_fp8 with a status word, in which the
  * threads that take over a thread block's sums act, from its item number give_up
  * (from 0, at most 65535) on, as if a wait of theirs had run out (-1: never).

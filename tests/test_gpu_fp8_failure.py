@@ -77,3 +77,37 @@ def test_logits_that_were_not_computed_are_nan(B, H, K, other):
     n = n if n < K else 0
     assert status == vt.VT_DEV_TIMEOUT
     assert torch.equal(z[:, :n], want[:, :n]) and bool(z[:, n:].isnan().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [0.0, 1.0])
+@pytest.mark.parametrize("B", [3, 100, 256])
+def test_a_long_predecessor_is_no_timeout(B, T):
+    """The product may start while a kernel ahead of the call, which let its successors start, has two seconds to
+    run; the limits of its waits, about a second, count from that kernel's end."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import drafter_sampling_gb300 as vt
+    H, K = 300, 5000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    hid = torch.randn((B, H), generator=g, device="cuda").to(torch.bfloat16)
+    W8, s, _ = vt.vt_quantize_head(torch.randn((K, H), generator=g, device="cuda").to(torch.bfloat16))
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    u = torch.rand(B, generator=g, device="cuda")
+    want = vt.vt_draft_step_fp8(hid, W8, s, ids, u, T)
+    got = [torch.empty_like(t) for t in want]
+    ws = torch.empty(vt.workspace_bytes("draft_fp8", B=B, H=H, K=K), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert vt.lib().vt_selftest_overlap(1 << 19, torch.cuda.current_stream().cuda_stream) == 0
+    vt.vt_draft_step_fp8(hid, W8, s, ids, u, T, q=got[0], tokens=got[1], dev_status=got[2], workspace=ws)
+    torch.cuda.synchronize()
+    assert int(got[2].item()) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_overlap_refusals():
+    from drafter_sampling_gb300 import _lib, build
+    build.build()
+    lib = _lib.load()
+    assert lib.vt_selftest_overlap(0, None) == _lib.VT_ERR_INVALID_ARG
+    assert lib.vt_selftest_overlap((1 << 20) + 1, None) == _lib.VT_ERR_INVALID_ARG
