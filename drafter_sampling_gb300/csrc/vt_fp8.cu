@@ -25,6 +25,7 @@ namespace vt {
 namespace {
 
 constexpr int kQB = 128;  // side of a scale block
+constexpr int kMaxRows = 65535 * kQB;  // K: the quantiser's grid, and far from where 32-bit row counts overflow
 
 // Exponent e of a block's scale 2^e from the bf16 bits of its largest
 // magnitude (sign cleared): the smallest e >= -126 with amax <= 448 * 2^e.
@@ -1520,6 +1521,7 @@ int check_fp8_args(const uint16_t* hidden, int B, int H, const uint8_t* W8, int6
                    const float* w_scale, int K, float T, bool allow_greedy) {
   if (!hidden || !W8 || !w_scale) return VT_ERR_INVALID_ARG;
   if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1) return VT_ERR_INVALID_ARG;
+  if (K > kMaxRows) return VT_ERR_UNSUPPORTED;
   if (ldw < H || ldw % 16 != 0 || (reinterpret_cast<uintptr_t>(W8) & 15) != 0)
     return VT_ERR_INVALID_ARG;
   if (!std::isfinite(T) || T < 0.f || (T == 0.f && !allow_greedy)) return VT_ERR_INVALID_ARG;
@@ -1536,8 +1538,8 @@ extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t
     return VT_ERR_INVALID_ARG;
   if (ldw < H || ldw % 16 != 0 || (reinterpret_cast<uintptr_t>(W8) & 15) != 0)
     return VT_ERR_INVALID_ARG;
+  if (K > kMaxRows) return VT_ERR_UNSUPPORTED;
   const int rows = (K + kQB - 1) / kQB;
-  if (rows > 65535) return VT_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int st = clear_status(s, dev_status);
   if (st != VT_OK) return st;
@@ -1558,7 +1560,7 @@ extern "C" int vt_quantize_head(const uint16_t* W, int32_t K, int32_t H, uint8_t
 }
 
 extern "C" size_t vt_draft_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K) {
-  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1) return 0;
+  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1 || K > vt::kMaxRows) return 0;
   return vt::carve_fp8(nullptr, B, H, K).bytes;
 }
 
@@ -1647,7 +1649,8 @@ int vt::draft_step_fp8_impl(const uint16_t* hidden, int32_t B, int32_t H, const 
 }
 
 extern "C" size_t vt_draft_topk_fp8_workspace_bytes(int32_t B, int32_t H, int32_t K, int32_t k) {
-  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1 || k < 1 || k > vt::kDraftTopkMax || k > K)
+  if (B < 1 || B > 4096 || H < 1 || H > 65536 || K < 1 || K > vt::kMaxRows || k < 1 ||
+      k > vt::kDraftTopkMax || k > K)
     return 0;
   return vt::align_up(vt_draft_fp8_workspace_bytes(B, H, K), 256) +
          vt::align_up((size_t)B * K * 4, 256);

@@ -389,7 +389,8 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
  *  w_scale  f32 [ceil(K/128), ceil(H/128)] out: s of each block
  *  dev_status int32 [1]       out: VT_DEV_NONFINITE (a NaN or infinity in W;
  *                             its block is unspecified)
- * 1 <= H <= 65536, 1 <= K <= 8388480 (65535 blocks).
+ * 1 <= H <= 65536, 1 <= K <= 8388480 (65535 blocks; above that the calls of this
+ * section return VT_ERR_UNSUPPORTED and the workspace queries 0).
  *
  * vt_draft_logits_fp8, vt_draft_step_fp8 and vt_draft_topk_fp8 are
  * vt_draft_logits, vt_draft_step and vt_draft_topk with

@@ -117,3 +117,21 @@ def test_binding_refusals_name_the_argument():
     assert vt.workspace_bytes("draft_fp8", B=2, H=64, K=100) > 0
     assert vt.workspace_bytes("draft_topk_fp8", B=2, H=64, K=100, k=8) > \
         vt.workspace_bytes("draft_fp8", B=2, H=64, K=100)
+
+
+@pytest.mark.parametrize("K", [65535 * 128 + 1, 2 ** 31 - 256, 2 ** 31 - 100, 2 ** 31 - 1])
+def test_heads_of_too_many_rows_are_refused(lib, K):
+    # rows beyond the quantiser's, up to where 32-bit counts of their blocks overflow
+    _, unsupported, _ = _bad()
+    huge = 1 << 50
+    assert lib.vt_quantize_head(FAKE, K, 64, FAKE, 64, FAKE, FAKE, None) == unsupported
+    for B in (2, 100, 200):
+        assert lib.vt_draft_fp8_workspace_bytes(B, 64, K) == 0
+        assert lib.vt_draft_topk_fp8_workspace_bytes(B, 64, K, 8) == 0
+        assert lib.vt_draft_logits_fp8(FAKE, B, 64, FAKE, 64, FAKE, K, 1.0, FAKE, K, FAKE, huge, None) == unsupported
+        for T in (0.0, 1.0):
+            assert lib.vt_draft_step_fp8(FAKE, B, 64, FAKE, 64, FAKE, FAKE, K, FAKE, T, FAKE, K, FAKE, 1, FAKE, FAKE,
+                                         huge, None) == unsupported
+        assert lib.vt_draft_topk_fp8(FAKE, B, 64, FAKE, 64, FAKE, FAKE, K, 8, 1.0, FAKE, FAKE, FAKE, FAKE, huge,
+                                     None) == unsupported
+    assert lib.vt_draft_fp8_workspace_bytes(2, 64, 65535 * 128) > 0
