@@ -55,6 +55,29 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr,
+                       const cuuint64_t (&dims)[2], cuuint64_t ld_bytes,
+                       const cuuint32_t (&box)[2]) {
+  const auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t strides[1] = {ld_bytes};
+  const cuuint32_t es[2] = {1, 1};
+  auto encode = [&] {
+    return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // a host thread that has made no CUDA runtime call yet has no current
+    // context, and the encoder is a driver call, which does not make one current
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    r = encode();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int kGemvNT = 256;        // 8 warps
@@ -891,15 +914,8 @@ int launch_gemv(cudaStream_t s, const uint16_t* hidden, int B, int H, const uint
 // 64 columns (128 bytes, 128-byte swizzle) x box_rows rows
 bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                    uint32_t box_rows) {
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, {cols, rows}, cols * 2,
+                           {64, box_rows});
 }
 
 bool umma_supported(const uint16_t* hidden, int B, int H, const uint16_t* W) {

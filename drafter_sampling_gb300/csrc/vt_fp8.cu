@@ -1360,15 +1360,8 @@ Fp8Ws carve_fp8(void* base, int B, int H, int K) {
 // ld bytes, boxes of 128 columns (128-byte swizzle) x box_rows rows
 bool make_e4m3_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                    uint32_t box_rows) {
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, {cols, rows}, ld,
+                           {128, box_rows});
 }
 
 // a launch that overlaps the kernel that quantises the hidden states, as a

@@ -12,6 +12,12 @@ namespace vt {
 // cuTensorMapEncodeTiled of the loaded driver, or nullptr
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// 2-D tensor map of rows of dims[0] elements, ld_bytes apart, dims[1] of them:
+// boxes of box[0] x box[1] elements, 128-byte swizzle, zeros outside.  false: failed.
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr,
+                       const cuuint64_t (&dims)[2], cuuint64_t ld_bytes,
+                       const cuuint32_t (&box)[2]);
+
 // Clears the status word of a call whose one kernel would otherwise need a
 // memset before it (which costs the call 2.5 us more).  The kernel behind it
 // is launched with programmatic stream serialization, so the two launches
