@@ -967,9 +967,12 @@ int calibrate_impl(const int32_t* ids, int64_t n, int32_t V, int32_t K, uint32_t
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)num_sms()));
     if (use_hot) {
       const size_t smem = ((size_t)(V + kLutIds - 1) / kLutIds + 1 + kHotMax) * 4;
+      // the most of any V, so that every call sets the same limit: another host
+      // thread may set it between here and the launch
+      constexpr int smem_max = (kHotBitmapMaxV / kLutIds + 2 + kHotMax) * 4;
       VT_RETURN_IF_CUDA(cudaFuncSetAttribute(hist_main_kernel<true>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem));
+                                             smem_max));
       VT_RETURN_IF_CUDA(launch_pdl(hist_main_kernel<true>, dim3((unsigned)grid), dim3(kMainNT),
                                    smem, s, ids, n, (int)V, (const int*)ws.hot_list,
                                    (const int*)ws.hot_n, (const unsigned long long*)ws.top_key,

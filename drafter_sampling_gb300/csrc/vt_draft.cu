@@ -878,7 +878,10 @@ cudaError_t launch_gemv_bt(int grid, cudaStream_t s, const uint16_t* hidden, int
   const size_t smem = (size_t)BT * H * sizeof(uint16_t);
   auto kern = draft_gemv_kernel<BT, 4>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most of any H (launch_gemv), so that every call sets the same limit:
+    // another host thread may set it between here and the launch
+    constexpr int smem_max = (BT == 1 ? 200 : 160) * 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
     if (e != cudaSuccess) return e;
   }
   kern<<<grid, kGemvNT, smem, s>>>(hidden, B, H, W, K, out_scale, out, ldo, part, zero_ints, nzero,

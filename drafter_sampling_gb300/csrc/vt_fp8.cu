@@ -1365,12 +1365,14 @@ bool make_e4m3_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols
 }
 
 // a launch that overlaps the kernel that quantises the hidden states, as a
-// grid of clusters of `cluster` CTAs
+// grid of clusters of `cluster` CTAs.  smem_max is the most that this kernel is
+// ever launched with: the kernel's limit is set to the same value by every
+// call, as another host thread may set it between here and the launch.
 template <typename K>
-int launch_product(cudaStream_t s, K kern, int grid, int threads, size_t smem, int cluster,
-                   const CUtensorMap& mw, const CUtensorMap& mx, const Fp8Args& fa) {
+int launch_product(cudaStream_t s, K kern, int grid, int threads, size_t smem, size_t smem_max,
+                   int cluster, const CUtensorMap& mw, const CUtensorMap& mx, const Fp8Args& fa) {
   VT_RETURN_IF_CUDA(
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -1404,22 +1406,26 @@ int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, 
   // longer ring (B = 50, K = 10007, H = 1500, greedy: 11.6 against 12.9 us; B = 64,
   // K = 19000, H = 4096: 19.0 against 20.0); with fewer columns that was slower by
   // up to 4%, the next call's product then starting later.
-  const int ring = (fa.items > kSms || BN < 64 ? 96 : 150) * 1024;
+  constexpr int kRing = 96 * 1024, kLongRing = 150 * 1024;
+  const int ring = fa.items > kSms || BN < 64 ? kRing : kLongRing;
   fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((ring - zt) / stage)));
   return launch_product(s, head_fp8_kernel<BN>, std::min(fa.items, 2 * kSms), kNarrowNT,
-                        (size_t)fa.h.stages * stage + zt + 1024, 1, mw, mx, fa);
+                        (size_t)fa.h.stages * stage + zt + 1024,
+                        (BN < 64 ? kRing : kLongRing) + 1024, 1, mw, mx, fa);
 }
 
 template <bool TWO>
 int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
   constexpr int stage = umma::kBM * 128 + (TWO ? 128 : 256) * 128, ctas = TWO ? 2 : 1;
+  constexpr int stages = 160 * 1024 / stage;  // five of a pair, three of a single CTA
   constexpr size_t out = (size_t)(kBatchNP / 32) * 32 * kOutPitch * sizeof(float);
-  fa.h.stages = 160 * 1024 / stage;  // five of a pair, three of a single CTA
+  constexpr size_t smem = stages * stage + out + 1024;
+  fa.h.stages = stages;
   fa.nchunk = fa.Bp / (128 * ctas);
   fa.items = (fa.h.K + kBatchRowsW - 1) / kBatchRowsW * fa.nchunk;
   return launch_product(s, fa.h.part != nullptr ? batch_fp8_kernel<TWO, true> : batch_fp8_kernel<TWO, false>,
-                        ctas * std::min(fa.items, kSms / ctas), kBatchNT,
-                        (size_t)fa.h.stages * stage + out + 1024, ctas, mw, mx, fa);
+                        ctas * std::min(fa.items, kSms / ctas), kBatchNT, smem, smem, ctas, mw,
+                        mx, fa);
 }
 
 // z = out_scale * hidden @ (scaled W8)^T; part[tile][b] partials of 128-row

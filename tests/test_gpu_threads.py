@@ -63,3 +63,43 @@ def test_first_call_of_a_thread(vt, make, bound):
     torch.cuda.synchronize()
     assert not failed, failed
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _calibrate(vt, i):
+    V, K = (3001, 400003)[i], 100
+    ids = torch.randint(0, V, (20000,), dtype=torch.int32, device="cuda")
+    out = dict(counts=torch.empty(V, dtype=torch.int32, device="cuda"),
+               topk_ids=torch.empty(K, dtype=torch.int32, device="cuda"),
+               dev_status=torch.empty(1, dtype=torch.int32, device="cuda"),
+               workspace=torch.empty(vt.workspace_bytes("calibrate", n=20000, V=V, K=K), dtype=torch.uint8,
+                                     device="cuda"))
+    return lambda st: vt.vt_calibrate_topk(ids, V, K, stream=st, **out)
+
+
+@pytest.mark.parametrize("make,calls", [(_fp8, 20000), (_bf16, 20000), (_calibrate, 5000)])
+def test_two_threads_at_once(vt, make, calls):
+    """Of sizes for which one kernel is launched with different amounts of shared memory."""
+    fns = [make(vt, i) for i in ((1, 2) if make is _bf16 else (0, 1))]
+    want = [[t.clone() for t in f(None)] for f in fns]
+    torch.cuda.synchronize()
+    failed, got = [], [None, None]
+
+    def run(i):
+        st = torch.cuda.Stream()
+        try:
+            for n in range(calls):
+                got[i] = fns[i](st)
+                if n % 100 == 99:             # no more in flight than the launch queue takes
+                    st.synchronize()
+        except Exception as e:                # noqa: BLE001 (reported below, from the main thread)
+            failed.append((i, n, e))
+        st.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
