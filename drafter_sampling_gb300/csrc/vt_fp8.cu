@@ -752,7 +752,7 @@ constexpr int kBatchNP = 256;                // promoting threads
 constexpr int kBatchNT = kBatchNP + 128;     // and a warpgroup: loads, MMAs, two idle warps
 constexpr int kBatchRowsW = 256;             // rows of W8 of an item: two tiles of 128
 constexpr int kTurn = 4;                     // groups whose scales are handed over at once
-constexpr int kUnit = 32;                    // groups that the tensor cores sum up
+constexpr int kUnit = 16;                    // groups that the tensor cores sum up
 constexpr int kTurns = 4;                    // turns whose scales are in tensor memory at once
 constexpr int kGroupCols = 16;               // tensor-memory columns of a group's scales
 // floats: a warp's 32 x 32 block on its way out; 16-byte accesses by row and by
@@ -844,16 +844,21 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
 // Where all weight scales of an item are powers of two, as this library's
 // quantiser leaves them, the tensor cores scale the products: both scales of a
 // group are then bytes in tensor memory, written by the promoting warps up to
-// four turns of four groups ahead, and a unit of up to 32 groups is summed there
+// four turns of four groups ahead, and a unit of up to 16 groups is summed there
 // before it is read and added to fp32 sums in registers.  The tensor cores hold
-// the running sum in fp32 but cut off, rather than round, each addition: 2.1e-7 of
-// the result (2-norm, H = 4096 and 8192) against 0.7e-7 with units of eight groups
-// or of one, which are slower.  Any other scales: units of one group, not scaled
+// the running sum in fp32 but cut off, rather than round, each addition, so the
+// unit's length is a choice between digits and speed.  Off in the 2-norm at H =
+// 4096 / 8192, and us at B = 256 / 1000 (K = 38016, H = 4096): units of 8 groups
+// 0.7 / 0.8e-7, 44 / 143; of 16, 1.1 / 1.1e-7, 41.0 / 122; of 32, 2.1 / 2.1e-7,
+// 40.4 / 115.  A plain fp32 product is off by 0.8 / 1.2e-7, the kernel for up to 64
+// rows by 0.9 / 1.3e-7, so 16 keeps fp32's digits (H = 2048: 1.0e-7 against 0.6e-7,
+// where units of 8 cost 4%).  Any other scales: units of one group, not scaled
 // by the tensor cores, in two accumulators (the second where the scales would
 // be), promoted times the scales.
 //
-// What bounds it, at B = 1000, K = 38016, H = 4096 (117 us, 2660 TFLOP/s): a group
-// is 513 cycles of MMAs, about 660 pass, of which 180 are waits for the loads (a
+// What bounds it, at B = 1000, K = 38016, H = 4096 (122 us, 2550 TFLOP/s; the figures
+// that follow are of units of 32 groups, 115 to 117 us): a group is 513 cycles of
+// MMAs, about 660 pass, of which 180 are waits for the loads (a
 // pair asks L2 for 64 KB a group; four stages instead of five: 123 us).  Other
 // scales: 195 us, as MMAs stand still while tensor memory is read, some 380 cycles
 // for a group's sums (B = 256: 53 against 41).  Two accumulators of 128 columns in
@@ -1160,8 +1165,9 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       if (scaled) {
         for (int kb = 0; kb < nk && ok; kb += kUnit) {
-          // with the scales of the next unit's first turns
-          const int upto = min(nk, kb + kUnit + kTurns * kTurn);
+          // with the scales of the next unit's first turns, but for the one that
+          // would wait for this unit's last MMAs: its sums come first
+          const int upto = min(nk, kb + kUnit + (kTurns - 1) * kTurn);
           for (; ahead < upto && ok; ahead += kTurn) {
             put_scales(b0, at, g, nk - ahead);
             g += kTurn;
@@ -1242,7 +1248,9 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         __syncwarp();
-        // the MMAs may be through with the next item's first turns
+        // the MMAs may be through with the next item's first turns, up to three of
+        // them while its first unit's sums are not read
+        static_assert(3 * kTurn <= kUnit, "a turn of the next unit would be waited for");
         if (!PART && c > 0 && ok && scaled && ahead > 0 && ahead < nk) {
           const int chunk = chunk_of(next);
           int ga = next / fa.nchunk % nk + ahead;
