@@ -1,5 +1,7 @@
 // Library-wide entry points of libvt: status text, ABI version and the
 // self-test of the bounded waits.
+#include <atomic>
+
 #include "vt_common.cuh"
 #include "vt_internal.h"
 #include "vt_umma.cuh"
@@ -56,6 +58,20 @@ __global__ void clear_status_kernel(int* dev_status) {
 }
 
 }  // namespace
+
+int num_sms() {
+  // per device, filled on first use; concurrent first calls store the same
+  // value (relaxed atomics, so there is no data race)
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 int clear_status(cudaStream_t s, int32_t* dev_status) {
   clear_status_kernel<<<1, 1, 0, s>>>(dev_status);

@@ -26,11 +26,11 @@
 //             counts, then tile-local scans that write trim_ids and inv_map),
 //             row gather of W.
 #include <algorithm>
-#include <atomic>
 #include <cooperative_groups.h>
 #include <utility>
 
 #include "vt_common.cuh"
+#include "vt_internal.h"
 
 namespace cg = cooperative_groups;
 
@@ -884,20 +884,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
-int num_sms() {
-  // per device, filled on first use; concurrent first calls store the same
-  // value (relaxed atomics, so there is no data race)
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  int n = cache[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cache[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 }  // namespace

@@ -1399,8 +1399,6 @@ int launch_product(cudaStream_t s, K kern, int grid, int threads, size_t smem, s
   return VT_OK;
 }
 
-constexpr int kSms = 152;
-
 template <int BN>
 int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp8Args fa) {
   constexpr int stage = umma::kABytes + BN * 128;
@@ -1415,9 +1413,10 @@ int launch_narrow(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, 
   // K = 19000, H = 4096: 19.0 against 20.0); with fewer columns that was slower by
   // up to 4%, the next call's product then starting later.
   constexpr int kRing = 96 * 1024, kLongRing = 150 * 1024;
-  const int ring = fa.items > kSms || BN < 64 ? kRing : kLongRing;
+  const int sms = num_sms();
+  const int ring = fa.items > sms || BN < 64 ? kRing : kLongRing;
   fa.h.stages = std::max(2, std::min(umma::kMaxStages, (int)((ring - zt) / stage)));
-  return launch_product(s, head_fp8_kernel<BN>, std::min(fa.items, 2 * kSms), kNarrowNT,
+  return launch_product(s, head_fp8_kernel<BN>, std::min(fa.items, 2 * sms), kNarrowNT,
                         (size_t)fa.h.stages * stage + zt + 1024,
                         (BN < 64 ? kRing : kLongRing) + 1024, 1, mw, mx, fa);
 }
@@ -1432,7 +1431,7 @@ int launch_wide(cudaStream_t s, const CUtensorMap& mw, const CUtensorMap& mx, Fp
   fa.nchunk = fa.Bp / (128 * ctas);
   fa.items = (fa.h.K + kBatchRowsW - 1) / kBatchRowsW * fa.nchunk;
   return launch_product(s, fa.h.part != nullptr ? batch_fp8_kernel<TWO, true> : batch_fp8_kernel<TWO, false>,
-                        ctas * std::min(fa.items, kSms / ctas), kBatchNT, smem, smem, ctas, mw,
+                        ctas * std::min(fa.items, num_sms() / ctas), kBatchNT, smem, smem, ctas, mw,
                         mx, fa);
 }
 

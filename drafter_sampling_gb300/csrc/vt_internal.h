@@ -18,6 +18,9 @@ bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr
                        const cuuint64_t (&dims)[2], cuuint64_t ld_bytes,
                        const cuuint32_t (&box)[2]);
 
+// Multiprocessors of the current device (152 where that cannot be asked)
+int num_sms();
+
 // Clears the status word of a call whose one kernel would otherwise need a
 // memset before it (which costs the call 2.5 us more).  The kernel behind it
 // is launched with programmatic stream serialization, so the two launches

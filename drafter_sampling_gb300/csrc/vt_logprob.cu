@@ -717,13 +717,14 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
 
 // Thread blocks per row: the count that gives the shortest schedule, taking a
 // block's time as its chunks plus three more for its start and its join, and
-// kLpPerSm blocks of the 152 SMs running at once.
+// kLpPerSm blocks of each SM running at once.
 int lp_cluster(int64_t R, int V, int elem) {
   const int64_t chunks = ((int64_t)V * elem + kLpChunk - 1) / kLpChunk;
+  const int64_t slots = (int64_t)num_sms() * kLpPerSm;
   int best = 1;
   int64_t least = INT64_MAX;
   for (int C = 1; C <= kLpMaxC && C <= chunks; C *= 2) {
-    const int64_t waves = (R * C + 152 * kLpPerSm - 1) / (152 * kLpPerSm);
+    const int64_t waves = (R * C + slots - 1) / slots;
     const int64_t t = waves * ((chunks + C - 1) / C + 3);
     if (t < least) {
       least = t;
@@ -739,7 +740,7 @@ int launch_logprobs(cudaStream_t s, const LpArgs& a, int C) {
   VT_RETURN_IF_CUDA(
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min(a.R, 152 * kLpPerSm)));
+  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min(a.R, num_sms() * kLpPerSm)));
   cfg.blockDim = dim3(kLpNT + 32);
   cfg.dynamicSmemBytes = kLpSmem;
   cfg.stream = s;
