@@ -601,7 +601,8 @@ def vt_draft_logits_fp8(hidden, W8, w_scale, temperature: float = 1.0, logits=No
                         stream=None):
     """vt_draft_logits through an e4m3 head (vt_quantize_head); the hidden
     states are quantised inside the call.  w_scale may hold any finite values;
-    with more than 64 rows, powers of two are faster."""
+    with 129 to 256 rows (and other even numbers of 128-row chunks), powers of two
+    are faster."""
     dev = _first(hidden, "hidden")
     K, H, ldw, p8, sp = _head_fp8(W8, w_scale, dev)
     B, hp = _hidden(hidden, H, dev)

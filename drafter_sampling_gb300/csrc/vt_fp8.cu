@@ -747,7 +747,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 // one warp issues the loads and one the MMAs.  A promoting thread sums 128
 // values and reads another 32 at a time, more registers than an even split over
 // the block gives, so the third warpgroup gives most of its own to the others:
-// 3 x 168 = 2 x 232 + 40 a thread.
+// 3 x 168 = 2 x 224 + 56 a thread, with which neither side spills (2 x 232 + 40:
+// the issuing warp did, 24 of 150 bytes in its loop; B = 1000: 124 against 119 us).
 constexpr int kBatchNP = 256;                // promoting threads
 constexpr int kBatchNT = kBatchNP + 128;     // and a warpgroup: loads, MMAs, two idle warps
 constexpr int kBatchRowsW = 256;             // rows of W8 of an item: two tiles of 128
@@ -841,30 +842,34 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
 // head_fp8_kernel; in a pair the first CTA issues the MMAs for both and holds
 // the barriers that they wait on.
 //
+// Single CTAs promote every group: its sums are read, and added times sw * sx to
+// fp32 sums in registers, while the next group is summed in the other of two
+// accumulators.  So do pairs with any scales that are not powers of two.
 // Where all weight scales of an item are powers of two, as this library's
-// quantiser leaves them, the tensor cores scale the products: both scales of a
-// group are then bytes in tensor memory, written by the promoting warps up to
-// four turns of four groups ahead, and a unit of up to 16 groups is summed there
-// before it is read and added to fp32 sums in registers.  The tensor cores hold
-// the running sum in fp32 but cut off, rather than round, each addition, so the
-// unit's length is a choice between digits and speed.  Off in the 2-norm at H =
-// 4096 / 8192, and us at B = 256 / 1000 (K = 38016, H = 4096): units of 8 groups
-// 0.7 / 0.8e-7, 44 / 143; of 16, 1.1 / 1.1e-7, 41.0 / 122; of 32, 2.1 / 2.1e-7,
-// 40.4 / 115.  A plain fp32 product is off by 0.8 / 1.2e-7, the kernel for up to 64
-// rows by 0.9 / 1.3e-7, so 16 keeps fp32's digits (H = 2048: 1.0e-7 against 0.6e-7,
-// where units of 8 cost 4%).  Any other scales: units of one group, not scaled
-// by the tensor cores, in two accumulators (the second where the scales would
-// be), promoted times the scales.
+// quantiser leaves them, a pair has the tensor cores scale the products: both
+// scales of a group are then bytes in tensor memory (where the second accumulator
+// would be), written by the promoting warps up to four turns of four groups
+// ahead, and a unit of up to 16 groups is summed there before it is read.  MMAs
+// stand still while tensor memory is read, some 380 cycles for a group's sums; a
+// pair is bound by its MMAs and gains from fewer reads (K = 38016, H = 4096: B = 256
+// 40.2 against 44.5 us, B = 1000 119 against 156), a single CTA, whose three
+// stages leave it waiting for loads, does not (K = 20000, H = 8192, B = 128: 40.7
+// against 44.0 scaled; B = 300: 59.9 against 60.3).
 //
-// What bounds it, at B = 1000, K = 38016, H = 4096 (122 us, 2550 TFLOP/s; the figures
-// that follow are of units of 32 groups, 115 to 117 us): a group is 513 cycles of
-// MMAs, about 660 pass, of which 180 are waits for the loads (a
-// pair asks L2 for 64 KB a group; four stages instead of five: 123 us).  Other
-// scales: 195 us, as MMAs stand still while tensor memory is read, some 380 cycles
-// for a group's sums (B = 256: 53 against 41).  Two accumulators of 128 columns in
-// turn, to hide the reads, made every MMA slower: they read the batch's stage
-// twice, and shared memory has the loads' traffic too (161 us).  A row's 64
-// instead of 128 bytes out in one piece, for a sixth stage: 127 us.
+// The tensor cores hold the running sum in fp32 but cut off, rather than round,
+// each addition, so the unit's length is a choice between digits and speed.  Off
+// in the 2-norm at H = 4096 / 8192, and us at B = 256 / 1000 (K = 38016, H = 4096):
+// units of 8 groups 0.7 / 0.8e-7, 44.9 / 144; of 16, 1.1 / 1.1e-7, 40.2 / 119; of 32,
+// 2.1 / 2.1e-7, 39.8 / 112.  A plain fp32 product is off by 0.8 / 1.2e-7, groups that
+// are promoted one by one by 0.7 / 1.0e-7, so 16 keeps fp32's digits.
+//
+// What bounds it, at B = 1000, K = 38016, H = 4096 (119 us, 2620 TFLOP/s): a group is
+// 513 cycles of MMAs, about 660 pass, of which 180 are waits for the loads (a
+// pair asks L2 for 64 KB a group; four stages instead of five cost 5%).  Two
+// accumulators of 128 columns in turn, to hide the reads, made every MMA slower:
+// they read the batch's stage twice, and shared memory has the loads' traffic
+// too (161 against 129 us, at an earlier step).  A row's 64 instead of 128 bytes out
+// in one piece, for a sixth stage: 10 us slower.
 template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -942,7 +947,7 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   // item -> block of W8 rows, batch chunk.  The chunks of a block are
   // neighbours, so its weights are read from HBM once.
   if (warp >= kPromWarps) {
-    regs_give<40>();
+    regs_give<56>();
     const bool leader = elect_one();  // one thread issues; the warp stays together
     if (warp == kPromWarps) {
       // TMA producer: the first stages' weights before the wait on the kernel
@@ -1018,56 +1023,72 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       int u = 0, t = 0, s = 0;  // units and turns so far; the next group's stage
       uint32_t sphase = 0;
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+      // one group's MMAs, once its operands are there
+      auto sum_group = [&](auto mma) {
+        fence_after_sync();
+        if (leader) {
+          const uint64_t xdesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
+          const uint64_t wdesc = xdesc + (kXBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 elements = 32 bytes per step
+            mma(kk, xdesc + 2 * kk, wdesc + 2 * kk);
+          commit(&empty_bar[s]);
+        }
+        if (++s == S) {
+          s = 0;
+          sphase ^= 1;
+        }
       };
       int at = 0;
       for (int item = first; item < items && ok; item += step, at ^= 1) {
         bool scaled = false;
-        for (int k = 0; k < nk && ok;) {
-          wait(&ready[u & 1], (u >> 1) & 1);
+        if constexpr (TWO) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&ready[u & 1], (u >> 1) & 1)) != 0;
           if (!ok) break;
-          if (k == 0) scaled = scaled_sh[at] != 0;
-          const int end = scaled ? min(nk, k + kUnit) : k + 1;
-          const uint32_t acc = tmem + (scaled ? 0u : (uint32_t)((u & 1) * NR));
-          uint32_t add = 0;
-          for (; k < end; ++k) {
-            if (scaled && k % kTurn == 0) wait(&scales_full[t % kTurns], t / kTurns & 1);
-            if (ok) wait(&full_bar[s], sphase);
+          scaled = scaled_sh[at] != 0;
+        }
+        // a loop for either kind of scales: with the choice inside, MMAs were issued
+        // so much later that units of one group took a quarter longer
+        if (!scaled) {
+          for (int k = 0; k < nk; ++k, ++u) {
+            const int p = u & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], sphase) &&
+                                             mbar_wait(&ready[p], (u >> 1) & 1)) != 0;
             if (!ok) break;
-            fence_after_sync();
+            const uint32_t acc = tmem + (uint32_t)(p * NR);
+            sum_group([&](int kk, uint64_t x, uint64_t w) {
+              mma_e4m3<TWO>(acc, x, w, idesc, kk > 0 ? 1u : 0u);
+            });
+            if (leader) commit(&acc_full[p]);
+          }
+          continue;
+        }
+        for (int k = 0; k < nk && ok; ++u) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&ready[u & 1], (u >> 1) & 1)) != 0;
+          uint32_t add = 0;
+          for (const int end = min(nk, k + kUnit); k < end && ok; ++k) {
+            const int turn = t % kTurns;
+            ok = __all_sync(0xffffffffu, mbar_wait(&scales_full[turn], t / kTurns & 1) &&
+                                             mbar_wait(&full_bar[s], sphase)) != 0;
+            if (!ok) break;
             const uint32_t scales = tmem + scale_cols(t) + (uint32_t)(k % kTurn * kGroupCols);
-            const bool turn_ends = scaled && (k % kTurn == kTurn - 1 || k + 1 == nk);
-            if (leader) {
-              const uint64_t xdesc = desc0 + (uint64_t)(s * (stage_bytes >> 4));
-              const uint64_t wdesc = xdesc + (kXBytes >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {  // 32 elements = 32 bytes per step
-                if (scaled)
-                  mma_e4m3_scaled<TWO>(acc, xdesc + 2 * kk, wdesc + 2 * kk, idesc_scaled, scales,
-                                       scales + 4, add);
-                else
-                  mma_e4m3<TWO>(acc, xdesc + 2 * kk, wdesc + 2 * kk, idesc, add);
-                add = 1;
-              }
-              commit(&empty_bar[s]);
-              if (turn_ends) commit(&scales_free[t % kTurns]);
-            }
-            if (turn_ends) ++t;
-            if (++s == S) {
-              s = 0;
-              sphase ^= 1;
+            sum_group([&](int, uint64_t x, uint64_t w) {
+              mma_e4m3_scaled<TWO>(tmem, x, w, idesc_scaled, scales, scales + 4, add);
+              add = 1;
+            });
+            if (k % kTurn == kTurn - 1 || k + 1 == nk) {
+              if (leader) commit(&scales_free[turn]);
+              ++t;
             }
           }
           if (ok && leader) commit(&acc_full[u & 1]);
-          ++u;
         }
       }
       if (!ok) atomicExch(&s_err, 1);
       if (leader) commit(&done_bar);
     }
   } else {
-    regs_take<232>();
+    regs_take<224>();
     // this thread's batch row (TMEM lane) and its half of the W8 rows
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
@@ -1095,7 +1116,8 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         two = two && is_pow2(s);
         sw_sh[at][half][g] = s;
       }
-      return barrier_and(1, kBatchNP, two);
+      two = barrier_and(1, kBatchNP, two);
+      return TWO && two;
     };
     // The scales of the next turn, of up to n groups from group g on.  Turns
     // alternate between the two halves' warps, each of which writes where its own
@@ -1338,8 +1360,8 @@ struct Fp8Ws {
 int pad_batch(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : (B + 127) / 128 * 128; }
 
 // Wide batches of an even number of 128-row chunks go to pairs of CTAs, an odd
-// number to single ones (K = 38016, H = 4096, B = 300: 60.5 us against 62.0 padded
-// to pairs; K = 32768, H = 2048, B = 128: 18.9 against 23.4)
+// number to single ones (K = 38016, H = 4096, B = 300: 59.9 us against 62.5 padded
+// to pairs; K = 32768, H = 2048, B = 128: 17.9 against 22.4)
 bool paired(int Bp) { return Bp % 256 == 0; }
 
 Fp8Ws carve_fp8(void* base, int B, int H, int K) {
