@@ -294,9 +294,13 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// No data in memory is handed over with this arrival (the tensor-memory reads
-// before it have completed), so it needs no release at cluster scope, which
-// would cost some 1000 cycles a group.
+// What is handed over with this arrival is tensor memory only: accumulators that
+// have been read, and scales that have been written, for the first CTA's MMAs.
+// A caller has waited for its loads and stores of tensor memory to complete
+// (tcgen05.wait::ld, ::st) and ordered them before the arrival
+// (tcgen05.fence::before_thread_sync; the issuing warp has the ::after one), so
+// it needs no release at cluster scope, which is for other memory and would cost
+// some 1000 cycles a group.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1096,7 +1100,8 @@ batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     int u = 0, t = 0;  // units read, and turns whose scales have been written, so far
     bool ok = true;  // once false it stays so: what a late wait would find belongs to another item
     auto chunk_of = [&](int item) { return (item - item / fa.nchunk * fa.nchunk) * kCtas * kBM + part * kBM; };
-    // one of this warp's arrivals, once its accesses to tensor memory are complete
+    // One of this warp's arrivals.  Its loads and stores of tensor memory have
+    // completed (tmem_ld32 waits, tmem_st_wait); the fence orders them before it.
     auto give = [&](uint64_t* bar) {
       fence_before_sync();
       __syncwarp();
