@@ -780,8 +780,8 @@ class BlockGraph:
     The tensors are fixed at capture and kept alive by this object; a replay
     reads what they hold when it runs.  Replays may run on any stream: the
     constructor waits until the current stream has no other use of their
-    memory, and their memory is not given to another while a stream that
-    launched the graph is at it.  Outputs (q, draft_tokens,
+    memory, and their memory is not given to another while a stream of torch's
+    that launched the graph is at it.  Outputs (q, draft_tokens,
     out_tokens, out_num_accepted, out_accept_prob, dev_status [2]) are
     attributes.  temperature == 0 captures the greedy block (u_draft,
     u_accept and u_resample may then be None).  With w_scale, W_trim is an
@@ -864,8 +864,10 @@ class BlockGraph:
         ptr = _stream_ptr(stream)
         if ptr not in self._known:
             self._known.add(ptr)
-            s = _TORCH.cuda.ExternalStream(ptr, device=self.q.device)
-            for t in (*self._keep, self.q, self.draft_tokens, self.out_tokens, self.out_num_accepted,
+            s = _TORCH.cuda.current_stream() if stream is None else stream
+            # (a stream of the caller's own may not live as long as the tensors)
+            own = not isinstance(s, _TORCH.cuda.Stream) or isinstance(s, _TORCH.cuda.ExternalStream)
+            for t in () if own else (*self._keep, self.q, self.draft_tokens, self.out_tokens, self.out_num_accepted,
                       self.out_accept_prob, self.dev_status, self.workspace):
                 if t is not None:
                     t.record_stream(s)

@@ -401,16 +401,16 @@ int vt_verify_tree(const void* target_logits, int32_t logits_dtype, int32_t B, i
  * x8, sx are the hidden states quantised inside the call by the rule above
  * per row and group.  A group's products are summed by the tensor cores and
  * its sum enters the fp32 sum over the groups times its two scales, so
- * w_scale may hold any finite fp32 values, not only powers of two.  For 129
- * to 256 rows, and every other even number of 128-row chunks, blocks of 256 rows
- * of W8 whose scales are all powers of two are faster: the tensor cores apply
- * both scales and sum up to 16 groups (in fp32, cutting off instead of
- * rounding).  Either way the logits are as near to
- * the exact sums as those of a plain fp32 product: on random inputs within
- * 1.5e-7 of them in the 2-norm for H <= 8192.  A row of hidden states with a NaN
- * or an infinity gives NaN logits in that row.  vt_draft_logits_fp8 returns no
- * status word: the logits that a wait which ran out (VT_DEV_TIMEOUT) kept from
- * being computed are NaN.
+ * w_scale may hold any finite fp32 values, not only powers of two (the two
+ * scales are multiplied in fp32: a product beyond it gives infinities or NaN).
+ * For 129 to 256 rows, and every other even number of 128-row chunks, blocks of
+ * 256 rows of W8 whose scales are all powers of two are faster: the tensor cores
+ * apply both scales and sum up to 16 groups (in fp32, cutting off instead of
+ * rounding).  Either way the logits are as near to the exact sums as those of a
+ * plain fp32 product: on random inputs within 1.5e-7 of them in the 2-norm for
+ * H <= 8192.  A row of hidden states with a NaN or an infinity gives NaN logits
+ * in that row.  vt_draft_logits_fp8 returns no status word: the logits that a
+ * wait which ran out (VT_DEV_TIMEOUT) kept from being computed are NaN.
  * hidden, logits, trim_ids, uniforms, q, tokens and the temperature are as
  * there; W8, ldw and w_scale as vt_quantize_head leaves them.  Like W_trim,
  * W8 and w_scale must not be written by a kernel that may still be running

@@ -200,3 +200,30 @@ def test_a_block_graph_made_while_its_stream_is_busy_and_launched_on_another():
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.uint8), want[2])
         del others, out
+
+
+@pytest.mark.gpu
+def test_a_block_graph_outlives_a_stream_of_the_callers_own():
+    """A raw stream, destroyed after its replay and before the graph: the tensors' memory is freed without it."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import ctypes
+    import gc
+
+    import drafter_sampling_gb300 as vt
+    rt = ctypes.CDLL("libcudart.so.13" if torch.version.cuda.startswith("13") else "libcudart.so")
+    raw = ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(raw), 1) == 0
+    ids = torch.arange(K, dtype=torch.int32, device="cuda")
+    inv = torch.cat([ids, torch.full((K,), -1, dtype=torch.int32, device="cuda")])
+    g = vt.BlockGraph(torch.randn((1, B, H), device="cuda").to(torch.bfloat16),
+                      torch.randn((K, H), device="cuda").to(torch.bfloat16), ids, inv,
+                      torch.randn((B, 2, 2 * K), device="cuda"), temperature=0.0)
+    torch.cuda.synchronize()
+    g.launch(torch.cuda.ExternalStream(raw.value))
+    assert rt.cudaStreamSynchronize(raw) == 0 and rt.cudaStreamDestroy(raw) == 0
+    assert g.dev_status.tolist() == [0, 0]
+    del g
+    gc.collect()
+    torch.empty(1 << 20, device="cuda").fill_(1.0)
+    torch.cuda.synchronize()
