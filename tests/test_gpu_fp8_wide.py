@@ -117,3 +117,32 @@ def test_logits_keep_the_digits_of_an_fp32_product(vt, B, H, other):
     ref = _dev(fp8.quantize_rows(hid)) @ w.T
     z = vt.vt_draft_logits_fp8(_dev(hid.view(np.int16)), W8, s)
     assert float((z.double() - ref).norm() / ref.norm()) <= 1.5e-7
+
+
+@pytest.mark.parametrize("B,H", [(100, 640), (256, 640), (256, 4200), (300, 4200), (512, 2110)])
+def test_rows_groups_and_blocks_of_very_different_scale(vt, B, H):
+    """Powers of two from 2^-110 to 2^100 between rows, groups and blocks, and groups and blocks of zeros (whose
+    scale is 2^-126): with A the sum of the terms' magnitudes, n roundings or cuts of 2^-23 A as in
+    tests/test_gpu_fp8.py; a tenth of the rows are far from the others' scale."""
+    K = 700
+    g = synthetic.rng(B + H, 22)
+    n, kb = -(-H // 128), -(-K // 128)
+    ex = g.integers(-3, 4, (B, n)) + np.where(np.arange(B) % 10 == 3, g.integers(-110, 90, B), 0)[:, None]
+    x = g.standard_normal((B, H)) * np.repeat(2.0 ** ex, 128, 1)[:, :H]
+    x[:, 128:256] *= 2.0 ** -30
+    x[5], x[7, 256:384] = 0.0, 0.0
+    w = g.standard_normal((K, H)) * np.repeat(np.repeat(2.0 ** g.integers(-20, 21, (kb, n)), 128, 0)[:K], 128, 1)[:, :H]
+    w[128:256] *= 2.0 ** -40
+    w[256:384, :128] = 0.0
+    hid, wb = synthetic.to_bf16_bits(x.astype(np.float32)), synthetic.to_bf16_bits(w.astype(np.float32))
+    W8, s, st = vt.vt_quantize_head(_dev(wb.view(np.int16)))
+    assert int(st.item()) == 0 and float(s.min()) == 2.0 ** -126
+    wd = W8.float().double() * s.double().repeat_interleave(128, 0)[:K].repeat_interleave(128, 1)[:, :H]
+    xd = _dev(fp8.quantize_rows(hid))
+    ref, A = xd @ wd.T, xd.abs() @ wd.abs().T
+    for other in (False, True):
+        z = vt.vt_draft_logits_fp8(_dev(hid.view(np.int16)), W8, s * 1.5 if other else s).double()
+        want = ref * 1.5 if other else ref
+        bound = (H + n + 6) * 2.0 ** -23 * A * (1.5 if other else 1.0) + 1e-30
+        assert bool(((z - want).abs() <= bound).all())
+        assert bool((z[5] == 0).all())
