@@ -867,9 +867,11 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
 // 2.1 / 2.1e-7, 39.8 / 112.  A plain fp32 product is off by 0.8 / 1.2e-7, groups that
 // are promoted one by one by 0.7 / 1.0e-7, so 16 keeps fp32's digits.
 //
-// What bounds it, at B = 1000, K = 38016, H = 4096 (119 us, 2620 TFLOP/s): a group is
-// 513 cycles of MMAs, about 660 pass, of which 180 are waits for the loads (a
-// pair asks L2 for 64 KB a group; four stages instead of five cost 5%).  Two
+// What bounds it, at B = 1000, K = 38016, H = 4096 (119 us, 2620 TFLOP/s): the loads'
+// latency.  A group is 513 cycles of MMAs, about 660 pass, of which 180 are waits for
+// the loads.  No unit is saturated (tensor pipe 60%, L2 44%), but 160 KB on their way
+// to each SM at 10.5 TB/s over all are 2.3 us of loaded latency; four stages
+// instead of five cost 5%.  Two
 // accumulators of 128 columns in turn, to hide the reads, made every MMA slower:
 // they read the batch's stage twice, and shared memory has the loads' traffic
 // too (161 against 129 us, at an earlier step).  A row's 64 instead of 128 bytes out

@@ -32,10 +32,11 @@
 // shared memory.
 //
 // Bound by HBM without alternatives (2304 rows of 152064 bf16 logits: 111 us, 6.3
-// TB/s), by instruction issue with them (k = 1: 121 us, k = 20: 145; 16 KB chunks
-// were 199 against 182 us at an earlier step), and by latency when rows are few: one
-// row of 128256 fp32 logits takes 5.0 us at k = 0 and 6.6 at k = 5; 112 rows, of which
-// 55 are scored, 16.1 at k = 8: 4 to the first chunk, 5.7 of stream, 3 of join.
+// TB/s).  With them (k = 1: 121 us, k = 20: 145) no unit is saturated, issue slots are
+// 66% busy: the warps that stream a row also rank and join its lists (16 KB chunks
+// were 199 against 182 us at an earlier step).  Latency when rows are few: one
+// row of 128256 fp32 logits takes 5.0 us at k = 0 and 6.8 at k = 5; 112 rows, of which
+// 59 are scored, 14.3 at k = 8: 4 to the first chunk, 5.7 of stream, 3 of join.
 #include <algorithm>
 #include <cmath>
 
