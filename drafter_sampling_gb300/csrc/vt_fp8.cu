@@ -751,8 +751,8 @@ head_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 // one warp issues the loads and one the MMAs.  A promoting thread sums 128
 // values and reads another 32 at a time, more registers than an even split over
 // the block gives, so the third warpgroup gives most of its own to the others:
-// 3 x 168 = 2 x 224 + 56 a thread, with which neither side spills (2 x 232 + 40:
-// the issuing warp did, 24 of 150 bytes in its loop; B = 1000: 124 against 119 us).
+// 3 x 168 = 2 x 224 + 56 a thread, with which neither side's loops spill (with 2 x
+// 232 + 40 the issuing warp's did; B = 1000: 124 against 119 us).
 constexpr int kBatchNP = 256;                // promoting threads
 constexpr int kBatchNT = kBatchNP + 128;     // and a warpgroup: loads, MMAs, two idle warps
 constexpr int kBatchRowsW = 256;             // rows of W8 of an item: two tiles of 128
