@@ -25,7 +25,8 @@ namespace vt {
 namespace {
 
 constexpr int kQB = 128;  // side of a scale block
-constexpr int kMaxRows = 65535 * kQB;  // K: the quantiser's grid, and far from where 32-bit row counts overflow
+// largest K: the quantiser's grid, and far from where 32-bit row counts overflow
+constexpr int kMaxRows = 65535 * kQB;
 
 // Exponent e of a block's scale 2^e from the bf16 bits of its largest
 // magnitude (sign cleared): the smallest e >= -126 with amax <= 448 * 2^e.
@@ -871,11 +872,10 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool x) {
 // latency.  A group is 513 cycles of MMAs, about 660 pass, of which 180 are waits for
 // the loads.  No unit is saturated (tensor pipe 60%, L2 44%), but 160 KB on their way
 // to each SM at 10.5 TB/s over all are 2.3 us of loaded latency; four stages
-// instead of five cost 5%.  Two
-// accumulators of 128 columns in turn, to hide the reads, made every MMA slower:
-// they read the batch's stage twice, and shared memory has the loads' traffic
-// too (161 against 129 us, at an earlier step).  A row's 64 instead of 128 bytes out
-// in one piece, for a sixth stage: 10 us slower.
+// instead of five cost 5%.  Two accumulators of 128 columns in turn, to hide the
+// reads, made every MMA slower: they read the batch's stage twice, and shared
+// memory has the loads' traffic too (161 against 129 us, at an earlier step).  A
+// row's 64 instead of 128 bytes out in one piece, for a sixth stage: 10 us slower.
 template <bool TWO, bool PART>
 __global__ void __launch_bounds__(kBatchNT, 1)
 batch_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
