@@ -244,7 +244,7 @@ def _prepare_distill(case, g, dev):
     state = {"op": case["op"], "logits": logits, "top_ids": ids, "top_logp": logp, "inv_map": inv_map,
              "rest": case["rest"], "T": case["T"], "weight": weight,
              "loss": torch.empty(R, dtype=torch.float32, device=dev),
-             "stats": torch.empty((R, 4), dtype=torch.float32, device=dev),
+             "stats": torch.empty((R, 5), dtype=torch.float32, device=dev),
              "status": torch.empty(1, dtype=torch.int32, device=dev)}
     if case["op"] != "loss":
         state["grad"] = torch.empty((R, K + case["pad"]), dtype=logits.dtype, device=dev)[:, :K]
@@ -329,36 +329,38 @@ def _plain_distill(s):
     a = t.sum(dim=1)
     scored = kept.any(dim=1)
     if s["op"] == "grad":
-        m, c_all, c_rest, c_t = s["stats"].unbind(1)
+        m, m_rest, c_all, c_rest, c_t = s["stats"].unbind(1)
     else:
         # the listed ids apart from the others, so that neither's sum is a difference
         hide = torch.zeros_like(x).scatter_add_(1, place, kept.float()) > 0
         others = x.masked_fill(hide, -math.inf)
-        m = torch.maximum(others.amax(dim=1), torch.where(kept, z, -math.inf).amax(dim=1))
+        m_rest = others.amax(dim=1)
+        m = torch.maximum(m_rest, torch.where(kept, z, -math.inf).amax(dim=1))
+        any_rest = m_rest > -math.inf
+        m_rest = torch.where(any_rest, m_rest, 0.0)
         m = torch.where(m == -math.inf, 0.0, m)
-        w_rest = ((others - m[:, None]) / T).exp().sum(dim=1)
-        S = w_rest + torch.where(kept, ((z - m[:, None]) / T).exp(), 0.0).sum(dim=1)
-        rest = (1.0 - a).clamp(min=0.0) * (w_rest > 0) * s["rest"]
+        s_rest = ((others - m_rest[:, None]) / T).exp().sum(dim=1).double()
+        down = (m_rest.double() - m) / T
+        S = torch.where(any_rest, s_rest * down.exp(), 0.0)
+        S = S + torch.where(kept, ((z.double() - m[:, None]) / T).exp(), 0.0).sum(dim=1)
+        rest = (1.0 - a).clamp(min=0.0) * any_rest * s["rest"]
         scored = scored & ((a > 0) | (rest > 0))
         A = a + rest
         scale = torch.ones_like(a) if s["rest"] else 1.0 / torch.where(a > 0, a, 1.0)
         # ln(t / p) of each listed id and of the rest
-        lnp = (z.double() - m[:, None]) / T - S.double().log()[:, None]
+        lnp = (z.double() - m[:, None]) / T - S.log()[:, None]
         loss = (t * torch.where(t > 0, logp - lnp, 0.0)).sum(dim=1) * scale + (A * scale) * scale.log()
-        lnq = w_rest.double().log() - S.double().log()
+        lnq = s_rest.log() + down - S.log()
         loss = loss + torch.where(rest > 0, rest * (rest.log() - lnq), 0.0)
         loss = torch.where(scored, loss, 0.0).float()
-        inv = scale / (S.double() * T)
-        q = w_rest.double() / S.double()
-        c_all, c_t = A * inv, scale / T
-        c_rest = (A - torch.where(rest > 0, rest / q, 0.0)) * inv
-        m, c_all, c_rest, c_t = (torch.where(scored, v, 0.0).float() for v in (m, c_all, c_rest, c_t))
+        c_all, c_t = A * scale / (S * T), scale / T
+        c_rest = torch.where(any_rest, A * scale * down.exp() / S - rest / s_rest, 0.0) / T
+        m, m_rest, c_all, c_rest, c_t = (torch.where(scored, v, 0.0).float() for v in (m, m_rest, c_all, c_rest, c_t))
         if s["op"] == "loss":
-            return {"loss": loss, "stats": torch.stack((m, c_all, c_rest, c_t), dim=1)}
+            return {"loss": loss, "stats": torch.stack((m, m_rest, c_all, c_rest, c_t), dim=1)}
     g = s["weight"]
-    w = ((x - m[:, None]) / T).exp()
-    d = w * (c_rest * g)[:, None]
-    listed = (w.gather(1, place) * c_all[:, None] - t.float() * c_t[:, None]) * g[:, None]
+    d = ((x - m_rest[:, None]) / T).exp() * (c_rest * g)[:, None]
+    listed = (((z - m[:, None]) / T).exp() * c_all[:, None] - t.float() * c_t[:, None]) * g[:, None]
     listed = torch.where(kept, listed - d.gather(1, place), 0.0)
     d = torch.where(scored[:, None], d.scatter_add_(1, place, listed), 0.0)
     d = d.to(s["logits"].dtype)
@@ -455,7 +457,7 @@ def _exact_distill(s):
     """From the definition, row by row: the drafter's softmax against the teacher's listed ids."""
     R, T, dev = s["logits"].shape[0], s["T"], s["logits"].device
     loss = torch.zeros(R, dtype=torch.float64, device=dev)
-    stats = torch.zeros((R, 4), dtype=torch.float64, device=dev)
+    stats = torch.zeros((R, 5), dtype=torch.float64, device=dev)
     grad = torch.zeros(s["logits"].shape, dtype=torch.float64, device=dev) if s["op"] != "loss" else None
     ids = s["top_ids"].long()
     if s["inv_map"] is not None:
@@ -478,12 +480,13 @@ def _exact_distill(s):
         if b > 0:
             lnq = torch.logsumexp(lnp[others], dim=0)
             loss[r] += b * (math.log(b) - lnq)
-        # the row's maximum and the factors of exp((z - maximum) / T), listed and not, and of the teacher's values
-        m, inv = y.max(), lnp.max().exp() / T
-        q = float(p[others].sum())
-        stats[r, 0], stats[r, 1] = m * T, (t.sum() + b) * inv
-        stats[r, 2] = (t.sum() + b - (b / q if b > 0 else 0.0)) * inv
-        stats[r, 3] = (1.0 if s["rest"] else 1.0 / float(s["top_logp"][r][use].double().exp().sum())) / T
+        # the largest logit of all and of the others, and the factors of the exponentials relative to them
+        stats[r, 0], stats[r, 2] = y.max() * T, (t.sum() + b) * lnp.max().exp() / T
+        if bool((p[others] > 0).any()):
+            stats[r, 1] = y[others].max() * T
+            top = lnp[others].max().exp()
+            stats[r, 3] = ((t.sum() + b) * top - b * top / p[others].sum()) / T
+        stats[r, 4] = (1.0 if s["rest"] else 1.0 / float(s["top_logp"][r][use].double().exp().sum())) / T
         if grad is not None:
             g = p * (t.sum() + b)
             g[at] -= t
