@@ -165,6 +165,11 @@ def _trim(K, g, dev):
     return ids.to(torch.int32), inv
 
 
+def _temperature(case) -> float:
+    """The case's temperature as the fp32 value that the calls take."""
+    return float(torch.tensor(case["T"], dtype=torch.float32))
+
+
 def _prepare_select(case, g, dev):
     B, W, N, K = case["B"], case["W"], case["N"], case["K"]
     logits = _logits(case, B * W, g, dev)
@@ -173,7 +178,7 @@ def _prepare_select(case, g, dev):
     scores = torch.empty((B, W), dtype=torch.float32, device=dev).normal_(-12.0, 2.0, generator=g)
     scores = scores.sort(dim=1, descending=True).values.contiguous()
     trim_ids = _trim(K, g, dev)[0] if case["trimmed"] else None
-    state = {"op": "select", "logits": logits.unflatten(0, (B, W)), "scores": scores, "N": N, "T": case["T"],
+    state = {"op": "select", "logits": logits.unflatten(0, (B, W)), "scores": scores, "N": N, "T": _temperature(case),
              "trim_ids": trim_ids, "done": None, "end_id": -1,
              "out_scores": torch.empty((B, N), dtype=torch.float32, device=dev),
              "out_parent": torch.empty((B, N), dtype=torch.int32, device=dev),
@@ -242,7 +247,7 @@ def _prepare_distill(case, g, dev):
     ids, logp = ids.masked_fill(skip, -1).to(torch.int32), logp.masked_fill(skip, math.nan)
     weight = torch.rand(R, generator=g, device=dev) * (2.0 / R)
     state = {"op": case["op"], "logits": logits, "top_ids": ids, "top_logp": logp, "inv_map": inv_map,
-             "rest": case["rest"], "T": case["T"], "weight": weight,
+             "rest": case["rest"], "T": _temperature(case), "weight": weight,
              "loss": torch.empty(R, dtype=torch.float32, device=dev),
              "stats": torch.empty((R, 5), dtype=torch.float32, device=dev),
              "status": torch.empty(1, dtype=torch.int32, device=dev)}
