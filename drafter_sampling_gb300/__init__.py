@@ -11,6 +11,8 @@ bf16 tensors may be passed as torch.bfloat16 or as int16/uint16 bit patterns.
 """
 from __future__ import annotations
 
+import functools
+
 from . import _lib
 from ._lib import (VT_BF16, VT_DEV_BAD_DRAFT, VT_DEV_BAD_ID,  # noqa: F401
                    VT_DEV_DUPLICATE_ID, VT_DEV_NONFINITE, VT_DEV_TIMEOUT,
@@ -21,6 +23,8 @@ __all__ = ["vt_selftest_wait", "vt_calibrate_topk", "vt_calibrate_top_p", "vt_ca
            "vt_draft_logits", "vt_draft_step", "vt_draft_topk", "vt_verify", "vt_verify_tree",
            "vt_quantize_head", "vt_draft_logits_fp8", "vt_draft_step_fp8", "vt_draft_topk_fp8",
            "vt_token_logprobs",
+           "vt_beam_select", "vt_beam_reorder",
+           "vt_distill_loss", "vt_distill_grad", "vt_distill_loss_grad",
            "BlockGraph",
            "workspace_bytes",
            "VtError", "lib"]
@@ -126,6 +130,8 @@ def workspace_bytes(kind: str, **kw) -> int:
         return L.vt_draft_topk_fp8_workspace_bytes(kw["B"], kw["H"], kw["K"], kw["k"])
     if kind == "verify":
         return L.vt_verify_workspace_bytes(kw["B"], kw["gamma"], kw["V"], kw["K"])
+    if kind == "beam_select":
+        return L.vt_beam_select_workspace_bytes(kw["B"], kw["W"], kw["K"], kw["n"])
     raise ValueError(kind)
 
 
@@ -454,16 +460,17 @@ def vt_verify_tree(target_logits, parent, tokens, temperature: float = 0.0, out_
 # Dtype tuples of the arguments below and torch's current-device getter, filled
 # at the first call.  These calls take a few microseconds on the GPU, so what
 # the binding does per tensor is kept to four attribute reads.
-_F32 = _I32 = _FP8 = _U8 = None
+_F32 = _I32 = _FP8 = _U8 = _FLAG = None
 _CUR_DEVICE = None
 _DEVICES = ()
 
 
 def _fast():
-    global _F32, _I32, _FP8, _U8, _CUR_DEVICE, _DEVICES
+    global _F32, _I32, _FP8, _U8, _FLAG, _CUR_DEVICE, _DEVICES
     torch = _torch()
     _DEVICES = tuple(torch.device("cuda", i) for i in range(torch.cuda.device_count()))
     _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+    _FLAG = (torch.bool, torch.uint8)
     _CUR_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _bf16_dtypes()
     _FP8 = (torch.float8_e4m3fn, torch.uint8)
@@ -684,19 +691,9 @@ def vt_draft_topk_fp8(hidden, W8, w_scale, trim_ids, k: int, temperature: float 
     return out_ids, out_logq, dev_status
 
 
-def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_logp=None,
-                      out_entropy=None, out_top_ids=None, out_top_logp=None, dev_status=None,
-                      stream=None, want_entropy: bool = True):
-    """Log probabilities of given tokens under rows of logits.
-
-    logits [R, V] or [B, R, V], float32 or bf16, unit inner stride and evenly
-    spaced rows; tokens int32 of logits' leading shape, contiguous, -1 = row
-    not scored.  All tensors are on the current device.
-    Returns (logp, entropy or None, top_ids, top_logp, dev_status), logp and
-    entropy of tokens' shape, top_ids int32 and top_logp [..., k] (None where
-    k == 0): the k best ids, ties to the lower, with their log probabilities.
-    """
-    dev = _first(logits, "logits")
+def _logit_rows(logits):
+    """(element type, leading shape, rows, row length, row stride) of logits
+    [R, V] or [B, R, V]."""
     dt = logits.dtype
     if dt in _F32:
         dt = VT_F32
@@ -719,6 +716,23 @@ def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_
         even = B == 1 or n == 1 or st[0] == n * ld
     if (st[-1] != 1 and V > 1) or not even or ld < V:
         raise ValueError("logits must have unit inner stride and evenly spaced rows")
+    return dt, shape, R, V, ld
+
+
+def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_logp=None,
+                      out_entropy=None, out_top_ids=None, out_top_logp=None, dev_status=None,
+                      stream=None, want_entropy: bool = True):
+    """Log probabilities of given tokens under rows of logits.
+
+    logits [R, V] or [B, R, V], float32 or bf16, unit inner stride and evenly
+    spaced rows; tokens int32 of logits' leading shape, contiguous, -1 = row
+    not scored.  All tensors are on the current device.
+    Returns (logp, entropy or None, top_ids, top_logp, dev_status), logp and
+    entropy of tokens' shape, top_ids int32 and top_logp [..., k] (None where
+    k == 0): the k best ids, ties to the lower, with their log probabilities.
+    """
+    dev = _first(logits, "logits")
+    dt, shape, R, V, ld = _logit_rows(logits)
     k = int(k)
     if not 0 <= k <= min(32, V):
         raise ValueError("k must be in [0, min(32, V)]")
@@ -749,6 +763,283 @@ def vt_token_logprobs(logits, tokens, k: int = 0, temperature: float = 1.0, out_
     if rc:
         _lib.check("vt_token_logprobs", rc)
     return out_logp, out_entropy, out_top_ids, out_top_logp, dev_status
+
+
+def vt_beam_select(logits, scores, n: int, temperature: float = 1.0, trim_ids=None, done=None,
+                   end_id: int = -1, out_scores=None, out_parent=None, out_tokens=None, out_done=None,
+                   dev_status=None, workspace=None, stream=None):
+    """One step of beam search: the n best continuations of each sequence's beams.
+
+    logits [B, W, K], float32 or bf16, unit inner stride and evenly spaced rows;
+    scores float32 [B, W] (-inf: no beam); trim_ids int32 [K] names the indices'
+    tokens; done bool or uint8 [B, W] marks beams that have ended with end_id
+    (they continue once, as they are).  All tensors are on the current device;
+    outputs overlap no input.
+    Returns (scores, parent int32, tokens int32, done or None, dev_status), each
+    [B, n], best first, ties to the lower beam and index; done where end_id >= 0.
+    Missing continuations have score -inf, parent -1 and token -1.
+    """
+    dev = _first(logits, "logits")
+    dt, shape, _, K, ld = _logit_rows(logits)
+    if len(shape) != 2:
+        raise ValueError("logits must be [B, W, K]")
+    B, W = shape
+    n, end_id = int(n), int(end_id)
+    if not 1 <= n <= 32 or W > 32:
+        raise ValueError("n and the number of beams must be in [1, 32]")
+    if end_id < -1 or end_id >= 1 << 31:
+        raise ValueError("end_id must be a token id, or -1")
+    sp = _arg(scores, "scores", _F32, shape, dev)
+    tp = gp = op = None
+    if trim_ids is not None:
+        tp = _arg(trim_ids, "trim_ids", _I32, (K,), dev)
+    if (done is not None or out_done is not None) and end_id < 0:
+        raise ValueError("done and out_done need end_id")
+    if done is not None:
+        gp = _arg(done, "done", _FLAG, shape, dev)
+    out = (B, n)
+    if out_scores is None:
+        out_scores = _new(out, _F32[0], dev, stream)
+    if out_parent is None:
+        out_parent = _new(out, _I32[0], dev, stream)
+    if out_tokens is None:
+        out_tokens = _new(out, _I32[0], dev, stream)
+    if end_id >= 0:
+        if out_done is None:
+            out_done = _new(out, _FLAG[0], dev, stream)
+        op = _arg(out_done, "out_done", _FLAG, out, dev)
+    if dev_status is None:
+        dev_status = _new(1, _I32[0], dev, stream)
+    L = lib()
+    ws, nb, workspace = _scratch(
+        workspace, L.vt_beam_select_workspace_bytes(B, W, K, n) if workspace is None else 0, dev, stream)
+    rc = L.vt_beam_select(logits.data_ptr(), dt, B, W, K, ld, sp, gp, end_id, tp, n, float(temperature),
+                          _arg(out_scores, "out_scores", _F32, out, dev),
+                          _arg(out_parent, "out_parent", _I32, out, dev),
+                          _arg(out_tokens, "out_tokens", _I32, out, dev), op,
+                          _arg(dev_status, "dev_status", _I32, (1,), dev), ws, nb, _on(stream, dev))
+    if rc:
+        _lib.check("vt_beam_select", rc)
+    return out_scores, out_parent, out_tokens, out_done, dev_status
+
+
+def _collapse(shape, strides):
+    """(extent, stride) of dimensions that one stride walks through, None where
+    none does; extents of 1 fit anywhere."""
+    n, st = 1, 0
+    for d in range(len(shape) - 1, -1, -1):
+        if shape[d] == 1:
+            continue
+        if n == 1:
+            st = strides[d]
+        elif strides[d] != st * n:
+            return None
+        n *= shape[d]
+    return n, st
+
+
+def _tail(shape, st, first):
+    """The first dimension, from `first` on, of those at the end that are contiguous."""
+    cut = len(shape)
+    while cut > first and _collapse(shape[cut - 1:], st[cut - 1:]) in ((_size(shape[cut - 1:]), 1), (1, 0)):
+        cut -= 1
+    return cut
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_parts(name, shape, st, ost, dim, len_dim):
+    """The five extents (outer, B, W, inner, positions), their strides in two tensors
+    of this shape (but for W) and these strides, and the row length, in elements, of
+    states with their sequences at `dim`."""
+    if len_dim is None:  # whole states, in rows as long as both tensors allow
+        mid = last = max(_tail(shape, st, dim + 2), _tail(shape, ost, dim + 2))
+    else:
+        mid, last = len_dim, len_dim + 1
+    n = _size(shape[last:])
+    steps = []
+    for s in (st, ost):
+        outer, inner = _collapse(shape[:dim], s[:dim]), _collapse(shape[dim + 2:mid], s[dim + 2:mid])
+        row = _collapse(shape[last:], s[last:])
+        if outer is None or inner is None or row is None or (n > 1 and row[1] != 1):
+            raise ValueError(f"{name} must have contiguous rows, and evenly spaced dimensions before its "
+                             "sequences and between its beams and positions")
+        steps.append((outer[1], s[dim], s[dim + 1], inner[1], s[len_dim] if len_dim is not None else 0))
+    ext = (outer[0], shape[dim], shape[dim + 1], inner[0], shape[len_dim] if len_dim is not None else 1)
+    a, b = (tuple(s if e > 1 else 0 for e, s in zip(ext, x)) for x in steps)
+    return ext, a, b, n
+
+
+def _size(shape):
+    n = 1
+    for s in shape:
+        n *= s
+    return n
+
+
+def _span(t):
+    """The addresses [first, end) that a tensor's elements lie in."""
+    p = t.data_ptr()
+    return p, p + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def vt_beam_reorder(state, parent, out=None, dim: int = 0, lengths=None, len_dim=None, dev_status=None,
+                    stream=None):
+    """The beams' states follow the beams that were chosen (vt_beam_select's parent).
+
+    state [..., B, W, ...] of any element type, its sequences at dimension dim and
+    their beams at dim + 1; parent int32 [B, n], -1: that slot stays as it is.
+    With lengths int32 [B], only the first lengths[b] positions along dimension
+    len_dim are moved.  Dimensions before dim, and those between dim + 1 and
+    len_dim, are evenly spaced; what follows len_dim is contiguous.
+    out None (or state itself): in place, n at most W; else a tensor like state, but for
+    its number of beams (at least n), that does not overlap it.  Returns (out, dev_status).
+    """
+    dev = _first(state, "state")
+    nd = state.dim()
+    dim = int(dim)
+    if dim < 0:
+        dim += nd
+    if not 0 <= dim <= nd - 2 or 0 in state.shape:
+        raise ValueError("state must be [..., B, W, ...] with its sequences at dim, and not empty")
+    if len_dim is not None:
+        len_dim = int(len_dim)
+        if len_dim < 0:
+            len_dim += nd
+        if not dim + 2 <= len_dim < nd:
+            raise ValueError("len_dim must be a dimension behind the beams")
+    elif lengths is not None:
+        raise ValueError("lengths needs len_dim")
+    shape, strides = state.shape, state.stride()
+    if out is None:
+        out = state
+    slots, ostr = shape[dim + 1], strides
+    if out is not state:
+        if not isinstance(out, _TORCH.Tensor) or out.get_device() != dev or out.dtype != state.dtype:
+            raise ValueError(f"out must be a tensor of {state.dtype} on cuda:{dev}")
+        if out.dim() != nd or out.shape[:dim + 1] != shape[:dim + 1] or out.shape[dim + 2:] != shape[dim + 2:]:
+            raise ValueError(f"out must be like state, {list(shape)}, but for its beams, got {list(out.shape)}")
+        slots, ostr = out.shape[dim + 1], out.stride()
+        if out.data_ptr() != state.data_ptr() or ostr != strides or slots != shape[dim + 1]:
+            a, b = _span(state), _span(out)
+            if a[0] < b[1] and b[0] < a[1]:
+                raise ValueError("out must be state, or not overlap it")
+    ext, st, ost, row = _beam_parts("state", shape, strides, ostr, dim, len_dim)
+    B, W = ext[1], ext[2]
+    pp = _arg(parent, "parent", _I32, None, dev)
+    if parent.dim() != 2 or parent.shape[0] != B or not 1 <= parent.shape[1] <= 32 or W > 32:
+        raise ValueError(f"parent must be [{B}, n] with n, and the number of beams, in [1, 32]")
+    n = parent.shape[1]
+    if n > slots:
+        raise ValueError(f"parent has {n} slots, out {slots} beams")
+    if W == 1:  # (its slots' stride is out's own)
+        ost = ost[:2] + (ostr[dim + 1] if slots > 1 else 0,) + ost[3:]
+    if any(s == 0 for s, e in zip(ost, (ext[0], B, n, ext[3], ext[4])) if e > 1):
+        raise ValueError("out must not be expanded")
+    lp = _arg(lengths, "lengths", _I32, (B,), dev) if lengths is not None else None
+    if dev_status is None:
+        dev_status = _new(1, _I32[0], dev, stream)
+    es = state.element_size()
+    five = _lib._i64 * 5
+    rc = lib().vt_beam_reorder(state.data_ptr(), out.data_ptr(), five(*(s * es for s in st)),
+                               five(*(s * es for s in ost)), ext[0], B, W, n, ext[3], ext[4], row * es, pp, lp,
+                               _arg(dev_status, "dev_status", _I32, (1,), dev), _on(stream, dev))
+    if rc:
+        _lib.check("vt_beam_reorder", rc)
+    return out, dev_status
+
+
+def _teacher(logits, top_ids, top_logp, inv_map):
+    """(device, element type, leading shape, rows, K, stride, addresses and sizes of
+    the teacher's list and the map) of a distillation call."""
+    dev = _first(logits, "logits")
+    dt, shape, R, K, ld = _logit_rows(logits)
+    ip = _arg(top_ids, "top_ids", _I32, None, dev)
+    full = top_ids.shape
+    if full[:-1] != shape or not 1 <= full[-1] <= 128:
+        raise ValueError(f"top_ids must be {list(shape)} + [k] with k in [1, 128], got {list(full)}")
+    lp = _arg(top_logp, "top_logp", _F32, full, dev)
+    mp, V = None, K
+    if inv_map is not None:
+        mp = _arg(inv_map, "inv_map", _I32, None, dev)
+        V = inv_map.numel()
+    return dev, dt, shape, R, K, ld, ip, lp, full[-1], mp, V
+
+
+def _grad_out(out_grad, logits, shape, R, K, dev, stream):
+    """(tensor, address, row stride) of the gradient of logits."""
+    if out_grad is None:
+        out_grad = _new((*shape, K), logits.dtype, dev, stream)
+    elif not isinstance(out_grad, _TORCH.Tensor) or out_grad.get_device() != dev or \
+            out_grad.dtype != logits.dtype or out_grad.shape != logits.shape:
+        raise ValueError(f"out_grad must be a tensor of {logits.dtype} on cuda:{dev}, {[*shape, K]}")
+    return out_grad, out_grad.data_ptr(), _logit_rows(out_grad)[4]
+
+
+def vt_distill_loss(logits, top_ids, top_logp, inv_map=None, rest: bool = True, temperature: float = 1.0,
+                    out_loss=None, out_stats=None, dev_status=None, stream=None):
+    """Distillation from a teacher's k best ids: the loss of each row of the drafter's logits.
+
+    logits [R, K] or [B, R, K], float32 or bf16, unit inner stride and evenly spaced
+    rows; top_ids int32 and top_logp float32 of logits' leading shape + [k], k <= 128, as
+    vt_token_logprobs returns them for the target's logits (-1: no entry); inv_map int32 [V]
+    (vt_trim_head's) takes the teacher's ids to the drafter's, -1 where it has none.
+    rest: what the listed ids leave of either distribution counts as one more outcome; otherwise
+    the teacher is renormalised over the ids listed.  Rows with nothing to learn have loss 0.
+    Returns (loss, stats, dev_status); stats [..., 5] is what vt_distill_grad needs.
+    """
+    dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
+    if out_loss is None:
+        out_loss = _new(shape, _F32[0], dev, stream)
+    if out_stats is None:
+        out_stats = _new((*shape, 5), _F32[0], dev, stream)
+    if dev_status is None:
+        dev_status = _new(1, _I32[0], dev, stream)
+    rc = lib().vt_distill_loss(logits.data_ptr(), dt, R, K, ld, ip, lp, k, mp, V, 1 if rest else 0,
+                               float(temperature), _arg(out_loss, "out_loss", _F32, shape, dev),
+                               _arg(out_stats, "out_stats", _F32, (*shape, 5), dev),
+                               _arg(dev_status, "dev_status", _I32, (1,), dev), _on(stream, dev))
+    if rc:
+        _lib.check("vt_distill_loss", rc)
+    return out_loss, out_stats, dev_status
+
+
+def vt_distill_grad(logits, top_ids, top_logp, stats, grad_loss=None, inv_map=None,
+                    temperature: float = 1.0, out_grad=None, stream=None):
+    """The gradient of vt_distill_loss with respect to the logits, from the same arguments and the
+    statistics it returned; grad_loss float32 of logits' leading shape (None: 1) is dL/dloss.
+    out_grad, of logits' shape and type, may be logits itself.  Returns out_grad."""
+    dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
+    gp = _arg(grad_loss, "grad_loss", _F32, shape, dev) if grad_loss is not None else None
+    out_grad, op, ldg = _grad_out(out_grad, logits, shape, R, K, dev, stream)
+    rc = lib().vt_distill_grad(logits.data_ptr(), dt, R, K, ld, ip, lp, k, mp, V, float(temperature),
+                               _arg(stats, "stats", _F32, (*shape, 5), dev), gp, op, ldg, _on(stream, dev))
+    if rc:
+        _lib.check("vt_distill_grad", rc)
+    return out_grad
+
+
+def vt_distill_loss_grad(logits, top_ids, top_logp, grad_loss=None, inv_map=None, rest: bool = True,
+                         temperature: float = 1.0, out_loss=None, out_grad=None, out_stats=None,
+                         dev_status=None, stream=None):
+    """vt_distill_loss and vt_distill_grad in one call: a training step that knows each row's weight
+    grad_loss beforehand.  Rows that fit on the chip are read once.  Returns (loss, grad, stats,
+    dev_status)."""
+    dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
+    gp = _arg(grad_loss, "grad_loss", _F32, shape, dev) if grad_loss is not None else None
+    if out_loss is None:
+        out_loss = _new(shape, _F32[0], dev, stream)
+    if out_stats is None:
+        out_stats = _new((*shape, 5), _F32[0], dev, stream)
+    if dev_status is None:
+        dev_status = _new(1, _I32[0], dev, stream)
+    out_grad, op, ldg = _grad_out(out_grad, logits, shape, R, K, dev, stream)
+    rc = lib().vt_distill_loss_grad(logits.data_ptr(), dt, R, K, ld, ip, lp, k, mp, V, 1 if rest else 0,
+                                    float(temperature), gp, _arg(out_loss, "out_loss", _F32, shape, dev),
+                                    _arg(out_stats, "out_stats", _F32, (*shape, 5), dev), op, ldg,
+                                    _arg(dev_status, "dev_status", _I32, (1,), dev), _on(stream, dev))
+    if rc:
+        _lib.check("vt_distill_loss_grad", rc)
+    return out_loss, out_grad, out_stats, dev_status
 
 
 def vt_selftest_wait(which: int, limit: int, flag=None, dev_status=None, stream=None):

@@ -83,6 +83,17 @@ SIGNATURES = {
                                     _p, _p, _sz, _p]),
     "vt_token_logprobs": (C.c_int, [_p, _i32, _i64, _i32, _i64, _p, _i32, _f32, _p, _p, _p, _p,
                                     _p, _p]),
+    "vt_beam_select_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "vt_beam_select": (C.c_int, [_p, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i32, _f32, _p,
+                                 _p, _p, _p, _p, _p, _sz, _p]),
+    "vt_beam_reorder": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _p, _p,
+                                  _p, _p]),
+    "vt_distill_loss": (C.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _p, _i32, _i32, _f32, _p,
+                                  _p, _p, _p]),
+    "vt_distill_grad": (C.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _p, _i32, _f32, _p, _p,
+                                  _p, _i64, _p]),
+    "vt_distill_loss_grad": (C.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _p, _i32, _i32, _f32,
+                                       _p, _p, _p, _p, _i64, _p, _p]),
     "vt_verify_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
     "vt_verify": (C.c_int, [_p, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _p, _f32, _p,
                             _p, _p, _p, _p, _sz, _p]),

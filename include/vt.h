@@ -470,6 +470,128 @@ int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64_t R, int32
                       float* out_top_logp, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------
+ * One step of beam search: the n best continuations of each sequence's W beams
+ * over the vocabulary.  With it a draft tree grows level by level: the beams are
+ * a level's nodes, their scores the path's log q, and the chosen continuations
+ * with their parents are the next level ([VT] section 4.1 drafts trees; the
+ * choice of nodes that vt_draft_topk leaves to the caller).
+ *
+ * Candidate j of beam w scores scores[b, w] + ln softmax(logits[b, w] / T)[j].
+ * The n best are returned best first, ties to the lower beam, then to the lower
+ * index.  Scores are compared in 64 bits and rounded to fp32 once, at the end;
+ * two of different beams that are within 1e-8 of each other, but not equal, may
+ * come in either order.
+ *
+ *  logits     [B, W, K], row stride ld_logits >= K, of logits_dtype; aligned to
+ *                          its element type, no more
+ *  scores     f32 [B, W]   log probability of each beam; -infinity: no beam (its
+ *                          row is not read)
+ *  done       uint8 [B, W] may be NULL; nonzero: the beam has ended.  Its row is
+ *                          not read; it has one candidate, token end_id with its
+ *                          score unchanged
+ *  end_id                  the token that ends a beam, or -1 (then done and
+ *                          out_done are NULL)
+ *  trim_ids   int32 [K]    may be NULL (then indices are tokens): the token of
+ *                          each index
+ *  out_scores f32 [B, n]   out: the continuations' scores
+ *  out_parent int32 [B, n] out: the beam that each continues
+ *  out_tokens int32 [B, n] out: its token
+ *  out_done   uint8 [B, n] out, needed with done: 1 where the parent had ended or
+ *                          the token is end_id
+ *  dev_status int32 [1]    out: VT_DEV_NONFINITE (a NaN or +infinity in a score or
+ *                          in a row that was read; that beam gives no candidates)
+ * An id at -infinity is no candidate.  Where a sequence has fewer than n, the
+ * rest is score -infinity, parent -1, token -1.  Outputs overlap no input.
+ * 1 <= W, n <= 32, 1 <= K <= 2^22, B W <= 2^24, 1e-30 <= T <= 1e30.  Workspace:
+ * vt_beam_select_workspace_bytes(B, W, K, n) bytes.
+ * ---------------------------------------------------------------------- */
+size_t vt_beam_select_workspace_bytes(int32_t B, int32_t W, int32_t K, int32_t n);
+int vt_beam_select(const void* logits, int32_t logits_dtype, int32_t B, int32_t W, int32_t K,
+                   int64_t ld_logits, const float* scores, const uint8_t* done, int32_t end_id,
+                   const int32_t* trim_ids, int32_t n, float temperature, float* out_scores,
+                   int32_t* out_parent, int32_t* out_tokens, uint8_t* out_done, int32_t* dev_status,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * vt_beam_reorder - the states of the beams follow the beams that were chosen:
+ * out[o, b, i, p, s] = state[o, b, parent[b, i], p, s] for every i < n with a
+ * parent, o < outer, p < inner, s < min(positions, lengths[b]); an element is
+ * row_bytes bytes.  Hidden states, token histories and caches have this form
+ * (a cache [2, B, W, heads, positions, D]: outer 2, inner heads).
+ * With out == state (and equal strides) the move is in place, whatever the
+ * parents; slots i whose parent is i are neither read nor written.  Otherwise
+ * out and state do not overlap.  Slots without a parent (-1), slots from n on and
+ * positions from lengths[b] on are left as they were.
+ *
+ *  strides, out_strides  HOST int64 [5]: bytes from one o, b, i, p and s to the
+ *                        next (>= 0; elements do not overlap)
+ *  parent     int32 [B, n]  as vt_beam_select leaves it
+ *  lengths    int32 [B]     may be NULL: all positions (values outside
+ *                           [0, positions] count as the nearer bound)
+ *  dev_status int32 [1]     out: VT_DEV_BAD_ID (a parent outside [0, W) other than
+ *                           -1; that slot is left as it was)
+ * 1 <= W, n <= 32; n <= W in place.
+ * ---------------------------------------------------------------------- */
+int vt_beam_reorder(const void* state, void* out, const int64_t* strides, const int64_t* out_strides,
+                    int64_t outer, int32_t B, int32_t W, int32_t n, int64_t inner, int64_t positions,
+                    int64_t row_bytes, const int32_t* parent, const int32_t* lengths,
+                    int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Distillation of the drafter from the target's best ids.  The teacher gives, per
+ * position, the k best ids with ln t, as vt_token_logprobs writes them; the
+ * drafter's logits range over K (usually trimmed) ids.  An entry is kept where its
+ * id is not -1, the drafter has it (inv_map[id] >= 0) and its logit there is
+ * above -infinity.  With p = softmax(z / T), a = sum t over the kept entries and
+ * q = sum p over the ids not listed:
+ *   rest = 1: the rest of either distribution is one more outcome.  b = max(0, 1 - a)
+ *             (0 where every unlisted logit is -infinity):
+ *               loss = sum t_i (ln t_i - ln p_i) + b (ln b - ln q)
+ *   rest = 0: the teacher is renormalised over the kept entries, t' = t / a:
+ *               loss = sum t'_i (ln t'_i - ln p_i)
+ * (the list's temperature is the caller's; a factor T^2, where wanted, goes into
+ * grad_loss).  A row with nothing kept, or with t = 0 in all of it and rest = 0, has
+ * loss and gradient 0; where no id is listed at all its logits are not read.
+ *
+ *  logits     [R, ld_logits] of logits_dtype, K logits a row; aligned to its
+ *                            element type, no more
+ *  top_ids    int32 [R, k]   the teacher's ids, -1: no entry; no id twice in a row
+ *  top_logp   f32 [R, k]     ln t, below 80 (-infinity: t = 0); not looked at
+ *                            where the entry is not kept
+ *  inv_map    int32 [V]      vt_trim_head's; NULL: ids are the drafter's (V == K)
+ *  out_loss   f32 [R]        out
+ *  out_stats  f32 [R, 5]     out: what the gradient needs: the largest logit of the
+ *                            row and that of its unlisted ids, and the factors of
+ *                            2^(z - largest), of the same for unlisted ids, and of
+ *                            t; zeros where the gradient is 0
+ *  grad_loss  f32 [R]        may be NULL (1): dL/dloss of each row
+ *  out_grad   [R, ld_grad]   out: dL/dlogits, of logits_dtype (bf16: rounded to
+ *                            nearest even, once); the logits' own buffer (with
+ *                            their stride), or one that does not overlap it
+ *  dev_status int32 [1]      out: VT_DEV_BAD_ID (an id outside [-1, V), or an
+ *                            inv_map value outside [-1, K)), VT_DEV_DUPLICATE_ID (two
+ *                            kept entries for one id), VT_DEV_NONFINITE (a logit that
+ *                            is NaN or +infinity, a kept ln t that is NaN or not
+ *                            below 80): NaN in that row's loss, statistics, gradient
+ * vt_distill_loss gives loss and statistics, vt_distill_grad the gradient from the
+ * same arguments and those statistics, vt_distill_loss_grad all of it.
+ * 1 <= k <= 128, 1 <= K <= 2^22, 1 <= R <= 2^24, 1e-30 <= T <= 1e30.  No workspace.
+ * ---------------------------------------------------------------------- */
+int vt_distill_loss(const void* logits, int32_t logits_dtype, int64_t R, int32_t K, int64_t ld_logits,
+                    const int32_t* top_ids, const float* top_logp, int32_t k, const int32_t* inv_map,
+                    int32_t V, int32_t rest, float temperature, float* out_loss, float* out_stats,
+                    int32_t* dev_status, void* stream);
+int vt_distill_grad(const void* logits, int32_t logits_dtype, int64_t R, int32_t K, int64_t ld_logits,
+                    const int32_t* top_ids, const float* top_logp, int32_t k, const int32_t* inv_map,
+                    int32_t V, float temperature, const float* stats, const float* grad_loss,
+                    void* out_grad, int64_t ld_grad, void* stream);
+int vt_distill_loss_grad(const void* logits, int32_t logits_dtype, int64_t R, int32_t K,
+                         int64_t ld_logits, const int32_t* top_ids, const float* top_logp, int32_t k,
+                         const int32_t* inv_map, int32_t V, int32_t rest, float temperature,
+                         const float* grad_loss, float* out_loss, float* out_stats, void* out_grad,
+                         int64_t ld_grad, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
  * One speculative block as a CUDA graph.  [VT] Appendix C.1, Algorithm 2:
  * draft k (= gamma) tokens through the trimmed head, then score and verify
  * them.  vt_block_graph_create records gamma vt_draft_step calls (step j
