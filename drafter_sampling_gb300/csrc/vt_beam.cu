@@ -12,11 +12,16 @@
 // sums those beams' rows again with pairs of fp32 values, in an order that
 // depends on the ids alone (equal beams give equal scores, whatever their rows'
 // alignment), and takes the lists again.
+#include <algorithm>
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "vt_internal.h"
-#include "vt_pair.cuh"
-#include "vt_verify_common.cuh"
+#include "vt_rows.cuh"
+#include "vt_umma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace vt {
 namespace {
@@ -31,16 +36,7 @@ constexpr int kBsNT = 256;
 // the sums add 1e-6; twice that for two rows.
 constexpr double kNear = 1e-5;
 
-typedef unsigned long long bs_key;
-__device__ __forceinline__ bs_key bs_key_of(float v, int id) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return (bs_key)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | (uint32_t)~id;
-}
-__device__ __forceinline__ float bs_value(bs_key q) {
-  const uint32_t o = (uint32_t)(q >> 32);
-  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-__device__ __forceinline__ int bs_id(bs_key q) { return (int)~(uint32_t)q; }
+typedef unsigned long long bs_key;  // an fp64 score, or a row's (value, id)
 
 // What the row kernel leaves of a beam: its largest logit, S = s + e, how many
 // candidates follow and the VT_DEV_* flags of its row
@@ -74,77 +70,237 @@ __device__ __forceinline__ bool bs_live(const BsArgs& a, int row) {
   return s > -INFINITY && s < INFINITY && !(a.done && a.done[row]);
 }
 
+// running sum of weights: the maximum m and S = s + e (e: what rounding took from s)
+struct RowSum {
+  float m, s, e;
+};
+// relative to a maximum m >= a.m
+__device__ __forceinline__ void sum_rescale(RowSum& a, float m, float c) {
+  const float f = exp2_approx((a.m - m) * c);
+  a.s *= f;
+  a.e *= f;
+  a.m = m;
+}
+__device__ __forceinline__ RowSum sum_join(RowSum a, RowSum b, float c) {
+  const float m = max_nan(a.m, b.m);
+  sum_rescale(a, m, c);
+  sum_rescale(b, m, c);
+  RowSum r;
+  r.m = m;
+  two_sum(a.s, b.s, r.s, r.e);
+  r.e += a.e + b.e;
+  return r;
+}
+// joins those of n lanes, a power of two
+__device__ __forceinline__ RowSum sum_lanes(RowSum a, int n, float c) {
+  for (int o = n >> 1; o > 0; o >>= 1) {
+    RowSum b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.e = __shfl_xor_sync(0xffffffffu, a.e, o);
+    a = sum_join(a, b, c);
+  }
+  return a;
+}
+// adds a chunk's vectors, none of which is above a.m
 template <typename T>
-__global__ void __launch_bounds__(kBsNT) beam_rows_kernel(BsArgs a) {
-  __shared__ float red_m[kBsNT / 32], red_s[kBsNT / 32], red_e[kBsNT / 32];
-  __shared__ bs_key red_k[kBsNT / 32];
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!bs_live(a, row)) {
-    if (tid == 0) {
-      const float s = a.scores[row];
-      a.rows[row] = BeamRow{0.f, 1.f, 0.f, 0, s == -INFINITY || fabsf(s) < INFINITY ? 0 : VT_DEV_NONFINITE};
+__device__ __forceinline__ void sum_add(RowSum& a, const uint4 (&v)[kLpU], float c) {
+  const f32x2 c2 = pack2(c, c);
+  f32x2 sum[kLpU];
+#pragma unroll
+  for (int u = 0; u < kLpU; ++u)
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kVec; e += 2) {
+      float t0, t1;
+      unpack2(mul2(Vec<T>::diff2(v[u], e, -a.m), c2), t0, t1);
+      const f32x2 w = pack2(exp2_approx(t0), exp2_approx(t1));
+      sum[u] = e == 0 ? w : add2(sum[u], w);
     }
-    return;
-  }
-  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  float m = -INFINITY;
-  bool nan = false;
-  for (int j = tid; j < a.K; j += kBsNT) {
-    const float x = Elem<T>::load(l + j);
-    nan |= x != x;
-    m = fmaxf(m, x);
-  }
-  if (nan) m = INFINITY;
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red_m[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < kBsNT / 32; ++w) m = fmaxf(m, red_m[w]);
-  if (!(fabsf(m) < INFINITY)) {  // uniform in the block
-    if (tid == 0) a.rows[row] = BeamRow{0.f, 1.f, 0.f, 0, m > 0.f ? VT_DEV_NONFINITE : 0};
-    return;
-  }
-  float s = 0.f, e = 0.f;
-  for (int j = tid; j < a.K; j += kBsNT) {
-    float t;
-    two_sum(s, exp2_approx((Elem<T>::load(l + j) - m) * a.c), s, t);
-    e += t;
-  }
-  for (int o = 16; o > 0; o >>= 1) {
-    const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
-    float t;
-    two_sum(s, s2, s, t);
-    e += e2 + t;
-  }
-  if (lane == 0) red_s[warp] = s, red_e[warp] = e;
-  bs_key last = ~0ull;
-  int n = 0;
-  for (; n < a.N; ++n) {
-    bs_key top = 0;
-    for (int j = tid; j < a.K; j += kBsNT) {
-      const float x = Elem<T>::load(l + j);
-      const bs_key q = x > -INFINITY ? bs_key_of(x, j) : 0;
-      if (q < last && q > top) top = q;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      const bs_key q = __shfl_xor_sync(0xffffffffu, top, o);
-      top = q > top ? q : top;
-    }
-    __syncthreads();
-    if (lane == 0) red_k[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < kBsNT / 32; ++w) top = red_k[w] > top ? red_k[w] : top;
-    if (top == 0) break;
-    if (tid == 0) a.best[(int64_t)row * a.N + n] = top;
-    last = top;
-  }
+#pragma unroll
+  for (int h = kLpU / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int u = 0; u < h; ++u) sum[u] = add2(sum[u], sum[u + h]);
+  float s0, s1, er;
+  unpack2(sum[0], s0, s1);
+  two_sum(a.s, s0 + s1, a.s, er);
+  a.e += er;
+}
+
+struct BsShared {
+  RowLists top;
+  alignas(8) uint64_t full[kLpStages], empty[kLpStages];
+  RowSum red[kLpWarps];
+  RowSum blk;      // this block's, as published
+  float edge[16];  // the row's edges
+  int timeout;
+};
+
+// Each cluster takes rows of logits as the log probabilities' kernel does (one warp
+// copies, eight consume), and leaves m, S and the N best.
+template <typename T>
+__global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) beam_rows_kernel(BsArgs a) {
+  constexpr int VE = Elem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ BsShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int N = a.N, R = a.B * a.W;
+  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
+  griddep_launch_dependents();  // the merge waits for this grid before it reads
   if (tid == 0) {
-    float S = 0.f, E = 0.f;
-    for (int w = 0; w < kBsNT / 32; ++w) {
-      float t;
-      two_sum(S, red_s[w], S, t);
-      E += red_e[w] + t;
+    for (int s = 0; s < kLpStages; ++s) {
+      umma::mbar_init(&sh.full[s], 1);
+      umma::mbar_init(&sh.empty[s], kLpWarps);
     }
-    a.rows[row] = BeamRow{m, S, E, n, 0};
+    sh.timeout = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (blockIdx.x == 0) *a.dev_status = 0;  // the merge adds the rows' flags
+  }
+  __syncthreads();
+
+  if (warp == kLpWarps) {
+    // the copying warp runs ahead of the consumers, into their next rows
+    if (lane == 0) {
+      bool ok = true;
+      int it = 0;  // chunks requested so far
+      for (int row = row0; row < R && ok; row += stride) {
+        if (!bs_live(a, row)) continue;
+        const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+        const Span sp = span_of<T>(l, a.K, rank, C);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head);
+        for (int i = 0; i < sp.mine; ++i, ++it) {
+          const int s = it % kLpStages;
+          if (it >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((it / kLpStages) - 1) & 1);
+          if (!ok) break;
+          const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
+          const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)sp.nvec * 16 - at);
+          umma::mbar_expect_tx(&sh.full[s], bytes);
+          umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
+        }
+      }
+      if (!ok) {
+        atomicExch(&sh.timeout, 1);
+        // every copy issued has landed before this block may exit
+        for (int s = 0; s < kLpStages; ++s)
+          for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
+      }
+    }
+    __syncwarp();
+    if (C > 1 && bs_live(a, row0)) {
+      cl.sync();
+      cl.sync();
+    }
+    return;
+  }
+
+  int it = 0;  // chunks consumed so far
+  uint32_t limit = umma::kWaitLimit;
+  for (int row = row0; row < R; row += stride) {
+    if (!bs_live(a, row)) {
+      if (rank == 0 && tid == 0) {
+        const float s = a.scores[row];
+        a.rows[row] = BeamRow{0.f, 1.f, 0.f, 0, s == -INFINITY || fabsf(s) < INFINITY ? 0 : VT_DEV_NONFINITE};
+      }
+      continue;
+    }
+    const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+    const Span sp = span_of<T>(l, a.K, rank, C);
+    // the row's edges, one element per thread of block 0, kept in shared memory until the end
+    const bool edge = rank == 0 && tid < 2 * VE;
+    if (edge) {
+      const int id = edge_id<VE>(sp, tid);
+      sh.edge[tid] = id < a.K ? Elem<T>::load(l + id) : -INFINITY;
+    }
+    RowSum st{kNegBig, 0.f, 0.f};
+    // an id at -infinity is no candidate: the bound starts above it
+    TopList top{sh.top.list[warp], 0, (lp_key)(lp_ord(-INFINITY) + 1) << 32, kNegBig};
+
+    for (int i = 0; i < sp.mine; ++i, ++it) {
+      const int s = it % kLpStages;
+      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (it / kLpStages) & 1, limit))) {
+        // gave up: go on without the data, so that no barrier is missed
+        limit = 1;
+        if (lane == 0) atomicExch(&sh.timeout, 1);
+      }
+      const int q0 = (rank + i * C) * (kLpNT * kLpU) + tid;  // first vector of this thread
+      const uint4* st4 = reinterpret_cast<const uint4*>(ring + s * kLpChunk) + tid;
+      const int have = min(kLpU, max(0, (sp.nvec - q0 + kLpNT - 1) / kLpNT));  // vectors in the row
+      float pm;
+      {
+        uint4 v[kLpU];
+#pragma unroll
+        for (int u = 0; u < kLpU; ++u)
+          v[u] = u < have ? st4[u * kLpNT]
+                          : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+        pm = Vec<T>::top(v);
+        if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
+        sum_add<T>(st, v, a.c);
+      }
+      top.renew(st.s > 0.f ? st.m : -INFINITY, i, sp.mine, sh.top.group, N, tid);
+      top.scan<T>(pm, st4, q0, sp, N, lane);
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
+    }
+
+    if (rank == 0) {
+      const float xe = edge ? sh.edge[tid] : -INFINITY;
+      if (!(xe <= st.m)) sum_rescale(st, max_nan(st.m, xe), a.c);
+      float er;
+      two_sum(st.s, exp2_approx((xe - st.m) * a.c), st.s, er);
+      st.e += er;
+      top.add(xe, edge_id<VE>(sp, tid), edge, N, lane);
+    }
+    st = sum_lanes(st, 32, a.c);
+    if (lane == 0) sh.red[warp] = st;
+    lists_join(sh.top, top.n, top.bound, N, warp, lane);
+    lp_bar();
+    RowSum r = sum_lanes(sh.red[lane % kLpWarps], kLpWarps, a.c);
+    lp_key q = 0;  // this thread's candidate for the N best
+    int rk = lane, n = 0;
+    bool late;
+    if (C == 1) {
+      if (warp == 0 && lane < N) q = sh.top.best[lane];
+      n = __popc(__ballot_sync(0xffffffffu, q != 0));
+      late = sh.timeout != 0;
+    } else {
+      if (tid == 0) sh.blk = r;
+      cl.sync();
+      if (rank != 0) {
+        // the first block reads this one's memory before it arrives in turn
+        cl.sync();
+        return;
+      }
+      // all blocks' sums, one per lane, and keys; warp w holds block w's
+      const int from = lane < C ? lane : 0;
+      r = *cl.map_shared_rank(&sh.blk, from);
+      if (lane >= C) r.s = r.e = 0.f;
+      const bool gave_up = *cl.map_shared_rank(&sh.timeout, from) != 0;
+      if (warp < C) {
+        if (lane < N) {
+          q = cl.map_shared_rank(sh.top.best, warp)[lane];
+          sh.top.all[warp * N + lane] = q;
+        }
+        if (warp == 0 && lane < 8) sh.top.all[C * N + lane] = 0;
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, q != 0);
+      if (lane == 0) sh.top.n[warp] = __popc(has);
+      late = __any_sync(0xffffffffu, gave_up);
+      r = sum_lanes(r, kLpMaxC, a.c);
+      lp_bar();  // every read of the other blocks' memory has returned
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // they may exit
+      if (q != 0) rk = count_before(sh.top.all, C * N, q);
+      for (int w = 0; w < kLpWarps; ++w) n += sh.top.n[w];
+      n = min(n, N);
+    }
+    const bool ok = !late && r.m < INFINITY;  // no NaN, no +infinity
+    if (tid == 0)
+      a.rows[row] = BeamRow{r.m, r.s, r.e, ok && r.s > 0.f ? n : 0, late ? VT_DEV_TIMEOUT : ok ? 0 : VT_DEV_NONFINITE};
+    if (q != 0 && rk < N) a.best[(int64_t)row * N + rk] = q;
+    if (C > 1)
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    else
+      lp_bar();  // the next row writes what this one has read
   }
 }
 
@@ -197,20 +353,12 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
   __shared__ unsigned again;           // beams whose S is summed again
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.W, N = a.N, row0 = b * W;
-  if (b == 0) {  // the call's status word
-    __shared__ int flags;
-    if (tid == 0) flags = 0;
-    __syncthreads();
-    int f = 0;
-    for (int r = tid; r < a.B * W; r += kBsNT) f |= a.rows[r].flags;
-    if (f) atomicOr(&flags, f);
-    __syncthreads();
-    if (tid == 0) *a.dev_status = flags;
-  }
+  griddep_wait();
   if (tid < W) {
     const int row = row0 + tid;
     const BeamRow r = a.rows[row];
     const float s = a.scores[row];
+    if (r.flags) atomicOr(a.dev_status, r.flags);
     count[tid] = r.n;
     top[tid] = r.m;
     off[tid] = (double)s - log((double)r.s + (double)r.e);
@@ -229,7 +377,7 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
     for (int i = tid; i < W * N; i += kBsNT) {
       const int w = i / N, j = i - w * N;
       if (j < count[w] && !(a.done && a.done[row0 + w])) {
-        const float v = bs_value(a.best[(int64_t)(row0 + w) * N + j]);
+        const float v = key_value(a.best[(int64_t)(row0 + w) * N + j]);
         key[w][j] = bs_order(((double)v - (double)top[w]) * a.inv_t + off[w]);
       }
     }
@@ -266,7 +414,7 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
           const bool over = a.done && a.done[row];
           int token = a.end_id;
           if (!over) {
-            token = bs_id(a.best[(int64_t)row * N + at]);
+            token = key_id(a.best[(int64_t)row * N + at]);
             if (a.trim_ids) token = a.trim_ids[token];
           }
           const int64_t o = (int64_t)b * N + n;
@@ -375,6 +523,37 @@ int launch_reorder(cudaStream_t s, const BrArgs& a) {
   return VT_OK;
 }
 
+template <typename T>
+int launch_select(cudaStream_t s, const BsArgs& a) {
+  auto rows = beam_rows_kernel<T>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
+  const int64_t R = (int64_t)a.B * a.W;
+  const int C = lp_cluster(R, a.K, (int)sizeof(T));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C > 1 ? R * C : std::min<int64_t>(R, num_sms() * kLpPerSm)));
+  cfg.blockDim = dim3(kLpNT + 32);
+  cfg.dynamicSmemBytes = kLpSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, rows, a));
+  cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B);
+  cfg.blockDim = dim3(kBsNT);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, beam_merge_kernel<T>, a));
+  return VT_OK;
+}
+
 size_t select_bytes(int64_t B, int64_t W, int64_t N) {
   return align_up((size_t)(B * W) * sizeof(BeamRow), 256) + (size_t)(B * W * N) * sizeof(bs_key);
 }
@@ -432,17 +611,7 @@ extern "C" int vt_beam_select(const void* logits, int32_t logits_dtype, int32_t 
   a.rows = static_cast<BeamRow*>(workspace);
   a.best = reinterpret_cast<bs_key*>(static_cast<uint8_t*>(workspace) +
                                      align_up((size_t)B * W * sizeof(BeamRow), 256));
-  if (elem == 4) {
-    beam_rows_kernel<float><<<B * W, kBsNT, 0, s>>>(a);
-    VT_RETURN_IF_LAUNCH_FAILED();
-    beam_merge_kernel<float><<<B, kBsNT, 0, s>>>(a);
-  } else {
-    beam_rows_kernel<uint16_t><<<B * W, kBsNT, 0, s>>>(a);
-    VT_RETURN_IF_LAUNCH_FAILED();
-    beam_merge_kernel<uint16_t><<<B, kBsNT, 0, s>>>(a);
-  }
-  VT_RETURN_IF_LAUNCH_FAILED();
-  return VT_OK;
+  return elem == 4 ? launch_select<float>(s, a) : launch_select<uint16_t>(s, a);
 }
 
 extern "C" int vt_beam_reorder(const void* state, void* out, const int64_t* strides,

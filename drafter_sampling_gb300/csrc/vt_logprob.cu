@@ -44,24 +44,13 @@
 #include <cooperative_groups.h>
 
 #include "vt_internal.h"
+#include "vt_rows.cuh"
 #include "vt_umma.cuh"
-#include "vt_verify_common.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace vt {
 namespace {
-
-constexpr int kLpNT = 256;           // consuming threads
-constexpr int kLpWarps = kLpNT / 32;
-constexpr int kLpU = 8;              // 16-byte vectors per thread and chunk
-constexpr int kLpChunk = kLpNT * kLpU * 16;  // bytes
-constexpr int kLpStages = 2;
-constexpr int kLpMaxK = 32;
-constexpr int kLpList = 64;          // entries of a warp's list (2 * kLpMaxK: a cut leaves room)
-constexpr int kLpMaxC = 8;
-constexpr int kLpSmem = kLpStages * kLpChunk;
-constexpr int kLpPerSm = 3;          // resident blocks per SM (shared memory)
 
 struct LpArgs {
   const void* logits;
@@ -77,123 +66,10 @@ struct LpArgs {
   int own_status;        // one row: its block stores the status word; else it is zeroed beforehand
 };
 
-// Order key of (value, id): higher value first, then lower id; 0 is after
-// every key.  -0 counts as 0.
-typedef unsigned long long lp_key;
-__device__ __forceinline__ uint32_t lp_ord(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ lp_key key_of(float v, int id) {
-  return (lp_key)lp_ord(v) << 32 | (uint32_t)~id;
-}
-__device__ __forceinline__ float key_value(lp_key q) {
-  const uint32_t o = (uint32_t)(q >> 32);
-  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-__device__ __forceinline__ int key_id(lp_key q) { return (int)~(uint32_t)q; }
-
-// how many of the n keys at `keys` come before q; keys is 16-byte aligned and
-// zero from n up to the next multiple of 8
-__device__ __forceinline__ int count_before(const lp_key* keys, int n, lp_key q) {
-  int r = 0;
-  for (int o = 0; o < n; o += 8) {
-#pragma unroll
-    for (int h = 0; h < 8; h += 2) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(keys + o + h);
-      r += (two.x > q ? 1 : 0) + (two.y > q ? 1 : 0);
-    }
-  }
-  return r;
-}
-
 // (x - m) / T, where x - m itself may lie beyond fp32 (halves differ exactly)
 __device__ __forceinline__ float scaled_diff(float x, float m, float inv_t) {
   return (0.5f * x - 0.5f * m) * (2.f * inv_t);
 }
-
-// larger of two, NaN if either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// two fp32 values in one 64-bit register, and arithmetic on both at once
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// the largest of a 16-byte vector's elements, NaN if one is
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-  __device__ static float top(uint4 v) {
-    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
-                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
-  }
-  __device__ static float top(const uint4 (&v)[kLpU]) {
-    float m = top(v[0]);
-#pragma unroll
-    for (int u = 1; u < kLpU; ++u) m = max_nan(m, top(v[u]));
-    return m;
-  }
-  // elements e, e + 1 of a vector, plus s
-  __device__ static f32x2 diff2(uint4 v, int e, float s) {
-    return add2(e == 0 ? pack2(__uint_as_float(v.x), __uint_as_float(v.y))
-                       : pack2(__uint_as_float(v.z), __uint_as_float(v.w)),
-                pack2(s, s));
-  }
-  static constexpr uint32_t kMasked = 0xff800000u;  // -infinity
-};
-template <> struct Vec<uint16_t> {
-  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-  }
-  __device__ static float top(uint4 v) {
-    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-  }
-  __device__ static float top(const uint4 (&v)[kLpU]) {
-    uint32_t m = max2(max2(v[0].x, v[0].y), max2(v[0].z, v[0].w));
-#pragma unroll
-    for (int u = 1; u < kLpU; ++u)
-      m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
-    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-  }
-  // elements e, e + 1 of a vector, plus s: bf16 operands widened by the addition
-  __device__ static f32x2 diff2(uint4 v, int e, float s) {
-    const uint32_t w = e == 0 ? v.x : e == 2 ? v.y : e == 4 ? v.z : v.w;
-    float a, b;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.bf16 %0, lo, %3;\n\tadd.rn.f32.bf16 %1, hi, %3;\n\t}"
-        : "=f"(a), "=f"(b)
-        : "r"(w), "f"(s));
-    return pack2(a, b);
-  }
-  static constexpr uint32_t kMasked = 0xff80ff80u;
-};
 
 // running statistics: the maximum m, S = s + e (e: what rounding took from s)
 // and d = sum w y, with y = x - m and w = 2^(y c)
@@ -205,11 +81,6 @@ struct Lse {
 // zero weight is not formed
 constexpr float kLpLow = 200.f;
 
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-  s = a + b;
-  const float t = s - a;
-  e = (a - (s - t)) + (b - t);
-}
 // the same statistics relative to a maximum m >= a.m
 __device__ __forceinline__ void lse_rescale(Lse& a, float m, float c, float low) {
   const float y = fmaxf(a.m - m, low);
@@ -288,130 +159,14 @@ __device__ __noinline__ Lse lse_add_bounded(Lse st, const uint4* src, int have, 
   return st;
 }
 
-// Ranks a warp's list of n keys by counting and cuts it to its k best, in
-// order; returns how many are left.
-__device__ __noinline__ int list_cut(lp_key* list, int n, int k) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-  lp_key q[kLpList / 32];
-  int r[kLpList / 32];
-#pragma unroll
-  for (int h = 0; h < kLpList / 32; ++h) {
-    const int j = lane + 32 * h;
-    q[h] = j < n ? list[j] : 0;
-    r[h] = j < n ? 0 : k;
-  }
-  for (int o = 0; o < n; ++o) {
-    const lp_key other = list[o];
-#pragma unroll
-    for (int h = 0; h < kLpList / 32; ++h) r[h] += other > q[h] ? 1 : 0;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int h = 0; h < kLpList / 32; ++h)
-    if (r[h] < k) list[r[h]] = q[h];
-  __syncwarp();
-  return min(n, k);
-}
-
-// the k-th largest of the 32 lanes' values (1 <= k <= 32), by a bitonic sort
-__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const float o = __shfl_xor_sync(0xffffffffu, v, stride);
-      v = ((lane & size) == 0) == ((lane & stride) == 0) ? fmaxf(v, o) : fminf(v, o);
-    }
-  return __shfl_sync(0xffffffffu, v, k - 1);
-}
-
-// the consuming warps' barrier
-__device__ __forceinline__ void lp_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kLpNT) : "memory");
-}
-
-// A row's layout for one block: ids [0, head) precede the first 16-byte
-// boundary, nvec whole vectors follow, then the rest; mine of the vectors'
-// chunks are this block's.
-struct Span {
-  int head, nvec, mine;
-};
-template <typename T>
-__device__ __forceinline__ Span span_of(const LpArgs& a, int row, int rank, int C) {
-  constexpr int VE = Elem<T>::kVec;
-  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
-  Span sp;
-  sp.head = min(a.V, off ? VE - off : 0);
-  sp.nvec = (a.V - sp.head) / VE;
-  const int chunks = (sp.nvec + kLpNT * kLpU - 1) / (kLpNT * kLpU);
-  sp.mine = chunks > rank ? (chunks - rank + C - 1) / C : 0;
-  return sp;
-}
-
-// the id of a row's edge element t: first those before the vectors, then those behind
-template <int VE>
-__device__ __forceinline__ int edge_id(const Span& sp, int t) {
-  return t < sp.head ? t : sp.nvec * VE + t;
-}
-
 struct LpShared {
-  alignas(16) lp_key list[kLpWarps][kLpList];        // the warps' lists
-  alignas(16) lp_key all[kLpWarps * kLpList + 8];    // all lists, joined
-  alignas(16) lp_key best[kLpMaxK];                  // this block's k best, as published
-  alignas(16) float group[32];                       // largest logit of each of 32 groups of threads
+  RowLists top;
   alignas(8) uint64_t full[kLpStages], empty[kLpStages];
-  int n[kLpWarps];
   Lse red[kLpWarps];
   Lse blk;                                           // this block's statistics, as published
   float edge[16], xt;                                // the row's edges; the given token's logit
   int timeout;
 };
-
-// Joins the warps' lists (n entries in this warp's, of which those not after
-// `bound` count) into the block's k best, ranked in sh.best (zero behind the
-// last).  All consuming warps call it.
-__device__ __forceinline__ void lists_join(LpShared& sh, int n, lp_key bound, int k, int warp,
-                                           int lane) {
-  lp_key mine[kLpList / 32];
-  __syncwarp();
-#pragma unroll
-  for (int h = 0; h < kLpList / 32; ++h) {
-    const int j = lane + 32 * h;
-    mine[h] = j < n ? sh.list[warp][j] : 0;
-    if (mine[h] < bound) mine[h] = 0;
-  }
-  unsigned has[kLpList / 32];
-  n = 0;
-#pragma unroll
-  for (int h = 0; h < kLpList / 32; ++h) {
-    has[h] = __ballot_sync(0xffffffffu, mine[h] != 0);
-    n += __popc(has[h]);
-  }
-  if (lane == 0) sh.n[warp] = n;
-  if (warp == 0) sh.best[lane] = 0;
-  lp_bar();
-  int at = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kLpWarps; ++w) {
-    const int nw = sh.n[w];
-    at += w < warp ? nw : 0;
-    total += nw;
-  }
-#pragma unroll
-  for (int h = 0; h < kLpList / 32; ++h) {
-    if (mine[h] != 0) sh.all[at + __popc(has[h] & ((1u << lane) - 1u))] = mine[h];
-    at += __popc(has[h]);
-  }
-  if (warp == kLpWarps - 1 && lane < 8) sh.all[total + lane] = 0;
-  lp_bar();
-  for (int j = warp * 32 + lane; j < total; j += kLpNT) {
-    const lp_key q = sh.all[j];
-    const int r = count_before(sh.all, total, q);
-    if (r < k) sh.best[r] = q;
-  }
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(LpArgs a) {
@@ -442,7 +197,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       int it = 0;  // chunks requested so far
       for (int row = row0; row < a.R && ok; row += stride) {
         if (a.tokens[row] == -1) continue;
-        const Span sp = span_of<T>(a, row, rank, C);
+        const Span sp = span_of<T>(static_cast<const T*>(a.logits) + (int64_t)row * a.ld, a.V, rank, C);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(
             static_cast<const T*>(a.logits) + (int64_t)row * a.ld + sp.head);
         for (int i = 0; i < sp.mine; ++i, ++it) {
@@ -492,8 +247,8 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       continue;
     }
     const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-    const Span sp = span_of<T>(a, row, rank, C);
-    const int head = sp.head, nvec = sp.nvec, mine = sp.mine;
+    const Span sp = span_of<T>(l, a.V, rank, C);
+    const int nvec = sp.nvec, mine = sp.mine;
     // the given token's logit and the row's edges, one element per thread of
     // block 0, kept in shared memory until the end: registers are short
     const bool edge = rank == 0 && tid < 2 * VE;
@@ -504,28 +259,8 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     }
     const float c = a.c, low = -kLpLow / c;
     Lse st{kNegBig, 0.f, 0.f, 0.f};
-    // this warp's list: n keys not after `bound`, whose value is tv
-    lp_key* const list = sh.list[warp];
-    int n = 0;
-    lp_key bound = 0;
-    float tv = -INFINITY;
+    TopList top{sh.top.list[warp], 0, 0, -INFINITY};
     bool bounded = false;
-    volatile float* const group = sh.group;
-    auto add = [&](float x, int id, bool valid) {
-      if (!__any_sync(0xffffffffu, valid && x >= tv)) return;  // a NaN is none
-      const lp_key q = key_of(x, id);
-      const bool take = valid && x >= tv && q >= bound;
-      const unsigned m = __ballot_sync(0xffffffffu, take);
-      if (n + __popc(m) > kLpList) {
-        n = list_cut(list, n, k);  // n > 32: k keys are left
-        if (list[k - 1] > bound) {
-          bound = list[k - 1];
-          tv = key_value(bound);
-        }
-      }
-      if (take) list[n + __popc(m & ((1u << lane) - 1u))] = q;
-      n += __popc(m);
-    };
 
     for (int i = 0; i < mine; ++i, ++it) {
       const int s = it % kLpStages;
@@ -567,42 +302,8 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
         continue;
       }
 
-      if ((i & (i + 1)) == 0 && (i == 0 || mine - 1 - i > i + 1)) {
-        // after 1, 2, 4 ... chunks, while more are to come than have been, the bound: the k-th largest of 32 groups'
-        // (8 lanes each) largest logits so far.  Only the first chunk needs every group's value;
-        // later a value of another warp may be an older one, which is as valid.
-        float g = st.s > 0.f ? st.m : -INFINITY;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if ((lane & 7) == 0) group[tid >> 3] = g;
-        if (i == 0)
-          lp_bar();
-        else
-          __syncwarp();
-        const float gk = kth_of_lanes(group[lane], k, lane);
-        const lp_key b = (lp_key)lp_ord(gk) << 32;
-        if (b > bound) {
-          bound = b;
-          tv = gk;
-        }
-      }
-      // the lanes that hold a candidate, usually few, one by one: the warp
-      // looks at that lane's vectors together, a word per lane
-      unsigned holders = __ballot_sync(0xffffffffu, pm >= tv);
-      while (holders) {
-        const int src = __ffs(holders) - 1;
-        holders &= holders - 1;
-        const int qv = q0 - lane + src + (lane >> 2) * kLpNT;
-        const uint32_t word =
-            reinterpret_cast<const uint32_t*>(st4 - lane + src + (lane >> 2) * kLpNT)[lane & 3];
-        const int id = head + qv * VE + (lane & 3) * (VE / 4);
-        if constexpr (VE == 4) {
-          add(__uint_as_float(word), id, qv < nvec);
-        } else {
-          add(__uint_as_float(word << 16), id, qv < nvec);
-          add(__uint_as_float(word & 0xffff0000u), id + 1, qv < nvec);
-        }
-      }
+      top.renew(st.s > 0.f ? st.m : -INFINITY, i, mine, sh.top.group, k, tid);
+      top.scan<T>(pm, st4, q0, sp, k, lane);
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
     }
@@ -618,7 +319,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       st.d = fmaf(w, y, st.d);
       if (k > 0) {
         const int id = edge_id<VE>(sp, tid);
-        add(xe, id, edge && id < a.V && xe == xe);
+        top.add(xe, id, edge && id < a.V && xe == xe, k, lane);
       }
     }
     // this block's statistics and ranked keys
@@ -632,7 +333,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       st = lse_join(st, w, c, low);
     }
     if (lane == 0) sh.red[warp] = st;
-    if (k > 0) lists_join(sh, n, bound, k, warp, lane);
+    if (k > 0) lists_join(sh.top, top.n, top.bound, k, warp, lane);
     lp_bar();
     Lse r = sh.red[lane % kLpWarps];
 #pragma unroll
@@ -648,7 +349,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     int rk = 0;    // ... and its rank
     bool late;
     if (C == 1) {
-      if (warp == 0 && lane < k) q = sh.best[lane];
+      if (warp == 0 && lane < k) q = sh.top.best[lane];
       rk = lane;
       late = sh.timeout != 0;
     } else {
@@ -666,10 +367,10 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       const bool gave_up = *cl.map_shared_rank(&sh.timeout, from) != 0;
       if (warp < C) {
         if (lane < k) {
-          q = cl.map_shared_rank(sh.best, warp)[lane];
-          sh.all[warp * k + lane] = q;
+          q = cl.map_shared_rank(sh.top.best, warp)[lane];
+          sh.top.all[warp * k + lane] = q;
         }
-        if (warp == 0 && lane < 8) sh.all[C * k + lane] = 0;
+        if (warp == 0 && lane < 8) sh.top.all[C * k + lane] = 0;
       }
       late = __any_sync(0xffffffffu, gave_up);
 #pragma unroll
@@ -687,7 +388,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
       r.d = __shfl_sync(0xffffffffu, r.d, 0);
       lp_bar();  // every read of the other blocks' memory has returned
       asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // they may exit
-      if (q != 0) rk = count_before(sh.all, C * k, q);
+      if (q != 0) rk = count_before(sh.top.all, C * k, q);
     }
     const bool ok = !late && r.s > 0.f && isfinite(r.s) && isfinite(r.m);
     const float lnS = log1pf((r.s - 1.f) + r.e);  // the largest logit's weight is exactly 1
@@ -715,25 +416,6 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) token_logprobs_kernel(Lp
     else
       lp_bar();  // the next row writes what this one has read
   }
-}
-
-// Thread blocks per row: the count that gives the shortest schedule, taking a
-// block's time as its chunks plus three more for its start and its join, and
-// kLpPerSm blocks of each SM running at once.
-int lp_cluster(int64_t R, int V, int elem) {
-  const int64_t chunks = ((int64_t)V * elem + kLpChunk - 1) / kLpChunk;
-  const int64_t slots = (int64_t)num_sms() * kLpPerSm;
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int C = 1; C <= kLpMaxC && C <= chunks; C *= 2) {
-    const int64_t waves = (R * C + slots - 1) / slots;
-    const int64_t t = waves * ((chunks + C - 1) / C + 3);
-    if (t < least) {
-      least = t;
-      best = C;
-    }
-  }
-  return best;
 }
 
 template <typename T>
