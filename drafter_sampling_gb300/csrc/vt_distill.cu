@@ -20,18 +20,33 @@
 // with m the largest logit of all, mr that of the unlisted ids (two, because either
 // may be out of fp32's range relative to the other) and the three factors kept
 // per row by the loss.
+#include <algorithm>
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "vt_internal.h"
-#include "vt_pair.cuh"
-#include "vt_verify_common.cuh"
+#include "vt_rows.cuh"
+#include "vt_umma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace vt {
 namespace {
 
 constexpr int kDsMaxK = 128;
+constexpr int kDsLane = kDsMaxK / 32;      // list entries of a lane
 constexpr int kDsNT = 256;
-constexpr int kDsWarps = kDsNT / 32;
+constexpr int kDsThreads = kLpNT + 64;     // consuming warps, one that copies, one for the list
+
+// what takes an element out of a sum
+template <typename T> struct Mask;
+template <> struct Mask<float> {
+  __device__ static uint32_t bits() { return 0xff800000u; }  // -infinity
+};
+template <> struct Mask<uint16_t> {
+  __device__ static uint16_t bits() { return 0xff80u; }
+};
 
 struct DsStats {
   float m, mr, c_all, c_rest, c_t;
@@ -43,7 +58,7 @@ struct DsArgs {
   int R, K, V, k;
   int rest;
   float c;                 // log2(e) / T
-  double inv_t;            // 1 / T
+  Pair inv_t;              // 1 / T
   const int* ids;          // [R][k]
   const float* logp;       // [R][k]
   const int* inv_map;      // [V] or nullptr (V == K)
@@ -53,6 +68,7 @@ struct DsArgs {
   void* grad;
   int64_t ld_grad;
   int* dev_status;
+  int own_status;          // one row: its block stores the status word; else it is zeroed beforehand
 };
 
 // the place of list entry i in the drafter's vocabulary, -1 where it has none,
@@ -66,180 +82,437 @@ __device__ __forceinline__ int ds_place(const DsArgs& a, int64_t i) {
   return p >= -1 && p < a.K ? p : -2;
 }
 
+// A row's list as the block's warps share it
 struct DsList {
-  int place[kDsMaxK];  // of kept entries, -1 of others
+  int place[kDsMaxK];  // of entries that the drafter has, else -1
+  int pos[kDsMaxK];    // bytes from the start of what this block reads of the row, -1: not there
   float z[kDsMaxK], logp[kDsMaxK];
-  int flags, kept;
+  unsigned edges;      // the row's edge elements that are listed
+  int any;             // an id is given
+  int flags;
+};
+// What the consuming warps leave of a row: the sum over its unlisted ids
+struct DsSum {
+  RowSum sum;
+  int late;
 };
 
-// Reads a row's list; all threads of the block call it.
-template <typename T>
-__device__ void ds_read_list(const DsArgs& a, int row, const T* l, DsList& sh) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  if (tid == 0) sh.flags = sh.kept = 0;
-  __syncthreads();
-  int p = -1;
-  if (tid < a.k) {
-    const int64_t i = (int64_t)row * a.k + tid;
-    p = ds_place(a, i);
-    float z = 0.f;
-    const float lp = a.logp[i];
-    if (p == -2) atomicOr(&sh.flags, VT_DEV_BAD_ID);
-    if (p >= 0) {
-      z = Elem<T>::load(l + p);
-      if (z == -INFINITY) p = -1;
+// The list of a row, read by one warp in two steps: the places, which the consuming
+// warps wait for, and what stands there.  at(place): the byte position in what this
+// block reads, or -1.
+template <typename T, typename At>
+__device__ __forceinline__ void ds_places(const DsArgs& a, int row, const Span& sp, bool edges, DsList& sh, int lane,
+                                          At at) {
+  int p[kDsLane];
+  bool any = false;
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    p[h] = -1;
+    if (i < a.k) {
+      const int id = __ldg(a.ids + (int64_t)row * a.k + i);
+      any |= id != -1;
+      p[h] = id == -1 ? -1 : id < 0 || id >= a.V ? -2 : id;
     }
-    if (p >= 0 && !(lp < 80.f)) atomicOr(&sh.flags, VT_DEV_NONFINITE);
-    if (p >= 0) atomicAdd(&sh.kept, 1);
-    sh.place[tid] = p < 0 ? -1 : p;
-    sh.z[tid] = z;
-    sh.logp[tid] = lp;
   }
-  __syncthreads();
-  if (p >= 0)
-    for (int i = 0; i < tid; ++i)
-      if (sh.place[i] == p) atomicOr(&sh.flags, VT_DEV_DUPLICATE_ID);
-  __syncthreads();
+  bool bad = false;
+  unsigned edge = 0;
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    if (p[h] >= 0 && a.inv_map) {
+      const int q = __ldg(a.inv_map + p[h]);
+      p[h] = q >= -1 && q < a.K ? q : -2;
+    }
+    bad |= p[h] == -2;
+    if (i < a.k) {
+      sh.place[i] = max(p[h], -1);
+      sh.pos[i] = p[h] >= 0 ? at(p[h]) : -1;
+    }
+    if (p[h] >= 0 && edges) {
+      const int t = p[h] < sp.head ? p[h] : p[h] - sp.nvec * Elem<T>::kVec;
+      if (p[h] < sp.head || t >= sp.head) edge |= 1u << t;
+    }
+  }
+  any = __any_sync(0xffffffffu, any);
+  bad = __any_sync(0xffffffffu, bad);
+  edge = __reduce_or_sync(0xffffffffu, edge);
+  if (lane == 0) {
+    sh.any = any;
+    sh.flags = bad ? VT_DEV_BAD_ID : 0;
+    sh.edges = edge;
+  }
+  __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void ds_entries(const DsArgs& a, int row, const T* l, DsList& sh, int lane) {
+  int flags = 0;
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    if (i >= a.k) break;
+    const int p = sh.place[i];
+    const float lp = __ldg(a.logp + (int64_t)row * a.k + i);
+    const float z = p >= 0 ? Elem<T>::load(l + p) : -INFINITY;
+    if (p >= 0 && z != -INFINITY) {  // kept
+      if (!(z < INFINITY) || !(lp < 80.f)) flags = VT_DEV_NONFINITE;
+      int twice = 0;
+      for (int o = 0; o < i; ++o) twice |= sh.place[o] == p;
+      if (twice) flags |= VT_DEV_DUPLICATE_ID;
+    }
+    sh.z[i] = z;
+    sh.logp[i] = lp;
+  }
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if (lane == 0) sh.flags |= flags;
+  __syncwarp();
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ Pair pair_warp_sum(Pair v) {
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair w;
+    w.h = __shfl_xor_sync(0xffffffffu, v.h, o);
+    w.l = __shfl_xor_sync(0xffffffffu, v.l, o);
+    v = pair_add(v, w);
+  }
   return v;
 }
-
-// Loss and statistics of a row, by one warp: from its list and the largest logit
-// mr and sum sr (relative to mr; 0: none) of the unlisted ids.
-__device__ void ds_finish(const DsArgs& a, const DsList& sh, float mr, double sr, int lane, float& loss,
-                          DsStats& st) {
-  float m = sr > 0.0 ? mr : -INFINITY;
-  for (int i = lane; i < a.k; i += 32)
-    if (sh.place[i] >= 0) m = fmaxf(m, sh.z[i]);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  double S = 0.0, mass = 0.0;
-  for (int i = lane; i < a.k; i += 32)
-    if (sh.place[i] >= 0) {
-      S += (double)exp2_approx((sh.z[i] - m) * a.c);
-      const Pair t = pair_exp(Pair{sh.logp[i], 0.f});
-      mass += (double)t.h + (double)t.l;
-    }
-  S = warp_sum(S);
-  mass = warp_sum(mass);
-  // ln of the unlisted ids' sum, relative to m, which may be far above mr
-  const double inv_t = a.inv_t;
-  double down = 0.0;
-  if (sr > 0.0) {
-    down = ((double)mr - (double)m) * inv_t;
-    S += sr * exp(down);
-  }
-  const double b = a.rest && sr > 0.0 ? fmax(0.0, 1.0 - mass) : 0.0;
-  const double A = mass + b;
-  if (!(A > 0.0)) {  // nothing to learn from this row
-    loss = 0.f;
-    st = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
-    return;
-  }
-  // four logarithms at once, one per lane
-  double v = lane == 0 ? S : lane == 1 ? sr : lane == 2 ? b : mass;
-  v = v > 0.0 ? log(v) : 0.0;
-  const double lnS = __shfl_sync(0xffffffffu, v, 0), lnr = __shfl_sync(0xffffffffu, v, 1);
-  const double lnb = __shfl_sync(0xffffffffu, v, 2), lna = __shfl_sync(0xffffffffu, v, 3);
-  double sum = 0.0;
-  for (int i = lane; i < a.k; i += 32)
-    if (sh.place[i] >= 0 && sh.logp[i] > -INFINITY) {
-      const Pair t = pair_exp(Pair{sh.logp[i], 0.f});
-      const double lnp = ((double)sh.z[i] - (double)m) * inv_t - lnS;
-      sum += ((double)t.h + (double)t.l) * ((double)sh.logp[i] - lnp);
-    }
-  sum = warp_sum(sum);
-  const double lnq = lnr + down - lnS;
-  const double all = inv_t / S, rest = sr > 0.0 ? all * exp(down) : 0.0;
-  if (a.rest) {
-    if (b > 0.0) sum += b * (lnb - lnq);
-    loss = (float)sum;
-    st.c_all = (float)(A * all);
-    st.c_rest = (float)(A * rest - (b > 0.0 ? inv_t * b / sr : 0.0));
-    st.c_t = (float)inv_t;
-  } else {
-    loss = (float)(sum / mass - lna);
-    st.c_all = (float)all;
-    st.c_rest = (float)rest;
-    st.c_t = (float)(inv_t / mass);
-  }
-  st.m = m;
-  st.mr = sr > 0.0 ? mr : 0.f;
+__device__ __forceinline__ Pair pair_from_lane(Pair v, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, v.h, lane), __shfl_sync(0xffffffffu, v.l, lane)};
 }
 
-__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+// Loss, statistics and flags of a row, by one warp: from its list and the sum of its
+// unlisted ids (s = 0: there are none above -infinity).
+__device__ void ds_finish(const DsArgs& a, const DsList& sh, const DsSum& un, int lane, float& loss, DsStats& st,
+                          int& flags) {
+  const float mr = un.sum.m;
+  const bool rest = !(un.sum.s == 0.f);  // (NaN: flagged below)
+  bool kept = false;
+  float m = rest ? mr : -INFINITY;
+  Pair mass{0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    if (i < a.k && sh.z[i] != -INFINITY) {
+      kept = true;
+      m = max_nan(m, sh.z[i]);
+      mass = pair_add(mass, pair_exp(Pair{sh.logp[i], 0.f}));
+    }
+  }
+  kept = __any_sync(0xffffffffu, kept);
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  mass = pair_warp_sum(mass);
+  loss = 0.f;
+  st = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
+  flags = sh.flags | (un.late ? VT_DEV_TIMEOUT : 0);
+  if (kept && !(m < INFINITY)) flags |= VT_DEV_NONFINITE;
+  if (flags) {
+    loss = __int_as_float(0x7fc00000);
+    st = DsStats{loss, loss, loss, loss, loss};
+    return;
+  }
+  // (z - m) / T; nothing of e^ it is left below -87
+  const auto below = [&](float z) {
+    Pair d;
+    two_sum(z, -m, d.h, d.l);
+    return pair_mul(d, a.inv_t);
+  };
+  const auto weight = [&](float z) {
+    return (z - m) * a.inv_t.h < -87.f ? Pair{0.f, 0.f} : pair_exp(below(z));
+  };
+  Pair b{0.f, 0.f};
+  if (a.rest && rest) b = pair_add(Pair{1.f, 0.f}, pair_neg(mass));
+  if (!(b.h > 0.f)) b = Pair{0.f, 0.f};
+  const Pair A = pair_add(mass, b);
+  if (!kept || !(A.h > 0.f)) return;  // nothing to learn from this row
+  Pair S{0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    if (i < a.k && sh.z[i] != -INFINITY) S = pair_add(S, weight(sh.z[i]));
+  }
+  S = pair_warp_sum(S);
+  const Pair sr = pair_of(un.sum.s, un.sum.e);
+  const Pair top = rest ? weight(mr) : Pair{0.f, 0.f};  // of the largest unlisted logit
+  S = pair_add(S, pair_mul(sr, top));
+  // four logarithms at once, one per lane
+  Pair v = lane == 0 ? S : lane == 1 ? sr : lane == 2 ? b : mass;
+  v = v.h > 0.f ? pair_log(v) : Pair{0.f, 0.f};
+  const Pair lnS = pair_from_lane(v, 0), lnr = pair_from_lane(v, 1), lnb = pair_from_lane(v, 2);
+  const Pair lna = pair_from_lane(v, 3);
+  Pair sum{0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    const int i = lane + 32 * h;
+    if (i < a.k && sh.z[i] != -INFINITY && sh.logp[i] > -INFINITY) {
+      const Pair lnp = pair_add(below(sh.z[i]), pair_neg(lnS));
+      const Pair lnt{sh.logp[i], 0.f};
+      sum = pair_add(sum, pair_mul(pair_exp(lnt), pair_add(lnt, pair_neg(lnp))));
+    }
+  }
+  sum = pair_warp_sum(sum);
+  const Pair all = pair_div(a.inv_t, S);
+  st.m = m;
+  st.mr = rest ? mr : 0.f;
+  if (a.rest) {
+    if (b.h > 0.f) {
+      const Pair lnq = pair_add(pair_add(lnr, below(mr)), pair_neg(lnS));
+      sum = pair_add(sum, pair_mul(b, pair_add(lnb, pair_neg(lnq))));
+    }
+    st.c_all = pair_mul(A, all).h;
+    Pair c = pair_mul(A, pair_mul(all, top));
+    if (b.h > 0.f) c = pair_add(c, pair_neg(pair_div(pair_mul(a.inv_t, b), sr)));
+    st.c_rest = c.h;
+    st.c_t = a.inv_t.h;
+  } else {
+    sum = pair_add(pair_div(sum, mass), pair_neg(lna));
+    st.c_all = all.h;
+    st.c_rest = pair_mul(all, top).h;
+    st.c_t = pair_div(a.inv_t, mass).h;
+  }
+  loss = sum.h;
+  if (loss != loss) loss = INFINITY;  // a term beyond fp32: they are positive
+}
 
+// Loss, statistics and flags of a row to where they go, by one thread
+__device__ __forceinline__ void ds_put(const DsArgs& a, int row, float loss, const DsStats& st, int flags) {
+  a.out_loss[row] = loss;
+  a.stats[row] = st;
+  if (a.own_status) {
+    *a.dev_status = flags;
+    return;
+  }
+  griddep_wait();  // the status word is clear
+  if (flags) atomicOr(a.dev_status, flags);
+}
+
+// Takes the listed elements out of what this warp is about to read: `first` bytes into
+// the block's part of the row begin `bytes` of it, at `buf`; vectors go to threads in turn.
 template <typename T>
-__global__ void __launch_bounds__(kDsNT) distill_loss_kernel(DsArgs a) {
-  __shared__ DsList sh;
-  __shared__ int hash[4 * kDsMaxK];
-  __shared__ float red[kDsWarps], red_s[kDsWarps], red_e[kDsWarps];
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  ds_read_list<T>(a, row, l, sh);
-  int flags = sh.flags;
-  if (sh.kept == 0 && flags == 0) {  // nothing listed: the row is not read
-    if (tid == 0) {
-      a.out_loss[row] = 0.f;
-      a.stats[row] = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void ds_mask(const DsList& sh, uint8_t* buf, int first, int bytes, int k, int warp, int lane) {
+  for (int i = lane; i < k; i += 32) {
+    const int p = sh.pos[i] - first;
+    if (p >= 0 && p < bytes && ((p >> 9) & (kLpWarps - 1)) == warp) {
+      *reinterpret_cast<decltype(Mask<T>::bits())*>(buf + p) = Mask<T>::bits();
+      // ahead of the next copy into this place
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ the loss
+struct DsShared {
+  DsList list[2];  // of the row in hand and the next one
+  DsSum sum[2];
+  RowSum red[2][kLpWarps];
+  RowSum blk;      // this block's sum, as published
+  float edge[2][16];
+  alignas(8) uint64_t full[kLpStages], empty[kLpStages], listed[2], summed[2];
+  int timeout;
+};
+
+// whether a row has an id listed; all lanes of a warp call it
+__device__ __forceinline__ bool ds_any(const DsArgs& a, int row, int lane) {
+  bool any = false;
+  for (int i = lane; i < a.k; i += 32) any |= __ldg(a.ids + (int64_t)row * a.k + i) != -1;
+  return __any_sync(0xffffffffu, any);
+}
+
+// Rows are streamed as the log probabilities' kernel does it: one warp copies, eight sum the
+// unlisted ids; another reads the next row's list meanwhile and finishes the last one.
+template <typename T>
+__global__ void __launch_bounds__(kDsThreads, kLpPerSm) distill_loss_kernel(DsArgs a) {
+  constexpr int VE = Elem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ DsShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
+  if (tid == 0) {
+    for (int s = 0; s < kLpStages; ++s) {
+      umma::mbar_init(&sh.full[s], 1);
+      umma::mbar_init(&sh.empty[s], kLpWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      umma::mbar_init(&sh.listed[s], 1);
+      umma::mbar_init(&sh.summed[s], kLpWarps);
+    }
+    sh.timeout = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  if (warp == kLpWarps) {
+    // the copying warp runs ahead of the consumers, into their next rows
+    bool ok = true, any = ds_any(a, row0, lane);
+    const bool first = any;
+    int it = 0;  // chunks requested so far
+    for (int row = row0; row < a.R; row += stride) {
+      if (any && ok && lane == 0) {
+        const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+        const Span sp = span_of<T>(l, a.K, rank, C);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head);
+        for (int i = 0; i < sp.mine; ++i, ++it) {
+          const int s = it % kLpStages;
+          if (it >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((it / kLpStages) - 1) & 1);
+          if (!ok) break;
+          const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
+          const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)sp.nvec * 16 - at);
+          umma::mbar_expect_tx(&sh.full[s], bytes);
+          umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
+        }
+      }
+      if (row + stride < a.R) any = ds_any(a, row + stride, lane);
+    }
+    if (!ok) {
+      atomicExch(&sh.timeout, 1);
+      // every copy issued has landed before this block may exit
+      for (int s = 0; s < kLpStages; ++s)
+        for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
+    }
+    __syncwarp();
+    if (C > 1 && first) {
+      cl.sync();
+      cl.sync();
     }
     return;
   }
-  for (int i = tid; i < 4 * kDsMaxK; i += kDsNT) hash[i] = -1;
-  __syncthreads();
-  if (tid < a.k && sh.place[tid] >= 0) {
-    int h = sh.place[tid] & (4 * kDsMaxK - 1);
-    while (atomicCAS(&hash[h], -1, sh.place[tid]) != -1) h = (h + 1) & (4 * kDsMaxK - 1);
-  }
-  __syncthreads();
-  auto listed = [&](int j) {
-    for (int h = j & (4 * kDsMaxK - 1); hash[h] != -1; h = (h + 1) & (4 * kDsMaxK - 1))
-      if (hash[h] == j) return true;
-    return false;
-  };
-  float m = -INFINITY;
-  bool bad = false;
-  for (int j = tid; j < a.K; j += kDsNT) {
-    const float x = Elem<T>::load(l + j);
-    bad |= !(x < INFINITY);
-    if (!listed(j)) m = fmaxf(m, x);
-  }
-  if (__syncthreads_or(bad)) flags |= VT_DEV_NONFINITE;
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < kDsWarps; ++w) m = fmaxf(m, red[w]);
-  float s = 0.f, e = 0.f;
-  if (m > -INFINITY)
-    for (int j = tid; j < a.K; j += kDsNT) {
-      if (listed(j)) continue;
-      float t;
-      two_sum(s, exp2_approx((Elem<T>::load(l + j) - m) * a.c), s, t);
-      e += t;
+
+  if (warp == kLpWarps + 1) {
+    // the list's warp: row r is finished after row r + 1's list has been read
+    uint32_t limit = umma::kWaitLimit;
+    const auto read = [&](int row, int slot) {
+      DsList& list = sh.list[slot];
+      const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+      const Span sp = span_of<T>(l, a.K, rank, C);
+      ds_places<T>(a, row, sp, rank == 0, list, lane, [&](int p) {
+        const int e = p - sp.head, v = e / VE;
+        if (e < 0 || v >= sp.nvec) return -1;
+        const int chunk = v / (kLpNT * kLpU), mine = chunk / C;
+        if (chunk - mine * C != rank) return -1;
+        return mine * kLpChunk + (v - chunk * (kLpNT * kLpU)) * 16 + (e - v * VE) * (int)sizeof(T);
+      });
+      if (lane == 0) umma::mbar_arrive(&sh.listed[slot]);
+      if (list.any && rank == 0) ds_entries<T>(a, row, l, list, lane);
+    };
+    read(row0, 0);
+    int n = 0;
+    bool first = sh.list[0].any;
+    for (int row = row0; row < a.R; row += stride, ++n) {
+      const int slot = n & 1;
+      if (row + stride < a.R) read(row + stride, slot ^ 1);
+      if (C > 1) break;  // (one row, finished below)
+      const bool any = sh.list[slot].any;
+      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.summed[slot], (n >> 1) & 1, limit))) {
+        limit = 1;
+        if (lane == 0) atomicExch(&sh.timeout, 1);
+        sh.sum[slot].late = 1;
+      }
+      __syncwarp();
+      float loss = 0.f;
+      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+      int flags = 0;
+      if (any) ds_finish(a, sh.list[slot], sh.sum[slot], lane, loss, st, flags);
+      if (lane == 0) ds_put(a, row, loss, st, flags);
+      __syncwarp();
     }
-  for (int o = 16; o > 0; o >>= 1) {
-    const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
-    float t;
-    two_sum(s, s2, s, t);
-    e += e2 + t;
+    if (C > 1) {
+      float loss = 0.f;
+      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+      int flags = 0;
+      if (first) {
+        cl.sync();
+        if (rank == 0) {
+          // all blocks' sums, one per lane
+          const int from = lane < C ? lane : 0;
+          RowSum r = *cl.map_shared_rank(&sh.blk, from);
+          const bool late = *cl.map_shared_rank(&sh.timeout, from) != 0;
+          if (lane >= C) r.s = r.e = 0.f;
+          r = sum_lanes(r, kLpMaxC, a.c);
+          DsSum un{r, __any_sync(0xffffffffu, late)};
+          un.sum.m = __shfl_sync(0xffffffffu, r.m, 0);
+          un.sum.s = __shfl_sync(0xffffffffu, r.s, 0);
+          un.sum.e = __shfl_sync(0xffffffffu, r.e, 0);
+          ds_finish(a, sh.list[0], un, lane, loss, st, flags);
+        }
+        cl.sync();  // the first block has read the others' memory
+      }
+      if (rank == 0 && lane == 0) ds_put(a, row0, loss, st, flags);
+    }
+    return;
   }
-  if (lane == 0) red_s[warp] = s, red_e[warp] = e;
-  __syncthreads();
-  if (warp != 0) return;
-  float loss = nan_f();
-  DsStats st{loss, loss, loss, loss, loss};
-  if (flags == 0) {
-    double sr = 0.0;
-    for (int w = 0; w < kDsWarps; ++w) sr += (double)red_s[w] + (double)red_e[w];
-    ds_finish(a, sh, m, sr, lane, loss, st);
-  }
-  if (lane == 0) {
-    a.out_loss[row] = loss;
-    a.stats[row] = st;
-    if (flags) atomicOr(a.dev_status, flags);
+
+  int it = 0, n = 0;  // chunks and rows consumed so far
+  uint32_t limit = umma::kWaitLimit;
+  for (int row = row0; row < a.R; row += stride, ++n) {
+    const int slot = n & 1;
+    const DsList& list = sh.list[slot];
+    const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+    const Span sp = span_of<T>(l, a.K, rank, C);
+    const bool edge = rank == 0 && tid < 2 * VE;
+    float xe = -INFINITY;
+    if (edge) {
+      const int id = edge_id<VE>(sp, tid);
+      if (id < a.K) xe = Elem<T>::load(l + id);
+    }
+    if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.listed[slot], (n >> 1) & 1, limit))) {
+      limit = 1;
+      if (lane == 0) atomicExch(&sh.timeout, 1);
+    }
+    if (!list.any) {
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
+      continue;
+    }
+    RowSum st{kNegBig, 0.f, 0.f};
+    for (int i = 0; i < sp.mine; ++i, ++it) {
+      const int s = it % kLpStages;
+      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (it / kLpStages) & 1, limit))) {
+        // gave up: go on without the data, so that no barrier is missed
+        limit = 1;
+        if (lane == 0) atomicExch(&sh.timeout, 1);
+      }
+      ds_mask<T>(list, ring + s * kLpChunk, i * kLpChunk, kLpChunk, a.k, warp, lane);
+      const int q0 = (rank + i * C) * (kLpNT * kLpU) + tid;  // first vector of this thread
+      const uint4* st4 = reinterpret_cast<const uint4*>(ring + s * kLpChunk) + tid;
+      const int have = min(kLpU, max(0, (sp.nvec - q0 + kLpNT - 1) / kLpNT));  // vectors in the row
+      uint4 v[kLpU];
+#pragma unroll
+      for (int u = 0; u < kLpU; ++u)
+        v[u] = u < have ? st4[u * kLpNT]
+                        : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+      const float pm = Vec<T>::top(v);
+      if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
+      sum_add<T>(st, v, a.c);
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
+    }
+    if (edge && !(list.edges >> tid & 1)) {
+      if (!(xe <= st.m)) sum_rescale(st, max_nan(st.m, xe), a.c);
+      float er;
+      two_sum(st.s, exp2_approx((xe - st.m) * a.c), st.s, er);
+      st.e += er;
+    }
+    st = sum_lanes(st, 32, a.c);
+    if (lane == 0) sh.red[slot][warp] = st;
+    lp_bar();
+    if (warp == 0) {
+      // (a warp that is ahead writes the other slot; it cannot reach the next but one
+      // row before this one has passed the next row's barrier)
+      const RowSum r = sum_lanes(sh.red[slot][lane % kLpWarps], kLpWarps, a.c);
+      if (lane == 0) {
+        sh.sum[slot] = DsSum{r, sh.timeout};
+        sh.blk = r;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
+    if (C > 1) {
+      cl.sync();
+      cl.sync();
+    }
   }
 }
 
@@ -256,7 +529,6 @@ template <> struct Store<uint16_t> {
 
 template <typename T>
 __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a) {
-  __shared__ DsList sh;
   const int row = blockIdx.x, tid = threadIdx.x;
   const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
   T* d = static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad;
@@ -266,15 +538,21 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a) {
     for (int j = tid; j < a.K; j += kDsNT) Store<T>::put(d + j, 0.f);
     return;
   }
-  ds_read_list<T>(a, row, l, sh);  // ahead of the first store: d may be l
+  int p = -1;
+  float z = 0.f, lp = 0.f;
+  if (tid < a.k) {
+    p = ds_place(a, (int64_t)row * a.k + tid);
+    lp = a.logp[(int64_t)row * a.k + tid];
+    if (p >= 0) z = Elem<T>::load(l + p);
+  }
+  __syncthreads();  // ahead of the first store: d may be l
   const float cr = g * st.c_rest;
   for (int j = tid; j < a.K; j += kDsNT)
     Store<T>::put(d + j, cr * exp2_approx((Elem<T>::load(l + j) - st.mr) * a.c));
   __syncthreads();
-  if (tid < a.k && sh.place[tid] >= 0) {
-    const Pair t = pair_exp(Pair{sh.logp[tid], 0.f});
-    Store<T>::put(d + sh.place[tid],
-                  g * (st.c_all * exp2_approx((sh.z[tid] - st.m) * a.c) - st.c_t * t.h));
+  if (p >= 0 && z != -INFINITY) {
+    const Pair t = pair_exp(Pair{lp, 0.f});
+    Store<T>::put(d + p, g * (st.c_all * exp2_approx((z - st.m) * a.c) - st.c_t * t.h));
   }
 }
 
@@ -313,7 +591,8 @@ DsArgs ds_args(const void* logits, int64_t R, int32_t K, int64_t ld, const int32
   a.k = k;
   a.rest = rest;
   a.c = VT_LOG2E / T;
-  a.inv_t = 1.0 / (double)T;
+  a.inv_t.h = (float)(1.0 / (double)T);
+  a.inv_t.l = (float)(1.0 / (double)T - (double)a.inv_t.h);
   a.ids = ids;
   a.logp = logp;
   a.inv_map = inv_map;
@@ -323,17 +602,38 @@ DsArgs ds_args(const void* logits, int64_t R, int32_t K, int64_t ld, const int32
   a.grad = grad;
   a.ld_grad = ld_grad;
   a.dev_status = dev_status;
+  a.own_status = R == 1;
   return a;
 }
 
-int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
-  VT_RETURN_IF_CUDA(cudaMemsetAsync(a.dev_status, 0, sizeof(int), s));
-  if (dtype == VT_F32)
-    distill_loss_kernel<float><<<a.R, kDsNT, 0, s>>>(a);
-  else
-    distill_loss_kernel<uint16_t><<<a.R, kDsNT, 0, s>>>(a);
-  VT_RETURN_IF_LAUNCH_FAILED();
+template <typename T>
+int ds_launch_loss(const DsArgs& a, cudaStream_t s) {
+  auto kern = distill_loss_kernel<T>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
+  if (!a.own_status) {
+    const int st = clear_status(s, a.dev_status);
+    if (st != VT_OK) return st;
+  }
+  const int C = lp_cluster(a.R, a.K, (int)sizeof(T));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min(a.R, num_sms() * kLpPerSm)));
+  cfg.blockDim = dim3(kDsThreads);
+  cfg.dynamicSmemBytes = kLpSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.own_status ? 1 : 2;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   return VT_OK;
+}
+int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
+  return dtype == VT_F32 ? ds_launch_loss<float>(a, s) : ds_launch_loss<uint16_t>(a, s);
 }
 
 int ds_launch_grad(const DsArgs& a, int32_t dtype, cudaStream_t s) {

@@ -33,7 +33,15 @@ __device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
   return pair_of(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
 }
 
-// e^x to a relative error below 2^-28 for -80 <= x.h <= 80; 0 below, +infinity
+__device__ __forceinline__ Pair pair_neg(Pair a) { return Pair{-a.h, -a.l}; }
+// a quotient, or product, or sum beyond fp32 is that infinity, or NaN, in h; l is of no use then
+__device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
+  const float q = a.h / b.h;
+  const float r = fmaf(-q, b.h, a.h) + fmaf(-q, b.l, a.l);
+  return pair_of(q, r / b.h);
+}
+
+// e^x to a relative error below 2^-28 for -87 <= x.h <= 88; 0 below, +infinity
 // above, NaN for NaN.  Cody and Waite's reduction x = n ln 2 + r with ln 2 as
 // 16 bits (whose multiples by n are exact) and a remainder, |r| <= 0.35, then the
 // Taylor series with 1, r and r^2 / 2 exact and the rest (below 0.008) in fp32
@@ -54,15 +62,22 @@ __device__ __forceinline__ Pair pair_exp(Pair x) {
   two_sum(s, 0.5f * q, s, e2);
   const float lo = e1 + e2 + fmaf(0.5f, ql, fmaf(p, q * r, fmaf(rl, r, rl)));
   Pair y = pair_of(s, lo);
-  if (!(x.h >= -80.f)) {
+  if (!(x.h >= -87.f)) {
     const float v = x.h != x.h ? x.h : 0.f;
     return Pair{v, 0.f};
   }
-  if (x.h > 80.f) return Pair{INFINITY, 0.f};
+  if (x.h > 88.f) return Pair{INFINITY, 0.f};
   const float f = __int_as_float(((int)n + 127) << 23);
   y.h *= f;
   y.l *= f;
   return y;
+}
+
+// ln x of 1e-37 <= x <= 1e37, to 2^-27 in absolute terms: one Newton step on the fp32 logarithm
+__device__ __forceinline__ Pair pair_log(Pair x) {
+  const float y = logf(x.h);
+  const Pair r = pair_add(pair_mul(x, pair_exp(Pair{-y, 0.f})), Pair{-1.f, 0.f});
+  return pair_of(y, r.h + r.l);
 }
 
 }  // namespace vt

@@ -326,6 +326,62 @@ struct TopList {
   }
 };
 
+// running sum of weights: the maximum m and S = s + e (e: what rounding took from s)
+struct RowSum {
+  float m, s, e;
+};
+// relative to a maximum m >= a.m
+__device__ __forceinline__ void sum_rescale(RowSum& a, float m, float c) {
+  const float f = exp2_approx((a.m - m) * c);
+  a.s *= f;
+  a.e *= f;
+  a.m = m;
+}
+__device__ __forceinline__ RowSum sum_join(RowSum a, RowSum b, float c) {
+  const float m = max_nan(a.m, b.m);
+  sum_rescale(a, m, c);
+  sum_rescale(b, m, c);
+  RowSum r;
+  r.m = m;
+  two_sum(a.s, b.s, r.s, r.e);
+  r.e += a.e + b.e;
+  return r;
+}
+// joins those of n lanes, a power of two
+__device__ __forceinline__ RowSum sum_lanes(RowSum a, int n, float c) {
+  for (int o = n >> 1; o > 0; o >>= 1) {
+    RowSum b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.e = __shfl_xor_sync(0xffffffffu, a.e, o);
+    a = sum_join(a, b, c);
+  }
+  return a;
+}
+// adds a chunk's vectors, none of which is above a.m
+template <typename T>
+__device__ __forceinline__ void sum_add(RowSum& a, const uint4 (&v)[kLpU], float c) {
+  const f32x2 c2 = pack2(c, c);
+  f32x2 sum[kLpU];
+#pragma unroll
+  for (int u = 0; u < kLpU; ++u)
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kVec; e += 2) {
+      float t0, t1;
+      unpack2(mul2(Vec<T>::diff2(v[u], e, -a.m), c2), t0, t1);
+      const f32x2 w = pack2(exp2_approx(t0), exp2_approx(t1));
+      sum[u] = e == 0 ? w : add2(sum[u], w);
+    }
+#pragma unroll
+  for (int h = kLpU / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int u = 0; u < h; ++u) sum[u] = add2(sum[u], sum[u + h]);
+  float s0, s1, er;
+  unpack2(sum[0], s0, s1);
+  two_sum(a.s, s0 + s1, a.s, er);
+  a.e += er;
+}
+
 // Thread blocks per row: the count that gives the shortest schedule, taking a
 // block's time as its chunks plus three more for its start and its join, and
 // kLpPerSm blocks of each SM running at once.
