@@ -516,44 +516,266 @@ __global__ void __launch_bounds__(kDsThreads, kLpPerSm) distill_loss_kernel(DsAr
   }
 }
 
+// -------------------------------------------------------------- the gradient
 template <typename T> struct Store;
 template <> struct Store<float> {
   __device__ static void put(float* p, float v) { *p = v; }
+  // factor * 2^((x - m) c) of a vector's elements
+  __device__ static uint4 grad(uint4 v, float m, float c, float factor) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      float t0, t1;
+      unpack2(mul2(Vec<float>::diff2(v, e, -m), pack2(c, c)), t0, t1);
+      unpack2(mul2(pack2(exp2_approx(t0), exp2_approx(t1)), pack2(factor, factor)), t0, t1);
+      w[e] = __float_as_uint(t0);
+      w[e + 1] = __float_as_uint(t1);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <> struct Store<uint16_t> {
   // round to nearest even; NaN stays NaN
   __device__ static void put(uint16_t* p, float v) {
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(v));
   }
+  __device__ static uint4 grad(uint4 v, float m, float c, float factor) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float t0, t1;
+      unpack2(mul2(Vec<uint16_t>::diff2(v, e, -m), pack2(c, c)), t0, t1);
+      unpack2(mul2(pack2(exp2_approx(t0), exp2_approx(t1)), pack2(factor, factor)), t0, t1);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e / 2]) : "f"(t1), "f"(t0));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 
+// the gradient at a listed id
+__device__ __forceinline__ float ds_listed(const DsArgs& a, const DsStats& st, float g, float z, float logp) {
+  return g * (st.c_all * exp2_approx((z - st.m) * a.c) - st.c_t * pair_exp(Pair{logp, 0.f}).h);
+}
+__device__ __forceinline__ bool ds_nothing(const DsStats& st) { return st.c_all == 0.f && st.c_t == 0.f; }
+
+// A vector's elements to an address that need not be aligned to it
 template <typename T>
-__global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a) {
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  T* d = static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad;
-  const DsStats st = a.stats[row];
-  const float g = a.weight ? a.weight[row] : 1.f;
-  if (st.c_all == 0.f && st.c_t == 0.f) {  // nothing to learn: not read
-    for (int j = tid; j < a.K; j += kDsNT) Store<T>::put(d + j, 0.f);
+__device__ __forceinline__ void store_vec(T* d, uint4 v, bool aligned) {
+  if (aligned) {
+    *reinterpret_cast<uint4*>(d) = v;
     return;
   }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<uint32_t*>(d)[e] = w[e];
+    } else {
+      d[2 * e] = (T)(w[e] & 0xffffu);
+      d[2 * e + 1] = (T)(w[e] >> 16);
+    }
+  }
+}
+
+constexpr int kDgU = 4;  // vectors per thread
+
+// Each block takes kDsNT * kDgU vectors of a row; the first also the row's edges.  What
+// it reads is in registers before it writes, so the gradient may take the logits' place.
+template <typename T>
+__global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int pieces) {
+  constexpr int VE = Elem<T>::kVec;
+  const int row = blockIdx.x / pieces, piece = blockIdx.x - row * pieces, tid = threadIdx.x;
+  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+  T* d = static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad;
+  const Span sp = span_of<T>(l, a.K, 0, 1);
+  const DsStats st = a.stats[row];
+  const float g = a.weight ? a.weight[row] : 1.f;
+  const bool nothing = ds_nothing(st);
+  const bool aligned = (reinterpret_cast<uintptr_t>(d + sp.head) & 15) == 0;
+  const uint4* l4 = reinterpret_cast<const uint4*>(l + sp.head);
+  const int q0 = piece * (kDsNT * kDgU) + tid;
+  uint4 v[kDgU];
+  if (!nothing) {
+#pragma unroll
+    for (int u = 0; u < kDgU; ++u)
+      if (q0 + u * kDsNT < sp.nvec) v[u] = l4[q0 + u * kDsNT];
+  }
+  // the edges, and the listed ids that this block has
+  const bool edge = piece == 0 && tid < 2 * VE && edge_id<VE>(sp, tid) < a.K;
+  float xe = 0.f, z = 0.f, lp = 0.f;
   int p = -1;
-  float z = 0.f, lp = 0.f;
-  if (tid < a.k) {
-    p = ds_place(a, (int64_t)row * a.k + tid);
-    lp = a.logp[(int64_t)row * a.k + tid];
-    if (p >= 0) z = Elem<T>::load(l + p);
+  if (!nothing) {
+    if (edge) xe = Elem<T>::load(l + edge_id<VE>(sp, tid));
+    if (tid < a.k) {
+      p = ds_place(a, (int64_t)row * a.k + tid);
+      const int q = (p - sp.head) / VE;
+      const bool inner = p >= sp.head && q < sp.nvec;
+      if (p >= 0 && (inner ? q / (kDsNT * kDgU) != piece : piece != 0)) p = -1;
+      if (p >= 0) {
+        lp = a.logp[(int64_t)row * a.k + tid];
+        z = Elem<T>::load(l + p);
+        if (z == -INFINITY) p = -1;
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();  // ahead of the first store: d may be l
-  const float cr = g * st.c_rest;
-  for (int j = tid; j < a.K; j += kDsNT)
-    Store<T>::put(d + j, cr * exp2_approx((Elem<T>::load(l + j) - st.mr) * a.c));
+  const float factor = g * st.c_rest;
+#pragma unroll
+  for (int u = 0; u < kDgU; ++u) {
+    const int q = q0 + u * kDsNT;
+    if (q < sp.nvec)
+      store_vec(d + sp.head + (int64_t)q * VE,
+                nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(v[u], st.mr, a.c, factor), aligned);
+  }
+  if (edge) Store<T>::put(d + edge_id<VE>(sp, tid), nothing ? 0.f : factor * exp2_approx((xe - st.mr) * a.c));
+  if (nothing) return;
   __syncthreads();
-  if (p >= 0 && z != -INFINITY) {
-    const Pair t = pair_exp(Pair{lp, 0.f});
-    Store<T>::put(d + p, g * (st.c_all * exp2_approx((z - st.m) * a.c) - st.c_t * t.h));
+  if (p >= 0) Store<T>::put(d + p, ds_listed(a, st, g, z, lp));
+}
+
+// ------------------------------------------------------- loss and gradient
+constexpr int kDtThreads = kLpNT + 32;  // consuming warps and one for the list
+constexpr int kDtPieces = 8;            // copies of kLpChunk bytes a block
+constexpr int kDtMaxC = 8;
+
+struct DtShared {
+  DsList list;
+  RowSum red[kLpWarps];
+  DsStats st;
+  float edge[16];
+  alignas(8) uint64_t full[kDtPieces];
+  int timeout;
+};
+
+// One row per cluster, kept in its blocks' shared memory between the sum and the
+// gradient: `share` vectors in each block.  Every block finishes the row for itself.
+template <typename T>
+__global__ void __launch_bounds__(kDtThreads) distill_train_kernel(DsArgs a, int share) {
+  constexpr int VE = Elem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t part[];
+  __shared__ DtShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / C;
+  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+  T* d = static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad;
+  const Span sp = span_of<T>(l, a.K, 0, 1);
+  const int v0 = min(rank * share, sp.nvec), mine = min(share, sp.nvec - v0);  // this block's vectors
+  const int pieces = (mine * 16 + kLpChunk - 1) / kLpChunk;
+  const bool edges = rank == 0;
+  if (tid == kLpNT) {
+    for (int i = 0; i < kDtPieces; ++i) umma::mbar_init(&sh.full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    sh.timeout = 0;
   }
+  __syncthreads();
+  float xe = -INFINITY;
+  if (warp == kLpWarps) {
+    const bool any = ds_any(a, row, lane);
+    if (any && lane == 0) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head) + (int64_t)v0 * 16;
+      for (int i = 0; i < pieces; ++i) {
+        const uint32_t bytes = (uint32_t)min(kLpChunk, mine * 16 - i * kLpChunk);
+        umma::mbar_expect_tx(&sh.full[i], bytes);
+        umma::bulk_load(part + i * kLpChunk, src + (int64_t)i * kLpChunk, bytes, &sh.full[i]);
+      }
+    }
+    __syncwarp();
+    ds_places<T>(a, row, sp, edges, sh.list, lane, [&](int p) {
+      const int e = p - sp.head, v = e / VE - v0;
+      return e < 0 || v < 0 || v >= mine ? -1 : v * 16 + (e % VE) * (int)sizeof(T);
+    });
+  } else if (edges && tid < 2 * VE) {
+    const int id = edge_id<VE>(sp, tid);
+    if (id < a.K) xe = Elem<T>::load(l + id);
+  }
+  __syncthreads();  // the places
+  const float g = a.weight ? a.weight[row] : 1.f;
+  const bool any = sh.list.any;
+  bool nothing = !any;
+  if (any) {
+    if (warp == kLpWarps) {
+      ds_entries<T>(a, row, l, sh.list, lane);
+    } else {
+      RowSum st{kNegBig, 0.f, 0.f};
+      for (int i = 0; i < pieces; ++i) {
+        if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[i], 0)) && lane == 0) atomicExch(&sh.timeout, 1);
+        ds_mask<T>(sh.list, part + i * kLpChunk, i * kLpChunk, kLpChunk, a.k, warp, lane);
+        const uint4* st4 = reinterpret_cast<const uint4*>(part + i * kLpChunk) + tid;
+        const int have = min(kLpU, max(0, (mine - i * (kLpNT * kLpU) - tid + kLpNT - 1) / kLpNT));
+        uint4 v[kLpU];
+#pragma unroll
+        for (int u = 0; u < kLpU; ++u)
+          v[u] = u < have ? st4[u * kLpNT]
+                          : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+        const float pm = Vec<T>::top(v);
+        if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
+        sum_add<T>(st, v, a.c);
+      }
+      if (edges && tid < 2 * VE && !(sh.list.edges >> tid & 1)) {
+        if (!(xe <= st.m)) sum_rescale(st, max_nan(st.m, xe), a.c);
+        float er;
+        two_sum(st.s, exp2_approx((xe - st.m) * a.c), st.s, er);
+        st.e += er;
+      }
+      st = sum_lanes(st, 32, a.c);
+      if (lane == 0) sh.red[warp] = st;
+    }
+    if (C > 1)
+      cl.sync();  // every block's sums; and what is read of the row has been read
+    else
+      __syncthreads();
+    if (warp == kLpWarps) {
+      DsSum un{RowSum{kNegBig, 0.f, 0.f}, 0};
+      for (int i = lane; i < C * kLpWarps; i += 32) {
+        const int from = i / kLpWarps;
+        un.sum = sum_join(un.sum, cl.map_shared_rank(sh.red, from)[i % kLpWarps], a.c);
+        un.late |= *cl.map_shared_rank(&sh.timeout, from);
+      }
+      un.sum = sum_lanes(un.sum, 32, a.c);
+      un.late = __any_sync(0xffffffffu, un.late != 0);
+      float loss;
+      DsStats st;
+      int flags;
+      ds_finish(a, sh.list, un, lane, loss, st, flags);
+      if (lane == 0) {
+        sh.st = st;
+        if (edges) ds_put(a, row, loss, st, flags);
+      }
+    }
+    __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // done with the others' memory
+    nothing = ds_nothing(sh.st);
+  } else if (edges && tid == 0) {
+    ds_put(a, row, 0.f, DsStats{0.f, 0.f, 0.f, 0.f, 0.f}, 0);
+  }
+  const DsStats st = any ? sh.st : DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
+  const float factor = g * st.c_rest;
+  if (warp < kLpWarps) {
+    T* out = d + sp.head + (int64_t)v0 * VE;
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const uint4* in = reinterpret_cast<const uint4*>(part);
+#pragma unroll 4
+    for (int q = tid; q < mine; q += kLpNT)
+      store_vec(out + (int64_t)q * VE,
+                nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(in[q], st.mr, a.c, factor), aligned);
+    if (edges && tid < 2 * VE && edge_id<VE>(sp, tid) < a.K)
+      Store<T>::put(d + edge_id<VE>(sp, tid), nothing ? 0.f : factor * exp2_approx((xe - st.mr) * a.c));
+  }
+  if (!nothing) {
+    __syncthreads();
+    if (warp == kLpWarps)
+      for (int i = lane; i < a.k; i += 32) {
+        const int p = sh.list.place[i];
+        const bool here = sh.list.pos[i] >= 0 || (edges && p >= 0 && (p < sp.head || p >= sp.head + sp.nvec * VE));
+        const float z = sh.list.z[i];
+        if (here && z != -INFINITY) Store<T>::put(d + p, ds_listed(a, st, g, z, sh.list.logp[i]));
+      }
+  }
+  if (sh.timeout && tid == 0)  // every copy issued has landed before this block may exit
+    for (int i = 0; any && i < pieces; ++i) umma::mbar_wait(&sh.full[i], 0, 1u << 12);
+  if (C > 1 && any) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // arguments that the three calls share
@@ -637,12 +859,56 @@ int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
 }
 
 int ds_launch_grad(const DsArgs& a, int32_t dtype, cudaStream_t s) {
-  if (dtype == VT_F32)
-    distill_grad_kernel<float><<<a.R, kDsNT, 0, s>>>(a);
+  const int elem = dtype == VT_F32 ? 4 : 2;
+  const int pieces = std::max(1, (int)(((int64_t)a.K * elem / 16 + kDsNT * kDgU - 1) / (kDsNT * kDgU)));
+  if ((int64_t)a.R * pieces > 0x7fffffff) return VT_ERR_UNSUPPORTED;
+  if (elem == 4)
+    distill_grad_kernel<float><<<(unsigned)a.R * pieces, kDsNT, 0, s>>>(a, pieces);
   else
-    distill_grad_kernel<uint16_t><<<a.R, kDsNT, 0, s>>>(a);
+    distill_grad_kernel<uint16_t><<<(unsigned)a.R * pieces, kDsNT, 0, s>>>(a, pieces);
   VT_RETURN_IF_LAUNCH_FAILED();
   return VT_OK;
+}
+
+// bytes of shared memory that a row's part may take: three blocks on an SM, or one
+constexpr int kDtThree = 68 << 10, kDtOne = 200 << 10;
+
+template <typename T>
+int ds_launch_train(const DsArgs& a, cudaStream_t s, int C, int share) {
+  auto kern = distill_train_kernel<T>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtOne));
+  if (!a.own_status) {
+    const int st = clear_status(s, a.dev_status);
+    if (st != VT_OK) return st;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.R * C));
+  cfg.blockDim = dim3(kDtThreads);
+  cfg.dynamicSmemBytes = (size_t)share * 16;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.own_status ? 1 : 2;
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a, share));
+  return VT_OK;
+}
+
+// Rows that the blocks of a cluster hold between them are read once; longer ones take the two calls.
+int ds_launch_both(const DsArgs& a, int32_t dtype, cudaStream_t s) {
+  const int64_t bytes = (int64_t)a.K * (dtype == VT_F32 ? 4 : 2);
+  int C = (int)std::min<int64_t>((bytes + kDtThree - 1) / kDtThree, kDtMaxC);
+  const int64_t vecs = bytes / 16, share = (vecs + C - 1) / C;
+  if (share * 16 > kDtOne || (int64_t)a.R * C > 0x7fffffff) {
+    const int rc = ds_launch_loss(a, dtype, s);
+    return rc != VT_OK ? rc : ds_launch_grad(a, dtype, s);
+  }
+  return dtype == VT_F32 ? ds_launch_train<float>(a, s, C, (int)share) : ds_launch_train<uint16_t>(a, s, C, (int)share);
 }
 
 }  // namespace
@@ -688,6 +954,5 @@ extern "C" int vt_distill_loss_grad(const void* logits, int32_t logits_dtype, in
   if (!out_loss || !dev_status || (rest != 0 && rest != 1)) return VT_ERR_INVALID_ARG;
   const DsArgs a = ds_args(logits, R, K, ld_logits, top_ids, top_logp, k, V, inv_map, rest, temperature, grad_loss,
                            out_loss, out_stats, out_grad, ld_grad, dev_status);
-  const int rc = ds_launch_loss(a, logits_dtype, static_cast<cudaStream_t>(stream));
-  return rc != VT_OK ? rc : ds_launch_grad(a, logits_dtype, static_cast<cudaStream_t>(stream));
+  return ds_launch_both(a, logits_dtype, static_cast<cudaStream_t>(stream));
 }
