@@ -21,6 +21,7 @@
 // may be out of fp32's range relative to the other) and the three factors kept
 // per row by the loss.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -37,7 +38,6 @@ namespace {
 constexpr int kDsMaxK = 128;
 constexpr int kDsLane = kDsMaxK / 32;      // list entries of a lane
 constexpr int kDsNT = 256;
-constexpr int kDsThreads = kLpNT + 64;     // consuming warps, one that copies, one for the list
 
 // what takes an element out of a sum
 template <typename T> struct Mask;
@@ -87,191 +87,251 @@ struct DsList {
   int place[kDsMaxK];  // of entries that the drafter has, else -1
   int pos[kDsMaxK];    // bytes from the start of what this block reads of the row, -1: not there
   float z[kDsMaxK], logp[kDsMaxK];
+  float val[kDsMaxK];  // t, then the gradient
+  uint8_t tag[4 * kDsMaxK];
   unsigned edges;      // the row's edge elements that are listed
   int any;             // an id is given
-  int flags;
-};
-// What the consuming warps leave of a row: the sum over its unlisted ids
-struct DsSum {
-  RowSum sum;
-  int late;
 };
 
-// The list of a row, read by one warp in two steps: the places, which the consuming
-// warps wait for, and what stands there.  at(place): the byte position in what this
-// block reads, or -1.
-template <typename T, typename At>
-__device__ __forceinline__ void ds_places(const DsArgs& a, int row, const Span& sp, bool edges, DsList& sh, int lane,
-                                          At at) {
-  int p[kDsLane];
-  bool any = false;
+// a warp's lanes hold entries lane, lane + 32, ...
+struct DsIds {
+  int id[kDsLane];
+};
+__device__ __forceinline__ DsIds ds_ids(const DsArgs& a, int64_t row, int lane) {
+  DsIds r;
 #pragma unroll
   for (int h = 0; h < kDsLane; ++h) {
     const int i = lane + 32 * h;
-    p[h] = -1;
-    if (i < a.k) {
-      const int id = __ldg(a.ids + (int64_t)row * a.k + i);
-      any |= id != -1;
-      p[h] = id == -1 ? -1 : id < 0 || id >= a.V ? -2 : id;
+    r.id[h] = row < a.R && i < a.k ? __ldg(a.ids + row * a.k + i) : -1;
+  }
+  return r;
+}
+// ids to places in the drafter's vocabulary: -1 none, -2 out of range; *any: an id is given
+__device__ __forceinline__ DsIds ds_map(const DsArgs& a, DsIds p, bool& any) {
+  any = false;
+#pragma unroll
+  for (int h = 0; h < kDsLane; ++h) {
+    any |= p.id[h] != -1;
+    if (p.id[h] != -1 && (p.id[h] < 0 || p.id[h] >= a.V)) p.id[h] = -2;
+    if (p.id[h] >= 0 && a.inv_map) {
+      const int q = __ldg(a.inv_map + p.id[h]);
+      p.id[h] = q >= -1 && q < a.K ? q : -2;
     }
   }
+  any = __any_sync(0xffffffffu, any);
+  return p;
+}
+// whether a row has an id listed; all lanes of a warp call it
+__device__ __forceinline__ bool ds_any(const DsArgs& a, int row, int lane) {
+  bool any = false;
+  for (int i = lane; i < a.k; i += 32) any |= __ldg(a.ids + (int64_t)row * a.k + i) != -1;
+  return __any_sync(0xffffffffu, any);
+}
+
+// Writes a row's places to its list; at(place): the byte position in what this block reads, or
+// -1.  Returns the flags.
+template <int VE, typename At>
+__device__ __forceinline__ int ds_places(const DsArgs& a, const DsIds& p, bool any, const Span& sp, bool edges,
+                                         DsList& sh, int lane, At at) {
   bool bad = false;
   unsigned edge = 0;
 #pragma unroll
   for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h;
-    if (p[h] >= 0 && a.inv_map) {
-      const int q = __ldg(a.inv_map + p[h]);
-      p[h] = q >= -1 && q < a.K ? q : -2;
-    }
-    bad |= p[h] == -2;
+    const int i = lane + 32 * h, q = p.id[h];
+    bad |= q == -2;
     if (i < a.k) {
-      sh.place[i] = max(p[h], -1);
-      sh.pos[i] = p[h] >= 0 ? at(p[h]) : -1;
+      sh.place[i] = max(q, -1);
+      sh.pos[i] = q >= 0 ? at(q) : -1;
     }
-    if (p[h] >= 0 && edges) {
-      const int t = p[h] < sp.head ? p[h] : p[h] - sp.nvec * Elem<T>::kVec;
-      if (p[h] < sp.head || t >= sp.head) edge |= 1u << t;
+    if (q >= 0 && edges) {
+      const int t = q < sp.head ? q : q - sp.nvec * VE;
+      if (q < sp.head || t >= sp.head) edge |= 1u << t;
     }
   }
-  any = __any_sync(0xffffffffu, any);
   bad = __any_sync(0xffffffffu, bad);
   edge = __reduce_or_sync(0xffffffffu, edge);
   if (lane == 0) {
     sh.any = any;
-    sh.flags = bad ? VT_DEV_BAD_ID : 0;
     sh.edges = edge;
   }
   __syncwarp();
+  return bad ? VT_DEV_BAD_ID : 0;
 }
+
+// What stands at the list's places; returns flags.
 template <typename T>
-__device__ __forceinline__ void ds_entries(const DsArgs& a, int row, const T* l, DsList& sh, int lane) {
+__device__ __forceinline__ int ds_entries(const DsArgs& a, int row, const T* l, DsList& sh, int lane) {
   int flags = 0;
+  unsigned open = 0;  // of this lane's entries, those not yet told apart from the others
 #pragma unroll
   for (int h = 0; h < kDsLane; ++h) {
     const int i = lane + 32 * h;
-    if (i >= a.k) break;
-    const int p = sh.place[i];
-    const float lp = __ldg(a.logp + (int64_t)row * a.k + i);
-    const float z = p >= 0 ? Elem<T>::load(l + p) : -INFINITY;
-    if (p >= 0 && z != -INFINITY) {  // kept
-      if (!(z < INFINITY) || !(lp < 80.f)) flags = VT_DEV_NONFINITE;
-      int twice = 0;
-      for (int o = 0; o < i; ++o) twice |= sh.place[o] == p;
-      if (twice) flags |= VT_DEV_DUPLICATE_ID;
+    if (i < a.k) {
+      const int p = sh.place[i];
+      const float lp = __ldg(a.logp + (int64_t)row * a.k + i);
+      const float z = p >= 0 ? Elem<T>::load(l + p) : -INFINITY;
+      if (z != -INFINITY) {  // kept
+        if (!(z < INFINITY) || !(lp < 80.f)) flags |= VT_DEV_NONFINITE;
+        open |= 1u << h;
+      }
+      sh.z[i] = z;
+      sh.logp[i] = lp;
     }
-    sh.z[i] = z;
-    sh.logp[i] = lp;
   }
-  flags = __reduce_or_sync(0xffffffffu, flags);
-  if (lane == 0) sh.flags |= flags;
-  __syncwarp();
+  // Two entries of one place: each entry leaves its number in a cell that its place gives.  One
+  // that finds another there has the same place, or tries again with other cells.
+  for (uint32_t mix = 1; __any_sync(0xffffffffu, open != 0); mix = mix * 0x9E3779B1u + 2) {
+    const auto cell = [&](int p) { return ((uint32_t)p * mix >> (mix == 1 ? 0 : 20)) & (4 * kDsMaxK - 1); };
+#pragma unroll
+    for (int h = 0; h < kDsLane; ++h)
+      if (open >> h & 1) sh.tag[cell(sh.place[lane + 32 * h])] = (uint8_t)(lane + 32 * h);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < kDsLane; ++h)
+      if (open >> h & 1) {
+        const int i = lane + 32 * h, o = sh.tag[cell(sh.place[i])];
+        if (o != i && sh.place[o] == sh.place[i]) flags |= VT_DEV_DUPLICATE_ID;
+        if (o == i || sh.place[o] == sh.place[i]) open &= ~(1u << h);
+      }
+    __syncwarp();
+  }
+  return __reduce_or_sync(0xffffffffu, flags);
 }
 
-__device__ __forceinline__ Pair pair_warp_sum(Pair v) {
-  for (int o = 16; o > 0; o >>= 1) {
-    Pair w;
-    w.h = __shfl_xor_sync(0xffffffffu, v.h, o);
-    w.l = __shfl_xor_sync(0xffffffffu, v.l, o);
-    v = pair_add(v, w);
-  }
-  return v;
-}
 __device__ __forceinline__ Pair pair_from_lane(Pair v, int lane) {
   return Pair{__shfl_sync(0xffffffffu, v.h, lane), __shfl_sync(0xffffffffu, v.l, lane)};
 }
+__device__ __forceinline__ Pair pair_xor(Pair v, int o) {
+  return Pair{__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// the lanes' sums as one (their five additions round: 2^-24 each)
+__device__ __forceinline__ RowSum warp_join(RowSum a, float c) {
+  const float m = warp_max_nan(a.m);
+  return RowSum{m, warp_add((a.s + a.e) * exp2_approx((a.m - m) * c)), 0.f};
+}
 
-// Loss, statistics and flags of a row, by one warp: from its list and the sum of its
-// unlisted ids (s = 0: there are none above -infinity).
-__device__ void ds_finish(const DsArgs& a, const DsList& sh, const DsSum& un, int lane, float& loss, DsStats& st,
-                          int& flags) {
-  const float mr = un.sum.m;
-  const bool rest = !(un.sum.s == 0.f);  // (NaN: flagged below)
-  bool kept = false;
-  float m = rest ? mr : -INFINITY;
-  Pair mass{0.f, 0.f};
+// What a row's list says by itself, the same in all lanes of the warp that holds it
+struct DsHead {
+  bool kept;    // an entry is
+  int flags;
+  float m, S;   // largest kept logit, sum of 2^((z - m) c) over the kept
+  Pair mass;    // sum of t
+  Pair cross;   // sum of t (ln t - (z - m) / T)
+};
+
+// (z - m) / T
+__device__ __forceinline__ Pair ds_below(float z, float m, Pair inv_t) {
+  Pair d;
+  two_sum(z, -m, d.h, d.l);
+  return pair_mul(d, inv_t);
+}
+
+__device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsList& sh, int flags, int lane) {
+  DsHead r;
+  float m = -INFINITY;
 #pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h;
-    if (i < a.k && sh.z[i] != -INFINITY) {
-      kept = true;
-      m = max_nan(m, sh.z[i]);
-      mass = pair_add(mass, pair_exp(Pair{sh.logp[i], 0.f}));
-    }
+  for (int h = 0; h < kDsLane; ++h)
+    if (lane + 32 * h < a.k) m = max_nan(m, sh.z[lane + 32 * h]);
+  r.m = m = warp_max_nan(m);
+  r.kept = !(m == -INFINITY);
+  r.flags = flags;
+  r.S = 0.f;
+  r.mass = r.cross = Pair{0.f, 0.f};
+#pragma unroll 2
+  for (int i = lane; i < a.k; i += 32) {
+    const float z = sh.z[i], lp = sh.logp[i];
+    const bool kept = z != -INFINITY;
+    r.S += kept ? exp2_approx((z - m) * a.c) : 0.f;
+    const Pair lnt{lp, 0.f}, t = kept ? pair_exp(lnt) : Pair{0.f, 0.f};
+    r.mass = pair_add(r.mass, t);
+    if (t.h > 0.f) r.cross = pair_add(r.cross, pair_mul(t, pair_add(lnt, pair_neg(ds_below(z, m, a.inv_t)))));
+    sh.val[i] = t.h;
   }
-  kept = __any_sync(0xffffffffu, kept);
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  mass = pair_warp_sum(mass);
-  loss = 0.f;
+  r.S = warp_add(r.S);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r.mass = pair_add(r.mass, pair_xor(r.mass, o));
+    r.cross = pair_add(r.cross, pair_xor(r.cross, o));
+  }
+  return r;
+}
+
+// What the consuming warps leave of a row: the sum over its unlisted ids (s = 0: there
+// are none above -infinity)
+struct DsSum {
+  float m, s;
+  int late;
+};
+// The row's statistics from both, and what the loss takes of them
+struct DsTotal {
+  float S;     // relative to the row's largest logit
+  float b;     // the teacher's rest
+  int flags;
+  bool learns;
+};
+__device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, const DsSum& un, DsStats& st) {
+  DsTotal r{0.f, 0.f, hd.flags | (un.late ? VT_DEV_TIMEOUT : 0), false};
+  const bool rest = !(un.s == 0.f);  // (NaN: flagged below)
+  const float m = rest ? max_nan(hd.m, un.m) : hd.m, inv_t = a.inv_t.h;
   st = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
-  flags = sh.flags | (un.late ? VT_DEV_TIMEOUT : 0);
-  if (kept && !(m < INFINITY)) flags |= VT_DEV_NONFINITE;
-  if (flags) {
-    loss = __int_as_float(0x7fc00000);
-    st = DsStats{loss, loss, loss, loss, loss};
-    return;
+  if (hd.kept && !(m < INFINITY)) r.flags |= VT_DEV_NONFINITE;
+  if (r.flags) {
+    const float nan = __int_as_float(0x7fc00000);
+    st = DsStats{nan, nan, nan, nan, nan};
+    return r;
   }
-  // (z - m) / T; nothing of e^ it is left below -87
-  const auto below = [&](float z) {
-    Pair d;
-    two_sum(z, -m, d.h, d.l);
-    return pair_mul(d, a.inv_t);
-  };
-  const auto weight = [&](float z) {
-    return (z - m) * a.inv_t.h < -87.f ? Pair{0.f, 0.f} : pair_exp(below(z));
-  };
-  Pair b{0.f, 0.f};
-  if (a.rest && rest) b = pair_add(Pair{1.f, 0.f}, pair_neg(mass));
-  if (!(b.h > 0.f)) b = Pair{0.f, 0.f};
-  const Pair A = pair_add(mass, b);
-  if (!kept || !(A.h > 0.f)) return;  // nothing to learn from this row
-  Pair S{0.f, 0.f};
-#pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h;
-    if (i < a.k && sh.z[i] != -INFINITY) S = pair_add(S, weight(sh.z[i]));
+  // what the list leaves of 1: its mass is good to 2^-28
+  if (a.rest && rest) r.b = fmaxf(0.f, (1.f - hd.mass.h) - hd.mass.l);
+  const float A = hd.mass.h + r.b;
+  if (!hd.kept || !(A > 0.f)) return r;  // nothing to learn from this row
+  r.learns = true;
+  const float top = rest ? exp2_approx((un.m - m) * a.c) : 0.f;
+  r.S = fmaf(un.s, top, hd.S * exp2_approx((hd.m - m) * a.c));
+  st.m = m;
+  st.mr = rest ? un.m : 0.f;
+  const float all = inv_t / r.S;
+  if (a.rest) {
+    st.c_all = A * all;
+    st.c_rest = rest ? A * all * top - inv_t * (r.b / un.s) : 0.f;
+    st.c_t = inv_t;
+  } else {
+    st.c_all = all;
+    st.c_rest = all * top;
+    st.c_t = inv_t / hd.mass.h;
   }
-  S = pair_warp_sum(S);
-  const Pair sr = pair_of(un.sum.s, un.sum.e);
-  const Pair top = rest ? weight(mr) : Pair{0.f, 0.f};  // of the largest unlisted logit
-  S = pair_add(S, pair_mul(sr, top));
+  return r;
+}
+
+// The loss, by the warp that holds the list
+__device__ __forceinline__ float ds_loss(const DsArgs& a, const DsHead& hd, const DsSum& un, const DsStats& st,
+                                         const DsTotal& r, int lane) {
+  if (r.flags) return __int_as_float(0x7fc00000);
+  if (!r.learns) return 0.f;
   // four logarithms at once, one per lane
-  Pair v = lane == 0 ? S : lane == 1 ? sr : lane == 2 ? b : mass;
+  Pair v = lane == 3 ? hd.mass : Pair{lane == 0 ? r.S : lane == 1 ? un.s : r.b, 0.f};
   v = v.h > 0.f ? pair_log(v) : Pair{0.f, 0.f};
   const Pair lnS = pair_from_lane(v, 0), lnr = pair_from_lane(v, 1), lnb = pair_from_lane(v, 2);
   const Pair lna = pair_from_lane(v, 3);
-  Pair sum{0.f, 0.f};
-#pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h;
-    if (i < a.k && sh.z[i] != -INFINITY && sh.logp[i] > -INFINITY) {
-      const Pair lnp = pair_add(below(sh.z[i]), pair_neg(lnS));
-      const Pair lnt{sh.logp[i], 0.f};
-      sum = pair_add(sum, pair_mul(pair_exp(lnt), pair_add(lnt, pair_neg(lnp))));
-    }
+  // ln p = (z - hd.m) / T + shift
+  const Pair shift = pair_add(ds_below(hd.m, st.m, a.inv_t), pair_neg(lnS));
+  Pair sum = pair_add(hd.cross, pair_neg(pair_mul(hd.mass, shift)));
+  if (!a.rest) {
+    sum = pair_add(pair_div(sum, hd.mass), pair_neg(lna));
+  } else if (r.b > 0.f) {
+    const Pair lnq = pair_add(pair_add(lnr, ds_below(un.m, st.m, a.inv_t)), pair_neg(lnS));
+    sum = pair_add(sum, pair_mul(Pair{r.b, 0.f}, pair_add(lnb, pair_neg(lnq))));
   }
-  sum = pair_warp_sum(sum);
-  const Pair all = pair_div(a.inv_t, S);
-  st.m = m;
-  st.mr = rest ? mr : 0.f;
-  if (a.rest) {
-    if (b.h > 0.f) {
-      const Pair lnq = pair_add(pair_add(lnr, below(mr)), pair_neg(lnS));
-      sum = pair_add(sum, pair_mul(b, pair_add(lnb, pair_neg(lnq))));
-    }
-    st.c_all = pair_mul(A, all).h;
-    Pair c = pair_mul(A, pair_mul(all, top));
-    if (b.h > 0.f) c = pair_add(c, pair_neg(pair_div(pair_mul(a.inv_t, b), sr)));
-    st.c_rest = c.h;
-    st.c_t = a.inv_t.h;
-  } else {
-    sum = pair_add(pair_div(sum, mass), pair_neg(lna));
-    st.c_all = all.h;
-    st.c_rest = pair_mul(all, top).h;
-    st.c_t = pair_div(a.inv_t, mass).h;
-  }
-  loss = sum.h;
-  if (loss != loss) loss = INFINITY;  // a term beyond fp32: they are positive
+  return sum.h != sum.h ? INFINITY : sum.h;  // (a term beyond fp32: they are positive)
 }
 
 // Loss, statistics and flags of a row to where they go, by one thread
@@ -286,234 +346,15 @@ __device__ __forceinline__ void ds_put(const DsArgs& a, int row, float loss, con
   if (flags) atomicOr(a.dev_status, flags);
 }
 
-// Takes the listed elements out of what this warp is about to read: `first` bytes into
-// the block's part of the row begin `bytes` of it, at `buf`; vectors go to threads in turn.
-template <typename T>
-__device__ __forceinline__ void ds_mask(const DsList& sh, uint8_t* buf, int first, int bytes, int k, int warp, int lane) {
+// Calls f(entry, byte position) for the listed elements of `bytes` bytes of the row that begin `first`
+// bytes into the block's part, in the vectors of this warp (they go to threads in turn).
+template <typename F>
+__device__ __forceinline__ void ds_each(const DsList& sh, int first, int bytes, int k, int warp, int lane, F f) {
   for (int i = lane; i < k; i += 32) {
     const int p = sh.pos[i] - first;
-    if (p >= 0 && p < bytes && ((p >> 9) & (kLpWarps - 1)) == warp) {
-      *reinterpret_cast<decltype(Mask<T>::bits())*>(buf + p) = Mask<T>::bits();
-      // ahead of the next copy into this place
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
+    if (p >= 0 && p < bytes && ((p >> 9) & (kLpWarps - 1)) == warp) f(i, p);
   }
   __syncwarp();
-}
-
-// ------------------------------------------------------------------ the loss
-struct DsShared {
-  DsList list[2];  // of the row in hand and the next one
-  DsSum sum[2];
-  RowSum red[2][kLpWarps];
-  RowSum blk;      // this block's sum, as published
-  float edge[2][16];
-  alignas(8) uint64_t full[kLpStages], empty[kLpStages], listed[2], summed[2];
-  int timeout;
-};
-
-// whether a row has an id listed; all lanes of a warp call it
-__device__ __forceinline__ bool ds_any(const DsArgs& a, int row, int lane) {
-  bool any = false;
-  for (int i = lane; i < a.k; i += 32) any |= __ldg(a.ids + (int64_t)row * a.k + i) != -1;
-  return __any_sync(0xffffffffu, any);
-}
-
-// Rows are streamed as the log probabilities' kernel does it: one warp copies, eight sum the
-// unlisted ids; another reads the next row's list meanwhile and finishes the last one.
-template <typename T>
-__global__ void __launch_bounds__(kDsThreads, kLpPerSm) distill_loss_kernel(DsArgs a) {
-  constexpr int VE = Elem<T>::kVec;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ DsShared sh;
-  cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
-  if (tid == 0) {
-    for (int s = 0; s < kLpStages; ++s) {
-      umma::mbar_init(&sh.full[s], 1);
-      umma::mbar_init(&sh.empty[s], kLpWarps);
-    }
-    for (int s = 0; s < 2; ++s) {
-      umma::mbar_init(&sh.listed[s], 1);
-      umma::mbar_init(&sh.summed[s], kLpWarps);
-    }
-    sh.timeout = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-
-  if (warp == kLpWarps) {
-    // the copying warp runs ahead of the consumers, into their next rows
-    bool ok = true, any = ds_any(a, row0, lane);
-    const bool first = any;
-    int it = 0;  // chunks requested so far
-    for (int row = row0; row < a.R; row += stride) {
-      if (any && ok && lane == 0) {
-        const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-        const Span sp = span_of<T>(l, a.K, rank, C);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head);
-        for (int i = 0; i < sp.mine; ++i, ++it) {
-          const int s = it % kLpStages;
-          if (it >= kLpStages) ok = umma::mbar_wait(&sh.empty[s], ((it / kLpStages) - 1) & 1);
-          if (!ok) break;
-          const int64_t at = (int64_t)(rank + i * C) * kLpChunk;
-          const uint32_t bytes = (uint32_t)min((int64_t)kLpChunk, (int64_t)sp.nvec * 16 - at);
-          umma::mbar_expect_tx(&sh.full[s], bytes);
-          umma::bulk_load(ring + s * kLpChunk, src + at, bytes, &sh.full[s]);
-        }
-      }
-      if (row + stride < a.R) any = ds_any(a, row + stride, lane);
-    }
-    if (!ok) {
-      atomicExch(&sh.timeout, 1);
-      // every copy issued has landed before this block may exit
-      for (int s = 0; s < kLpStages; ++s)
-        for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
-    }
-    __syncwarp();
-    if (C > 1 && first) {
-      cl.sync();
-      cl.sync();
-    }
-    return;
-  }
-
-  if (warp == kLpWarps + 1) {
-    // the list's warp: row r is finished after row r + 1's list has been read
-    uint32_t limit = umma::kWaitLimit;
-    const auto read = [&](int row, int slot) {
-      DsList& list = sh.list[slot];
-      const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-      const Span sp = span_of<T>(l, a.K, rank, C);
-      ds_places<T>(a, row, sp, rank == 0, list, lane, [&](int p) {
-        const int e = p - sp.head, v = e / VE;
-        if (e < 0 || v >= sp.nvec) return -1;
-        const int chunk = v / (kLpNT * kLpU), mine = chunk / C;
-        if (chunk - mine * C != rank) return -1;
-        return mine * kLpChunk + (v - chunk * (kLpNT * kLpU)) * 16 + (e - v * VE) * (int)sizeof(T);
-      });
-      if (lane == 0) umma::mbar_arrive(&sh.listed[slot]);
-      if (list.any && rank == 0) ds_entries<T>(a, row, l, list, lane);
-    };
-    read(row0, 0);
-    int n = 0;
-    bool first = sh.list[0].any;
-    for (int row = row0; row < a.R; row += stride, ++n) {
-      const int slot = n & 1;
-      if (row + stride < a.R) read(row + stride, slot ^ 1);
-      if (C > 1) break;  // (one row, finished below)
-      const bool any = sh.list[slot].any;
-      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.summed[slot], (n >> 1) & 1, limit))) {
-        limit = 1;
-        if (lane == 0) atomicExch(&sh.timeout, 1);
-        sh.sum[slot].late = 1;
-      }
-      __syncwarp();
-      float loss = 0.f;
-      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-      int flags = 0;
-      if (any) ds_finish(a, sh.list[slot], sh.sum[slot], lane, loss, st, flags);
-      if (lane == 0) ds_put(a, row, loss, st, flags);
-      __syncwarp();
-    }
-    if (C > 1) {
-      float loss = 0.f;
-      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-      int flags = 0;
-      if (first) {
-        cl.sync();
-        if (rank == 0) {
-          // all blocks' sums, one per lane
-          const int from = lane < C ? lane : 0;
-          RowSum r = *cl.map_shared_rank(&sh.blk, from);
-          const bool late = *cl.map_shared_rank(&sh.timeout, from) != 0;
-          if (lane >= C) r.s = r.e = 0.f;
-          r = sum_lanes(r, kLpMaxC, a.c);
-          DsSum un{r, __any_sync(0xffffffffu, late)};
-          un.sum.m = __shfl_sync(0xffffffffu, r.m, 0);
-          un.sum.s = __shfl_sync(0xffffffffu, r.s, 0);
-          un.sum.e = __shfl_sync(0xffffffffu, r.e, 0);
-          ds_finish(a, sh.list[0], un, lane, loss, st, flags);
-        }
-        cl.sync();  // the first block has read the others' memory
-      }
-      if (rank == 0 && lane == 0) ds_put(a, row0, loss, st, flags);
-    }
-    return;
-  }
-
-  int it = 0, n = 0;  // chunks and rows consumed so far
-  uint32_t limit = umma::kWaitLimit;
-  for (int row = row0; row < a.R; row += stride, ++n) {
-    const int slot = n & 1;
-    const DsList& list = sh.list[slot];
-    const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-    const Span sp = span_of<T>(l, a.K, rank, C);
-    const bool edge = rank == 0 && tid < 2 * VE;
-    float xe = -INFINITY;
-    if (edge) {
-      const int id = edge_id<VE>(sp, tid);
-      if (id < a.K) xe = Elem<T>::load(l + id);
-    }
-    if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.listed[slot], (n >> 1) & 1, limit))) {
-      limit = 1;
-      if (lane == 0) atomicExch(&sh.timeout, 1);
-    }
-    if (!list.any) {
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
-      continue;
-    }
-    RowSum st{kNegBig, 0.f, 0.f};
-    for (int i = 0; i < sp.mine; ++i, ++it) {
-      const int s = it % kLpStages;
-      if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[s], (it / kLpStages) & 1, limit))) {
-        // gave up: go on without the data, so that no barrier is missed
-        limit = 1;
-        if (lane == 0) atomicExch(&sh.timeout, 1);
-      }
-      ds_mask<T>(list, ring + s * kLpChunk, i * kLpChunk, kLpChunk, a.k, warp, lane);
-      const int q0 = (rank + i * C) * (kLpNT * kLpU) + tid;  // first vector of this thread
-      const uint4* st4 = reinterpret_cast<const uint4*>(ring + s * kLpChunk) + tid;
-      const int have = min(kLpU, max(0, (sp.nvec - q0 + kLpNT - 1) / kLpNT));  // vectors in the row
-      uint4 v[kLpU];
-#pragma unroll
-      for (int u = 0; u < kLpU; ++u)
-        v[u] = u < have ? st4[u * kLpNT]
-                        : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
-      const float pm = Vec<T>::top(v);
-      if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
-      sum_add<T>(st, v, a.c);
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(&sh.empty[s]);
-    }
-    if (edge && !(list.edges >> tid & 1)) {
-      if (!(xe <= st.m)) sum_rescale(st, max_nan(st.m, xe), a.c);
-      float er;
-      two_sum(st.s, exp2_approx((xe - st.m) * a.c), st.s, er);
-      st.e += er;
-    }
-    st = sum_lanes(st, 32, a.c);
-    if (lane == 0) sh.red[slot][warp] = st;
-    lp_bar();
-    if (warp == 0) {
-      // (a warp that is ahead writes the other slot; it cannot reach the next but one
-      // row before this one has passed the next row's barrier)
-      const RowSum r = sum_lanes(sh.red[slot][lane % kLpWarps], kLpWarps, a.c);
-      if (lane == 0) {
-        sh.sum[slot] = DsSum{r, sh.timeout};
-        sh.blk = r;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
-    if (C > 1) {
-      cl.sync();
-      cl.sync();
-    }
-  }
 }
 
 // -------------------------------------------------------------- the gradient
@@ -553,8 +394,8 @@ template <> struct Store<uint16_t> {
 };
 
 // the gradient at a listed id
-__device__ __forceinline__ float ds_listed(const DsArgs& a, const DsStats& st, float g, float z, float logp) {
-  return g * (st.c_all * exp2_approx((z - st.m) * a.c) - st.c_t * pair_exp(Pair{logp, 0.f}).h);
+__device__ __forceinline__ float ds_listed(const DsArgs& a, const DsStats& st, float g, float z, float t) {
+  return g * (st.c_all * exp2_approx((z - st.m) * a.c) - st.c_t * t);
 }
 __device__ __forceinline__ bool ds_nothing(const DsStats& st) { return st.c_all == 0.f && st.c_t == 0.f; }
 
@@ -630,152 +471,372 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
   if (edge) Store<T>::put(d + edge_id<VE>(sp, tid), nothing ? 0.f : factor * exp2_approx((xe - st.mr) * a.c));
   if (nothing) return;
   __syncthreads();
-  if (p >= 0) Store<T>::put(d + p, ds_listed(a, st, g, z, lp));
+  if (p >= 0) Store<T>::put(d + p, ds_listed(a, st, g, z, pair_exp(Pair{lp, 0.f}).h));
 }
 
-// ------------------------------------------------------- loss and gradient
-constexpr int kDtThreads = kLpNT + 32;  // consuming warps and one for the list
-constexpr int kDtPieces = 8;            // copies of kLpChunk bytes a block
+// ------------------------------------------------------- loss, and with it the gradient
+constexpr int kDtThreads = kLpNT + 96;  // consuming warps, one that copies, two for the lists
 constexpr int kDtMaxC = 8;
+constexpr int kDtParts = kLpWarps + 1;  // sums that a block sends: its consuming warps', its edges'
+constexpr int kDtZero = 1024;
+
+struct alignas(16) DtPart {
+  float m, s;
+  int late, none;
+};
 
 struct DtShared {
-  DsList list;
-  RowSum red[kLpWarps];
-  DsStats st;
-  float edge[16];
-  alignas(8) uint64_t full[kDtPieces];
+  DsList list[2];                        // of every other row
+  DsStats st[2];
+  DtPart got[2][kDtMaxC * kDtParts];     // the blocks' sums
+  alignas(16) uint8_t zero[kDtZero];
+  alignas(8) uint64_t full[2], done[2];  // the parts in shared memory
+  alignas(8) uint64_t listed[2], summed[2], ready[2], graded[2];
   int timeout;
 };
 
-// One row per cluster, kept in its blocks' shared memory between the sum and the
-// gradient: `share` vectors in each block.  Every block finishes the row for itself.
-template <typename T>
-__global__ void __launch_bounds__(kDtThreads) distill_train_kernel(DsArgs a, int share) {
+// an address in shared memory of a block of the cluster
+__device__ __forceinline__ uint32_t map_block(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(umma::smem_u32(p)), "r"(rank));
+  return a;
+}
+// a sum to a block of the cluster, counted by its barrier
+__device__ __forceinline__ void send_part(const DtPart& v, DtPart* to, uint64_t* bar, int rank) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          map_block(to, rank)),
+      "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(v.late), "r"(v.none), "r"(map_block(bar, rank))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_block(uint64_t* bar, int rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_block(bar, rank)) : "memory");
+}
+// one poll for what other blocks have sent
+__device__ __forceinline__ bool try_parts(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(umma::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(umma::smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// A row per cluster and turn.  Each block has `share` of its vectors, in chunks of `chunk`
+// bytes: one warp copies them, eight sum the unlisted ids and send their sums to
+// the blocks that need them, and of two more each has the list of every other row: it reads
+// the list ahead, takes the sums together and finishes the row.
+// With the gradient a part is one chunk, and stays in shared memory until the statistics are there: the
+// consuming warps put the gradient in its place, the copying warp takes it out.  Every block finishes
+// every row for itself.  Without, only the first block does.
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, int share, int chunk) {
   constexpr int VE = Elem<T>::kVec;
-  extern __shared__ __align__(16) uint8_t part[];
+  extern __shared__ __align__(16) uint8_t buf[];  // two chunks
   __shared__ DtShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / C;
-  const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  T* d = static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad;
-  const Span sp = span_of<T>(l, a.K, 0, 1);
-  const int v0 = min(rank * share, sp.nvec), mine = min(share, sp.nvec - v0);  // this block's vectors
-  const int pieces = (mine * 16 + kLpChunk - 1) / kLpChunk;
-  const bool edges = rank == 0;
-  if (tid == kLpNT) {
-    for (int i = 0; i < kDtPieces; ++i) umma::mbar_init(&sh.full[i], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
+  const bool first = rank == 0, finishes = kGrad || first;
+  uint32_t limit = umma::kWaitLimit;
+  // a bounded wait of a whole warp; one that gives up is noted and the next ones are short
+  const auto late = [&](bool ok) {
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      limit = 1;
+      if (lane == 0) atomicExch(&sh.timeout, 1);
+    }
+    return ok;
+  };
+  const auto wait = [&](uint64_t* bar, int phase) { return late(umma::mbar_wait(bar, phase & 1, limit)); };
+  const auto wait_parts = [&](uint64_t* bar, int phase) {
+    bool ok = false;
+    for (uint32_t i = 0; i < limit && !ok; ++i) ok = try_parts(bar, phase & 1);
+    return late(ok);
+  };
+  const auto logits = [&](int row) { return static_cast<const T*>(a.logits) + (int64_t)row * a.ld; };
+  const auto grads = [&](int row) { return static_cast<T*>(a.grad) + (int64_t)row * a.ld_grad; };
+  // this block's vectors of a row
+  struct Mine {
+    int v0, n;
+  };
+  const auto mine_of = [&](const Span& sp) {
+    const int v0 = min(rank * share, sp.nvec);
+    return Mine{v0, min(share, sp.nvec - v0)};
+  };
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      umma::mbar_init(&sh.full[s], 1);
+      umma::mbar_init(&sh.done[s], kLpWarps);
+      umma::mbar_init(&sh.listed[s], 1);
+      umma::mbar_init(&sh.summed[s], finishes ? 1 : kLpWarps);
+      umma::mbar_init(&sh.ready[s], 1);
+      umma::mbar_init(&sh.graded[s], kLpWarps);
+    }
     sh.timeout = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
-  float xe = -INFINITY;
+  if (kGrad) {
+    for (int i = tid; i < kDtZero / 4; i += kDtThreads) reinterpret_cast<uint32_t*>(sh.zero)[i] = 0;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (C > 1)
+    cl.sync();  // every block's barriers are there
+  else
+    __syncthreads();
+
   if (warp == kLpWarps) {
-    const bool any = ds_any(a, row, lane);
-    if (any && lane == 0) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head) + (int64_t)v0 * 16;
-      for (int i = 0; i < pieces; ++i) {
-        const uint32_t bytes = (uint32_t)min(kLpChunk, mine * 16 - i * kLpChunk);
-        umma::mbar_expect_tx(&sh.full[i], bytes);
-        umma::bulk_load(part + i * kLpChunk, src + (int64_t)i * kLpChunk, bytes, &sh.full[i]);
+    // copies, up to two chunks ahead of the consumers
+    bool ok = true, any = ds_any(a, row0, lane);
+    int it = 0;
+    int held[2] = {-1, -1};  // the rows whose gradients the chunks hold
+    const auto put = [&](int s) {
+      if (!kGrad || held[s] < 0) return;
+      const Span sp = span_of<T>(logits(held[s]), a.K, 0, 1);
+      const Mine me = mine_of(sp);
+      T* d = grads(held[s]) + sp.head + (int64_t)me.v0 * VE;
+      if (me.n > 0 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) bulk_store(d, buf + (size_t)s * chunk, me.n * 16);
+    };
+    for (int row = row0; row < a.R; row += stride) {
+      if (ok && lane == 0) {
+        const T* l = logits(row);
+        const Span sp = span_of<T>(l, a.K, 0, 1);
+        const Mine me = mine_of(sp);
+        if (any) {
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head) + (int64_t)me.v0 * 16;
+          for (int at = 0; at < me.n * 16; at += chunk, ++it) {
+            const int s = it & 1;
+            if (it >= 2) {
+              ok = umma::mbar_wait(&sh.done[s], ((it >> 1) - 1) & 1);
+              if (!ok) break;
+              if (kGrad) {
+                put(s);
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              }
+            }
+            held[s] = row;
+            const uint32_t bytes = (uint32_t)min(chunk, me.n * 16 - at);
+            umma::mbar_expect_tx(&sh.full[s], bytes);
+            umma::bulk_load(buf + (size_t)s * chunk, src + at, bytes, &sh.full[s]);
+          }
+        } else if (kGrad) {
+          T* d = grads(row) + sp.head + (int64_t)me.v0 * VE;
+          if ((reinterpret_cast<uintptr_t>(d) & 15) == 0)
+            for (int at = 0; at < me.n * 16; at += kDtZero)
+              bulk_store(reinterpret_cast<uint8_t*>(d) + at, sh.zero, min(kDtZero, me.n * 16 - at));
+        }
       }
+      if (row + stride < a.R) any = ds_any(a, row + stride, lane);
+    }
+    if (kGrad && ok && lane == 0)
+      for (int i = max(0, it - 2); i < it && ok; ++i) {
+        ok = umma::mbar_wait(&sh.done[i & 1], (i >> 1) & 1);
+        if (ok) put(i & 1);
+      }
+    if (kGrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok) {
+      atomicExch(&sh.timeout, 1);
+      // every copy issued has landed before this block may exit
+      for (int s = 0; s < 2; ++s)
+        for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
     }
     __syncwarp();
-    ds_places<T>(a, row, sp, edges, sh.list, lane, [&](int p) {
-      const int e = p - sp.head, v = e / VE - v0;
-      return e < 0 || v < 0 || v >= mine ? -1 : v * 16 + (e % VE) * (int)sizeof(T);
-    });
-  } else if (edges && tid < 2 * VE) {
-    const int id = edge_id<VE>(sp, tid);
-    if (id < a.K) xe = Elem<T>::load(l + id);
-  }
-  __syncthreads();  // the places
-  const float g = a.weight ? a.weight[row] : 1.f;
-  const bool any = sh.list.any;
-  bool nothing = !any;
-  if (any) {
-    if (warp == kLpWarps) {
-      ds_entries<T>(a, row, l, sh.list, lane);
-    } else {
-      RowSum st{kNegBig, 0.f, 0.f};
-      for (int i = 0; i < pieces; ++i) {
-        if (!__all_sync(0xffffffffu, umma::mbar_wait(&sh.full[i], 0)) && lane == 0) atomicExch(&sh.timeout, 1);
-        ds_mask<T>(sh.list, part + i * kLpChunk, i * kLpChunk, kLpChunk, a.k, warp, lane);
-        const uint4* st4 = reinterpret_cast<const uint4*>(part + i * kLpChunk) + tid;
-        const int have = min(kLpU, max(0, (mine - i * (kLpNT * kLpU) - tid + kLpNT - 1) / kLpNT));
-        uint4 v[kLpU];
-#pragma unroll
-        for (int u = 0; u < kLpU; ++u)
-          v[u] = u < have ? st4[u * kLpNT]
-                          : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
-        const float pm = Vec<T>::top(v);
-        if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
-        sum_add<T>(st, v, a.c);
-      }
-      if (edges && tid < 2 * VE && !(sh.list.edges >> tid & 1)) {
-        if (!(xe <= st.m)) sum_rescale(st, max_nan(st.m, xe), a.c);
-        float er;
-        two_sum(st.s, exp2_approx((xe - st.m) * a.c), st.s, er);
-        st.e += er;
-      }
-      st = sum_lanes(st, 32, a.c);
-      if (lane == 0) sh.red[warp] = st;
-    }
-    if (C > 1)
-      cl.sync();  // every block's sums; and what is read of the row has been read
-    else
-      __syncthreads();
-    if (warp == kLpWarps) {
-      DsSum un{RowSum{kNegBig, 0.f, 0.f}, 0};
-      for (int i = lane; i < C * kLpWarps; i += 32) {
-        const int from = i / kLpWarps;
-        un.sum = sum_join(un.sum, cl.map_shared_rank(sh.red, from)[i % kLpWarps], a.c);
-        un.late |= *cl.map_shared_rank(&sh.timeout, from);
-      }
-      un.sum = sum_lanes(un.sum, 32, a.c);
-      un.late = __any_sync(0xffffffffu, un.late != 0);
-      float loss;
-      DsStats st;
-      int flags;
-      ds_finish(a, sh.list, un, lane, loss, st, flags);
+  } else if (warp > kLpWarps) {
+    // the lists: one warp has the even turns, the other the odd ones
+    const int slot = warp - kLpWarps - 1;
+    DsList& list = sh.list[slot];
+    int64_t row64 = row0 + (int64_t)slot * stride;
+    bool any;
+    DsIds p = ds_map(a, ds_ids(a, row64, lane), any);
+    for (int n = 0; row64 < a.R; ++n) {
+      const int row = (int)row64;
+      row64 += 2 * (int64_t)stride;
+      const T* l = logits(row);
+      const Span sp = span_of<T>(l, a.K, 0, 1);
+      const Mine me = mine_of(sp);
+      int flags = ds_places<VE>(a, p, any, sp, first, list, lane, [&](int q) {
+        const int e = q - sp.head, v = e / VE - me.v0;
+        return e < 0 || v < 0 || v >= me.n ? -1 : v * 16 + (e % VE) * (int)sizeof(T);
+      });
       if (lane == 0) {
-        sh.st = st;
-        if (edges) ds_put(a, row, loss, st, flags);
+        if (finishes) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * (kGrad ? kDtParts : kLpWarps) * sizeof(DtPart)));
+        umma::mbar_arrive(&sh.listed[slot]);
+      }
+      const DsIds ahead = ds_ids(a, row64, lane);
+      bool any_ahead;
+      if (!finishes) {
+        p = ds_map(a, ahead, any_ahead);
+        wait(&sh.summed[slot], n);
+        any = any_ahead;
+        continue;
+      }
+      // the row's edges, one per lane
+      const bool edge = first && lane < 2 * VE && edge_id<VE>(sp, lane) < a.K;
+      float xe = edge && any ? Elem<T>::load(l + edge_id<VE>(sp, lane)) : -INFINITY;
+      if (any) flags |= ds_entries<T>(a, row, l, list, lane);
+      const bool un_edge = edge && !(list.edges >> lane & 1);
+      DtPart ends{-INFINITY, 0.f, 0, 0};
+      if (first && any && __any_sync(0xffffffffu, un_edge)) {
+        ends.m = warp_max_nan(un_edge ? xe : -INFINITY);
+        const float w = exp2_approx((xe - ends.m) * a.c);
+        ends.s = ends.m == -INFINITY ? 0.f : warp_add(un_edge ? w : 0.f);
+      }
+      // (sent when what this warp reads of the logits has been read: when all sums are there, the
+      // gradient may take the logits' place)
+      if (kGrad && lane < C) send_part(ends, &sh.got[slot][rank * kDtParts + kLpWarps], &sh.summed[slot], lane);
+      const float g = kGrad && a.weight ? a.weight[row] : 1.f;
+      DsHead hd{};
+      if (any) hd = ds_head(a, list, flags, lane);
+      p = ds_map(a, ahead, any_ahead);
+      const bool ok = wait_parts(&sh.summed[slot], n);
+      DsSum un{kGrad ? -INFINITY : ends.m, 0.f, !ok};
+      constexpr int kMost = kDtMaxC * kDtParts;
+      const int parts = C * (kGrad ? kDtParts : kLpWarps);
+      float pm[(kMost + 31) / 32], ps[(kMost + 31) / 32];
+#pragma unroll
+      for (int h = 0; h < (kMost + 31) / 32; ++h) {
+        const int i = lane + 32 * h;
+        DtPart v{-INFINITY, 0.f, 0, 0};
+        if (i < parts) v = sh.got[slot][i];
+        un.late |= v.late;
+        pm[h] = v.m;
+        ps[h] = v.s;
+        un.m = max_nan(un.m, v.m);
+      }
+      un.m = warp_max_nan(un.m);
+      un.late = __any_sync(0xffffffffu, un.late != 0);
+      // (m is the lowest finite value where nothing was summed; kept from -infinity minus itself)
+      const auto part = [&](float m, float s) { return s == 0.f ? 0.f : s * exp2_approx((m - un.m) * a.c); };
+#pragma unroll
+      for (int h = 0; h < (kMost + 31) / 32; ++h) un.s += part(pm[h], ps[h]);
+      un.s = warp_add(un.s);
+      if (!kGrad) un.s += part(ends.m, ends.s);
+      if (!kGrad && lane < C) arrive_block(&sh.ready[slot], lane);  // the sums' places are free
+      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+      DsTotal r{};
+      if (any) r = ds_stats(a, hd, un, st);
+      if (kGrad) {
+        if (any)
+          for (int i = lane; i < a.k; i += 32) list.val[i] = ds_listed(a, st, g, list.z[i], list.val[i]);
+        if (lane == 0) sh.st[slot] = st;
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sh.ready[slot]);
+      }
+      if (first) {
+        const float loss = any ? ds_loss(a, hd, un, st, r, lane) : 0.f;
+        if (lane == 0) ds_put(a, row, loss, st, r.flags);
+        __syncwarp();
+      }
+      if (kGrad) {
+        // the edges' gradients
+        T* d = grads(row);
+        const bool nothing = ds_nothing(st);
+        if (edge && (nothing || un_edge || xe == -INFINITY))
+          Store<T>::put(d + edge_id<VE>(sp, lane),
+                        nothing ? 0.f : g * st.c_rest * exp2_approx((xe - st.mr) * a.c));
+        if (first && !nothing && list.edges)
+          for (int i = lane; i < a.k; i += 32) {
+            const int q = list.place[i];
+            if (q >= 0 && (q < sp.head || q >= sp.head + sp.nvec * VE) && list.z[i] != -INFINITY)
+              Store<T>::put(d + q, list.val[i]);
+          }
+        wait(&sh.graded[slot], n);  // the list has been used
+      }
+      any = any_ahead;
+    }
+  } else {
+    int it = 0, n = 0;  // chunks and rows consumed
+    for (int row = row0; row < a.R; row += stride, ++n) {
+      const int slot = n & 1;
+      const DsList& list = sh.list[slot];
+      const Span sp = span_of<T>(logits(row), a.K, 0, 1);
+      const Mine me = mine_of(sp);
+      wait(&sh.listed[slot], n >> 1);
+      const bool any = list.any;
+      RowSum sum{kNegBig, 0.f, 0.f};
+      if (any)
+        for (int at = 0; at < me.n * 16; at += chunk) {
+          const int s = it & 1, have = min(chunk, me.n * 16 - at) / 16;
+          uint8_t* const b = buf + (size_t)s * chunk;
+          const uint4* in = reinterpret_cast<const uint4*>(b);
+          wait(&sh.full[s], it >> 1);
+          ds_each(list, at, chunk, a.k, warp, lane, [&](int, int q) {
+            *reinterpret_cast<decltype(Mask<T>::bits())*>(b + q) = Mask<T>::bits();
+            // ahead of the next copy into this place
+            if (!kGrad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          });
+          for (int q0 = tid; q0 - tid < have; q0 += kLpNT * kLpU) {
+            uint4 v[kLpU];
+#pragma unroll
+            for (int u = 0; u < kLpU; ++u)
+              v[u] = q0 + u * kLpNT < have
+                         ? in[q0 + u * kLpNT]
+                         : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+            const float pm = Vec<T>::top(v);
+            if (!(pm <= sum.m)) sum_rescale(sum, max_nan(sum.m, pm), a.c);
+            sum_add<T>(sum, v, a.c);
+          }
+          if (!kGrad) {
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&sh.done[s]);
+            ++it;
+          }
+        }
+      // (a row that is not read is exchanged too: no block gets two turns ahead of another)
+      const RowSum w = warp_join(sum, a.c);
+      const DtPart part{w.m, w.s, *reinterpret_cast<volatile int*>(&sh.timeout), 0};
+      if (!kGrad && n >= 2) wait(&sh.ready[slot], (n >> 1) - 1);
+      if (lane < (kGrad ? C : 1))
+        send_part(part, &sh.got[slot][rank * (kGrad ? kDtParts : kLpWarps) + warp], &sh.summed[slot], lane);
+      if (!finishes) {
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
+      }
+      if (kGrad) {
+        T* const out = grads(row) + sp.head + (int64_t)me.v0 * VE;
+        const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+        const float g = a.weight ? __ldg(a.weight + row) : 1.f;
+        wait(&sh.ready[slot], n >> 1);
+        if (any && me.n > 0) {
+          const int s = it & 1;
+          uint8_t* const b = buf + (size_t)s * chunk;
+          uint4* const in = reinterpret_cast<uint4*>(b);
+          const DsStats st = sh.st[slot];
+          const bool nothing = ds_nothing(st);
+          const float factor = g * st.c_rest;
+#pragma unroll 4
+          for (int q = tid; q < me.n; q += kLpNT)
+            in[q] = nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(in[q], st.mr, a.c, factor);
+          __syncwarp();
+          if (!nothing)
+            ds_each(list, 0, chunk, a.k, warp, lane, [&](int i, int q) {
+              if (list.z[i] != -INFINITY) Store<T>::put(reinterpret_cast<T*>(b + q), list.val[i]);
+            });
+          if (!aligned)
+            for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, in[q], false);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(&sh.done[s]);
+          ++it;
+        } else if (!any && !aligned) {
+          for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, make_uint4(0, 0, 0, 0), false);
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sh.graded[slot]);
       }
     }
-    __syncthreads();
-    if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // done with the others' memory
-    nothing = ds_nothing(sh.st);
-  } else if (edges && tid == 0) {
-    ds_put(a, row, 0.f, DsStats{0.f, 0.f, 0.f, 0.f, 0.f}, 0);
   }
-  const DsStats st = any ? sh.st : DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
-  const float factor = g * st.c_rest;
-  if (warp < kLpWarps) {
-    T* out = d + sp.head + (int64_t)v0 * VE;
-    const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-    const uint4* in = reinterpret_cast<const uint4*>(part);
-#pragma unroll 4
-    for (int q = tid; q < mine; q += kLpNT)
-      store_vec(out + (int64_t)q * VE,
-                nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(in[q], st.mr, a.c, factor), aligned);
-    if (edges && tid < 2 * VE && edge_id<VE>(sp, tid) < a.K)
-      Store<T>::put(d + edge_id<VE>(sp, tid), nothing ? 0.f : factor * exp2_approx((xe - st.mr) * a.c));
-  }
-  if (!nothing) {
-    __syncthreads();
-    if (warp == kLpWarps)
-      for (int i = lane; i < a.k; i += 32) {
-        const int p = sh.list.place[i];
-        const bool here = sh.list.pos[i] >= 0 || (edges && p >= 0 && (p < sp.head || p >= sp.head + sp.nvec * VE));
-        const float z = sh.list.z[i];
-        if (here && z != -INFINITY) Store<T>::put(d + p, ds_listed(a, st, g, z, sh.list.logp[i]));
-      }
-  }
-  if (sh.timeout && tid == 0)  // every copy issued has landed before this block may exit
-    for (int i = 0; any && i < pieces; ++i) umma::mbar_wait(&sh.full[i], 0, 1u << 12);
-  if (C > 1 && any) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (C > 1) cl.sync();  // nothing more is sent to a block that has left
 }
 
 // arguments that the three calls share
@@ -828,36 +889,6 @@ DsArgs ds_args(const void* logits, int64_t R, int32_t K, int64_t ld, const int32
   return a;
 }
 
-template <typename T>
-int ds_launch_loss(const DsArgs& a, cudaStream_t s) {
-  auto kern = distill_loss_kernel<T>;
-  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem));
-  if (!a.own_status) {
-    const int st = clear_status(s, a.dev_status);
-    if (st != VT_OK) return st;
-  }
-  const int C = lp_cluster(a.R, a.K, (int)sizeof(T));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(C > 1 ? a.R * C : std::min(a.R, num_sms() * kLpPerSm)));
-  cfg.blockDim = dim3(kDsThreads);
-  cfg.dynamicSmemBytes = kLpSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.own_status ? 1 : 2;
-  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
-  return VT_OK;
-}
-int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
-  return dtype == VT_F32 ? ds_launch_loss<float>(a, s) : ds_launch_loss<uint16_t>(a, s);
-}
-
 int ds_launch_grad(const DsArgs& a, int32_t dtype, cudaStream_t s) {
   const int elem = dtype == VT_F32 ? 4 : 2;
   const int pieces = std::max(1, (int)(((int64_t)a.K * elem / 16 + kDsNT * kDgU - 1) / (kDsNT * kDgU)));
@@ -870,45 +901,92 @@ int ds_launch_grad(const DsArgs& a, int32_t dtype, cudaStream_t s) {
   return VT_OK;
 }
 
-// bytes of shared memory that a row's part may take: three blocks on an SM, or one
-constexpr int kDtThree = 68 << 10, kDtOne = 200 << 10;
+// How a row is spread: C blocks with `share` vectors each, in chunks; two chunks of kDtPart[tier]
+// bytes leave room for 3 - tier blocks on an SM, which work while one waits for its cluster.
+struct DtPlan {
+  int C, share, chunk, tier;
+};
+constexpr int kDtPart[3] = {32 << 10, 50 << 10, 100 << 10};
 
-template <typename T>
-int ds_launch_train(const DsArgs& a, cudaStream_t s, int C, int share) {
-  auto kern = distill_train_kernel<T>;
-  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtOne));
-  if (!a.own_status) {
-    const int st = clear_status(s, a.dev_status);
-    if (st != VT_OK) return st;
+// few rows: more blocks to each
+void dt_spread(int64_t R, int64_t bytes, DtPlan& p) {
+  const int slots = num_sms() * (3 - p.tier);
+  while (p.C < kDtMaxC && R * p.C * 2 <= slots && bytes / p.C > (4 << 10)) p.C = std::min(p.C * 2, kDtMaxC);
+  p.share = std::max(1, (int)((bytes / 16 + p.C - 1) / p.C));
+}
+// with the gradient a part is one chunk
+bool dt_plan_grad(int64_t R, int64_t bytes, DtPlan& p) {
+  for (p.tier = 0; p.tier < 3; ++p.tier) {
+    const int64_t C = std::max<int64_t>(1, (bytes + kDtPart[p.tier] - 1) / kDtPart[p.tier]);
+    if (C > kDtMaxC) continue;
+    p.C = (int)C;
+    dt_spread(R, bytes, p);
+    p.chunk = p.share * 16;
+    return true;
   }
+  return false;
+}
+DtPlan dt_plan_loss(int64_t R, int64_t bytes) {
+  DtPlan p;
+  p.tier = 0;
+  p.C = (int)std::max<int64_t>(1, std::min<int64_t>((bytes + kDtPart[0] - 1) / kDtPart[0], kDtMaxC));
+  dt_spread(R, bytes, p);
+  const int chunks = (p.share * 16 + kDtPart[0] - 1) / kDtPart[0];
+  p.chunk = (p.share + chunks - 1) / chunks * 16;  // evenly
+  return p;
+}
+
+template <typename T, bool kGrad>
+int ds_launch_rows(const DsArgs& a, cudaStream_t s, const DtPlan& p) {
+  auto kern = distill_rows_kernel<T, kGrad>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kDtPart[2]));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.R * C));
   cfg.blockDim = dim3(kDtThreads);
-  cfg.dynamicSmemBytes = (size_t)share * 16;
+  cfg.dynamicSmemBytes = (size_t)2 * kDtPart[p.tier];
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.x = (unsigned)p.C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that run at once, by device and spread: a property of the device, asked once
+  static std::atomic<int> cache[64][3][kDtMaxC];
+  int dev = 0;
+  VT_RETURN_IF_CUDA(cudaGetDevice(&dev));
+  int clusters = dev < 64 ? cache[dev][p.tier][p.C - 1].load(std::memory_order_relaxed) : 0;
+  if (clusters == 0) {
+    cfg.gridDim = dim3((unsigned)(p.C * num_sms() * 3));
+    VT_RETURN_IF_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg));
+    if (clusters < 1) return VT_ERR_CUDA;
+    if (dev < 64) cache[dev][p.tier][p.C - 1].store(clusters, std::memory_order_relaxed);
+  }
+  if (!a.own_status) {
+    const int st = clear_status(s, a.dev_status);
+    if (st != VT_OK) return st;
+  }
+  cfg.gridDim = dim3((unsigned)(std::min(a.R, clusters) * p.C));
   cfg.numAttrs = a.own_status ? 1 : 2;
-  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a, share));
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a, p.share, p.chunk));
   return VT_OK;
+}
+
+int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
+  const DtPlan p = dt_plan_loss(a.R, (int64_t)a.K * (dtype == VT_F32 ? 4 : 2));
+  return dtype == VT_F32 ? ds_launch_rows<float, false>(a, s, p) : ds_launch_rows<uint16_t, false>(a, s, p);
 }
 
 // Rows that the blocks of a cluster hold between them are read once; longer ones take the two calls.
 int ds_launch_both(const DsArgs& a, int32_t dtype, cudaStream_t s) {
-  const int64_t bytes = (int64_t)a.K * (dtype == VT_F32 ? 4 : 2);
-  int C = (int)std::min<int64_t>((bytes + kDtThree - 1) / kDtThree, kDtMaxC);
-  const int64_t vecs = bytes / 16, share = (vecs + C - 1) / C;
-  if (share * 16 > kDtOne || (int64_t)a.R * C > 0x7fffffff) {
+  DtPlan p;
+  if (!dt_plan_grad(a.R, (int64_t)a.K * (dtype == VT_F32 ? 4 : 2), p)) {
     const int rc = ds_launch_loss(a, dtype, s);
     return rc != VT_OK ? rc : ds_launch_grad(a, dtype, s);
   }
-  return dtype == VT_F32 ? ds_launch_train<float>(a, s, C, (int)share) : ds_launch_train<uint16_t>(a, s, C, (int)share);
+  return dtype == VT_F32 ? ds_launch_rows<float, true>(a, s, p) : ds_launch_rows<uint16_t, true>(a, s, p);
 }
 
 }  // namespace
