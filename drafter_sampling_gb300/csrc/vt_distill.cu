@@ -36,7 +36,6 @@ namespace vt {
 namespace {
 
 constexpr int kDsMaxK = 128;
-constexpr int kDsLane = kDsMaxK / 32;      // list entries of a lane
 constexpr int kDsNT = 256;
 
 // what takes an element out of a sum
@@ -84,42 +83,50 @@ __device__ __forceinline__ int ds_place(const DsArgs& a, int64_t i) {
 
 // A row's list as the block's warps share it
 struct DsList {
-  int place[kDsMaxK];  // of entries that the drafter has, else -1
   int pos[kDsMaxK];    // bytes from the start of what this block reads of the row, -1: not there
-  float z[kDsMaxK], logp[kDsMaxK];
-  float val[kDsMaxK];  // t, then the gradient
-  uint8_t tag[4 * kDsMaxK];
-  unsigned edges;      // the row's edge elements that are listed
+  float val[kDsMaxK];  // the gradient there
   int any;             // an id is given
 };
 
-// a warp's lanes hold entries lane, lane + 32, ...
-struct DsIds {
-  int id[kDsLane];
+// What one warp holds of a row's list: its lanes have entries lane, lane + 32, ..., H each
+template <int H>
+struct DsEntries {
+  int p[H];           // first the ids, then places in the drafter's vocabulary: -1 none, -2 out of range
+  float z[H], lp[H];  // of kept entries; z = -infinity: not kept
+  bool any;           // an id is given
 };
-__device__ __forceinline__ DsIds ds_ids(const DsArgs& a, int64_t row, int lane) {
-  DsIds r;
+template <int H>
+__device__ __forceinline__ void ds_ids(const DsArgs& a, int64_t row, int lane, int (&id)[H]) {
 #pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
+  for (int h = 0; h < H; ++h) {
     const int i = lane + 32 * h;
-    r.id[h] = row < a.R && i < a.k ? __ldg(a.ids + row * a.k + i) : -1;
+    id[h] = row < a.R && i < a.k ? __ldg(a.ids + row * a.k + i) : -1;
   }
-  return r;
 }
-// ids to places in the drafter's vocabulary: -1 none, -2 out of range; *any: an id is given
-__device__ __forceinline__ DsIds ds_map(const DsArgs& a, DsIds p, bool& any) {
-  any = false;
+template <int H>
+__device__ __forceinline__ void ds_map(const DsArgs& a, const int (&id)[H], DsEntries<H>& e) {
+  e.any = false;
 #pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    any |= p.id[h] != -1;
-    if (p.id[h] != -1 && (p.id[h] < 0 || p.id[h] >= a.V)) p.id[h] = -2;
-    if (p.id[h] >= 0 && a.inv_map) {
-      const int q = __ldg(a.inv_map + p.id[h]);
-      p.id[h] = q >= -1 && q < a.K ? q : -2;
+  for (int h = 0; h < H; ++h) {
+    int p = id[h];
+    e.any |= p != -1;
+    if (p != -1 && (p < 0 || p >= a.V)) p = -2;
+    if (p >= 0 && a.inv_map) {
+      const int q = __ldg(a.inv_map + p);
+      p = q >= -1 && q < a.K ? q : -2;
     }
+    e.p[h] = p;
   }
-  any = __any_sync(0xffffffffu, any);
-  return p;
+  e.any = __any_sync(0xffffffffu, e.any);
+}
+template <typename T, int H>
+__device__ __forceinline__ void ds_values(const DsArgs& a, int64_t row, int lane, DsEntries<H>& e) {
+  const T* l = static_cast<const T*>(a.logits) + row * a.ld;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    e.z[h] = e.p[h] >= 0 ? Elem<T>::load(l + e.p[h]) : -INFINITY;
+    e.lp[h] = e.p[h] >= 0 ? __ldg(a.logp + row * a.k + lane + 32 * h) : 0.f;
+  }
 }
 // whether a row has an id listed; all lanes of a warp call it
 __device__ __forceinline__ bool ds_any(const DsArgs& a, int row, int lane) {
@@ -128,70 +135,49 @@ __device__ __forceinline__ bool ds_any(const DsArgs& a, int row, int lane) {
   return __any_sync(0xffffffffu, any);
 }
 
-// Writes a row's places to its list; at(place): the byte position in what this block reads, or
-// -1.  Returns the flags.
-template <int VE, typename At>
-__device__ __forceinline__ int ds_places(const DsArgs& a, const DsIds& p, bool any, const Span& sp, bool edges,
-                                         DsList& sh, int lane, At at) {
-  bool bad = false;
-  unsigned edge = 0;
-#pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h, q = p.id[h];
-    bad |= q == -2;
-    if (i < a.k) {
-      sh.place[i] = max(q, -1);
-      sh.pos[i] = q >= 0 ? at(q) : -1;
-    }
-    if (q >= 0 && edges) {
-      const int t = q < sp.head ? q : q - sp.nvec * VE;
-      if (q < sp.head || t >= sp.head) edge |= 1u << t;
-    }
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  edge = __reduce_or_sync(0xffffffffu, edge);
-  if (lane == 0) {
-    sh.any = any;
-    sh.edges = edge;
-  }
-  __syncwarp();
-  return bad ? VT_DEV_BAD_ID : 0;
+// a row's edge element that place p is, or -1
+template <int VE>
+__device__ __forceinline__ int ds_edge(const Span& sp, int p) {
+  if (p < 0) return -1;
+  if (p < sp.head) return p;
+  const int t = p - sp.nvec * VE;
+  return t >= sp.head ? t : -1;
 }
 
-// What stands at the list's places; returns flags.
-template <typename T>
-__device__ __forceinline__ int ds_entries(const DsArgs& a, int row, const T* l, DsList& sh, int lane) {
+// Flags of the entries' values; two kept entries of one place among them: each leaves its number
+// in a cell that its place gives, and one that finds another there has the same place, or
+// tries again with other cells.
+constexpr int kDsCells = 512;
+struct DsCells {
+  int place[kDsMaxK];
+  uint8_t tag[kDsCells];
+};
+template <int H>
+__device__ __forceinline__ int ds_flags(const DsEntries<H>& e, DsCells& sh, int lane) {
   int flags = 0;
   unsigned open = 0;  // of this lane's entries, those not yet told apart from the others
 #pragma unroll
-  for (int h = 0; h < kDsLane; ++h) {
-    const int i = lane + 32 * h;
-    if (i < a.k) {
-      const int p = sh.place[i];
-      const float lp = __ldg(a.logp + (int64_t)row * a.k + i);
-      const float z = p >= 0 ? Elem<T>::load(l + p) : -INFINITY;
-      if (z != -INFINITY) {  // kept
-        if (!(z < INFINITY) || !(lp < 80.f)) flags |= VT_DEV_NONFINITE;
-        open |= 1u << h;
-      }
-      sh.z[i] = z;
-      sh.logp[i] = lp;
+  for (int h = 0; h < H; ++h) {
+    if (e.p[h] == -2) flags |= VT_DEV_BAD_ID;
+    if (e.z[h] != -INFINITY) {
+      if (!(e.z[h] < INFINITY) || !(e.lp[h] < 80.f)) flags |= VT_DEV_NONFINITE;
+      open |= 1u << h;
     }
+    sh.place[lane + 32 * h] = e.p[h];
   }
-  // Two entries of one place: each entry leaves its number in a cell that its place gives.  One
-  // that finds another there has the same place, or tries again with other cells.
   for (uint32_t mix = 1; __any_sync(0xffffffffu, open != 0); mix = mix * 0x9E3779B1u + 2) {
-    const auto cell = [&](int p) { return ((uint32_t)p * mix >> (mix == 1 ? 0 : 20)) & (4 * kDsMaxK - 1); };
+    const auto cell = [&](int p) { return ((uint32_t)p * mix >> (mix == 1 ? 0 : 20)) & (kDsCells - 1); };
 #pragma unroll
-    for (int h = 0; h < kDsLane; ++h)
-      if (open >> h & 1) sh.tag[cell(sh.place[lane + 32 * h])] = (uint8_t)(lane + 32 * h);
+    for (int h = 0; h < H; ++h)
+      if (open >> h & 1) sh.tag[cell(e.p[h])] = (uint8_t)(lane + 32 * h);
     __syncwarp();
 #pragma unroll
-    for (int h = 0; h < kDsLane; ++h)
+    for (int h = 0; h < H; ++h)
       if (open >> h & 1) {
-        const int i = lane + 32 * h, o = sh.tag[cell(sh.place[i])];
-        if (o != i && sh.place[o] == sh.place[i]) flags |= VT_DEV_DUPLICATE_ID;
-        if (o == i || sh.place[o] == sh.place[i]) open &= ~(1u << h);
+        const int i = lane + 32 * h, o = sh.tag[cell(e.p[h])];
+        const bool same = sh.place[o] == e.p[h];
+        if (o != i && same) flags |= VT_DEV_DUPLICATE_ID;
+        if (same) open &= ~(1u << h);
       }
     __syncwarp();
   }
@@ -236,26 +222,26 @@ __device__ __forceinline__ Pair ds_below(float z, float m, Pair inv_t) {
   return pair_mul(d, inv_t);
 }
 
-__device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsList& sh, int flags, int lane) {
+// (leaves t in lp)
+template <int H>
+__device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsEntries<H>& e, int flags) {
   DsHead r;
   float m = -INFINITY;
 #pragma unroll
-  for (int h = 0; h < kDsLane; ++h)
-    if (lane + 32 * h < a.k) m = max_nan(m, sh.z[lane + 32 * h]);
+  for (int h = 0; h < H; ++h) m = max_nan(m, e.z[h]);
   r.m = m = warp_max_nan(m);
   r.kept = !(m == -INFINITY);
   r.flags = flags;
   r.S = 0.f;
   r.mass = r.cross = Pair{0.f, 0.f};
-#pragma unroll 2
-  for (int i = lane; i < a.k; i += 32) {
-    const float z = sh.z[i], lp = sh.logp[i];
-    const bool kept = z != -INFINITY;
-    r.S += kept ? exp2_approx((z - m) * a.c) : 0.f;
-    const Pair lnt{lp, 0.f}, t = kept ? pair_exp(lnt) : Pair{0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (e.z[h] == -INFINITY) continue;
+    r.S += exp2_approx((e.z[h] - m) * a.c);
+    const Pair lnt{e.lp[h], 0.f}, t = pair_exp(lnt);
     r.mass = pair_add(r.mass, t);
-    if (t.h > 0.f) r.cross = pair_add(r.cross, pair_mul(t, pair_add(lnt, pair_neg(ds_below(z, m, a.inv_t)))));
-    sh.val[i] = t.h;
+    if (t.h > 0.f) r.cross = pair_add(r.cross, pair_mul(t, pair_add(lnt, pair_neg(ds_below(e.z[h], m, a.inv_t)))));
+    e.lp[h] = t.h;
   }
   r.S = warp_add(r.S);
 #pragma unroll
@@ -299,10 +285,11 @@ __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, c
   r.S = fmaf(un.s, top, hd.S * exp2_approx((hd.m - m) * a.c));
   st.m = m;
   st.mr = rest ? un.m : 0.f;
-  const float all = inv_t / r.S;
+  // (quotients to two units of the last place: S and the unlisted sum are in [1, 2^23])
+  const float all = __fdividef(inv_t, r.S);
   if (a.rest) {
     st.c_all = A * all;
-    st.c_rest = rest ? A * all * top - inv_t * (r.b / un.s) : 0.f;
+    st.c_rest = rest ? A * all * top - inv_t * __fdividef(r.b, un.s) : 0.f;
     st.c_t = inv_t;
   } else {
     st.c_all = all;
@@ -479,19 +466,22 @@ constexpr int kDtThreads = kLpNT + 96;  // consuming warps, one that copies, two
 constexpr int kDtMaxC = 8;
 constexpr int kDtParts = kLpWarps + 1;  // sums that a block sends: its consuming warps', its edges'
 constexpr int kDtZero = 1024;
+constexpr int kDtRing = 4;              // rows whose lists and sums are in hand
+constexpr int kDtStages = 3;
 
-struct alignas(16) DtPart {
+// a sum on its way between blocks; s = -1: a wait has run out
+struct alignas(8) DtPart {
   float m, s;
-  int late, none;
 };
 
 struct DtShared {
-  DsList list[2];                        // of every other row
-  DsStats st[2];
-  DtPart got[2][kDtMaxC * kDtParts];     // the blocks' sums
+  DsList list[kDtRing];
+  DsStats st[kDtRing];
+  DsCells cells[2];
+  DtPart got[kDtRing][kDtMaxC * kDtParts];  // the blocks' sums
   alignas(16) uint8_t zero[kDtZero];
-  alignas(8) uint64_t full[2], done[2];  // the parts in shared memory
-  alignas(8) uint64_t listed[2], summed[2], ready[2], graded[2];
+  alignas(8) uint64_t full[kDtStages], done[kDtStages];  // chunks of the row in shared memory
+  alignas(8) uint64_t listed[kDtRing], summed[kDtRing], ready[kDtRing], used[kDtRing];
   int timeout;
 };
 
@@ -503,16 +493,15 @@ __device__ __forceinline__ uint32_t map_block(const void* p, int rank) {
 }
 // a sum to a block of the cluster, counted by its barrier
 __device__ __forceinline__ void send_part(const DtPart& v, DtPart* to, uint64_t* bar, int rank) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-          map_block(to, rank)),
-      "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(v.late), "r"(v.none), "r"(map_block(bar, rank))
-      : "memory");
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+                   map_block(to, rank)),
+               "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(map_block(bar, rank))
+               : "memory");
 }
 __device__ __forceinline__ void arrive_block(uint64_t* bar, int rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_block(bar, rank)) : "memory");
 }
-// one poll for what other blocks have sent
+// one poll for what other blocks have done
 __device__ __forceinline__ bool try_parts(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -531,23 +520,29 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// A row per cluster and turn.  Each block has `share` of its vectors, in chunks of `chunk`
-// bytes: one warp copies them, eight sum the unlisted ids and send their sums to
-// the blocks that need them, and of two more each has the list of every other row: it reads
-// the list ahead, takes the sums together and finishes the row.
-// With the gradient a part is one chunk, and stays in shared memory until the statistics are there: the
-// consuming warps put the gradient in its place, the copying warp takes it out.  Every block finishes
-// every row for itself.  Without, only the first block does.
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, int share, int chunk) {
+struct DtSplit {
+  int share, chunk, stages;  // vectors of a row in each block, bytes of a chunk, chunks in shared memory
+};
+
+// A row per cluster and turn.  Each block has `share` of its vectors, in chunks: one warp
+// copies them, eight sum the unlisted ids and send their sums to the blocks that need them, and
+// of two more each has the list of every other row, which it reads a turn ahead; it
+// takes the sums together and finishes the row.
+// With the gradient a part is one chunk, and stays in shared memory until the statistics are there,
+// which takes longer than a sum: the consuming warps sum the next row meanwhile, then put the
+// gradient in the logits' place, and the copying warp takes it out.  Every block finishes every row
+// for itself.  Without the gradient the blocks finish rows in turn.
+template <typename T, bool kGrad, int H>
+__global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, DtSplit split) {
   constexpr int VE = Elem<T>::kVec;
-  extern __shared__ __align__(16) uint8_t buf[];  // two chunks
+  extern __shared__ __align__(16) uint8_t buf[];
   __shared__ DtShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row0 = blockIdx.x / C, stride = gridDim.x / C;
-  const bool first = rank == 0, finishes = kGrad || first;
+  const int chunk = split.chunk, NS = split.stages;
+  const bool first = rank == 0;  // has the rows' edges
   uint32_t limit = umma::kWaitLimit;
   // a bounded wait of a whole warp; one that gives up is noted and the next ones are short
   const auto late = [&](bool ok) {
@@ -559,7 +554,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
     return ok;
   };
   const auto wait = [&](uint64_t* bar, int phase) { return late(umma::mbar_wait(bar, phase & 1, limit)); };
-  const auto wait_parts = [&](uint64_t* bar, int phase) {
+  const auto wait_blocks = [&](uint64_t* bar, int phase) {
     bool ok = false;
     for (uint32_t i = 0; i < limit && !ok; ++i) ok = try_parts(bar, phase & 1);
     return late(ok);
@@ -571,17 +566,19 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
     int v0, n;
   };
   const auto mine_of = [&](const Span& sp) {
-    const int v0 = min(rank * share, sp.nvec);
-    return Mine{v0, min(share, sp.nvec - v0)};
+    const int v0 = min(rank * split.share, sp.nvec);
+    return Mine{v0, min(split.share, sp.nvec - v0)};
   };
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kDtStages; ++s) {
       umma::mbar_init(&sh.full[s], 1);
       umma::mbar_init(&sh.done[s], kLpWarps);
+    }
+    for (int s = 0; s < kDtRing; ++s) {
       umma::mbar_init(&sh.listed[s], 1);
-      umma::mbar_init(&sh.summed[s], finishes ? 1 : kLpWarps);
+      umma::mbar_init(&sh.summed[s], 1);
       umma::mbar_init(&sh.ready[s], 1);
-      umma::mbar_init(&sh.graded[s], kLpWarps);
+      umma::mbar_init(&sh.used[s], kLpWarps);
     }
     sh.timeout = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -596,16 +593,21 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
     __syncthreads();
 
   if (warp == kLpWarps) {
-    // copies, up to two chunks ahead of the consumers
+    // copies, as far ahead of the consumers as there are chunks
     bool ok = true, any = ds_any(a, row0, lane);
-    int it = 0;
-    int held[2] = {-1, -1};  // the rows whose gradients the chunks hold
-    const auto put = [&](int s) {
-      if (!kGrad || held[s] < 0) return;
-      const Span sp = span_of<T>(logits(held[s]), a.K, 0, 1);
+    int s = 0, lap = 0;          // the next chunk's place, and how often that has been gone round
+    int held[kDtStages];         // the rows whose gradients the chunks will hold
+#pragma unroll
+    for (int i = 0; i < kDtStages; ++i) held[i] = -1;
+    const auto put = [&](int at) {
+      int row = -1;
+#pragma unroll
+      for (int i = 0; i < kDtStages; ++i)
+        if (i == at) row = held[i];
+      const Span sp = span_of<T>(logits(row), a.K, 0, 1);
       const Mine me = mine_of(sp);
-      T* d = grads(held[s]) + sp.head + (int64_t)me.v0 * VE;
-      if (me.n > 0 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) bulk_store(d, buf + (size_t)s * chunk, me.n * 16);
+      T* d = grads(row) + sp.head + (int64_t)me.v0 * VE;
+      if ((reinterpret_cast<uintptr_t>(d) & 15) == 0) bulk_store(d, buf + (size_t)at * chunk, me.n * 16);
     };
     for (int row = row0; row < a.R; row += stride) {
       if (ok && lane == 0) {
@@ -614,20 +616,22 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
         const Mine me = mine_of(sp);
         if (any) {
           const uint8_t* src = reinterpret_cast<const uint8_t*>(l + sp.head) + (int64_t)me.v0 * 16;
-          for (int at = 0; at < me.n * 16; at += chunk, ++it) {
-            const int s = it & 1;
-            if (it >= 2) {
-              ok = umma::mbar_wait(&sh.done[s], ((it >> 1) - 1) & 1);
+          for (int at = 0; at < me.n * 16; at += chunk) {
+            if (lap > 0) {
+              ok = umma::mbar_wait(&sh.done[s], (lap - 1) & 1);
               if (!ok) break;
               if (kGrad) {
                 put(s);
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
               }
             }
-            held[s] = row;
+#pragma unroll
+            for (int i = 0; i < kDtStages; ++i)
+              if (i == s) held[i] = row;
             const uint32_t bytes = (uint32_t)min(chunk, me.n * 16 - at);
             umma::mbar_expect_tx(&sh.full[s], bytes);
             umma::bulk_load(buf + (size_t)s * chunk, src + at, bytes, &sh.full[s]);
+            if (++s == NS) s = 0, ++lap;
           }
         } else if (kGrad) {
           T* d = grads(row) + sp.head + (int64_t)me.v0 * VE;
@@ -638,138 +642,160 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
       }
       if (row + stride < a.R) any = ds_any(a, row + stride, lane);
     }
-    if (kGrad && ok && lane == 0)
-      for (int i = max(0, it - 2); i < it && ok; ++i) {
-        ok = umma::mbar_wait(&sh.done[i & 1], (i >> 1) & 1);
-        if (ok) put(i & 1);
+    if (kGrad && lane == 0) {
+      // the last rows' gradients, oldest first
+      for (int i = 0; i < NS && ok; ++i) {
+        const bool old = lap > 0 || s > 0 ? true : false;
+        if (!old) break;
+        if (lap == 0 && i >= s) break;                 // places that were never filled
+        const int at = lap == 0 ? i : (s + i) % NS;
+        ok = umma::mbar_wait(&sh.done[at], (lap - (at >= s ? 1 : 0)) & 1);
+        if (ok) put(at);
       }
-    if (kGrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
     if (!ok) {
       atomicExch(&sh.timeout, 1);
       // every copy issued has landed before this block may exit
-      for (int s = 0; s < 2; ++s)
-        for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[s], par, 1u << 12);
+      for (int i = 0; i < kDtStages; ++i)
+        for (int par = 0; par < 2; ++par) umma::mbar_wait(&sh.full[i], par, 1u << 12);
     }
     __syncwarp();
   } else if (warp > kLpWarps) {
-    // the lists: one warp has the even turns, the other the odd ones
-    const int slot = warp - kLpWarps - 1;
-    DsList& list = sh.list[slot];
-    int64_t row64 = row0 + (int64_t)slot * stride;
-    bool any;
-    DsIds p = ds_map(a, ds_ids(a, row64, lane), any);
-    for (int n = 0; row64 < a.R; ++n) {
-      const int row = (int)row64;
-      row64 += 2 * (int64_t)stride;
-      const T* l = logits(row);
-      const Span sp = span_of<T>(l, a.K, 0, 1);
+    // the lists: one warp has the even turns, the other the odd ones.  What a turn reads was asked for
+    // in the turn before: the ids two turns ahead, places and values one.
+    const int mod = C % 4 == 0 ? C : C % 2 == 0 ? 2 * C : 4 * C;  // turns between two uses of a sums' place
+    DsCells& cells = sh.cells[warp - kLpWarps - 1];
+    int n = warp - kLpWarps - 1;
+    int64_t row64 = row0 + (int64_t)n * stride;
+    DsEntries<H> e;
+    int id[H];
+    ds_ids<H>(a, row64, lane, id);
+    ds_map<H>(a, id, e);
+    if (kGrad || n % C == rank) ds_values<T, H>(a, row64, lane, e);
+    ds_ids<H>(a, row64 + 2 * (int64_t)stride, lane, id);
+    for (; row64 < a.R; n += 2, row64 += 2 * (int64_t)stride) {
+      const int row = (int)row64, slot = n & 3;
+      const bool mine = n % C == rank, finishes = kGrad || mine;
+      DsList& list = sh.list[slot];
+      const Span sp = span_of<T>(logits(row), a.K, 0, 1);
       const Mine me = mine_of(sp);
-      int flags = ds_places<VE>(a, p, any, sp, first, list, lane, [&](int q) {
-        const int e = q - sp.head, v = e / VE - me.v0;
-        return e < 0 || v < 0 || v >= me.n ? -1 : v * 16 + (e % VE) * (int)sizeof(T);
-      });
+      if (n >= kDtRing) wait(&sh.used[slot], (n >> 2) - 1);
+      unsigned edges = 0;  // those that are listed
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int i = lane + 32 * h, q = e.p[h];
+        if (i < a.k) {
+          const int x = q - sp.head, v = x / VE - me.v0;
+          list.pos[i] = q < 0 || x < 0 || v < 0 || v >= me.n ? -1 : v * 16 + (x % VE) * (int)sizeof(T);
+        }
+        const int t = first ? ds_edge<VE>(sp, q) : -1;
+        if (t >= 0) edges |= 1u << t;
+      }
+      if (lane == 0) list.any = e.any;
+      __syncwarp();
       if (lane == 0) {
-        if (finishes) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * (kGrad ? kDtParts : kLpWarps) * sizeof(DtPart)));
+        if (finishes) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * kDtParts * sizeof(DtPart)));
         umma::mbar_arrive(&sh.listed[slot]);
       }
-      const DsIds ahead = ds_ids(a, row64, lane);
-      bool any_ahead;
-      if (!finishes) {
-        p = ds_map(a, ahead, any_ahead);
-        wait(&sh.summed[slot], n);
-        any = any_ahead;
-        continue;
-      }
+      DsEntries<H> ahead;
+      ds_map<H>(a, id, ahead);
+      ds_ids<H>(a, row64 + 4 * (int64_t)stride, lane, id);
       // the row's edges, one per lane
       const bool edge = first && lane < 2 * VE && edge_id<VE>(sp, lane) < a.K;
-      float xe = edge && any ? Elem<T>::load(l + edge_id<VE>(sp, lane)) : -INFINITY;
-      if (any) flags |= ds_entries<T>(a, row, l, list, lane);
-      const bool un_edge = edge && !(list.edges >> lane & 1);
-      DtPart ends{-INFINITY, 0.f, 0, 0};
-      if (first && any && __any_sync(0xffffffffu, un_edge)) {
-        ends.m = warp_max_nan(un_edge ? xe : -INFINITY);
-        const float w = exp2_approx((xe - ends.m) * a.c);
-        ends.s = ends.m == -INFINITY ? 0.f : warp_add(un_edge ? w : 0.f);
+      float xe = -INFINITY;
+      DtPart ends{-INFINITY, 0.f};
+      bool un_edge = false;
+      if (first && e.any) {
+        edges = __reduce_or_sync(0xffffffffu, edges);
+        un_edge = edge && !(edges >> lane & 1);
+        if (edge) xe = Elem<T>::load(logits(row) + edge_id<VE>(sp, lane));
+        if (__any_sync(0xffffffffu, un_edge)) {
+          ends.m = warp_max_nan(un_edge ? xe : -INFINITY);
+          const float w = exp2_approx((xe - ends.m) * a.c);
+          ends.s = ends.m == -INFINITY ? 0.f : warp_add(un_edge ? w : 0.f);
+        }
       }
-      // (sent when what this warp reads of the logits has been read: when all sums are there, the
-      // gradient may take the logits' place)
-      if (kGrad && lane < C) send_part(ends, &sh.got[slot][rank * kDtParts + kLpWarps], &sh.summed[slot], lane);
-      const float g = kGrad && a.weight ? a.weight[row] : 1.f;
       DsHead hd{};
-      if (any) hd = ds_head(a, list, flags, lane);
-      p = ds_map(a, ahead, any_ahead);
-      const bool ok = wait_parts(&sh.summed[slot], n);
-      DsSum un{kGrad ? -INFINITY : ends.m, 0.f, !ok};
-      constexpr int kMost = kDtMaxC * kDtParts;
-      const int parts = C * (kGrad ? kDtParts : kLpWarps);
-      float pm[(kMost + 31) / 32], ps[(kMost + 31) / 32];
+      if (finishes && e.any) hd = ds_head<H>(a, e, ds_flags<H>(e, cells, lane));
+      // (sent when what this warp reads of the row has been read: when all sums are there, the gradient
+      // may take the logits' place)
+      if (!kGrad && n >= kDtRing) wait_blocks(&sh.ready[slot], (n >> 2) - 1);
+      if (kGrad ? lane < C : lane == 0)
+        send_part(ends, &sh.got[slot][rank * kDtParts + kLpWarps], &sh.summed[slot], kGrad ? lane : n % C);
+      if (kGrad || (n + 2) % C == rank) ds_values<T, H>(a, row64 + 2 * (int64_t)stride, lane, ahead);
+      if (finishes) {
+        const float g = kGrad && a.weight ? __ldg(a.weight + row) : 1.f;
+        const bool ok = wait_blocks(&sh.summed[slot], kGrad ? n >> 2 : n / mod);
+        DsSum un{-INFINITY, 0.f, !ok};
+        constexpr int kMost = (kDtMaxC * kDtParts + 31) / 32;
+        float pm[kMost], ps[kMost];
 #pragma unroll
-      for (int h = 0; h < (kMost + 31) / 32; ++h) {
-        const int i = lane + 32 * h;
-        DtPart v{-INFINITY, 0.f, 0, 0};
-        if (i < parts) v = sh.got[slot][i];
-        un.late |= v.late;
-        pm[h] = v.m;
-        ps[h] = v.s;
-        un.m = max_nan(un.m, v.m);
-      }
-      un.m = warp_max_nan(un.m);
-      un.late = __any_sync(0xffffffffu, un.late != 0);
-      // (m is the lowest finite value where nothing was summed; kept from -infinity minus itself)
-      const auto part = [&](float m, float s) { return s == 0.f ? 0.f : s * exp2_approx((m - un.m) * a.c); };
+        for (int h = 0; h < kMost; ++h) {
+          const int i = lane + 32 * h;
+          DtPart v{-INFINITY, 0.f};
+          if (i < C * kDtParts) v = sh.got[slot][i];
+          un.late |= v.s < 0.f;
+          pm[h] = v.m;
+          ps[h] = v.s;
+          un.m = max_nan(un.m, v.m);
+        }
+        un.m = warp_max_nan(un.m);
+        un.late = __any_sync(0xffffffffu, un.late != 0);
+        // (0 and -infinity where nothing was summed)
 #pragma unroll
-      for (int h = 0; h < (kMost + 31) / 32; ++h) un.s += part(pm[h], ps[h]);
-      un.s = warp_add(un.s);
-      if (!kGrad) un.s += part(ends.m, ends.s);
-      if (!kGrad && lane < C) arrive_block(&sh.ready[slot], lane);  // the sums' places are free
-      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-      DsTotal r{};
-      if (any) r = ds_stats(a, hd, un, st);
-      if (kGrad) {
-        if (any)
-          for (int i = lane; i < a.k; i += 32) list.val[i] = ds_listed(a, st, g, list.z[i], list.val[i]);
-        if (lane == 0) sh.st[slot] = st;
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&sh.ready[slot]);
-      }
-      if (first) {
-        const float loss = any ? ds_loss(a, hd, un, st, r, lane) : 0.f;
-        if (lane == 0) ds_put(a, row, loss, st, r.flags);
-        __syncwarp();
-      }
-      if (kGrad) {
-        // the edges' gradients
-        T* d = grads(row);
+        for (int h = 0; h < kMost; ++h) un.s += ps[h] == 0.f ? 0.f : ps[h] * exp2_approx((pm[h] - un.m) * a.c);
+        un.s = warp_add(un.s);
+        if (!kGrad && lane < C) arrive_block(&sh.ready[slot], lane);  // the sums' place is free
+        DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+        DsTotal r{};
+        if (e.any) r = ds_stats(a, hd, un, st);
         const bool nothing = ds_nothing(st);
-        if (edge && (nothing || un_edge || xe == -INFINITY))
-          Store<T>::put(d + edge_id<VE>(sp, lane),
-                        nothing ? 0.f : g * st.c_rest * exp2_approx((xe - st.mr) * a.c));
-        if (first && !nothing && list.edges)
-          for (int i = lane; i < a.k; i += 32) {
-            const int q = list.place[i];
-            if (q >= 0 && (q < sp.head || q >= sp.head + sp.nvec * VE) && list.z[i] != -INFINITY)
-              Store<T>::put(d + q, list.val[i]);
+        if (kGrad) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            e.lp[h] = e.z[h] == -INFINITY ? 0.f : ds_listed(a, st, g, e.z[h], e.lp[h]);
+            if (lane + 32 * h < a.k) list.val[lane + 32 * h] = e.lp[h];
           }
-        wait(&sh.graded[slot], n);  // the list has been used
+          if (lane == 0) sh.st[slot] = st;
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(&sh.ready[slot]);
+        }
+        if (mine) {
+          const float loss = e.any ? ds_loss(a, hd, un, st, r, lane) : 0.f;
+          if (lane == 0) ds_put(a, row, loss, st, r.flags);
+          __syncwarp();
+        }
+        if (kGrad && first) {
+          // the edges' gradients
+          T* d = grads(row);
+          if (edge && (nothing || un_edge))
+            Store<T>::put(d + edge_id<VE>(sp, lane), nothing ? 0.f : g * st.c_rest * exp2_approx((xe - st.mr) * a.c));
+          if (!nothing)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              if (ds_edge<VE>(sp, e.p[h]) >= 0) Store<T>::put(d + e.p[h], e.lp[h]);
+        }
       }
-      any = any_ahead;
+      e = ahead;
     }
   } else {
-    int it = 0, n = 0;  // chunks and rows consumed
-    for (int row = row0; row < a.R; row += stride, ++n) {
-      const int slot = n & 1;
+    int in_at = 0, in_lap = 0, out_at = 0;  // chunks' places
+    // sums row n and sends the sum
+    const auto sum_row = [&](int row, int n) {
+      const int slot = n & 3;
       const DsList& list = sh.list[slot];
       const Span sp = span_of<T>(logits(row), a.K, 0, 1);
       const Mine me = mine_of(sp);
-      wait(&sh.listed[slot], n >> 1);
-      const bool any = list.any;
+      wait(&sh.listed[slot], n >> 2);
       RowSum sum{kNegBig, 0.f, 0.f};
-      if (any)
+      if (list.any)
         for (int at = 0; at < me.n * 16; at += chunk) {
-          const int s = it & 1, have = min(chunk, me.n * 16 - at) / 16;
+          const int s = in_at, have = min(chunk, me.n * 16 - at) / 16;
           uint8_t* const b = buf + (size_t)s * chunk;
           const uint4* in = reinterpret_cast<const uint4*>(b);
-          wait(&sh.full[s], it >> 1);
+          wait(&sh.full[s], in_lap);
+          if (++in_at == NS) in_at = 0, ++in_lap;
           ds_each(list, at, chunk, a.k, warp, lane, [&](int, int q) {
             *reinterpret_cast<decltype(Mask<T>::bits())*>(b + q) = Mask<T>::bits();
             // ahead of the next copy into this place
@@ -789,50 +815,64 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, i
           if (!kGrad) {
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&sh.done[s]);
-            ++it;
           }
         }
-      // (a row that is not read is exchanged too: no block gets two turns ahead of another)
+      // (a row that is not read is exchanged too, so that no block gets ahead of another: a place for
+      // sums is taken again after four turns, when all blocks have read it)
       const RowSum w = warp_join(sum, a.c);
-      const DtPart part{w.m, w.s, *reinterpret_cast<volatile int*>(&sh.timeout), 0};
-      if (!kGrad && n >= 2) wait(&sh.ready[slot], (n >> 1) - 1);
-      if (lane < (kGrad ? C : 1))
-        send_part(part, &sh.got[slot][rank * (kGrad ? kDtParts : kLpWarps) + warp], &sh.summed[slot], lane);
-      if (!finishes) {
+      if (!kGrad && n >= kDtRing) wait_blocks(&sh.ready[slot], (n >> 2) - 1);
+      const DtPart part{w.m, *reinterpret_cast<volatile int*>(&sh.timeout) ? -1.f : w.s};
+      if (kGrad ? lane < C : lane == 0)
+        send_part(part, &sh.got[slot][rank * kDtParts + warp], &sh.summed[slot], kGrad ? lane : n % C);
+      if (!kGrad) {
         __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&sh.summed[slot]);
+        if (lane == 0) umma::mbar_arrive(&sh.used[slot]);
       }
-      if (kGrad) {
-        T* const out = grads(row) + sp.head + (int64_t)me.v0 * VE;
-        const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        const float g = a.weight ? __ldg(a.weight + row) : 1.f;
-        wait(&sh.ready[slot], n >> 1);
-        if (any && me.n > 0) {
-          const int s = it & 1;
-          uint8_t* const b = buf + (size_t)s * chunk;
-          uint4* const in = reinterpret_cast<uint4*>(b);
-          const DsStats st = sh.st[slot];
-          const bool nothing = ds_nothing(st);
-          const float factor = g * st.c_rest;
+    };
+    // the gradient of row n
+    const auto grad_row = [&](int row, int n) {
+      const int slot = n & 3;
+      const DsList& list = sh.list[slot];
+      const Span sp = span_of<T>(logits(row), a.K, 0, 1);
+      const Mine me = mine_of(sp);
+      T* const out = grads(row) + sp.head + (int64_t)me.v0 * VE;
+      const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+      const float g = a.weight ? __ldg(a.weight + row) : 1.f;
+      wait(&sh.ready[slot], n >> 2);
+      if (list.any && me.n > 0) {
+        const int s = out_at;
+        if (++out_at == NS) out_at = 0;
+        uint8_t* const b = buf + (size_t)s * chunk;
+        uint4* const in = reinterpret_cast<uint4*>(b);
+        const DsStats st = sh.st[slot];
+        const bool nothing = ds_nothing(st);
+        const float factor = g * st.c_rest;
 #pragma unroll 4
-          for (int q = tid; q < me.n; q += kLpNT)
-            in[q] = nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(in[q], st.mr, a.c, factor);
-          __syncwarp();
-          if (!nothing)
-            ds_each(list, 0, chunk, a.k, warp, lane, [&](int i, int q) {
-              if (list.z[i] != -INFINITY) Store<T>::put(reinterpret_cast<T*>(b + q), list.val[i]);
-            });
-          if (!aligned)
-            for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, in[q], false);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) umma::mbar_arrive(&sh.done[s]);
-          ++it;
-        } else if (!any && !aligned) {
-          for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, make_uint4(0, 0, 0, 0), false);
-        }
+        for (int q = tid; q < me.n; q += kLpNT)
+          in[q] = nothing ? make_uint4(0, 0, 0, 0) : Store<T>::grad(in[q], st.mr, a.c, factor);
         __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&sh.graded[slot]);
+        if (!nothing)
+          ds_each(list, 0, chunk, a.k, warp, lane,
+                  [&](int i, int q) { Store<T>::put(reinterpret_cast<T*>(b + q), list.val[i]); });
+        if (!aligned)
+          for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, in[q], false);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sh.done[s]);
+      } else if (!list.any && !aligned) {
+        for (int q = tid; q < me.n; q += kLpNT) store_vec(out + (int64_t)q * VE, make_uint4(0, 0, 0, 0), false);
+      }
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&sh.used[slot]);
+    };
+    if (kGrad) sum_row(row0, 0);
+    int n = 0;
+    for (int row = row0; row < a.R; row += stride, ++n) {
+      if (!kGrad) {
+        sum_row(row, n);
+      } else {
+        if (row + stride < a.R) sum_row(row + stride, n + 1);
+        grad_row(row, n);
       }
     }
   }
@@ -901,48 +941,54 @@ int ds_launch_grad(const DsArgs& a, int32_t dtype, cudaStream_t s) {
   return VT_OK;
 }
 
-// How a row is spread: C blocks with `share` vectors each, in chunks; two chunks of kDtPart[tier]
-// bytes leave room for 3 - tier blocks on an SM, which work while one waits for its cluster.
+// How a row is spread: C blocks with `share` vectors each, in chunks; kDtBytes[tier] bytes of them
+// leave room for 3 - tier blocks on an SM, which work while one waits for its cluster.
 struct DtPlan {
-  int C, share, chunk, tier;
+  int C, tier;
+  DtSplit split;
 };
-constexpr int kDtPart[3] = {32 << 10, 50 << 10, 100 << 10};
+constexpr int kDtBytes[3] = {64 << 10, 100 << 10, 200 << 10};
 
 // few rows: more blocks to each
 void dt_spread(int64_t R, int64_t bytes, DtPlan& p) {
   const int slots = num_sms() * (3 - p.tier);
   while (p.C < kDtMaxC && R * p.C * 2 <= slots && bytes / p.C > (4 << 10)) p.C = std::min(p.C * 2, kDtMaxC);
-  p.share = std::max(1, (int)((bytes / 16 + p.C - 1) / p.C));
+  p.split.share = std::max(1, (int)((bytes / 16 + p.C - 1) / p.C));
 }
-// with the gradient a part is one chunk
+// with the gradient a part is one chunk, and three of them are in work
 bool dt_plan_grad(int64_t R, int64_t bytes, DtPlan& p) {
-  for (p.tier = 0; p.tier < 3; ++p.tier) {
-    const int64_t C = std::max<int64_t>(1, (bytes + kDtPart[p.tier] - 1) / kDtPart[p.tier]);
-    if (C > kDtMaxC) continue;
-    p.C = (int)C;
-    dt_spread(R, bytes, p);
-    p.chunk = p.share * 16;
-    return true;
-  }
+  for (int stages = 3; stages >= 2; --stages)
+    for (p.tier = 0; p.tier < 3; ++p.tier) {
+      const int64_t part = kDtBytes[p.tier] / stages / 16 * 16;
+      const int64_t C = std::max<int64_t>(1, (bytes + part - 1) / part);
+      if (C > kDtMaxC) continue;
+      p.C = (int)C;
+      dt_spread(R, bytes, p);
+      p.split.chunk = p.split.share * 16;
+      p.split.stages = stages;
+      return true;
+    }
   return false;
 }
 DtPlan dt_plan_loss(int64_t R, int64_t bytes) {
   DtPlan p;
   p.tier = 0;
-  p.C = (int)std::max<int64_t>(1, std::min<int64_t>((bytes + kDtPart[0] - 1) / kDtPart[0], kDtMaxC));
+  p.split.stages = 2;
+  const int64_t part = kDtBytes[0] / p.split.stages;
+  p.C = (int)std::max<int64_t>(1, std::min<int64_t>((bytes + part - 1) / part, kDtMaxC));
   dt_spread(R, bytes, p);
-  const int chunks = (p.share * 16 + kDtPart[0] - 1) / kDtPart[0];
-  p.chunk = (p.share + chunks - 1) / chunks * 16;  // evenly
+  const int64_t chunks = (p.split.share * 16 + part - 1) / part;
+  p.split.chunk = (int)((p.split.share + chunks - 1) / chunks) * 16;  // evenly
   return p;
 }
 
-template <typename T, bool kGrad>
+template <typename T, bool kGrad, int H>
 int ds_launch_rows(const DsArgs& a, cudaStream_t s, const DtPlan& p) {
-  auto kern = distill_rows_kernel<T, kGrad>;
-  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kDtPart[2]));
+  auto kern = distill_rows_kernel<T, kGrad, H>;
+  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtBytes[2]));
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kDtThreads);
-  cfg.dynamicSmemBytes = (size_t)2 * kDtPart[p.tier];
+  cfg.dynamicSmemBytes = (size_t)kDtBytes[p.tier];
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -970,13 +1016,20 @@ int ds_launch_rows(const DsArgs& a, cudaStream_t s, const DtPlan& p) {
   }
   cfg.gridDim = dim3((unsigned)(std::min(a.R, clusters) * p.C));
   cfg.numAttrs = a.own_status ? 1 : 2;
-  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a, p.share, p.chunk));
+  VT_RETURN_IF_CUDA(cudaLaunchKernelEx(&cfg, kern, a, p.split));
   return VT_OK;
+}
+template <bool kGrad>
+int ds_launch_rows(const DsArgs& a, int32_t dtype, cudaStream_t s, const DtPlan& p) {
+  if (a.k <= 32)
+    return dtype == VT_F32 ? ds_launch_rows<float, kGrad, 1>(a, s, p) : ds_launch_rows<uint16_t, kGrad, 1>(a, s, p);
+  return dtype == VT_F32 ? ds_launch_rows<float, kGrad, kDsMaxK / 32>(a, s, p)
+                         : ds_launch_rows<uint16_t, kGrad, kDsMaxK / 32>(a, s, p);
 }
 
 int ds_launch_loss(const DsArgs& a, int32_t dtype, cudaStream_t s) {
   const DtPlan p = dt_plan_loss(a.R, (int64_t)a.K * (dtype == VT_F32 ? 4 : 2));
-  return dtype == VT_F32 ? ds_launch_rows<float, false>(a, s, p) : ds_launch_rows<uint16_t, false>(a, s, p);
+  return ds_launch_rows<false>(a, dtype, s, p);
 }
 
 // Rows that the blocks of a cluster hold between them are read once; longer ones take the two calls.
@@ -986,7 +1039,7 @@ int ds_launch_both(const DsArgs& a, int32_t dtype, cudaStream_t s) {
     const int rc = ds_launch_loss(a, dtype, s);
     return rc != VT_OK ? rc : ds_launch_grad(a, dtype, s);
   }
-  return dtype == VT_F32 ? ds_launch_rows<float, true>(a, s, p) : ds_launch_rows<uint16_t, true>(a, s, p);
+  return ds_launch_rows<true>(a, dtype, s, p);
 }
 
 }  // namespace
