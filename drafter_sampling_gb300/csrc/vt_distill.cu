@@ -222,7 +222,7 @@ __device__ __forceinline__ Pair ds_below(float z, float m, Pair inv_t) {
   return pair_mul(d, inv_t);
 }
 
-// (leaves t in lp)
+// (leaves the entries' weights 2^((z - m) c) in z and t in lp; both 0 where not kept)
 template <int H>
 __device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsEntries<H>& e, int flags) {
   DsHead r;
@@ -236,12 +236,16 @@ __device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsEntries<H>& e, int 
   r.mass = r.cross = Pair{0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    if (e.z[h] == -INFINITY) continue;
-    r.S += exp2_approx((e.z[h] - m) * a.c);
-    const Pair lnt{e.lp[h], 0.f}, t = pair_exp(lnt);
+    const bool kept = e.z[h] != -INFINITY;
+    const float z = kept ? e.z[h] : m;
+    const Pair lnt{kept ? e.lp[h] : -INFINITY, 0.f}, t = pair_exp(lnt);
+    const Pair d = pair_add(Pair{t.h > 0.f ? lnt.h : 0.f, 0.f}, pair_neg(ds_below(z, m, a.inv_t)));
+    const Pair x = pair_mul(t, d);
     r.mass = pair_add(r.mass, t);
-    if (t.h > 0.f) r.cross = pair_add(r.cross, pair_mul(t, pair_add(lnt, pair_neg(ds_below(e.z[h], m, a.inv_t)))));
+    r.cross = pair_add(r.cross, t.h > 0.f ? x : Pair{0.f, 0.f});
     e.lp[h] = t.h;
+    e.z[h] = kept ? exp2_approx((z - m) * a.c) : 0.f;
+    r.S += e.z[h];
   }
   r.S = warp_add(r.S);
 #pragma unroll
@@ -662,69 +666,89 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
     }
     __syncwarp();
   } else if (warp > kLpWarps) {
-    // the lists: one warp has the even turns, the other the odd ones.  What a turn reads was asked for
-    // in the turn before: the ids two turns ahead, places and values one.
+    // the lists: one warp has the even turns, the other the odd ones.  A row's statistics are what the
+    // consuming warps wait for, so all else of a turn is done ahead: at row n's turn its own list has
+    // been taken in, row n + 2's places go to the consuming warps and its values arrive, row n + 4's ids.
     const int mod = C % 4 == 0 ? C : C % 2 == 0 ? 2 * C : 4 * C;  // turns between two uses of a sums' place
     DsCells& cells = sh.cells[warp - kLpWarps - 1];
+    const int64_t step = 2 * (int64_t)stride;
     int n = warp - kLpWarps - 1;
     int64_t row64 = row0 + (int64_t)n * stride;
-    DsEntries<H> e;
-    int id[H];
-    ds_ids<H>(a, row64, lane, id);
-    ds_map<H>(a, id, e);
-    if (kGrad || n % C == rank) ds_values<T, H>(a, row64, lane, e);
-    ds_ids<H>(a, row64 + 2 * (int64_t)stride, lane, id);
-    for (; row64 < a.R; n += 2, row64 += 2 * (int64_t)stride) {
-      const int row = (int)row64, slot = n & 3;
-      const bool mine = n % C == rank, finishes = kGrad || mine;
-      DsList& list = sh.list[slot];
-      const Span sp = span_of<T>(logits(row), a.K, 0, 1);
+    const auto finishes = [&](int n) { return kGrad || n % C == rank; };
+    // row n's places to the consuming warps
+    const auto publish = [&](const DsEntries<H>& e, int64_t row, int n) {
+      if (row >= a.R) return;
+      DsList& list = sh.list[n & 3];
+      const Span sp = span_of<T>(logits((int)row), a.K, 0, 1);
       const Mine me = mine_of(sp);
-      if (n >= kDtRing) wait(&sh.used[slot], (n >> 2) - 1);
-      unsigned edges = 0;  // those that are listed
+      if (n >= kDtRing) wait(&sh.used[n & 3], (n >> 2) - 1);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        const int i = lane + 32 * h, q = e.p[h];
-        if (i < a.k) {
-          const int x = q - sp.head, v = x / VE - me.v0;
-          list.pos[i] = q < 0 || x < 0 || v < 0 || v >= me.n ? -1 : v * 16 + (x % VE) * (int)sizeof(T);
-        }
-        const int t = first ? ds_edge<VE>(sp, q) : -1;
-        if (t >= 0) edges |= 1u << t;
+        const int i = lane + 32 * h, x = e.p[h] - sp.head, v = x / VE - me.v0;
+        if (i < a.k)
+          list.pos[i] = e.p[h] < 0 || x < 0 || v < 0 || v >= me.n ? -1 : v * 16 + (x % VE) * (int)sizeof(T);
       }
       if (lane == 0) list.any = e.any;
       __syncwarp();
-      if (lane == 0) {
-        if (finishes) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * kDtParts * sizeof(DtPart)));
-        umma::mbar_arrive(&sh.listed[slot]);
-      }
-      DsEntries<H> ahead;
-      ds_map<H>(a, id, ahead);
-      ds_ids<H>(a, row64 + 4 * (int64_t)stride, lane, id);
-      // the row's edges, one per lane
-      const bool edge = first && lane < 2 * VE && edge_id<VE>(sp, lane) < a.K;
-      float xe = -INFINITY;
+      if (lane == 0) umma::mbar_arrive(&sh.listed[n & 3]);
+    };
+    // what row n's list says, and the row's edges, one per lane: their sum goes to where the others
+    // go.  (When all sums are there this warp has read what it reads of the row, and the gradient may
+    // take the logits' place.)
+    struct Edges {
+      float x;      // -infinity: none
+      bool here, unlisted;
+    };
+    const auto take_in = [&](DsEntries<H>& e, int64_t row, int n, Edges& edge) {
+      DsHead hd{};
+      if (row >= a.R) return hd;
       DtPart ends{-INFINITY, 0.f};
-      bool un_edge = false;
-      if (first && e.any) {
-        edges = __reduce_or_sync(0xffffffffu, edges);
-        un_edge = edge && !(edges >> lane & 1);
-        if (edge) xe = Elem<T>::load(logits(row) + edge_id<VE>(sp, lane));
-        if (__any_sync(0xffffffffu, un_edge)) {
-          ends.m = warp_max_nan(un_edge ? xe : -INFINITY);
-          const float w = exp2_approx((xe - ends.m) * a.c);
-          ends.s = ends.m == -INFINITY ? 0.f : warp_add(un_edge ? w : 0.f);
+      edge = Edges{-INFINITY, false, false};
+      if (first) {
+        const T* l = logits((int)row);
+        const Span sp = span_of<T>(l, a.K, 0, 1);
+        edge.here = lane < 2 * VE && edge_id<VE>(sp, lane) < a.K;
+        if (e.any && __any_sync(0xffffffffu, edge.here)) {
+          unsigned listed = 0;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const int t = ds_edge<VE>(sp, e.p[h]);
+            if (t >= 0) listed |= 1u << t;
+          }
+          listed = __reduce_or_sync(0xffffffffu, listed);
+          edge.unlisted = edge.here && !(listed >> lane & 1);
+          if (edge.unlisted) edge.x = Elem<T>::load(l + edge_id<VE>(sp, lane));
+          ends.m = warp_max_nan(edge.x);
+          const float w = exp2_approx((edge.x - ends.m) * a.c);
+          ends.s = ends.m == -INFINITY ? 0.f : warp_add(w);
         }
       }
-      DsHead hd{};
-      if (finishes && e.any) hd = ds_head<H>(a, e, ds_flags<H>(e, cells, lane));
-      // (sent when what this warp reads of the row has been read: when all sums are there, the gradient
-      // may take the logits' place)
+      const int slot = n & 3;
+      if (finishes(n)) {
+        if (lane == 0) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * kDtParts * sizeof(DtPart)));
+        if (e.any) hd = ds_head<H>(a, e, ds_flags<H>(e, cells, lane));
+      }
       if (!kGrad && n >= kDtRing) wait_blocks(&sh.ready[slot], (n >> 2) - 1);
       if (kGrad ? lane < C : lane == 0)
         send_part(ends, &sh.got[slot][rank * kDtParts + kLpWarps], &sh.summed[slot], kGrad ? lane : n % C);
-      if (kGrad || (n + 2) % C == rank) ds_values<T, H>(a, row64 + 2 * (int64_t)stride, lane, ahead);
-      if (finishes) {
+      return hd;
+    };
+    DsEntries<H> e, next;
+    int id[H], id2[H];
+    ds_ids<H>(a, row64, lane, id);
+    ds_ids<H>(a, row64 + step, lane, id2);
+    ds_map<H>(a, id, e);
+    if (finishes(n)) ds_values<T, H>(a, row64, lane, e);
+    publish(e, row64, n);
+    ds_map<H>(a, id2, next);
+    ds_ids<H>(a, row64 + 2 * step, lane, id);
+    Edges edge;
+    DsHead hd = take_in(e, row64, n, edge);
+    for (; row64 < a.R; n += 2, row64 += step) {
+      const int row = (int)row64, slot = n & 3;
+      if (finishes(n + 2)) ds_values<T, H>(a, row64 + step, lane, next);
+      publish(next, row64 + step, n + 2);
+      if (finishes(n)) {
         const float g = kGrad && a.weight ? __ldg(a.weight + row) : 1.f;
         const bool ok = wait_blocks(&sh.summed[slot], kGrad ? n >> 2 : n / mod);
         DsSum un{-INFINITY, 0.f, !ok};
@@ -750,18 +774,18 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
         DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
         DsTotal r{};
         if (e.any) r = ds_stats(a, hd, un, st);
-        const bool nothing = ds_nothing(st);
         if (kGrad) {
+          const float all = g * st.c_all * (r.learns ? exp2_approx((hd.m - st.m) * a.c) : 1.f), ct = g * st.c_t;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
-            e.lp[h] = e.z[h] == -INFINITY ? 0.f : ds_listed(a, st, g, e.z[h], e.lp[h]);
-            if (lane + 32 * h < a.k) list.val[lane + 32 * h] = e.lp[h];
+            e.lp[h] = all * e.z[h] - ct * e.lp[h];
+            if (lane + 32 * h < a.k) sh.list[slot].val[lane + 32 * h] = e.lp[h];
           }
           if (lane == 0) sh.st[slot] = st;
           __syncwarp();
           if (lane == 0) umma::mbar_arrive(&sh.ready[slot]);
         }
-        if (mine) {
+        if (n % C == rank) {
           const float loss = e.any ? ds_loss(a, hd, un, st, r, lane) : 0.f;
           if (lane == 0) ds_put(a, row, loss, st, r.flags);
           __syncwarp();
@@ -769,15 +793,21 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
         if (kGrad && first) {
           // the edges' gradients
           T* d = grads(row);
-          if (edge && (nothing || un_edge))
-            Store<T>::put(d + edge_id<VE>(sp, lane), nothing ? 0.f : g * st.c_rest * exp2_approx((xe - st.mr) * a.c));
+          const Span sp = span_of<T>(logits(row), a.K, 0, 1);
+          const bool nothing = ds_nothing(st);
+          if (edge.here && (nothing || edge.unlisted))
+            Store<T>::put(d + edge_id<VE>(sp, lane),
+                          nothing ? 0.f : g * st.c_rest * exp2_approx((edge.x - st.mr) * a.c));
           if (!nothing)
 #pragma unroll
             for (int h = 0; h < H; ++h)
               if (ds_edge<VE>(sp, e.p[h]) >= 0) Store<T>::put(d + e.p[h], e.lp[h]);
         }
       }
-      e = ahead;
+      e = next;
+      ds_map<H>(a, id, next);
+      ds_ids<H>(a, row64 + 3 * step, lane, id);
+      hd = take_in(e, row64 + step, n + 2, edge);
     }
   } else {
     int in_at = 0, in_lap = 0, out_at = 0;  // chunks' places

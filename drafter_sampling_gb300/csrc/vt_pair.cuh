@@ -62,14 +62,13 @@ __device__ __forceinline__ Pair pair_exp(Pair x) {
   two_sum(s, 0.5f * q, s, e2);
   const float lo = e1 + e2 + fmaf(0.5f, ql, fmaf(p, q * r, fmaf(rl, r, rl)));
   Pair y = pair_of(s, lo);
-  if (!(x.h >= -87.f)) {
-    const float v = x.h != x.h ? x.h : 0.f;
-    return Pair{v, 0.f};
-  }
-  if (x.h > 88.f) return Pair{INFINITY, 0.f};
-  const float f = __int_as_float(((int)n + 127) << 23);
+  const float f = __int_as_float((max(-126, min(127, (int)n)) + 127) << 23);
   y.h *= f;
   y.l *= f;
+  // (selections, so that several of these overlap)
+  const bool in = x.h >= -87.f && x.h <= 88.f;
+  y.h = in ? y.h : x.h > 88.f ? INFINITY : x.h < -87.f ? 0.f : x.h;
+  y.l = in ? y.l : 0.f;
   return y;
 }
 
