@@ -95,12 +95,28 @@ struct DsEntries {
   float z[H], lp[H];  // of kept entries; z = -infinity: not kept
   bool any;           // an id is given
 };
+// (loads that stay where they are issued: a turn ahead of their use)
+__device__ __forceinline__ uint32_t load_ahead(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ float value_ahead(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(load_ahead(p));
+  } else {
+    uint16_t v;
+    asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    return bf16_bits_to_float(v);
+  }
+}
 template <int H>
 __device__ __forceinline__ void ds_ids(const DsArgs& a, int64_t row, int lane, int (&id)[H]) {
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int i = lane + 32 * h;
-    id[h] = row < a.R && i < a.k ? __ldg(a.ids + row * a.k + i) : -1;
+    id[h] = row < a.R && i < a.k ? (int)load_ahead(a.ids + row * a.k + i) : -1;
   }
 }
 template <int H>
@@ -112,7 +128,7 @@ __device__ __forceinline__ void ds_map(const DsArgs& a, const int (&id)[H], DsEn
     e.any |= p != -1;
     if (p != -1 && (p < 0 || p >= a.V)) p = -2;
     if (p >= 0 && a.inv_map) {
-      const int q = __ldg(a.inv_map + p);
+      const int q = (int)load_ahead(a.inv_map + p);
       p = q >= -1 && q < a.K ? q : -2;
     }
     e.p[h] = p;
@@ -124,8 +140,8 @@ __device__ __forceinline__ void ds_values(const DsArgs& a, int64_t row, int lane
   const T* l = static_cast<const T*>(a.logits) + row * a.ld;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    e.z[h] = e.p[h] >= 0 ? Elem<T>::load(l + e.p[h]) : -INFINITY;
-    e.lp[h] = e.p[h] >= 0 ? __ldg(a.logp + row * a.k + lane + 32 * h) : 0.f;
+    e.z[h] = e.p[h] >= 0 ? value_ahead(l + e.p[h]) : -INFINITY;
+    e.lp[h] = e.p[h] >= 0 ? __uint_as_float(load_ahead(a.logp + row * a.k + lane + 32 * h)) : 0.f;
   }
 }
 // whether a row has an id listed; all lanes of a warp call it
@@ -469,9 +485,9 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
 constexpr int kDtThreads = kLpNT + 96;  // consuming warps, one that copies, two for the lists
 constexpr int kDtMaxC = 8;
 constexpr int kDtParts = kLpWarps + 1;  // sums that a block sends: its consuming warps', its edges'
-constexpr int kDtZero = 1024;
+constexpr int kDtZero = 2048;
 constexpr int kDtRing = 4;              // rows whose lists and sums are in hand
-constexpr int kDtStages = 3;
+constexpr int kDtStages = 4;
 
 // a sum on its way between blocks; s = -1: a wait has run out
 struct alignas(8) DtPart {
@@ -521,12 +537,18 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(umma::smem_u32(src)),
                "r"(bytes)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 struct DtSplit {
   int share, chunk, stages;  // vectors of a row in each block, bytes of a chunk, chunks in shared memory
 };
+
+// The row that a cluster has in turn n, of `stride` clusters: another place among that turn's rows each
+// time, so that rows that take longer in a regular pattern (first positions of sequences) are shared out.
+__device__ __forceinline__ int64_t dt_row(int cluster, int n, int stride) {
+  return (int64_t)n * stride + (cluster + ((uint32_t)n * 0x9E3779B1u >> 16)) % (uint32_t)stride;
+}
 
 // A row per cluster and turn.  Each block has `share` of its vectors, in chunks: one warp
 // copies them, eight sum the unlisted ids and send their sums to the blocks that need them, and
@@ -537,14 +559,16 @@ struct DtSplit {
 // gradient in the logits' place, and the copying warp takes it out.  Every block finishes every row
 // for itself.  Without the gradient the blocks finish rows in turn.
 template <typename T, bool kGrad, int H>
-__global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, DtSplit split) {
+__global__ void __launch_bounds__(kDtThreads, H == 1 ? 3 : 2) distill_rows_kernel(DsArgs a, DtSplit split) {
   constexpr int VE = Elem<T>::kVec;
   extern __shared__ __align__(16) uint8_t buf[];
   __shared__ DtShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row0 = blockIdx.x / C, stride = gridDim.x / C;
+  const int cluster = blockIdx.x / C, stride = gridDim.x / C;
+  const auto row_of = [&](int n) { return dt_row(cluster, n, stride); };
+  const int turns = a.R / stride + (row_of(a.R / stride) < a.R ? 1 : 0);
   const int chunk = split.chunk, NS = split.stages;
   const bool first = rank == 0;  // has the rows' edges
   uint32_t limit = umma::kWaitLimit;
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
 
   if (warp == kLpWarps) {
     // copies, as far ahead of the consumers as there are chunks
-    bool ok = true, any = ds_any(a, row0, lane);
+    bool ok = true, any = turns > 0 && ds_any(a, (int)row_of(0), lane);
     int s = 0, lap = 0;          // the next chunk's place, and how often that has been gone round
     int held[kDtStages];         // the rows whose gradients the chunks will hold
 #pragma unroll
@@ -612,9 +636,11 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
       const Mine me = mine_of(sp);
       T* d = grads(row) + sp.head + (int64_t)me.v0 * VE;
       if ((reinterpret_cast<uintptr_t>(d) & 15) == 0) bulk_store(d, buf + (size_t)at * chunk, me.n * 16);
+      bulk_commit();
     };
-    for (int row = row0; row < a.R; row += stride) {
+    for (int n = 0; n < turns; ++n) {
       if (ok && lane == 0) {
+        const int row = (int)row_of(n);
         const T* l = logits(row);
         const Span sp = span_of<T>(l, a.K, 0, 1);
         const Mine me = mine_of(sp);
@@ -642,9 +668,10 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
           if ((reinterpret_cast<uintptr_t>(d) & 15) == 0)
             for (int at = 0; at < me.n * 16; at += kDtZero)
               bulk_store(reinterpret_cast<uint8_t*>(d) + at, sh.zero, min(kDtZero, me.n * 16 - at));
+          bulk_commit();
         }
       }
-      if (row + stride < a.R) any = ds_any(a, row + stride, lane);
+      if (n + 1 < turns) any = ds_any(a, (int)row_of(n + 1), lane);
     }
     if (kGrad && lane == 0) {
       // the last rows' gradients, oldest first
@@ -671,9 +698,8 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
     // been taken in, row n + 2's places go to the consuming warps and its values arrive, row n + 4's ids.
     const int mod = C % 4 == 0 ? C : C % 2 == 0 ? 2 * C : 4 * C;  // turns between two uses of a sums' place
     DsCells& cells = sh.cells[warp - kLpWarps - 1];
-    const int64_t step = 2 * (int64_t)stride;
     int n = warp - kLpWarps - 1;
-    int64_t row64 = row0 + (int64_t)n * stride;
+    const auto row_at = [&](int n) { return n < turns ? row_of(n) : (int64_t)a.R; };  // (R: none)
     const auto finishes = [&](int n) { return kGrad || n % C == rank; };
     // row n's places to the consuming warps
     const auto publish = [&](const DsEntries<H>& e, int64_t row, int n) {
@@ -735,19 +761,20 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
     };
     DsEntries<H> e, next;
     int id[H], id2[H];
-    ds_ids<H>(a, row64, lane, id);
-    ds_ids<H>(a, row64 + step, lane, id2);
+    ds_ids<H>(a, row_at(n), lane, id);
+    ds_ids<H>(a, row_at(n + 2), lane, id2);
     ds_map<H>(a, id, e);
-    if (finishes(n)) ds_values<T, H>(a, row64, lane, e);
-    publish(e, row64, n);
+    if (finishes(n)) ds_values<T, H>(a, row_at(n), lane, e);
+    publish(e, row_at(n), n);
     ds_map<H>(a, id2, next);
-    ds_ids<H>(a, row64 + 2 * step, lane, id);
+    ds_ids<H>(a, row_at(n + 4), lane, id);
     Edges edge;
-    DsHead hd = take_in(e, row64, n, edge);
-    for (; row64 < a.R; n += 2, row64 += step) {
-      const int row = (int)row64, slot = n & 3;
-      if (finishes(n + 2)) ds_values<T, H>(a, row64 + step, lane, next);
-      publish(next, row64 + step, n + 2);
+    DsHead hd = take_in(e, row_at(n), n, edge);
+    for (; n < turns; n += 2) {
+      const int row = (int)row_of(n), slot = n & 3;
+      const int64_t after = row_at(n + 2);
+      if (finishes(n + 2)) ds_values<T, H>(a, after, lane, next);
+      publish(next, after, n + 2);
       if (finishes(n)) {
         const float g = kGrad && a.weight ? __ldg(a.weight + row) : 1.f;
         const bool ok = wait_blocks(&sh.summed[slot], kGrad ? n >> 2 : n / mod);
@@ -806,8 +833,8 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
       }
       e = next;
       ds_map<H>(a, id, next);
-      ds_ids<H>(a, row64 + 3 * step, lane, id);
-      hd = take_in(e, row64 + step, n + 2, edge);
+      ds_ids<H>(a, row_at(n + 6), lane, id);
+      hd = take_in(e, after, n + 2, edge);
     }
   } else {
     int in_at = 0, in_lap = 0, out_at = 0;  // chunks' places
@@ -895,14 +922,13 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_rows_kernel(DsArgs a, D
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(&sh.used[slot]);
     };
-    if (kGrad) sum_row(row0, 0);
-    int n = 0;
-    for (int row = row0; row < a.R; row += stride, ++n) {
+    if (kGrad && turns > 0) sum_row((int)row_of(0), 0);
+    for (int n = 0; n < turns; ++n) {
       if (!kGrad) {
-        sum_row(row, n);
+        sum_row((int)row_of(n), n);
       } else {
-        if (row + stride < a.R) sum_row(row + stride, n + 1);
-        grad_row(row, n);
+        if (n + 1 < turns) sum_row((int)row_of(n + 1), n + 1);
+        grad_row((int)row_of(n), n);
       }
     }
   }
