@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kLpNT + 32, kLpPerSm) beam_rows_kernel(BsArgs 
                           : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
         pm = Vec<T>::top(v);
         if (!(pm <= st.m)) sum_rescale(st, max_nan(st.m, pm), a.c);
-        sum_add<T>(st, v, a.c);
+        sum_add<T, kLpU>(st, v, a.c);
       }
       top.renew(st.s > 0.f ? st.m : -INFINITY, i, sp.mine, sh.top.group, N, tid);
       top.scan<T>(pm, st4, q0, sp, N, lane);

@@ -92,10 +92,11 @@ template <> struct Vec<float> {
     return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                    max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
-  __device__ static float top(const uint4 (&v)[kLpU]) {
+  template <int U>
+  __device__ static float top(const uint4 (&v)[U]) {
     float m = top(v[0]);
 #pragma unroll
-    for (int u = 1; u < kLpU; ++u) m = max_nan(m, top(v[u]));
+    for (int u = 1; u < U; ++u) m = max_nan(m, top(v[u]));
     return m;
   }
   // elements e, e + 1 of a vector, plus s
@@ -116,10 +117,11 @@ template <> struct Vec<uint16_t> {
     const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
-  __device__ static float top(const uint4 (&v)[kLpU]) {
+  template <int U>
+  __device__ static float top(const uint4 (&v)[U]) {
     uint32_t m = max2(max2(v[0].x, v[0].y), max2(v[0].z, v[0].w));
 #pragma unroll
-    for (int u = 1; u < kLpU; ++u)
+    for (int u = 1; u < U; ++u)
       m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
@@ -359,12 +361,12 @@ __device__ __forceinline__ RowSum sum_lanes(RowSum a, int n, float c) {
   return a;
 }
 // adds a chunk's vectors, none of which is above a.m
-template <typename T>
-__device__ __forceinline__ void sum_add(RowSum& a, const uint4 (&v)[kLpU], float c) {
+template <typename T, int U>
+__device__ __forceinline__ void sum_add(RowSum& a, const uint4 (&v)[U], float c) {
   const f32x2 c2 = pack2(c, c);
-  f32x2 sum[kLpU];
+  f32x2 sum[U];
 #pragma unroll
-  for (int u = 0; u < kLpU; ++u)
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < Elem<T>::kVec; e += 2) {
       float t0, t1;
@@ -373,7 +375,7 @@ __device__ __forceinline__ void sum_add(RowSum& a, const uint4 (&v)[kLpU], float
       sum[u] = e == 0 ? w : add2(sum[u], w);
     }
 #pragma unroll
-  for (int h = kLpU / 2; h > 0; h >>= 1)
+  for (int h = U / 2; h > 0; h >>= 1)
 #pragma unroll
     for (int u = 0; u < h; ++u) sum[u] = add2(sum[u], sum[u + h]);
   float s0, s1, er;
