@@ -846,7 +846,6 @@ def _tail(shape, st, first):
     return cut
 
 
-@functools.lru_cache(maxsize=256)
 def _beam_parts(name, shape, st, ost, dim, len_dim):
     """The five extents (outer, B, W, inner, positions), their strides in two tensors
     of this shape (but for W) and these strides, and the row length, in elements, of
@@ -869,17 +868,42 @@ def _beam_parts(name, shape, st, ost, dim, len_dim):
     return ext, a, b, n
 
 
+@functools.lru_cache(maxsize=256)
+def _beam_plan(shape, st, oshape, ostr, size, dim, len_dim, n):
+    """What vt_beam_reorder passes on of two tensors' layouts (`size` bytes an element): dim
+    and the byte strides as the library takes them, extents, bytes of a row and of
+    either tensor from its first element to its last."""
+    nd = len(shape)
+    dim += nd if dim < 0 else 0
+    if not 0 <= dim <= nd - 2 or 0 in shape:
+        raise ValueError("state must be [..., B, W, ...] with its sequences at dim, and not empty")
+    if len_dim is not None:
+        len_dim += nd if len_dim < 0 else 0
+        if not dim + 2 <= len_dim < nd:
+            raise ValueError("len_dim must be a dimension behind the beams")
+    if len(oshape) != nd or oshape[:dim + 1] != shape[:dim + 1] or oshape[dim + 2:] != shape[dim + 2:]:
+        raise ValueError(f"out must be like state, {list(shape)}, but for its beams, got {list(oshape)}")
+    ext, a, b, row = _beam_parts("state", shape, st, ostr, dim, len_dim)
+    B, W, slots = ext[1], ext[2], oshape[dim + 1]
+    if not 1 <= n <= 32 or W > 32:
+        raise ValueError("the slots of parent and the number of beams must be in [1, 32]")
+    if n > slots:
+        raise ValueError(f"parent has {n} slots, out {slots} beams")
+    if W == 1:  # (its slots' stride is out's own)
+        b = b[:2] + (ostr[dim + 1] if slots > 1 else 0,) + b[3:]
+    if any(s == 0 for s, e in zip(b, (ext[0], B, n, ext[3], ext[4])) if e > 1):
+        raise ValueError("out must not be expanded")
+    five = _lib._i64 * 5
+    span = lambda shape, st: (sum((e - 1) * s for e, s in zip(shape, st)) + 1) * size
+    return (B, W, five(*(s * size for s in a)), five(*(s * size for s in b)), ext[0], ext[3], ext[4], row * size,
+            span(shape, st), span(oshape, ostr))
+
+
 def _size(shape):
     n = 1
     for s in shape:
         n *= s
     return n
-
-
-def _span(t):
-    """The addresses [first, end) that a tensor's elements lie in."""
-    p = t.data_ptr()
-    return p, p + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
 def vt_beam_reorder(state, parent, out=None, dim: int = 0, lengths=None, len_dim=None, dev_status=None,
@@ -895,53 +919,31 @@ def vt_beam_reorder(state, parent, out=None, dim: int = 0, lengths=None, len_dim
     its number of beams (at least n), that does not overlap it.  Returns (out, dev_status).
     """
     dev = _first(state, "state")
-    nd = state.dim()
-    dim = int(dim)
-    if dim < 0:
-        dim += nd
-    if not 0 <= dim <= nd - 2 or 0 in state.shape:
-        raise ValueError("state must be [..., B, W, ...] with its sequences at dim, and not empty")
-    if len_dim is not None:
-        len_dim = int(len_dim)
-        if len_dim < 0:
-            len_dim += nd
-        if not dim + 2 <= len_dim < nd:
-            raise ValueError("len_dim must be a dimension behind the beams")
-    elif lengths is not None:
-        raise ValueError("lengths needs len_dim")
     shape, strides = state.shape, state.stride()
-    if out is None:
-        out = state
-    slots, ostr = shape[dim + 1], strides
-    if out is not state:
+    sp = state.data_ptr()
+    if lengths is not None and len_dim is None:
+        raise ValueError("lengths needs len_dim")
+    pp = _arg(parent, "parent", _I32, None, dev)
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, n]")
+    pB, n = parent.shape
+    if out is None or out is state:
+        out, op = state, sp
+        plan = _beam_plan(shape, strides, shape, strides, state.element_size(), int(dim), len_dim, n)
+    else:
         if not isinstance(out, _TORCH.Tensor) or out.get_device() != dev or out.dtype != state.dtype:
             raise ValueError(f"out must be a tensor of {state.dtype} on cuda:{dev}")
-        if out.dim() != nd or out.shape[:dim + 1] != shape[:dim + 1] or out.shape[dim + 2:] != shape[dim + 2:]:
-            raise ValueError(f"out must be like state, {list(shape)}, but for its beams, got {list(out.shape)}")
-        slots, ostr = out.shape[dim + 1], out.stride()
-        if out.data_ptr() != state.data_ptr() or ostr != strides or slots != shape[dim + 1]:
-            a, b = _span(state), _span(out)
-            if a[0] < b[1] and b[0] < a[1]:
-                raise ValueError("out must be state, or not overlap it")
-    ext, st, ost, row = _beam_parts("state", shape, strides, ostr, dim, len_dim)
-    B, W = ext[1], ext[2]
-    pp = _arg(parent, "parent", _I32, None, dev)
-    if parent.dim() != 2 or parent.shape[0] != B or not 1 <= parent.shape[1] <= 32 or W > 32:
-        raise ValueError(f"parent must be [{B}, n] with n, and the number of beams, in [1, 32]")
-    n = parent.shape[1]
-    if n > slots:
-        raise ValueError(f"parent has {n} slots, out {slots} beams")
-    if W == 1:  # (its slots' stride is out's own)
-        ost = ost[:2] + (ostr[dim + 1] if slots > 1 else 0,) + ost[3:]
-    if any(s == 0 for s, e in zip(ost, (ext[0], B, n, ext[3], ext[4])) if e > 1):
-        raise ValueError("out must not be expanded")
+        op, oshape, ostr = out.data_ptr(), out.shape, out.stride()
+        plan = _beam_plan(shape, strides, oshape, ostr, state.element_size(), int(dim), len_dim, n)
+        if sp < op + plan[9] and op < sp + plan[8] and (op != sp or ostr != strides or oshape != shape):
+            raise ValueError("out must be state, or not overlap it")
+    B, W, st, ost, outer, inner, positions, row = plan[:8]
+    if pB != B:
+        raise ValueError(f"parent must be [{B}, n], got {list(parent.shape)}")
     lp = _arg(lengths, "lengths", _I32, (B,), dev) if lengths is not None else None
     if dev_status is None:
         dev_status = _new(1, _I32[0], dev, stream)
-    es = state.element_size()
-    five = _lib._i64 * 5
-    rc = lib().vt_beam_reorder(state.data_ptr(), out.data_ptr(), five(*(s * es for s in st)),
-                               five(*(s * es for s in ost)), ext[0], B, W, n, ext[3], ext[4], row * es, pp, lp,
+    rc = lib().vt_beam_reorder(sp, op, st, ost, outer, B, W, n, inner, positions, row, pp, lp,
                                _arg(dev_status, "dev_status", _I32, (1,), dev), _on(stream, dev))
     if rc:
         _lib.check("vt_beam_reorder", rc)

@@ -289,7 +289,7 @@ __device__ double bs_exact_sum(const BsArgs& a, int row, float m, Pair inv_t, Pa
 
 template <typename T>
 __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
-  __shared__ bs_key key[kBsMaxBeams][kBsMaxN];
+  __shared__ bs_key key[kBsMaxBeams][kBsMaxN + 1];
   __shared__ double off[kBsMaxBeams];  // score minus ln S of each beam
   __shared__ float top[kBsMaxBeams];
   __shared__ int count[kBsMaxBeams];
@@ -297,19 +297,25 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
   __shared__ unsigned again;           // beams whose S is summed again
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.W, N = a.N, row0 = b * W;
+  const int w0 = tid / N, j0 = tid - w0 * N;
+  const bool ended = tid < W && a.done && a.done[row0 + tid];
+  const unsigned over = __ballot_sync(0xffffffffu, ended);  // (of the first warp's use)
+  const float score = tid < W ? a.scores[row0 + tid] : 0.f;
   griddep_wait();
+  // this thread's first candidate, asked for together with the rows
+  bs_key first = 0;
+  if (w0 < W) first = a.best[(int64_t)(row0 + w0) * N + j0];
   if (tid < W) {
-    const int row = row0 + tid;
-    const BeamRow r = a.rows[row];
-    const float s = a.scores[row];
+    const BeamRow r = a.rows[row0 + tid];
     if (r.flags) atomicOr(a.dev_status, r.flags);
     count[tid] = r.n;
     top[tid] = r.m;
-    off[tid] = (double)s - log((double)r.s + (double)r.e);
-    if (a.done && a.done[row] && fabsf(s) < INFINITY) {
+    const Pair lnS = pair_log(pair_of(r.s, r.e));
+    off[tid] = ((double)score - (double)lnS.h) - (double)lnS.l;
+    if (ended && fabsf(score) < INFINITY) {
       // a beam that has ended continues once, as it is
       count[tid] = 1;
-      key[tid][0] = bs_order((double)s);
+      key[tid][0] = bs_order((double)score);
     }
   }
   __syncthreads();
@@ -317,66 +323,67 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
   inv_t.h = (float)a.inv_t;
   inv_t.l = (float)(a.inv_t - (double)inv_t.h);
   unsigned exact = 0;  // beams whose S is the precise one
-  for (;;) {
-    for (int i = tid; i < W * N; i += kBsNT) {
-      const int w = i / N, j = i - w * N;
+  for (bool start = true;; start = false) {
+    for (int i = tid, w = w0, j = j0; i < W * N; i += kBsNT, w = i / N, j = i - w * N)
       if (j < count[w] && !(a.done && a.done[row0 + w])) {
-        const float v = key_value(a.best[(int64_t)(row0 + w) * N + j]);
+        const float v = key_value(start && i == tid ? first : a.best[(int64_t)(row0 + w) * N + j]);
         key[w][j] = bs_order(((double)v - (double)top[w]) * a.inv_t + off[w]);
       }
-    }
     __syncthreads();
     if (warp == 0) {
-      // lane w holds beam w's place in its list
+      // lane w holds beam w's place in its list, lane n the n-th chosen
       const int mine = lane < W ? count[lane] : 0;
-      int at = 0, before = -1;
-      double above = 0.0;
-      unsigned near = 0;
+      int at = 0, from = -1, place = 0, behind = -1;
+      bs_key q = mine > 0 ? key[lane][0] : 0, won = 0, last = 0;
       for (int n = 0; n <= N; ++n) {
-        const bs_key q = at < mine ? key[lane][at] : 0;
         const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(q >> 32));
-        const bool h = q != 0 && (unsigned)(q >> 32) == hi;
-        const unsigned lo = __reduce_max_sync(0xffffffffu, h ? (unsigned)q : 0u);
-        const unsigned who = __ballot_sync(0xffffffffu, h && (unsigned)q == lo);
-        if (who == 0) {
-          if (lane == 0)
-            for (; n < N; ++n) {
-              const int64_t o = (int64_t)b * N + n;
-              a.out_scores[o] = -INFINITY;
-              a.out_parent[o] = a.out_tokens[o] = -1;
-              if (a.out_done) a.out_done[o] = 0;
-            }
-          break;
+        if (hi == 0) break;  // (no finite score has a zero there)
+        const bool h = (unsigned)(q >> 32) == hi;
+        unsigned who = __ballot_sync(0xffffffffu, h);
+        if (who & (who - 1)) {
+          const unsigned lo = __reduce_max_sync(0xffffffffu, h ? (unsigned)q : 0u);
+          who = __ballot_sync(0xffffffffu, h && (unsigned)q == lo);
         }
         const int w = __ffs(who) - 1;  // ties to the lower beam
-        const double score = bs_score((bs_key)hi << 32 | lo);
-        if (n > 0 && w != before && above - score < kNear) near |= 1u << w | 1u << before;
-        above = score;
-        before = w;
-        if (lane == w && n < N) {
-          const int row = row0 + w;
-          const bool over = a.done && a.done[row];
-          int token = a.end_id;
-          if (!over) {
-            token = key_id(a.best[(int64_t)row * N + at]);
-            if (a.trim_ids) token = a.trim_ids[token];
-          }
-          const int64_t o = (int64_t)b * N + n;
-          a.out_scores[o] = (float)score;
-          a.out_parent[o] = w;
-          a.out_tokens[o] = token;
-          if (a.out_done) a.out_done[o] = over || token == a.end_id;
-        }
-        at += lane == w;
+        const bs_key best = __shfl_sync(0xffffffffu, q, w);
+        const int best_at = __shfl_sync(0xffffffffu, at, w);
+        if (lane == n) won = best, from = w, place = best_at;
+        if (n == 32) last = best, behind = w;  // the one behind 32
+        if (lane == w) q = ++at < mine ? key[lane][at] : 0;
       }
+      // neighbours of different beams that are too near to be told apart
+      bs_key below = __shfl_down_sync(0xffffffffu, won, 1);
+      int next = __shfl_down_sync(0xffffffffu, from, 1);
+      if (lane == 31) {
+        below = last;
+        next = behind;
+      }
+      unsigned near = 0;
+      if (lane < N && won != 0 && below != 0 && next != from && bs_score(won) - bs_score(below) < kNear)
+        near = 1u << from | 1u << next;
+      near = __reduce_or_sync(0xffffffffu, near) & ~over;  // beams that have ended have their scores exactly
       if (lane == 0) again = near;
+      if ((near & ~exact) == 0 && lane < N) {
+        const int64_t o = (int64_t)b * N + lane;
+        int token = -1;
+        bool done = false;
+        if (won != 0) {
+          done = over >> from & 1;
+          token = a.end_id;
+          if (!done) {
+            token = key_id(a.best[(int64_t)(row0 + from) * N + place]);
+            if (a.trim_ids) token = a.trim_ids[token];
+            done = token == a.end_id;
+          }
+        }
+        a.out_scores[o] = won != 0 ? (float)bs_score(won) : -INFINITY;
+        a.out_parent[o] = won != 0 ? from : -1;
+        a.out_tokens[o] = token;
+        if (a.out_done) a.out_done[o] = done;
+      }
     }
     __syncthreads();
-    // beams that have ended have their scores exactly
     unsigned todo = again & ~exact;
-    if (a.done)
-      for (int w = 0; w < W; ++w)
-        if (a.done[row0 + w]) todo &= ~(1u << w);
     if (todo == 0) break;
     exact |= todo;
     while (todo) {
@@ -460,8 +467,9 @@ int launch_reorder(cudaStream_t s, const BrArgs& a) {
   const int64_t pieces = (per + kBrNT - 1) / kBrNT, blocks = a.O * a.B * a.P * pieces;
   if (blocks > 0x7fffffff) return VT_ERR_UNSUPPORTED;
   const int smem = a.W * kBrNT * (int)sizeof(V);
-  VT_RETURN_IF_CUDA(cudaFuncSetAttribute(beam_reorder_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kBsMaxBeams * kBrNT * (int)sizeof(V)));
+  if (smem > 48 << 10)
+    VT_RETURN_IF_CUDA(cudaFuncSetAttribute(beam_reorder_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kBsMaxBeams * kBrNT * (int)sizeof(V)));
   beam_reorder_kernel<V><<<(unsigned)blocks, kBrNT, smem, s>>>(a, pieces);
   VT_RETURN_IF_LAUNCH_FAILED();
   return VT_OK;
