@@ -607,6 +607,8 @@ extern "C" int vt_beam_reorder(const void* state, void* out, const int64_t* stri
   if (total > 1e15) return VT_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (align % 16 == 0) return launch_reorder<uint4>(s, a);
+  if (align % 8 == 0) return launch_reorder<uint2>(s, a);
   if (align % 4 == 0) return launch_reorder<uint32_t>(s, a);
+  if (align % 2 == 0) return launch_reorder<uint16_t>(s, a);
   return launch_reorder<uint8_t>(s, a);
 }

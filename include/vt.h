@@ -499,7 +499,8 @@ int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64_t R, int32
  *  out_done   uint8 [B, n] out, needed with done: 1 where the parent had ended or
  *                          the token is end_id
  *  dev_status int32 [1]    out: VT_DEV_NONFINITE (a NaN or +infinity in a score or
- *                          in a row that was read; that beam gives no candidates)
+ *                          in a row that was read; that beam gives no candidates),
+ *                          VT_DEV_TIMEOUT
  * An id at -infinity is no candidate.  Where a sequence has fewer than n, the
  * rest is score -infinity, parent -1, token -1.  Outputs overlap no input.
  * 1 <= W, n <= 32, 1 <= K <= 2^22, B W <= 2^24, 1e-30 <= T <= 1e30.  Workspace:

@@ -173,6 +173,43 @@ def test_strides_and_alignment(vt, dt, pad, lead):
             assert gp == 0 or bool((out[gl:].view(6, K + gp)[:, K:] == 7).all())
 
 
+@pytest.mark.parametrize("dt,R,K,k,pad", [(torch.float32, 3000, 300, 3, 0), (torch.bfloat16, 1500, 5000, 40, 3),
+                                          (torch.float32, 420, 20000, 20, 0), (torch.bfloat16, 200, 70001, 9, 1),
+                                          (torch.float32, 3, 170001, 100, 0)])
+def test_more_rows_than_run_at_once(vt, dt, R, K, k, pad):
+    # blocks take several rows in turn, some of them not scored
+    x, ids, lnt, inv, w = _inputs(K, R, K, k, dt, pad, trimmed=True)
+    skip = torch.arange(R, device="cuda") % 5 > 2
+    ids[skip] = -1
+    lnt[skip] = float("nan")
+    x[skip] = float("nan")
+    _check(vt, x, ids, lnt, inv, w, R % 2 == 0)
+
+
+@pytest.mark.parametrize("rest", [True, False])
+def test_rows_do_not_depend_on_the_batch(vt, rest):
+    # long rows in many turns of clusters, against the same rows a few at a time: each is within
+    # the bound E of the exact value, and the gradients' c_all and c_rest with them
+    R, K, k = 470, 128256, 12
+    x, ids, lnt, _, w = _inputs(77, R, K, k, torch.float32)
+    ids[torch.arange(R, device="cuda") % 7 > 4] = -1
+    E = U * (K / 256 + 90)
+    loss, stats, st = vt.vt_distill_loss(x, ids, lnt, rest=rest)
+    assert int(st.item()) == 0
+    l2, g2, s2, st = vt.vt_distill_loss_grad(x, ids, lnt, w, rest=rest, out_grad=x.clone())
+    assert int(st.item()) == 0
+    for r in range(0, R, 47):
+        part = slice(r, r + 5)
+        l1, g1, s1, _ = vt.vt_distill_loss_grad(x[part], ids[part].contiguous(), lnt[part].contiguous(),
+                                                w[part].contiguous(), rest=rest)
+        for l, s in ((loss, stats), (l2, s2)):
+            assert torch.all((l[part] - l1).abs() <= 8 * E + 4 * U * l1.abs())
+            assert torch.equal(s[part, :2], s1[:, :2])              # the largest logits: exact
+            assert torch.all((s[part, 2:] - s1[:, 2:]).abs() <= 4 * E * s1[:, 2:].abs().amax(1, True))
+        # the bound of a gradient entry, twice, with A p + pull <= 2 and |d| <= 40
+        assert torch.all((g2[part] - g1).abs() <= 4 * w[part, None].abs() * (E + 130 * U) * g1.abs().amax(1, True).clamp(min=1e-3))
+
+
 def test_batched_logits_and_no_weight(vt):
     x, ids, lnt, _, w = _inputs(3, 12, 700, 6, torch.float32)
     _check(vt, x.view(3, 4, 700), ids.view(3, 4, 6), lnt.view(3, 4, 6), None, w.view(3, 4))
