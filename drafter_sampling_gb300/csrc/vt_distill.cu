@@ -228,7 +228,8 @@ __device__ __forceinline__ RowSum warp_join(RowSum a, float c) {
 struct DsHead {
   bool kept;    // an entry is
   int flags;
-  float m, S;   // largest kept logit, sum of 2^((z - m) c) over the kept
+  float m;      // largest kept logit
+  Pair S;       // sum of e^((z - m) / T) over the kept
   Pair mass;    // sum of t
   Pair cross;   // sum of t (ln t - (z - m) / T)
 };
@@ -250,24 +251,26 @@ __device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsEntries<H>& e, int 
   r.m = m = warp_max_nan(m);
   r.kept = !(m == -INFINITY);
   r.flags = flags;
-  r.S = 0.f;
-  r.mass = r.cross = Pair{0.f, 0.f};
+  r.S = r.mass = r.cross = Pair{0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const bool kept = e.z[h] != -INFINITY;
     const float z = kept ? e.z[h] : m;
     const Pair lnt{kept ? e.lp[h] : -INFINITY, 0.f}, t = pair_exp(lnt);
-    const Pair d = pair_add(Pair{t.h > 0.f ? lnt.h : 0.f, 0.f}, pair_neg(ds_below(z, m, a.inv_t)));
+    const Pair y = ds_below(z, m, a.inv_t), d = pair_add(Pair{t.h > 0.f ? lnt.h : 0.f, 0.f}, pair_neg(y));
     const Pair x = pair_mul(t, d);
     r.mass = pair_add(r.mass, t);
     r.cross = pair_add(r.cross, t.h > 0.f ? x : Pair{0.f, 0.f});
     e.lp[h] = t.h;
-    e.z[h] = kept ? exp2_approx((z - m) * a.c) : 0.f;
-    r.S += e.z[h];
+    // (a listed id's weight to its last place: the list usually has most of S)
+    Pair w = pair_exp(y);
+    if (!(kept && (z - m) * a.c > -125.f)) w = Pair{0.f, 0.f};
+    r.S = pair_add(r.S, w);
+    e.z[h] = w.h;
   }
-  r.S = warp_add(r.S);
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
+    r.S = pair_add(r.S, pair_xor(r.S, o));
     r.mass = pair_add(r.mass, pair_xor(r.mass, o));
     r.cross = pair_add(r.cross, pair_xor(r.cross, o));
   }
@@ -282,13 +285,14 @@ struct DsSum {
 };
 // The row's statistics from both, and what the loss takes of them
 struct DsTotal {
-  float S;     // relative to the row's largest logit
-  float b;     // the teacher's rest
+  Pair w;      // e^((l - m) / T) of the lower of the list's and the others' maxima
+  Pair b;      // the teacher's rest: what the list leaves of 1, good to 2^-28
   int flags;
   bool learns;
 };
+// The consuming warps wait for this, so it is plain fp32 but for the exponential and b: a few roundings.
 __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, const DsSum& un, DsStats& st) {
-  DsTotal r{0.f, 0.f, hd.flags | (un.late ? VT_DEV_TIMEOUT : 0), false};
+  DsTotal r{Pair{0.f, 0.f}, Pair{0.f, 0.f}, hd.flags | (un.late ? VT_DEV_TIMEOUT : 0), false};
   const bool rest = !(un.s == 0.f);  // (NaN: flagged below)
   const float m = rest ? max_nan(hd.m, un.m) : hd.m, inv_t = a.inv_t.h;
   st = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
@@ -298,20 +302,23 @@ __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, c
     st = DsStats{nan, nan, nan, nan, nan};
     return r;
   }
-  // what the list leaves of 1: its mass is good to 2^-28
-  if (a.rest && rest) r.b = fmaxf(0.f, (1.f - hd.mass.h) - hd.mass.l);
-  const float A = hd.mass.h + r.b;
+  if (a.rest && rest) r.b = pair_add(Pair{1.f, 0.f}, pair_neg(hd.mass));
+  if (!(r.b.h > 0.f)) r.b = Pair{0.f, 0.f};
+  const float A = hd.mass.h + r.b.h;
   if (!hd.kept || !(A > 0.f)) return r;  // nothing to learn from this row
   r.learns = true;
-  const float top = rest ? exp2_approx((un.m - m) * a.c) : 0.f;
-  r.S = fmaf(un.s, top, hd.S * exp2_approx((hd.m - m) * a.c));
+  // one of the two maxima is m
+  const float lower = rest ? fminf(hd.m, un.m) : m;
+  r.w = pair_exp(ds_below(lower, m, a.inv_t));
+  if (!((lower - m) * a.c > -125.f)) r.w = Pair{0.f, 0.f};
+  const float top = rest ? un.m < m ? r.w.h : 1.f : 0.f;
+  const float S = fmaf(un.s, top, hd.m < m ? hd.S.h * r.w.h : hd.S.h);
   st.m = m;
   st.mr = rest ? un.m : 0.f;
-  // (quotients to two units of the last place: S and the unlisted sum are in [1, 2^23])
-  const float all = __fdividef(inv_t, r.S);
+  const float all = inv_t / S, each = inv_t / un.s;
   if (a.rest) {
     st.c_all = A * all;
-    st.c_rest = rest ? A * all * top - inv_t * __fdividef(r.b, un.s) : 0.f;
+    st.c_rest = rest ? fmaf(A * all, top, -(r.b.h * each)) : 0.f;
     st.c_t = inv_t;
   } else {
     st.c_all = all;
@@ -321,13 +328,15 @@ __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, c
   return r;
 }
 
-// The loss, by the warp that holds the list
-__device__ __forceinline__ float ds_loss(const DsArgs& a, const DsHead& hd, const DsSum& un, const DsStats& st,
-                                         const DsTotal& r, int lane) {
+// The loss, by the warp that holds the list (sr: the unlisted ids' sum again, with what rounding took)
+__device__ __forceinline__ float ds_loss(const DsArgs& a, const DsHead& hd, const DsSum& un, Pair sr,
+                                         const DsStats& st, const DsTotal& r, int lane) {
   if (r.flags) return __int_as_float(0x7fc00000);
   if (!r.learns) return 0.f;
+  Pair S = hd.m < st.m ? pair_mul(hd.S, r.w) : hd.S;
+  if (un.s > 0.f) S = pair_add(S, un.m < st.m ? pair_mul(sr, r.w) : sr);
   // four logarithms at once, one per lane
-  Pair v = lane == 3 ? hd.mass : Pair{lane == 0 ? r.S : lane == 1 ? un.s : r.b, 0.f};
+  Pair v = lane == 0 ? S : lane == 1 ? sr : lane == 2 ? r.b : hd.mass;
   v = v.h > 0.f ? pair_log(v) : Pair{0.f, 0.f};
   const Pair lnS = pair_from_lane(v, 0), lnr = pair_from_lane(v, 1), lnb = pair_from_lane(v, 2);
   const Pair lna = pair_from_lane(v, 3);
@@ -336,9 +345,9 @@ __device__ __forceinline__ float ds_loss(const DsArgs& a, const DsHead& hd, cons
   Pair sum = pair_add(hd.cross, pair_neg(pair_mul(hd.mass, shift)));
   if (!a.rest) {
     sum = pair_add(pair_div(sum, hd.mass), pair_neg(lna));
-  } else if (r.b > 0.f) {
+  } else if (r.b.h > 0.f) {
     const Pair lnq = pair_add(pair_add(lnr, ds_below(un.m, st.m, a.inv_t)), pair_neg(lnS));
-    sum = pair_add(sum, pair_mul(Pair{r.b, 0.f}, pair_add(lnb, pair_neg(lnq))));
+    sum = pair_add(sum, pair_mul(r.b, pair_add(lnb, pair_neg(lnq))));
   }
   return sum.h != sum.h ? INFINITY : sum.h;  // (a term beyond fp32: they are positive)
 }
@@ -484,7 +493,9 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
 }
 
 // ------------------------------------------------------- loss, and with it the gradient
-constexpr int kDtMore = 96;             // threads of the warp that copies and the two for the lists
+constexpr int kDtLists = 2;             // warps for the lists
+template <int NW>
+constexpr int kDtThreads = 32 * (NW + 1 + kDtLists);
 constexpr int kDtU = 4;                 // vectors that a thread takes together
 constexpr int kDtMaxC = 8;
 constexpr int kDtZero = 2048;
@@ -500,7 +511,7 @@ template <int NW>
 struct DtShared {
   DsList list[kDtRing];
   DsStats st[kDtRing];
-  DsCells cells[2];
+  DsCells cells[kDtLists];
   DtPart got[kDtRing][kDtMaxC * (NW + 1)];  // the blocks' sums: their consuming warps', their edges'
   alignas(16) uint8_t zero[kDtZero];
   alignas(8) uint64_t full[kDtStages], done[kDtStages];  // chunks of the row in shared memory
@@ -562,7 +573,7 @@ __device__ __forceinline__ int64_t dt_row(int cluster, int n, int stride) {
 // gradient in the logits' place, and the copying warp takes it out.  Every block finishes every row
 // for itself.  Without the gradient the blocks finish rows in turn.
 template <typename T, bool kGrad, int H, int NW>
-__global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kDtThreads<NW>, NW > kLpWarps ? 1 : H == 1 ? 3 : 2)
     distill_rows_kernel(DsArgs a, DtSplit split) {
   constexpr int NT = 32 * NW;    // consuming threads
   constexpr int kParts = NW + 1;
@@ -619,7 +630,7 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (kGrad) {
-    for (int i = tid; i < kDtZero / 4; i += NT + kDtMore) reinterpret_cast<uint32_t*>(sh.zero)[i] = 0;
+    for (int i = tid; i < kDtZero / 4; i += kDtThreads<NW>) reinterpret_cast<uint32_t*>(sh.zero)[i] = 0;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (C > 1)
@@ -706,9 +717,9 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
     }
     __syncwarp();
   } else if (warp > NW) {
-    // the lists: one warp has the even turns, the other the odd ones.  A row's statistics are what the
-    // consuming warps wait for, so all else of a turn is done ahead: at row n's turn its own list has
-    // been taken in, row n + 2's places go to the consuming warps and its values arrive, row n + 4's ids.
+    // the lists: one warp has the even turns, the other the odd ones.  A row's statistics are what the consuming warps
+    // wait for, so all else of a turn is done ahead: at row n's turn its own list has been taken in, the
+    // values of row n + 2 arrive, and row n + 4's ids.
     const int mod = C % 4 == 0 ? C : C % 2 == 0 ? 2 * C : 4 * C;  // turns between two uses of a sums' place
     DsCells& cells = sh.cells[warp - NW - 1];
     int n = warp - NW - 1;
@@ -737,9 +748,8 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
       float x;      // -infinity: none
       bool here, unlisted;
     };
-    const auto take_in = [&](DsEntries<H>& e, int64_t row, int n, Edges& edge) {
-      DsHead hd{};
-      if (row >= a.R) return hd;
+    const auto send_ends = [&](const DsEntries<H>& e, int64_t row, int n, Edges& edge) {
+      if (row >= a.R) return;
       DtPart ends{-INFINITY, 0.f};
       edge = Edges{-INFINITY, false, false};
       if (first) {
@@ -762,37 +772,33 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
         }
       }
       const int slot = n & 3;
-      if (finishes(n)) {
-        if (lane == 0) umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * kParts * sizeof(DtPart)));
-        if (e.any) hd = ds_head<H>(a, e, ds_flags<H>(e, cells, lane));
-      }
+      if (finishes(n) && lane == 0)
+        umma::mbar_expect_tx(&sh.summed[slot], (uint32_t)(C * kParts * sizeof(DtPart)));
+      // A place for sums is taken again after four turns, when all blocks have read it: as each has said
+      // (without the gradient), or as those have that have sent their sums of row n - 2, which this warp has
       if (!kGrad && n >= kDtRing) wait_blocks(&sh.ready[slot], (n >> 2) - 1);
       if (kGrad ? lane < C : lane == 0)
         send_part(ends, &sh.got[slot][rank * kParts + NW], &sh.summed[slot], kGrad ? lane : n % C);
-      return hd;
     };
-    DsEntries<H> e, next;
-    int id[H], id2[H];
+    DsEntries<H> e{}, next;
+    int id[H];
     ds_ids<H>(a, row_at(n), lane, id);
-    ds_ids<H>(a, row_at(n + 2), lane, id2);
-    ds_map<H>(a, id, e);
-    if (finishes(n)) ds_values<T, H>(a, row_at(n), lane, e);
-    publish(e, row_at(n), n);
-    ds_map<H>(a, id2, next);
-    ds_ids<H>(a, row_at(n + 4), lane, id);
-    Edges edge;
-    DsHead hd = take_in(e, row_at(n), n, edge);
-    for (; n < turns; n += 2) {
-      const int row = (int)row_of(n), slot = n & 3;
+    ds_map<H>(a, id, next);
+    ds_ids<H>(a, row_at(n + 2), lane, id);
+    Edges edge{};
+    DsHead hd{};
+    for (n -= 2; n < turns; n += 2) {  // (the first time round takes in the first row alone)
+      const int row = n < 0 ? 0 : (int)row_of(n), slot = n & 3;
       const int64_t after = row_at(n + 2);
       if (finishes(n + 2)) ds_values<T, H>(a, after, lane, next);
-      publish(next, after, n + 2);
-      if (finishes(n)) {
+      DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+      DsTotal r{};
+      DsSum un{-INFINITY, 0.f, 0};
+      constexpr int kMost = (kDtMaxC * kParts + 31) / 32;
+      float pm[kMost], ps[kMost];
+      if (n >= 0 && finishes(n)) {
         const float g = kGrad && a.weight ? __ldg(a.weight + row) : 1.f;
-        const bool ok = wait_blocks(&sh.summed[slot], kGrad ? n >> 2 : n / mod);
-        DsSum un{-INFINITY, 0.f, !ok};
-        constexpr int kMost = (kDtMaxC * kParts + 31) / 32;
-        float pm[kMost], ps[kMost];
+        un.late = !wait_blocks(&sh.summed[slot], kGrad ? n >> 2 : n / mod);
 #pragma unroll
         for (int h = 0; h < kMost; ++h) {
           const int i = lane + 32 * h;
@@ -807,11 +813,12 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
         un.late = __any_sync(0xffffffffu, un.late != 0);
         // (0 and -infinity where nothing was summed)
 #pragma unroll
-        for (int h = 0; h < kMost; ++h) un.s += ps[h] == 0.f ? 0.f : ps[h] * exp2_approx((pm[h] - un.m) * a.c);
+        for (int h = 0; h < kMost; ++h) {
+          ps[h] = ps[h] == 0.f ? 0.f : ps[h] * exp2_approx((pm[h] - un.m) * a.c);
+          un.s += ps[h];
+        }
         un.s = warp_add(un.s);
         if (!kGrad && lane < C) arrive_block(&sh.ready[slot], lane);  // the sums' place is free
-        DsStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-        DsTotal r{};
         if (e.any) r = ds_stats(a, hd, un, st);
         if (kGrad) {
           const float all = g * st.c_all * (r.learns ? exp2_approx((hd.m - st.m) * a.c) : 1.f), ct = g * st.c_t;
@@ -823,30 +830,41 @@ __global__ void __launch_bounds__(32 * NW + kDtMore, NW > kLpWarps ? 1 : H == 1 
           if (lane == 0) sh.st[slot] = st;
           __syncwarp();
           if (lane == 0) umma::mbar_arrive(&sh.ready[slot]);
-        }
-        if (n % C == rank) {
-          const float loss = e.any ? ds_loss(a, hd, un, st, r, lane) : 0.f;
-          if (lane == 0) ds_put(a, row, loss, st, r.flags);
-          __syncwarp();
-        }
-        if (kGrad && first) {
-          // the edges' gradients
-          T* d = grads(row);
-          const Span sp = span_of<T>(logits(row), a.K, 0, 1);
-          const bool nothing = ds_nothing(st);
-          if (edge.here && (nothing || edge.unlisted))
-            Store<T>::put(d + edge_id<VE>(sp, lane),
-                          nothing ? 0.f : g * st.c_rest * exp2_approx((edge.x - st.mr) * a.c));
-          if (!nothing)
+          if (first) {
+            // the edges' gradients
+            T* d = grads(row);
+            const Span sp = span_of<T>(logits(row), a.K, 0, 1);
+            const bool nothing = ds_nothing(st);
+            if (edge.here && (nothing || edge.unlisted))
+              Store<T>::put(d + edge_id<VE>(sp, lane),
+                            nothing ? 0.f : g * st.c_rest * exp2_approx((edge.x - st.mr) * a.c));
+            if (!nothing)
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-              if (ds_edge<VE>(sp, e.p[h]) >= 0) Store<T>::put(d + e.p[h], e.lp[h]);
+              for (int h = 0; h < H; ++h)
+                if (ds_edge<VE>(sp, e.p[h]) >= 0) Store<T>::put(d + e.p[h], e.lp[h]);
+          }
         }
       }
+      // the next row's places, and what its sums wait for, ahead of this row's loss
+      publish(next, after, n + 2);
+      const bool learns = e.any, counts = n >= 0 && n % C == rank;
       e = next;
       ds_map<H>(a, id, next);
       ds_ids<H>(a, row_at(n + 6), lane, id);
-      hd = take_in(e, after, n + 2, edge);
+      const bool more = finishes(n + 2) && e.any;
+      const int flags = more ? ds_flags<H>(e, cells, lane) : 0;
+      send_ends(e, after, n + 2, edge);
+      if (counts) {
+        Pair sr{0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < kMost; ++h) sr = pair_add(sr, Pair{ps[h], 0.f});
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) sr = pair_add(sr, pair_xor(sr, o));
+        const float loss = learns ? ds_loss(a, hd, un, sr, st, r, lane) : 0.f;
+        if (lane == 0) ds_put(a, row, loss, st, r.flags);
+        __syncwarp();
+      }
+      hd = more ? ds_head<H>(a, e, flags) : DsHead{};
     }
   } else {
     int in_at = 0, in_lap = 0, out_at = 0;  // chunks' places
@@ -1077,7 +1095,7 @@ int ds_launch_rows(const DsArgs& a, cudaStream_t s, const DtPlan& p) {
   auto kern = distill_rows_kernel<T, kGrad, H, NW>;
   VT_RETURN_IF_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtBytes[2]));
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(32 * NW + kDtMore);
+  cfg.blockDim = dim3(kDtThreads<NW>);
   cfg.dynamicSmemBytes = (size_t)kDtBytes[p.tier];
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -46,7 +46,7 @@ __device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
 // 16 bits (whose multiples by n are exact) and a remainder, |r| <= 0.35, then the
 // Taylor series with 1, r and r^2 / 2 exact and the rest (below 0.008) in fp32
 // (2.6e-9 is the largest of 2e7 arguments).
-__device__ __forceinline__ Pair pair_exp(Pair x) {
+static __device__ __noinline__ Pair pair_exp(Pair x) {
   const float n = rintf(x.h * VT_LOG2E);
   float r, rl;
   two_sum(fmaf(n, -0.693145751953125f, x.h), fmaf(n, -1.42860682e-6f, x.l), r, rl);
