@@ -691,7 +691,7 @@ def vt_draft_topk_fp8(hidden, W8, w_scale, trim_ids, k: int, temperature: float 
     return out_ids, out_logq, dev_status
 
 
-def _logit_rows(logits):
+def _logit_rows(logits, name="logits"):
     """(element type, leading shape, rows, row length, row stride) of logits
     [R, V] or [B, R, V]."""
     dt = logits.dtype
@@ -700,10 +700,10 @@ def _logit_rows(logits):
     elif dt in _BF16:
         dt = VT_BF16
     else:
-        raise TypeError("logits must be float32 or bf16")
+        raise TypeError(f"{name} must be float32 or bf16")
     full, st = logits.shape, logits.stride()
     if len(full) not in (2, 3) or 0 in full:
-        raise ValueError("logits must be [R, V] or [B, R, V]")
+        raise ValueError(f"{name} must be [R, V] or [B, R, V]")
     shape, V = full[:-1], full[-1]
     if len(full) == 2:
         R = shape[0]
@@ -715,7 +715,7 @@ def _logit_rows(logits):
         ld = st[1] if n > 1 else st[0] if B > 1 else V
         even = B == 1 or n == 1 or st[0] == n * ld
     if (st[-1] != 1 and V > 1) or not even or ld < V:
-        raise ValueError("logits must have unit inner stride and evenly spaced rows")
+        raise ValueError(f"{name} must have unit inner stride and evenly spaced rows")
     return dt, shape, R, V, ld
 
 
@@ -974,7 +974,7 @@ def _grad_out(out_grad, logits, shape, R, K, dev, stream):
     elif not isinstance(out_grad, _TORCH.Tensor) or out_grad.get_device() != dev or \
             out_grad.dtype != logits.dtype or out_grad.shape != logits.shape:
         raise ValueError(f"out_grad must be a tensor of {logits.dtype} on cuda:{dev}, {[*shape, K]}")
-    return out_grad, out_grad.data_ptr(), _logit_rows(out_grad)[4]
+    return out_grad, out_grad.data_ptr(), _logit_rows(out_grad, "out_grad")[4]
 
 
 def vt_distill_loss(logits, top_ids, top_logp, inv_map=None, rest: bool = True, temperature: float = 1.0,

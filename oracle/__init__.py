@@ -57,6 +57,12 @@ pages or the mathematics fix (none is "parity unpinned"):
                          tables; equals the stochastic verify at a vanishing
                          temperature for any uniforms; hand-worked blocks
                          (tests/test_oracle_greedy.py)
+* beam.beam_select       beams of full width against exhaustive search; hand-
+                         worked ties, ends and missing beams
+* beam.beam_reorder      hand-worked parents and lengths
+* distill.distill        gradient against central differences of the loss; zero
+                         between equal distributions; rows with nothing to learn
+                         (tests/test_oracle_beam_distill.py)
 * verify_tree_greedy     a chain equals verify_greedy; the deepest accepted
                          path equals the best root-to-leaf chain (brute
                          force); lossless tree decoding on the toy tables;
