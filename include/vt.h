@@ -574,6 +574,8 @@ int vt_beam_reorder(const void* state, void* out, const int64_t* strides, const 
  *                            kept entries for one id), VT_DEV_NONFINITE (a logit that
  *                            is NaN or +infinity, a kept ln t that is NaN or not
  *                            below 80): NaN in that row's loss, statistics, gradient
+ *                            (all of it); VT_DEV_TIMEOUT likewise.  A t below 1e-37
+ *                            counts as 0
  * vt_distill_loss gives loss and statistics, vt_distill_grad the gradient from the
  * same arguments and those statistics, vt_distill_loss_grad all of it.
  * 1 <= k <= 128, 1 <= K <= 2^22, 1 <= R <= 2^24, 1e-30 <= T <= 1e30.  No workspace.

@@ -417,3 +417,30 @@ def test_a_trimmed_head_learns_from_the_targets_alternatives(vt):
         want = ref["grad"].T @ hidden.double().cpu().numpy()
         assert np.linalg.norm(dW - want) <= 2e-5 * np.linalg.norm(want)
         assert not loss[5:8].any() and not grad[5:8].any()
+
+
+@pytest.mark.parametrize("call", ["vt_distill_loss", "vt_distill_loss_grad", "vt_beam_select"])
+def test_the_first_call_of_a_process_may_be_captured(vt, call):
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import torch
+import drafter_sampling_gb300 as vt
+x = torch.randn((6, 5, 3000), device="cuda")
+ids = torch.arange(6 * 5 * 2, device="cuda", dtype=torch.int32).view(6, 5, 2)
+low = torch.full((6, 5, 2), -1.0, device="cuda")
+torch.cuda.synchronize()
+f = (lambda: vt.vt_beam_select(x, low[:, :, 0].contiguous(), 4)[:3]) if "{call}" == "vt_beam_select" else (
+    lambda: vt.{call}(x, ids, low)[:2])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = f()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, f()))
+print("equal")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
