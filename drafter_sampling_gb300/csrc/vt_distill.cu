@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
         if (z == -INFINITY) p = -1;
       }
     }
-    __syncthreads();
+    if (a.grad == a.logits) __syncthreads();
   }
   const float factor = g * st.c_rest;
 #pragma unroll
