@@ -25,7 +25,7 @@
 // bf16 logits 39.6 us (4.4 TB/s; 25.9 at the measured copy rate), of which 3 to the first chunk, 3 for
 // the last rows' statistics and losses, and a sixth round of rows for 24 of 456 blocks.  112
 // rows of 128256 fp32, 59 of them scored: 12.4 (latencies; 4.5 by bytes).  The gradient alone reads and
-// writes them: the same bf16 rows 55.1 (6.4 TB/s).  Both in one call read and write once: 2048 rows of
+// writes them: the same bf16 rows 54.6 (6.4 TB/s).  Both in one call read and write once: 2048 rows of
 // 32768 fp32 92.5 us (5.8 TB/s; 79 by bytes), 1024 rows of 128256 bf16, 576 scored, 103 (60.6 by bytes):
 // there a row's two passes of exponentials take 2/3 of its turn, a block's warps idle in the rest.
 // All in graphs of calls.
