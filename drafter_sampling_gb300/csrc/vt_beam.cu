@@ -342,9 +342,9 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
     if (warp == 0) {
       // lane w holds beam w's place in its list, lane n the n-th chosen
       const int mine = lane < W ? count[lane] : 0;
-      int at = 0, from = -1, place = 0, behind = -1;
-      bs_key q = mine > 0 ? key[lane][0] : 0, won = 0, last = 0;
-      for (int n = 0; n <= N; ++n) {
+      int at = 0, from = -1, place = 0;
+      bs_key q = mine > 0 ? key[lane][0] : 0, won = 0;
+      for (int n = 0; n < N; ++n) {
         const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(q >> 32));
         if (hi == 0) break;  // (no finite score has a zero there)
         const bool h = (unsigned)(q >> 32) == hi;
@@ -357,19 +357,20 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
         const bs_key best = __shfl_sync(0xffffffffu, q, w);
         const int best_at = __shfl_sync(0xffffffffu, at, w);
         if (lane == n) won = best, from = w, place = best_at;
-        if (n == 32) last = best, behind = w;  // the one behind 32
         if (lane == w) q = ++at < mine ? key[lane][at] : 0;
       }
-      // neighbours of different beams that are too near to be told apart
-      bs_key below = __shfl_down_sync(0xffffffffu, won, 1);
-      int next = __shfl_down_sync(0xffffffffu, from, 1);
-      if (lane == 31) {
-        below = last;
-        next = behind;
-      }
+      // Beams that are too near to be told apart: neighbours among the chosen, and the last chosen
+      // with every other beam that has a candidate left (its best is q).  A beam that should
+      // change places with another is within kNear of it, so of all chosen between them.
+      const bs_key below = __shfl_down_sync(0xffffffffu, won, 1);
+      const int next = __shfl_down_sync(0xffffffffu, from, 1);
+      const bs_key end = __shfl_sync(0xffffffffu, won, N - 1);
+      const int end_from = __shfl_sync(0xffffffffu, from, N - 1);
       unsigned near = 0;
-      if (lane < N && won != 0 && below != 0 && next != from && bs_score(won) - bs_score(below) < kNear)
+      if (lane < N - 1 && below != 0 && next != from && bs_score(won) - bs_score(below) < kNear)
         near = 1u << from | 1u << next;
+      if (end != 0 && q != 0 && lane != end_from && bs_score(end) - bs_score(q) < kNear)
+        near |= 1u << lane | 1u << end_from;
       near = __reduce_or_sync(0xffffffffu, near) & ~over;  // beams that have ended have their scores exactly
       if (lane == 0) again = near;
       if ((near & ~exact) == 0 && lane < N) {
