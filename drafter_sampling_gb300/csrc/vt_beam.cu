@@ -494,7 +494,8 @@ int launch_reorder(cudaStream_t s, const BrArgs& a) {
   const int64_t pieces = (per + kBrNT - 1) / kBrNT, blocks = a.O * a.B * a.P * pieces;
   if (blocks > 0x7fffffff) return VT_ERR_UNSUPPORTED;
   const int smem = a.W * kBrNT * (int)sizeof(V);
-  if (smem > 48 << 10)
+  // what a launch may take without asking is 48 KB together with the kernel's own few hundred bytes
+  if (smem > 47 << 10)
     VT_RETURN_IF_CUDA(cudaFuncSetAttribute(beam_reorder_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kBsMaxBeams * kBrNT * (int)sizeof(V)));
   beam_reorder_kernel<V><<<(unsigned)blocks, kBrNT, smem, s>>>(a, pieces);
