@@ -877,7 +877,8 @@ cudaError_t launch_gemv_bt(int grid, cudaStream_t s, const uint16_t* hidden, int
                            int vec_ok, int greedy) {
   const size_t smem = (size_t)BT * H * sizeof(uint16_t);
   auto kern = draft_gemv_kernel<BT, 4>;
-  if (smem > 48 * 1024) {
+  // (48 KB without asking, the kernel's own MS sred, at most 1 KB, among them)
+  if (smem > 47 * 1024) {
     // the most of any H (launch_gemv), so that every call sets the same limit:
     // another host thread may set it between here and the launch
     constexpr int smem_max = (BT == 1 ? 200 : 160) * 1024;
