@@ -9,9 +9,9 @@
 //
 // Scores are compared in fp64.  S itself is a sum of fp32 exponentials, so two
 // beams' candidates nearer than kNear are not yet told apart: the merge then
-// sums those beams' rows again with pairs of fp32 values, in an order that
-// depends on the ids alone (equal beams give equal scores, whatever their rows'
-// alignment), and takes the lists again.
+// sums those beams' rows again, exponentials as pairs of fp32 values added as integers
+// (equal beams give equal scores, whatever their rows' alignment or the order of their logits),
+// and takes the lists again.
 //
 // The rows are streamed as the log probabilities' are: a cluster of up to 8 blocks to a row where rows
 // are few, one persistent block for row after row where they are many.  256 x 8 beams over 38016 fp32
@@ -59,7 +59,7 @@ struct BsArgs {
   int64_t ld;
   int B, W, K, N;
   float c;
-  double inv_t;
+  double t, inv_t;         // T and 1 / T
   const float* scores;     // [B][W]
   const uint8_t* done;     // [B][W] or nullptr
   int end_id;
@@ -267,43 +267,85 @@ __device__ __forceinline__ double bs_score(bs_key q) {
   return __longlong_as_double(b < 0 ? b ^ (1ll << 63) : ~b);
 }
 
-// S of one row again, by all threads of the block: the exponentials and their sum
-// as pairs, good to 2^-27.  Thread t takes ids t, t + kBsNT, ...
+// S of one row again, by all threads of the block.  The exponentials are pairs, good to 2^-28,
+// and are added as integers in units of 2^-54: a weight's multiples of 2^-30 and what it has beyond
+// them apart, each below 2^30 in size, so that 2^22 of them fit 64 bits.  So S is the same in whatever order
+// it is added: rows of the same logits in other places, or behind a constant, have equal sums.
 template <typename T>
-__device__ double bs_exact_sum(const BsArgs& a, int row, float m, Pair inv_t, Pair* red) {
+__device__ __noinline__ double bs_exact_sum(const BsArgs& a, int row, float m, Pair inv_t, long long (*red)[2]) {
+  constexpr int U = 4;  // ids of a thread in flight
   const T* l = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
-  Pair sum{0.f, 0.f};
-  for (int j = threadIdx.x; j < a.K; j += kBsNT) {
-    const float x = Elem<T>::load(l + j);
-    float d, e;
-    two_sum(x, -m, d, e);
-    if (!((double)d * a.inv_t > -80.0)) continue;  // e^-80 of 2^22 ids is nothing to S >= 1
-    const Pair y = pair_exp(pair_mul(Pair{d, e}, inv_t));
-    sum = pair_add(sum, y);
+  long long hi = 0, lo = 0;
+  for (int j = threadIdx.x; j < a.K; j += U * kBsNT) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = j + u * kBsNT < a.K ? Elem<T>::load(l + j + u * kBsNT) : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Pair d;
+      two_sum(x[u], -m, d.h, d.l);
+      if (!(d.h * inv_t.h > -80.f)) continue;  // e^-80 of 2^22 ids is nothing to S >= 1
+      const Pair w = pair_exp(pair_mul(d, inv_t));
+      const float y = w.h * 0x1p30f;
+      const int whole = __float2int_rz(y);
+      hi += whole;
+      lo += __float2int_rn(((y - (float)whole) + w.l * 0x1p30f) * 0x1p24f);  // (off by two units at most)
+    }
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int o = 16; o > 0; o >>= 1) {
-    Pair w;
-    w.h = __shfl_xor_sync(0xffffffffu, sum.h, o);
-    w.l = __shfl_xor_sync(0xffffffffu, sum.l, o);
-    sum = pair_add(sum, w);
+    hi += __shfl_xor_sync(0xffffffffu, hi, o);
+    lo += __shfl_xor_sync(0xffffffffu, lo, o);
   }
   __syncthreads();
-  if (lane == 0) red[warp] = sum;
+  if (lane == 0) {
+    red[warp][0] = hi;
+    red[warp][1] = lo;
+  }
   __syncthreads();
-  sum = red[0];
-  for (int w = 1; w < kBsNT / 32; ++w) sum = pair_add(sum, red[w]);
-  return (double)sum.h + (double)sum.l;
+  hi = lo = 0;
+  for (int w = 0; w < kBsNT / 32; ++w) {
+    hi += red[w][0];
+    lo += red[w][1];
+  }
+  return (double)hi * 0x1p-30 + (double)lo * 0x1p-54;
+}
+
+// What the merge's threads share
+struct BsMerge {
+  bs_key key[kBsMaxBeams][kBsMaxN + 1];
+  double off[kBsMaxBeams];       // score minus ln S of each beam
+  float top[kBsMaxBeams];
+  int count[kBsMaxBeams];
+  long long red[kBsNT / 32][2];
+  unsigned again;                // beams whose S is summed again
+};
+
+// Sums the rows of the beams in `todo` again and scores their candidates from these sums.  (Apart from the kernel,
+// which seldom comes here and is slower with this code among its own.)
+template <typename T>
+__device__ __noinline__ void bs_again(const BsArgs& a, int row0, unsigned todo, BsMerge& sh) {
+  Pair inv_t;
+  inv_t.h = (float)a.inv_t;
+  inv_t.l = (float)(a.inv_t - (double)inv_t.h);
+  for (; todo; todo &= todo - 1) {
+    const int w = __ffs(todo) - 1;
+    const double lnS = log(bs_exact_sum<T>(a, row0 + w, sh.top[w], inv_t, sh.red));
+    const double score = (double)a.scores[row0 + w];
+    for (int j = threadIdx.x; j < sh.count[w]; j += kBsNT) {
+      const double d = (double)key_value(a.best[(int64_t)(row0 + w) * a.N + j]) - (double)sh.top[w];
+      // d / T, after a Newton step, so that a quotient that fp64 has is that one, and ln S last, so
+      // that totals of score and logit that are equal stay so
+      double x = d * a.inv_t;
+      x = fma(fma(-x, a.t, d), a.inv_t, x);
+      sh.key[w][j] = bs_order((x + score) - lnS);
+    }
+  }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
-  __shared__ bs_key key[kBsMaxBeams][kBsMaxN + 1];
-  __shared__ double off[kBsMaxBeams];  // score minus ln S of each beam
-  __shared__ float top[kBsMaxBeams];
-  __shared__ int count[kBsMaxBeams];
-  __shared__ Pair red[kBsNT / 32];
-  __shared__ unsigned again;           // beams whose S is summed again
+  __shared__ BsMerge sh;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.W, N = a.N, row0 = b * W;
   const int w0 = tid / N, j0 = tid - w0 * N;
@@ -317,33 +359,30 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
   if (tid < W) {
     const BeamRow r = a.rows[row0 + tid];
     if (r.flags) atomicOr(a.dev_status, r.flags);
-    count[tid] = r.n;
-    top[tid] = r.m;
+    sh.count[tid] = r.n;
+    sh.top[tid] = r.m;
     const Pair lnS = pair_log(pair_of(r.s, r.e));
-    off[tid] = ((double)score - (double)lnS.h) - (double)lnS.l;
+    sh.off[tid] = ((double)score - (double)lnS.h) - (double)lnS.l;
     if (ended && fabsf(score) < INFINITY) {
       // a beam that has ended continues once, as it is
-      count[tid] = 1;
-      key[tid][0] = bs_order((double)score);
+      sh.count[tid] = 1;
+      sh.key[tid][0] = bs_order((double)score);
     }
   }
   __syncthreads();
-  Pair inv_t;
-  inv_t.h = (float)a.inv_t;
-  inv_t.l = (float)(a.inv_t - (double)inv_t.h);
+  for (int i = tid, w = w0, j = j0; i < W * N; i += kBsNT, w = i / N, j = i - w * N)
+    if (j < sh.count[w] && !(a.done && a.done[row0 + w])) {
+      const float v = key_value(i == tid ? first : a.best[(int64_t)(row0 + w) * N + j]);
+      sh.key[w][j] = bs_order(((double)v - (double)sh.top[w]) * a.inv_t + sh.off[w]);
+    }
   unsigned exact = 0;  // beams whose S is the precise one
-  for (bool start = true;; start = false) {
-    for (int i = tid, w = w0, j = j0; i < W * N; i += kBsNT, w = i / N, j = i - w * N)
-      if (j < count[w] && !(a.done && a.done[row0 + w])) {
-        const float v = key_value(start && i == tid ? first : a.best[(int64_t)(row0 + w) * N + j]);
-        key[w][j] = bs_order(((double)v - (double)top[w]) * a.inv_t + off[w]);
-      }
+  for (;;) {
     __syncthreads();
     if (warp == 0) {
       // lane w holds beam w's place in its list, lane n the n-th chosen
-      const int mine = lane < W ? count[lane] : 0;
+      const int mine = lane < W ? sh.count[lane] : 0;
       int at = 0, from = -1, place = 0;
-      bs_key q = mine > 0 ? key[lane][0] : 0, won = 0;
+      bs_key q = mine > 0 ? sh.key[lane][0] : 0, won = 0;
       for (int n = 0; n < N; ++n) {
         const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(q >> 32));
         if (hi == 0) break;  // (no finite score has a zero there)
@@ -357,7 +396,7 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
         const bs_key best = __shfl_sync(0xffffffffu, q, w);
         const int best_at = __shfl_sync(0xffffffffu, at, w);
         if (lane == n) won = best, from = w, place = best_at;
-        if (lane == w) q = ++at < mine ? key[lane][at] : 0;
+        if (lane == w) q = ++at < mine ? sh.key[lane][at] : 0;
       }
       // Beams that are too near to be told apart: neighbours among the chosen, and the last chosen
       // with every other beam that has a candidate left (its best is q).  A beam that should
@@ -372,7 +411,7 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
       if (end != 0 && q != 0 && lane != end_from && bs_score(end) - bs_score(q) < kNear)
         near |= 1u << lane | 1u << end_from;
       near = __reduce_or_sync(0xffffffffu, near) & ~over;  // beams that have ended have their scores exactly
-      if (lane == 0) again = near;
+      if (lane == 0) sh.again = near;
       if ((near & ~exact) == 0 && lane < N) {
         const int64_t o = (int64_t)b * N + lane;
         int token = -1;
@@ -393,16 +432,10 @@ __global__ void __launch_bounds__(kBsNT) beam_merge_kernel(BsArgs a) {
       }
     }
     __syncthreads();
-    unsigned todo = again & ~exact;
+    const unsigned todo = sh.again & ~exact;
     if (todo == 0) break;
     exact |= todo;
-    while (todo) {
-      const int w = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const double S = bs_exact_sum<T>(a, row0 + w, top[w], inv_t, red);
-      if (tid == 0) off[w] = (double)a.scores[row0 + w] - log(S);
-    }
-    __syncthreads();
+    bs_again<T>(a, row0, todo, sh);
   }
 }
 
@@ -578,7 +611,8 @@ extern "C" int vt_beam_select(const void* logits, int32_t logits_dtype, int32_t 
   a.K = K;
   a.N = n;
   a.c = VT_LOG2E / temperature;
-  a.inv_t = 1.0 / (double)temperature;
+  a.t = (double)temperature;
+  a.inv_t = 1.0 / a.t;
   a.scores = scores;
   a.done = done;
   a.end_id = end_id;

@@ -2,7 +2,8 @@
 
 Equal beams have equal scores, and equal scores tie to the lower beam, then to the lower id: what a
 sequence returns then follows from the logits alone and is worked out here without any
-softmax: the rows have one ln S, so their candidates compare by score + logit - largest.
+softmax.  Rows whose logits are equal but for their places or a constant have one ln S, so their
+candidates compare by score + logit - largest, which fp64 holds exactly for the values taken here.
 Scores are within 5e-6 + 2^-24 |ref| (half of the distance within which the library sums again).
 """
 import numpy as np
@@ -73,6 +74,45 @@ def test_equal_beams_at_every_cut(vt, W, K, pad, dt, tied):
     x[:] = row
     s = torch.full((B, W), -3.25, device="cuda")
     _check(vt, x, s, range(1, 33))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_equal_beams_among_others(vt, dt):
+    # three groups of equal beams, their numbers mixed; only the groups' scores tell them apart
+    g = _gen(5)
+    B, W, K = 20, 12, 9001
+    row = (torch.randn((B, 1, K), generator=g, device="cuda") * 2).to(dt)
+    x = torch.zeros((B, W, K + 5), dtype=dt, device="cuda")[:, :, :K]
+    x[:] = row
+    s = torch.full((B, W), -4.0, device="cuda")
+    s[:, 1::3], s[:, 2::3] = -3.5, -4.5
+    _check(vt, x, s, (1, 2, 3, 4, 5, 7, 8, 11, 20, 32))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_equal_beams_in_other_orders_of_ids(vt, dt):
+    # rows of the same logits in other places, and behind constants that the sum takes out again
+    g = _gen(6)
+    B, W, K = 10, 8, 6007
+    row = (torch.randn((B, 1, K), generator=g, device="cuda") * 24).round().clamp(-127, 127) / 8.0
+    perm = torch.rand((B, W, K), generator=g, device="cuda").argsort(2)
+    x = row.expand(B, W, K).gather(2, perm)
+    s = torch.full((B, W), -3.25, device="cuda")
+    _check(vt, x.to(dt), s, (1, 2, 3, 5, 8, 9, 17, 32))
+    up = (torch.arange(W, device="cuda") * 3 % 8).float()[None, :, None]
+    _check(vt, (x + up).to(dt), s, (1, 2, 3, 5, 8, 9, 17, 32))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_scores_and_logits_of_one_total(vt, dt):
+    # totals of score and logit that are equal by different terms
+    g = _gen(7)
+    B, W, K = 40, 8, 3001
+    row = (torch.randn((B, 1, K), generator=g, device="cuda") * 24).round().clamp(-127, 127) / 8.0
+    perm = torch.rand((B, W, K), generator=g, device="cuda").argsort(2)
+    x = row.expand(B, W, K).gather(2, perm).to(dt)
+    s = -3.0 - torch.randint(0, 12, (B, W), generator=g, device="cuda") / 8.0
+    _check(vt, x, s, (1, 2, 3, 5, 8, 13, 32))
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 4])
