@@ -110,13 +110,17 @@ __device__ __forceinline__ uint32_t load_ahead(const void* p) {
   asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
+// A logit.  Not by a load that promises that nothing writes there while the kernel runs: the gradient
+// may take the logits' place.
 template <typename T>
-__device__ __forceinline__ float value_ahead(const T* p) {
+__device__ __forceinline__ float logit(const T* p) {
   if constexpr (sizeof(T) == 4) {
-    return __uint_as_float(load_ahead(p));
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return __uint_as_float(v);
   } else {
     uint16_t v;
-    asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
     return bf16_bits_to_float(v);
   }
 }
@@ -149,7 +153,7 @@ __device__ __forceinline__ void ds_values(const DsArgs& a, int64_t row, int lane
   const T* l = static_cast<const T*>(a.logits) + row * a.ld;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    e.z[h] = e.p[h] >= 0 ? value_ahead(l + e.p[h]) : -INFINITY;
+    e.z[h] = e.p[h] >= 0 ? logit(l + e.p[h]) : -INFINITY;
     e.lp[h] = e.p[h] >= 0 ? __uint_as_float(load_ahead(a.logp + row * a.k + lane + 32 * h)) : 0.f;
   }
 }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
   float xe = 0.f, z = 0.f, lp = 0.f;
   int p = -1;
   if (!nothing) {
-    if (edge) xe = Elem<T>::load(l + edge_id<VE>(sp, tid));
+    if (edge) xe = logit(l + edge_id<VE>(sp, tid));
     if (tid < a.k) {
       p = ds_place(a, (int64_t)row * a.k + tid);
       const int q = (p - sp.head) / VE;
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kDsNT) distill_grad_kernel(DsArgs a, int piece
       if (p >= 0 && (inner ? q / (kDsNT * kDgU) != piece : piece != 0)) p = -1;
       if (p >= 0) {
         lp = a.logp[(int64_t)row * a.k + tid];
-        z = Elem<T>::load(l + p);
+        z = logit(l + p);
         if (z == -INFINITY) p = -1;
       }
     }
@@ -776,7 +780,7 @@ __global__ void __launch_bounds__(kDtThreads<NW>, NW > kLpWarps ? 1 : H == 1 ? 3
           }
           listed = __reduce_or_sync(0xffffffffu, listed);
           edge.unlisted = edge.here && !(listed >> lane & 1);
-          if (edge.unlisted) edge.x = Elem<T>::load(l + edge_id<VE>(sp, lane));
+          if (edge.unlisted) edge.x = logit(l + edge_id<VE>(sp, lane));
           ends.m = warp_max_nan(edge.x);
           const float w = exp2_approx((edge.x - ends.m) * a.c);
           ends.s = ends.m == -INFINITY ? 0.f : warp_add(w);
