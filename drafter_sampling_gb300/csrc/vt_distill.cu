@@ -60,13 +60,16 @@ struct DsStats {
   float m, mr, c_all, c_rest, c_t;
 };
 
+// (128 bytes: with more of them the row kernels spill, 107 instead of 104 us for 1024 rows of 128256 bf16)
 struct DsArgs {
   const void* logits;
   int64_t ld;
   int R, K, V, k;
-  int rest;
+  bool rest;
+  bool own_status;         // one row: its block stores the status word; else it is zeroed beforehand
   float c;                 // log2(e) / T
-  Pair inv_t;              // 1 / T
+  Pair twice;              // 2 / T in units of `unit`, a power of two such that it is at most 1
+  float unit, inv_t;       // inv_t: 1 / T
   const int* ids;          // [R][k]
   const float* logp;       // [R][k]
   const int* inv_map;      // [V] or nullptr (V == K)
@@ -76,8 +79,13 @@ struct DsArgs {
   void* grad;
   int64_t ld_grad;
   int* dev_status;
-  int own_status;          // one row: its block stores the status word; else it is zeroed beforehand
 };
+
+static_assert(sizeof(DsArgs) <= 128, "");
+// 1 / a.unit
+__device__ __forceinline__ float ds_per_unit(const DsArgs& a) {
+  return __int_as_float(0x7f000000 - __float_as_int(a.unit));
+}
 
 // the place of list entry i in the drafter's vocabulary, -1 where it has none,
 // -2 where the id or the map is out of range
@@ -244,15 +252,19 @@ struct DsHead {
   float m;      // largest kept logit
   Pair S;       // sum of e^((z - m) / T) over the kept
   Pair mass;    // sum of t
-  Pair cross;   // sum of t (ln t - (z - m) / T)
+  Pair cross;   // sum of t (ln t - (z - m) / T), in units of DsArgs::unit
 };
 
-// (z - m) / T
-__device__ __forceinline__ Pair ds_below(float z, float m, Pair inv_t) {
+// (z - m) / T in units of a.unit: z - m may lie beyond fp32, its quotient too where T < 1, and what the
+// loss makes of them not.  (Halves differ exactly.)
+__device__ __forceinline__ Pair ds_below(const DsArgs& a, float z, float m) {
   Pair d;
-  two_sum(z, -m, d.h, d.l);
-  return pair_mul(d, inv_t);
+  two_sum(0.5f * z, -0.5f * m, d.h, d.l);
+  return pair_mul(d, a.twice);
 }
+__device__ __forceinline__ Pair pair_scale(Pair v, float f) { return Pair{v.h * f, v.l * f}; }  // f: a power of two
+// e^(y a.unit); 0 where fp32 has no such number
+__device__ __forceinline__ Pair ds_exp(const DsArgs& a, Pair y) { return pair_exp(pair_scale(y, a.unit)); }
 
 // (leaves the entries' weights 2^((z - m) c) in z and t in lp; both 0 where not kept)
 template <int H>
@@ -270,14 +282,13 @@ __device__ __forceinline__ DsHead ds_head(const DsArgs& a, DsEntries<H>& e, int 
     const bool kept = e.z[h] != -INFINITY;
     const float z = kept ? e.z[h] : m;
     const Pair lnt{kept ? e.lp[h] : -INFINITY, 0.f}, t = pair_exp(lnt);
-    const Pair y = ds_below(z, m, a.inv_t), d = pair_add(Pair{t.h > 0.f ? lnt.h : 0.f, 0.f}, pair_neg(y));
+    const Pair y = ds_below(a, z, m), d = pair_add(Pair{t.h > 0.f ? lnt.h * ds_per_unit(a) : 0.f, 0.f}, pair_neg(y));
     const Pair x = pair_mul(t, d);
     r.mass = pair_add(r.mass, t);
     r.cross = pair_add(r.cross, t.h > 0.f ? x : Pair{0.f, 0.f});
     e.lp[h] = t.h;
     // (a listed id's weight to its last place: the list usually has most of S)
-    Pair w = pair_exp(y);
-    if (!(kept && (z - m) * a.c > -125.f)) w = Pair{0.f, 0.f};
+    const Pair w = kept ? ds_exp(a, y) : Pair{0.f, 0.f};
     r.S = pair_add(r.S, w);
     e.z[h] = w.h;
   }
@@ -307,7 +318,7 @@ struct DsTotal {
 __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, const DsSum& un, DsStats& st) {
   DsTotal r{Pair{0.f, 0.f}, Pair{0.f, 0.f}, hd.flags | (un.late ? VT_DEV_TIMEOUT : 0), false};
   const bool rest = !(un.s == 0.f);  // (NaN: flagged below)
-  const float m = rest ? max_nan(hd.m, un.m) : hd.m, inv_t = a.inv_t.h;
+  const float m = rest ? max_nan(hd.m, un.m) : hd.m, inv_t = a.inv_t;
   st = DsStats{0.f, 0.f, 0.f, 0.f, 0.f};
   if (hd.kept && !(m < INFINITY)) r.flags |= VT_DEV_NONFINITE;
   if (r.flags) {
@@ -322,8 +333,7 @@ __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, c
   r.learns = true;
   // one of the two maxima is m
   const float lower = rest ? fminf(hd.m, un.m) : m;
-  r.w = pair_exp(ds_below(lower, m, a.inv_t));
-  if (!((lower - m) * a.c > -125.f)) r.w = Pair{0.f, 0.f};
+  r.w = ds_exp(a, ds_below(a, lower, m));
   const float top = rest ? un.m < m ? r.w.h : 1.f : 0.f;
   const float S = fmaf(un.s, top, hd.m < m ? hd.S.h * r.w.h : hd.S.h);
   st.m = m;
@@ -350,19 +360,19 @@ __device__ __forceinline__ float ds_loss(const DsArgs& a, const DsHead& hd, cons
   if (un.s > 0.f) S = pair_add(S, un.m < st.m ? pair_mul(sr, r.w) : sr);
   // four logarithms at once, one per lane
   Pair v = lane == 0 ? S : lane == 1 ? sr : lane == 2 ? r.b : hd.mass;
-  v = v.h > 0.f ? pair_log(v) : Pair{0.f, 0.f};
+  v = v.h > 0.f ? pair_scale(pair_log(v), ds_per_unit(a)) : Pair{0.f, 0.f};
   const Pair lnS = pair_from_lane(v, 0), lnr = pair_from_lane(v, 1), lnb = pair_from_lane(v, 2);
   const Pair lna = pair_from_lane(v, 3);
   // ln p = (z - hd.m) / T + shift
-  const Pair shift = pair_add(ds_below(hd.m, st.m, a.inv_t), pair_neg(lnS));
+  const Pair shift = pair_add(ds_below(a, hd.m, st.m), pair_neg(lnS));
   Pair sum = pair_add(hd.cross, pair_neg(pair_mul(hd.mass, shift)));
   if (!a.rest) {
     sum = pair_add(pair_div(sum, hd.mass), pair_neg(lna));
   } else if (r.b.h > 0.f) {
-    const Pair lnq = pair_add(pair_add(lnr, ds_below(un.m, st.m, a.inv_t)), pair_neg(lnS));
+    const Pair lnq = pair_add(pair_add(lnr, ds_below(a, un.m, st.m)), pair_neg(lnS));
     sum = pair_add(sum, pair_mul(r.b, pair_add(lnb, pair_neg(lnq))));
   }
-  return sum.h != sum.h ? INFINITY : sum.h;  // (a term beyond fp32: they are positive)
+  return sum.h != sum.h ? INFINITY : sum.h * a.unit;  // (NaN: a term beyond fp32; they are positive)
 }
 
 // Loss, statistics and flags of a row to where they go, by one thread
@@ -1018,10 +1028,14 @@ DsArgs ds_args(const void* logits, int64_t R, int32_t K, int64_t ld, const int32
   a.K = K;
   a.V = V;
   a.k = k;
-  a.rest = rest;
+  a.rest = rest != 0;
   a.c = VT_LOG2E / T;
-  a.inv_t.h = (float)(1.0 / (double)T);
-  a.inv_t.l = (float)(1.0 / (double)T - (double)a.inv_t.h);
+  double twice = 2.0 / (double)T;
+  a.unit = 1.f;
+  for (; twice > 1.0; twice *= 0.5) a.unit *= 2.f;
+  a.inv_t = (float)(1.0 / (double)T);
+  a.twice.h = (float)twice;
+  a.twice.l = (float)(twice - (double)a.twice.h);
   a.ids = ids;
   a.logp = logp;
   a.inv_map = inv_map;
