@@ -63,8 +63,10 @@ def distill(logits, top_ids, top_logp, inv_map=None, rest: bool = True, temperat
             b, lnq = 0.0, 0.0
             if rest and un.any() and d[un].max() > -np.inf:
                 b = max(0.0, 1.0 - a)
-                top = d[un].max()
-                lnq = top + np.log(np.exp(d[un] - top).sum()) - lse
+                # (relative to their own maximum: of lnp - lnq nothing is left where both are far from 0)
+                share = np.exp((z[r][un] - z[r][un].max()) / temperature)
+                lnq = d[un].max() + np.log(share.sum()) - lse
+                share /= share.sum()
             scale = 1.0 if rest else (1.0 / a if a > 0 else 0.0)
             if not (a + b > 0 and scale > 0):
                 continue
@@ -78,7 +80,7 @@ def distill(logits, top_ids, top_logp, inv_map=None, rest: bool = True, temperat
         pull = np.zeros(K)
         pull[at] = -t * scale
         if b > 0:
-            pull[un] = -b * np.exp(lnp[un] - lnq)
+            pull[un] = -b * share
         A = (a + b) * scale
         w = 1.0 if grad_loss is None else float(grad_loss[r])
         out["loss"][r] = loss

@@ -69,3 +69,27 @@ def test_differences_beyond_fp32(vt, dt, T, rest):
         assert np.isposinf(got[over]).all()
         assert np.all(np.abs(got - ref)[big] <= 2.0 ** -23 * np.abs(ref[big]) + 4 * E + 2.0 ** -25)
     assert bool(stats.isfinite().all()) and bool(s2.isfinite().all())
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [0.3, 0.7, 1.0, 4.0, 1e30])
+@pytest.mark.parametrize("rest", [True, False])
+def test_gradients_of_such_rows(vt, dt, T, rest):
+    """Each is A p_j minus what the teacher pulls, both off by E, by their exponential (4 u, and three roundings
+    of |z - max| / T, u = 2^-24) and by 6 roundings, the rest's pull by 2^-27 / q p_j more; then rounded
+    to the logits' type."""
+    x, ids, lnt = _rows(dt)
+    u = 2.0 ** -24
+    h = lambda t: t.float().cpu().numpy()  # noqa: E731
+    T32 = float(np.float32(T))
+    ref = distill(h(x), ids.cpu().numpy(), h(lnt), None, rest, T32)
+    z = h(x).astype(np.float64)
+    d = np.minimum((z.max(1, keepdims=True) - z) / T32, 300.0)
+    E, q = u * (700 / 256 + 90), np.exp(np.clip(ref["lnq"], -600, 0))[:, None]
+    more = np.where((ref["left"][:, None] > 0) & (ref["pull"] < 0), 2.0 ** -27 * np.minimum(ref["p"] / q, 1.0), 0.0)
+    tol = ((ref["p"] + np.abs(ref["pull"])) * (E + u * (10 + 3 * d)) + more) / T32 + 1e-37
+    tol += np.abs(ref["grad"]) * (2.0 ** -8 if dt == torch.bfloat16 else u)
+    _, stats, _ = vt.vt_distill_loss(x, ids, lnt, rest=rest, temperature=T)
+    for g in (vt.vt_distill_grad(x, ids, lnt, stats, temperature=T),
+              vt.vt_distill_loss_grad(x, ids, lnt, rest=rest, temperature=T)[1]):
+        assert np.all(np.abs(h(g).astype(np.float64) - ref["grad"]) <= tol)
