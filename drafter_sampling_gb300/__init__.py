@@ -777,7 +777,8 @@ def vt_beam_select(logits, scores, n: int, temperature: float = 1.0, trim_ids=No
     outputs overlap no input.
     Returns (scores, parent int32, tokens int32, done or None, dev_status), each
     [B, n], best first, ties to the lower beam and index; done where end_id >= 0.
-    Missing continuations have score -inf, parent -1 and token -1.
+    Missing continuations have score -inf, parent -1 and token -1.  Equal and nearly
+    equal beams (within 1e-5) are ordered in 64 bits, for which their rows are read again.
     """
     dev = _first(logits, "logits")
     dt, shape, _, K, ld = _logit_rows(logits)
@@ -987,7 +988,9 @@ def vt_distill_loss(logits, top_ids, top_logp, inv_map=None, rest: bool = True, 
     (vt_trim_head's) takes the teacher's ids to the drafter's, -1 where it has none.
     rest: what the listed ids leave of either distribution counts as one more outcome; otherwise
     the teacher is renormalised over the ids listed.  Rows with nothing to learn have loss 0.
-    Returns (loss, stats, dev_status); stats [..., 5] is what vt_distill_grad needs.
+    Returns (loss, stats, dev_status); stats [..., 5] is what vt_distill_grad needs.  As with every call of
+    this package, autograd does not see it: the results carry no graph, whether logits require a
+    gradient or not, and the backward pass is vt_distill_grad.
     """
     dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
     if out_loss is None:
@@ -1009,7 +1012,8 @@ def vt_distill_grad(logits, top_ids, top_logp, stats, grad_loss=None, inv_map=No
                     temperature: float = 1.0, out_grad=None, stream=None):
     """The gradient of vt_distill_loss with respect to the logits, from the same arguments and the
     statistics it returned; grad_loss float32 of logits' leading shape (None: 1) is dL/dloss.
-    out_grad, of logits' shape and type, may be logits itself.  Returns out_grad."""
+    out_grad, of logits' shape and type, may be logits itself.  Returns out_grad, for the caller
+    to pass on (torch.autograd.backward(logits, out_grad), or a product with the hidden states)."""
     dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
     gp = _arg(grad_loss, "grad_loss", _F32, shape, dev) if grad_loss is not None else None
     out_grad, op, ldg = _grad_out(out_grad, logits, shape, R, K, dev, stream)
@@ -1025,7 +1029,7 @@ def vt_distill_loss_grad(logits, top_ids, top_logp, grad_loss=None, inv_map=None
                          dev_status=None, stream=None):
     """vt_distill_loss and vt_distill_grad in one call: a training step that knows each row's weight
     grad_loss beforehand.  Rows that fit on the chip are read once.  Returns (loss, grad, stats,
-    dev_status)."""
+    dev_status), none of which autograd knows of (see vt_distill_loss)."""
     dev, dt, shape, R, K, ld, ip, lp, k, mp, V = _teacher(logits, top_ids, top_logp, inv_map)
     gp = _arg(grad_loss, "grad_loss", _F32, shape, dev) if grad_loss is not None else None
     if out_loss is None:

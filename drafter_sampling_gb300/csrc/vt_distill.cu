@@ -22,13 +22,13 @@
 // per row by the loss.
 //
 // The loss reads R K logits once and is bound by HBM in the middle of a launch: 2304 rows of 38016
-// bf16 logits 39.6 us (4.4 TB/s; 25.9 at the measured copy rate), of which 3 to the first chunk, 3 for
+// bf16 logits 39.8 us (4.4 TB/s; 25.9 at the measured copy rate), of which 3 to the first chunk, 3 for
 // the last rows' statistics and losses, and a sixth round of rows for 24 of 456 blocks.  112
-// rows of 128256 fp32, 59 of them scored: 12.4 (latencies; 4.5 by bytes).  The gradient alone reads and
-// writes them: the same bf16 rows 54.6 (6.4 TB/s).  Both in one call read and write once: 2048 rows of
-// 32768 fp32 92.5 us (5.8 TB/s; 79 by bytes), 1024 rows of 128256 bf16, 576 scored, 103 (60.6 by bytes):
-// there a row's two passes of exponentials take 2/3 of its turn, a block's warps idle in the rest.
-// All in graphs of calls.
+// rows of 128256 fp32, 59 of them scored: 12.5 (latencies; 4.5 by bytes).  The gradient alone reads and
+// writes them: the same bf16 rows 54.9 (6.4 TB/s), 58.8 in the logits' place.  Both in one call read and
+// write once: 2048 rows of 32768 fp32 92.4 us (5.8 TB/s; 79 by bytes), in place 93.4; 1024 rows of 128256 bf16,
+// 576 scored, 104 (60.9 by bytes), in place as well: there a row's two passes of exponentials take 2/3 of its
+// turn, a block's warps idle in the rest.  All in graphs of calls.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -314,7 +314,9 @@ struct DsTotal {
   int flags;
   bool learns;
 };
-// The consuming warps wait for this, so it is plain fp32 but for the exponential and b: a few roundings.
+// The consuming warps wait for this, so it is plain fp32 but for the exponential and b: a few roundings.  Those
+// of c_all and c_rest are common to a row; where drafter and teacher agree on the rest, c_rest is a small difference and
+// every unlisted id's gradient is off by them, and by the sums' own roundings, in one direction.
 __device__ __forceinline__ DsTotal ds_stats(const DsArgs& a, const DsHead& hd, const DsSum& un, DsStats& st) {
   DsTotal r{Pair{0.f, 0.f}, Pair{0.f, 0.f}, hd.flags | (un.late ? VT_DEV_TIMEOUT : 0), false};
   const bool rest = !(un.s == 0.f);  // (NaN: flagged below)
@@ -1072,7 +1074,7 @@ constexpr int kDtBytes[3] = {64 << 10, 100 << 10, 200 << 10};
 // With the gradient a part is one chunk, two or three of them are in work.  A turn costs about 2500
 // cycles besides its bytes, and clusters of many blocks do not fill the device (76 pairs fit where 51
 // clusters of eight do), so: whole rows in one block where they fit (several on an SM), else few large
-// parts.  us at 2048 rows of 32768 fp32 logits: 2 blocks with 3 x 64 KB 89, 4 with 3 x 32 89 (two on an
+// parts.  us, before the loss's sums were pairs, at 2048 rows of 32768 fp32 logits: 2 blocks with 3 x 64 KB 89, 4 with 3 x 32 89 (two on an
 // SM), 4 with 2 x 32 102 (three), 6 with 3 x 21 127.  2304 rows of 32003 bf16: 1 with 3 x 64 62, 2 with
 // 3 x 32 75, 3 with 3 x 21 80.  4000 rows of 2000 fp32: three blocks on an SM 34, two 39, one 57.
 // false: the row does not fit.
@@ -1097,8 +1099,10 @@ bool dt_plan_grad(int64_t R, int64_t bytes, DtPlan& p) {
 
 // Without it a block streams its part through two chunks of 32 KB, three blocks on an SM.  The number of
 // blocks to a row is the one with the shortest schedule, a turn taking its chunks and one more, or two
-// where sums go between blocks (2304 rows of 38016 bf16 logits: 1 block 37 us, 2 43, 3 47; 112 rows of
-// 128256 fp32, 59 of them scored: 3 blocks 11.8 us, 4 10.4, 8 11.2).
+// where sums go between blocks (before the loss's sums were pairs, 2304 rows of 38016 bf16 logits: 1 block
+// 37 us, 2 43, 3 47; 112 rows of 128256 fp32, 59 of them scored: 3 blocks 11.8 us, 4 10.4, 8 11.2).  Lists of
+// more than 32 leave room for two blocks on an SM only.  The schedule counts three for them too: counted as two, 160 rows
+// of 38016 bf16 take 10.6 instead of 11.4 us and 60 of 128256 12.5 instead of 11.5.
 DtPlan dt_plan_loss(int64_t R, int64_t bytes) {
   DtPlan p;
   p.tier = 0;

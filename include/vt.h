@@ -478,9 +478,12 @@ int vt_token_logprobs(const void* logits, int32_t logits_dtype, int64_t R, int32
  *
  * Candidate j of beam w scores scores[b, w] + ln softmax(logits[b, w] / T)[j].
  * The n best are returned best first, ties to the lower beam, then to the lower
- * index.  Scores are compared in 64 bits and rounded to fp32 once, at the end;
- * two of different beams that are within 1e-8 of each other, but not equal, may
- * come in either order.
+ * index.  Scores are compared in 64 bits and rounded to fp32 once, at the end (a
+ * score below fp32's range becomes -infinity, its parent and token are given all
+ * the same); two of different beams that are within 1e-8 of each other, but not
+ * equal, may come in either order.  Beams with candidates within 1e-5 of each
+ * other that decide the result are read once more, one after another, which takes
+ * longer than the rest of the call.
  *
  *  logits     [B, W, K], row stride ld_logits >= K, of logits_dtype; aligned to
  *                          its element type, no more
@@ -563,19 +566,23 @@ int vt_beam_reorder(const void* state, void* out, const int64_t* strides, const 
  *  out_loss   f32 [R]        out
  *  out_stats  f32 [R, 5]     out: what the gradient needs: the largest logit of the
  *                            row and that of its unlisted ids, and the factors of
- *                            2^(z - largest), of the same for unlisted ids, and of
- *                            t; zeros where the gradient is 0
- *  grad_loss  f32 [R]        may be NULL (1): dL/dloss of each row
+ *                            e^((z - largest) / T), of the same for unlisted ids,
+ *                            and of t; zeros where the gradient is 0
+ *  grad_loss  f32 [R]        may be NULL (1): dL/dloss of each row.  The gradient's
+ *                            factors are fp32: grad_loss / T, over a with rest = 0,
+ *                            has to stay within it
  *  out_grad   [R, ld_grad]   out: dL/dlogits, of logits_dtype (bf16: rounded to
  *                            nearest even, once); the logits' own buffer (with
  *                            their stride), or one that does not overlap it
  *  dev_status int32 [1]      out: VT_DEV_BAD_ID (an id outside [-1, V), or an
  *                            inv_map value outside [-1, K)), VT_DEV_DUPLICATE_ID (two
  *                            kept entries for one id), VT_DEV_NONFINITE (a logit that
- *                            is NaN or +infinity, a kept ln t that is NaN or not
- *                            below 80): NaN in that row's loss, statistics, gradient
- *                            (all of it); VT_DEV_TIMEOUT likewise.  A t below 1e-37
- *                            counts as 0
+ *                            is NaN or +infinity in a row that keeps an entry, a kept
+ *                            ln t that is NaN or not below 80): NaN in that row's loss,
+ *                            statistics, gradient (all of it); VT_DEV_TIMEOUT
+ *                            likewise.  A t below 1e-37 counts as 0
+ * A loss beyond fp32 is +infinity.  Of the outputs only out_grad may take an input's
+ * place, the logits'.
  * vt_distill_loss gives loss and statistics, vt_distill_grad the gradient from the
  * same arguments and those statistics, vt_distill_loss_grad all of it.
  * 1 <= k <= 128, 1 <= K <= 2^22, 1 <= R <= 2^24, 1e-30 <= T <= 1e30.  No workspace.
