@@ -18,7 +18,7 @@
 //
 // The rows are streamed as the log probabilities' are: a cluster of up to 8 blocks to a row where rows
 // are few, one persistent block for row after row where they are many.  256 x 8 beams over 38016 fp32
-// logits, 8 best: 55.2 us in a graph of calls (5.6 TB/s; 45.9 at the measured copy rate): about 53 of rows
+// logits, 8 best: 55.2 us in a graph of calls (5.6 TB/s; 45.9 at the measured copy rate): 53.8 of rows alone
 // (DRAM at 74%, issue slots at 58%; 4.5 rows a block are five rounds) and what the merge's start under
 // them does not hide of its 7.  16 x 8 beams over 32768: 11.2, one row of 32768: 7.9, latencies:
 // 5 to 8 of rows, 3 of the merge, whose lists start with logarithms by pairs of fp32 values (in fp64 it
